@@ -350,6 +350,181 @@ int topk_segmented_i32(const int32_t *in, int64_t n, const int64_t *offsets,
 int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
                   int32_t nbins, int64_t *out, libtopk_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators on a paged key-value cache of a decoder: attention of one new
+ * token, append, and eviction by accumulated attention weight.
+ *
+ * The cache holds K and V rows of `dim` elements in pages of `page` slots.
+ * Sequence b's slot t (0 <= t < lens[b]) of head h is the row at
+ *
+ *     k + table[b * table_stride + t / page] * k_page_stride
+ *       + h * k_head_stride + (t % page) * k_slot_stride      (elements)
+ *
+ * and likewise in v, so both orders within a page (heads outside slots, or
+ * slots outside heads) and any padding are strides.  `lens` and `table` are
+ * read on the device: no call needs a length on the host.
+ *
+ *  - A length is read as if clamped to [0, table_width * page] (and to the
+ *    slots of the ledger, where a call takes one).
+ *  - A table entry outside [0, pages) names no page.  Attention leaves its
+ *    slots out (score -infinity, weight unchanged), append and evict neither
+ *    read nor write rows there.  Nothing outside the given arrays is ever
+ *    read or written.
+ *  - Pages that append or evict write to must belong to one sequence alone;
+ *    attention may share them.
+ *
+ * Workspace: per (device, stream), grown on demand by doubling; an area is
+ * kept until cache_release() (or process exit) once it has been used, so a
+ * captured graph that uses it stays valid.  Under stream capture nothing is
+ * allocated: a call that needs a larger area then returns LIBTOPK_ERR_NOMEM,
+ * so make one call of the same sizes on the stream before capturing it.  A
+ * captured graph uses the workspace of the stream that it was captured on:
+ * its replays must not overlap with calls on that stream.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of queries and cache rows. */
+enum {
+    LIBTOPK_BF16 = 0,
+    LIBTOPK_F16 = 1,
+    LIBTOPK_E4M3 = 2 /* 8-bit float, 4 exponent bits, no infinity; cache only */
+};
+
+/* Largest row length of a cache. */
+#define LIBTOPK_MAX_DIM 256
+
+typedef struct libtopk_cache {
+    void *k; /* device, 16-byte aligned */
+    void *v;
+    int64_t k_page_stride, k_head_stride, k_slot_stride; /* elements; each a */
+    int64_t v_page_stride, v_head_stride, v_slot_stride; /* multiple of 16 B */
+    int64_t pages;        /* pages of k and of v, 0 <= pages < 2^31       */
+    int64_t table_stride; /* entries between two sequences' table rows    */
+    const int32_t *table; /* device, int32[batch][table_width]            */
+    const int32_t *lens;  /* device, int32[batch]: slots in use           */
+    int32_t batch;        /* 0 <= batch                                   */
+    int32_t table_width;  /* 1 <= table_width; table_width * page < 2^30  */
+    int32_t heads;        /* 1 <= heads <= 65535                          */
+    int32_t page;         /* slots of a page, 1 <= page                   */
+    int32_t dim;          /* 1 <= dim <= LIBTOPK_MAX_DIM, rows of a whole
+                             number of 16-byte units                      */
+    int32_t dtype;        /* LIBTOPK_BF16, LIBTOPK_F16 or LIBTOPK_E4M3    */
+} libtopk_cache_t;
+
+/* What is kept for every slot besides its rows: the attention weight that it
+ * has drawn, and its token's position.  Entry t of sequence b, head h is
+ * weights[b * weights_batch_stride + h * weights_head_stride + t]. */
+typedef struct libtopk_ledger {
+    float *weights;     /* device */
+    int32_t *positions; /* device */
+    int64_t weights_batch_stride, weights_head_stride;
+    int64_t positions_batch_stride, positions_head_stride;
+    int32_t slots; /* entries of a row, >= 1 */
+} libtopk_ledger_t;
+
+/*
+ * cache_attend -- attention of one new token a sequence over its slots.
+ * q_heads / heads consecutive query heads share a head of the cache (query
+ * head j reads head j / (q_heads / heads)).  With x[j][t] = scale *
+ * k_scale[h] * (q[b][j] . K[b][h][t]) over the slots t of sequence b:
+ *
+ *     lse[b][j] = ln sum_t exp x[j][t]
+ *     out[b][j] = v_scale[h] * sum_t exp(x[j][t] - lse[b][j]) V[b][h][t]
+ *     weights[b][h][t] += sum_{j of h} exp(x[j][t] - lse[b][j])
+ *
+ * A sequence with no slot gets out = 0 and lse = -infinity.  Scores, sums and
+ * the running output are float32; only out is rounded, once.  Results do not
+ * depend on the order in which workgroups run.
+ *
+ *   q        device, q_dtype (LIBTOPK_BF16 or LIBTOPK_F16; the cache's own,
+ *            or either over an LIBTOPK_E4M3 cache), 16-byte aligned, element
+ *            strides q_batch_stride and q_head_stride (multiples of 8)
+ *   q_heads  a positive multiple of cache->heads
+ *   k_scale, v_scale   device, float32[heads], or NULL for 1
+ *   ledger   NULL, or where the weights are accumulated (positions unused)
+ *   out      device, q_dtype[batch][q_heads][dim], contiguous, 16-byte
+ *            aligned
+ *   lse      device, float32[batch][q_heads], contiguous
+ *
+ * Workspace: partial results of at most 1024 workgroups, and with a ledger
+ * one float32 a query head and slot of the table's width.
+ *
+ * Errors: LIBTOPK_ERR_INVALID for a NULL or misaligned pointer, a size,
+ * stride or type outside the above, or outputs that overlap an input.
+ */
+int cache_attend(const libtopk_cache_t *cache, const void *q, int32_t q_dtype,
+                 int32_t q_heads, int64_t q_batch_stride,
+                 int64_t q_head_stride, float scale, const float *k_scale,
+                 const float *v_scale, const libtopk_ledger_t *ledger,
+                 void *out, float *lse, libtopk_stream_t stream);
+
+/*
+ * cache_append -- the new token's rows enter the cache.  For sequence b and
+ * head h, slot s = lens[b] while lens[b] < limit; afterwards the slot that is
+ * last in the order of retention among the lens[b] in use:
+ *
+ *     t comes before u when key(t) > key(u), or key(t) = key(u) and t < u;
+ *     key(t) = the largest int32 for a protected slot (its position below
+ *     `sinks`, or at least seen[b] - recent), otherwise weights[b][h][t] in
+ *     the order-preserving map of float32 bits to int32 (numerical order;
+ *     NaN beyond the infinity of its sign).
+ *
+ * The rows of slot s become k_new[b][h] and v_new[b][h], its weight 0 and its
+ * position seen[b].  out_slots[b][h] = s, and out_lens[b] = lens[b] + 1 if
+ * lens[b] < limit, otherwise lens[b].  Where slot s would lie beyond the table
+ * or the ledger, nothing is written, out_slots is -1 and the length stays.
+ * A replaced slot whose table entry names no page loses weight and position
+ * as any other; only its rows are written nowhere.
+ *
+ *   k_new, v_new   device, the cache's type, 16-byte aligned, element strides
+ *                  new_batch_stride and new_head_stride (multiples of 16 B)
+ *   limit    >= 1 slots
+ *   seen     device, int32[batch]: tokens before this one (its position)
+ *   ledger   weights and positions, both updated in place
+ *   sinks, recent   >= 0
+ *   out_lens   device, int32[batch]; may not be cache->lens
+ *   out_slots  device, int32[batch][heads]
+ *
+ * Errors: as cache_attend.
+ */
+int cache_append(const libtopk_cache_t *cache, const void *k_new,
+                 const void *v_new, int64_t new_batch_stride,
+                 int64_t new_head_stride, int32_t limit, const int32_t *seen,
+                 const libtopk_ledger_t *ledger, int32_t sinks, int32_t recent,
+                 int32_t *out_lens, int32_t *out_slots,
+                 libtopk_stream_t stream);
+
+/*
+ * cache_evict -- cut every sequence back to its `keep` first slots in the
+ * order of retention (see cache_append), each head for itself.  The kept slots
+ * below `keep` stay where they are; the i-th kept slot at or beyond `keep`
+ * (ascending) moves, rows, weight and position, to the i-th slot below `keep`
+ * that is not kept (ascending).  Sequences of at most `keep` slots do not
+ * change.
+ *
+ * weights and positions of `after` get the `keep` entries of every row
+ * (entries past the new length: 0 and -1); out_lens[b] = min(lens[b], keep).
+ * `ledger` is only read.
+ *
+ *   keep     1 <= keep <= after->slots
+ *   after    device arrays that overlap neither the ledger nor each other
+ *   out_lens device, int32[batch]; may not be cache->lens
+ *
+ * Errors: as cache_attend.
+ */
+int cache_evict(const libtopk_cache_t *cache, const int32_t *seen,
+                const libtopk_ledger_t *ledger, int32_t keep, int32_t sinks,
+                int32_t recent, const libtopk_ledger_t *after,
+                int32_t *out_lens, libtopk_stream_t stream);
+
+/* Free the workspaces of the cache_* calls after synchronising their
+ * devices.  Must not race with other calls, nor precede the replay of a graph
+ * that captured one. */
+void cache_release(void);
+
+/* Test hook, as libtopk_debug_scramble: overwrite the completion tickets of
+ * the cache_* calls on `stream` with pseudo-random words. */
+int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
+
 /* Static, human-readable text for a status code (never NULL). */
 const char *libtopk_strerror(int status);
 

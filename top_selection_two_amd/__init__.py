@@ -26,6 +26,16 @@ if the library is not built, importing this package raises.
     topk_segmented(x, offsets, k)
                     -> (int32 [nseg, k], int32 counts [nseg]): the top-k of
                        every segment x[offsets[s] .. offsets[s+1])
+    cache_attend(q, k, v, table, lens, ...)
+                    -> (out [B, Hq, D], lse [B, Hq]): attention of one new
+                       token a sequence over a paged key-value cache
+    cache_append(k_new, v_new, k, v, table, lens, ...)
+                    -> (lens [B], slots [B, H]): the new token's rows enter
+                       the cache, in a full one in the place of the slot of
+                       the lowest accumulated attention weight
+    cache_evict(k, v, table, lens, seen, weights, positions, keep, ...)
+                    -> (weights [B, H, keep], positions, lens [B]): the cache
+                       cut back to the slots of the largest weight
 """
 from __future__ import annotations
 
@@ -40,9 +50,38 @@ MAX_K_SELECT = 16384   # LIBTOPK_MAX_K_SELECT: largest k of topk()
 MAX_BINS = 4096        # LIBTOPK_MAX_BINS
 SUM, MAX, MIN = 0, 1, 2
 OPS = {"sum": SUM, "max": MAX, "min": MIN}
+BF16, F16, E4M3 = 0, 1, 2   # element types of a cache
+MAX_DIM = 256               # LIBTOPK_MAX_DIM
+
+_VP = ctypes.c_void_p
+
+
+class CacheStruct(ctypes.Structure):
+    """libtopk_cache_t of include/libtopk.h."""
+    _fields_ = ([("k", _VP), ("v", _VP)]
+                + [(n, ctypes.c_int64) for n in
+                   ("k_page_stride", "k_head_stride", "k_slot_stride",
+                    "v_page_stride", "v_head_stride", "v_slot_stride",
+                    "pages", "table_stride")]
+                + [("table", _VP), ("lens", _VP)]
+                + [(n, ctypes.c_int32) for n in
+                   ("batch", "table_width", "heads", "page", "dim",
+                    "dtype")])
+
+
+class LedgerStruct(ctypes.Structure):
+    """libtopk_ledger_t of include/libtopk.h."""
+    _fields_ = ([("weights", _VP), ("positions", _VP)]
+                + [(n, ctypes.c_int64) for n in
+                   ("weights_batch_stride", "weights_head_stride",
+                    "positions_batch_stride", "positions_head_stride")]
+                + [("slots", ctypes.c_int32)])
+
+
+_CACHE = ctypes.POINTER(CacheStruct)
+_LEDGER = ctypes.POINTER(LedgerStruct)
 
 # Entry points of include/libtopk.h with their ctypes signatures.
-_VP = ctypes.c_void_p
 SIGNATURES = {
     "topk_i32": ([_VP, ctypes.c_int64, ctypes.c_int32, _VP, _VP],
                  ctypes.c_int),
@@ -64,6 +103,16 @@ SIGNATURES = {
                             ctypes.c_int32, _VP, _VP, _VP], ctypes.c_int),
     "histogram_i32": ([_VP, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32,
                        ctypes.c_int32, _VP, _VP], ctypes.c_int),
+    "cache_attend": ([_CACHE, _VP, ctypes.c_int32, ctypes.c_int32,
+                      ctypes.c_int64, ctypes.c_int64, ctypes.c_float, _VP,
+                      _VP, _LEDGER, _VP, _VP, _VP], ctypes.c_int),
+    "cache_append": ([_CACHE, _VP, _VP, ctypes.c_int64, ctypes.c_int64,
+                      ctypes.c_int32, _VP, _LEDGER, ctypes.c_int32,
+                      ctypes.c_int32, _VP, _VP, _VP], ctypes.c_int),
+    "cache_evict": ([_CACHE, _VP, _LEDGER, ctypes.c_int32, ctypes.c_int32,
+                     ctypes.c_int32, _LEDGER, _VP, _VP], ctypes.c_int),
+    "cache_release": ([], None),
+    "cache_debug_scramble": ([_VP, ctypes.c_uint64], ctypes.c_int),
     "libtopk_strerror": ([ctypes.c_int], ctypes.c_char_p),
     "libtopk_max_k": ([], ctypes.c_int),
     "libtopk_set_grid": ([ctypes.c_int32], ctypes.c_int),
@@ -123,18 +172,22 @@ def grid_for(n: int) -> int:
 
 
 def release() -> None:
+    """Free every scratch area and workspace of the library."""
     lib.libtopk_release()
+    lib.cache_release()
 
 
 def debug_scramble(which: int = 0, seed: int = 1, stream: int | None = None):
     """Overwrite the tickets and histogram counters that later calls on the
     current stream (which=0) or topk_i32_noalloc (which=1) use with
-    pseudo-random words: no result may depend on them (a test hook)."""
+    pseudo-random words: no result may depend on them (a test hook).
+    which=2: the tickets of the cache_* calls on the current stream."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream().cuda_stream
-    rc = lib.libtopk_debug_scramble(stream or None, which,
-                                    seed & (2 ** 64 - 1))
+    seed &= 2 ** 64 - 1
+    rc = (lib.cache_debug_scramble(stream or None, seed) if which == 2 else
+          lib.libtopk_debug_scramble(stream or None, which, seed))
     if rc != OK:
         raise LibtopkError(rc, "libtopk_debug_scramble")
 
@@ -446,3 +499,234 @@ def histogram(x, lo: int, shift: int, nbins: int, out=None):
     if rc != OK:
         raise LibtopkError(rc, "histogram_i32")
     return out
+
+
+# ------------------------------------------------- paged key-value cache
+# Checked on the host, from metadata alone: shapes, types, strides, and last
+# that the tensors are a GPU's.  (Length, table and position values stay on
+# the device; the kernels bound what they read there.)
+def _tensor(x, name, dtype, shape, device, dense=True):
+    import torch
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor" % name)
+    if x.dtype != dtype:
+        raise TypeError("%s: expected %s, got %s" % (name, dtype, x.dtype))
+    if x.device != device:
+        raise ValueError("%s: expected a tensor on %s, got %s"
+                         % (name, device, x.device))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError("%s: expected shape %s, got %s"
+                         % (name, tuple(shape), tuple(x.shape)))
+    if dense and not x.is_contiguous():
+        raise ValueError("%s: expected a contiguous tensor" % name)
+
+
+def _ptr(x):
+    return None if x is None else x.data_ptr() or None
+
+
+def _stride(x, i):
+    return x.stride(i) if x.size(i) > 1 else 0
+
+
+def _cache_struct(k, v, table, lens):
+    import torch
+    dtypes = {torch.bfloat16: BF16, torch.float16: F16,
+              torch.float8_e4m3fn: E4M3}
+    for x, name in ((k, "k"), (v, "v")):
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("%s: expected a torch.Tensor" % name)
+        if x.dtype not in dtypes:
+            raise TypeError("%s: expected bfloat16, float16 or float8_e4m3fn,"
+                            " got %s" % (name, x.dtype))
+        if x.dim() != 4:
+            raise ValueError("%s: expected [pages, heads, page, dim]" % name)
+        if x.size(1) < 1 or x.size(2) < 1 or x.size(3) < 1:
+            raise ValueError("%s: no axis but the pages may be empty" % name)
+        if x.size(3) > 1 and x.stride(3) != 1:
+            raise ValueError("%s: expected unit stride in the last axis"
+                             % name)
+    _tensor(v, "v", k.dtype, k.shape, k.device, dense=False)
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("table: expected [batch, pages of a sequence]")
+    batch, width = table.shape
+    _tensor(table, "table", torch.int32, (batch, width), k.device,
+            dense=False)
+    if width < 1 or (width > 1 and table.stride(1) != 1):
+        raise ValueError("table: expected at least one column, unit stride")
+    _tensor(lens, "lens", torch.int32, (batch,), k.device)
+    if k.size(3) > MAX_DIM or k.size(3) * k.element_size() % 16:
+        raise ValueError("rows of %d elements of %s: expected at most %d and "
+                         "a multiple of 16 bytes"
+                         % (k.size(3), k.dtype, MAX_DIM))
+    return CacheStruct(
+        k=_ptr(k), v=_ptr(v),
+        k_page_stride=_stride(k, 0), k_head_stride=_stride(k, 1),
+        k_slot_stride=_stride(k, 2),
+        v_page_stride=_stride(v, 0), v_head_stride=_stride(v, 1),
+        v_slot_stride=_stride(v, 2),
+        pages=k.size(0), table_stride=_stride(table, 0), table=_ptr(table),
+        lens=_ptr(lens), batch=batch, table_width=width, heads=k.size(1),
+        page=k.size(2), dim=k.size(3), dtype=dtypes[k.dtype])
+
+
+def _ledger_struct(weights, positions, c, device, names):
+    """weights (and positions) [batch, heads, slots], unit stride in slots."""
+    import torch
+    slots = None
+    for x, name, dtype in ((weights, names[0], torch.float32),
+                           (positions, names[1], torch.int32)):
+        if x is None:
+            continue
+        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+            raise ValueError("%s: expected [batch, heads, slots]" % name)
+        slots = x.size(2) if slots is None else slots
+        _tensor(x, name, dtype, (c.batch, c.heads, slots), device,
+                dense=False)
+        if slots < 1 or (slots > 1 and x.stride(2) != 1):
+            raise ValueError("%s: expected at least one slot, unit stride"
+                             % name)
+    p = positions
+    return LedgerStruct(
+        weights=_ptr(weights), positions=_ptr(p),
+        weights_batch_stride=_stride(weights, 0),
+        weights_head_stride=_stride(weights, 1),
+        positions_batch_stride=_stride(p, 0) if p is not None else 0,
+        positions_head_stride=_stride(p, 1) if p is not None else 0,
+        slots=slots)
+
+
+def _int32(x, name, least):
+    x = int(x)
+    if not least <= x < 2 ** 31:
+        raise ValueError("%s: expected %d .. 2^31 - 1, got %d"
+                         % (name, least, x))
+    return x
+
+
+def _cache_call(name, device, *args):
+    import torch
+    if device.type != "cuda":
+        raise ValueError("expected device tensors, got %s" % device)
+    with torch.cuda.device(device):
+        stream = torch.cuda.current_stream(device).cuda_stream
+        rc = getattr(lib, name)(*args, stream or None)
+    if rc != OK:
+        raise LibtopkError(rc, name)
+
+
+def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
+                 v_scale=None, out=None):
+    """Attention of one new token a sequence over its slots in a paged cache
+    (see cache_attend in include/libtopk.h).
+
+    q [B, Hq, D] (bfloat16 or float16); k, v [pages, H, page, D] of q's type
+    or float8_e4m3fn, any strides that are multiples of 16 bytes (a cache
+    stored [pages, page, H, D] is passed as its transpose(1, 2)); table
+    [B, width] int32 pages of each sequence; lens [B] int32 slots in use;
+    scale of the scores (default D ** -0.5); k_scale, v_scale float32 [H]
+    factors of the rows.  weights float32 [B, H, slots] gets each slot's
+    attention weights, summed over the Hq / H queries of its head, added in
+    place.  Returns (out [B, Hq, D] of q's type, lse float32 [B, Hq]); out
+    may be given as that pair of tensors."""
+    import torch
+    c = _cache_struct(k, v, table, lens)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected [batch, query heads, dim]")
+    heads = q.size(1)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("q: expected bfloat16 or float16, got %s" % q.dtype)
+    if c.dtype != E4M3 and q.dtype != k.dtype:
+        raise TypeError("q is %s, the cache %s" % (q.dtype, k.dtype))
+    _tensor(q, "q", q.dtype, (c.batch, heads, c.dim), k.device, dense=False)
+    if heads < 1 or heads % c.heads:
+        raise ValueError("q: %d query heads over %d heads" % (heads, c.heads))
+    if c.dim > 1 and q.stride(2) != 1:
+        raise ValueError("q: expected unit stride in the last axis")
+    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if x is not None:
+            _tensor(x, name, torch.float32, (c.heads,), k.device)
+    ledger = None
+    if weights is not None:
+        ledger = _ledger_struct(weights, None, c, k.device,
+                                ("weights", "positions"))
+    if out is None:
+        o = torch.empty((c.batch, heads, c.dim), dtype=q.dtype,
+                        device=k.device)
+        lse = torch.empty((c.batch, heads), dtype=torch.float32,
+                          device=k.device)
+    else:
+        o, lse = out
+        _tensor(o, "out", q.dtype, (c.batch, heads, c.dim), k.device)
+        _tensor(lse, "lse", torch.float32, (c.batch, heads), k.device)
+    _cache_call("cache_attend", k.device, c, _ptr(q),
+                BF16 if q.dtype == torch.bfloat16 else F16, heads,
+                _stride(q, 0), _stride(q, 1),
+                c.dim ** -0.5 if scale is None else float(scale),
+                _ptr(k_scale), _ptr(v_scale), ledger, _ptr(o), _ptr(lse))
+    return o, lse
+
+
+def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
+                 positions, sinks=0, recent=0):
+    """The new token's rows k_new, v_new [B, H, D] (the cache's type) enter
+    the cache (see cache_append in include/libtopk.h): at slot lens[b] while
+    lens[b] < limit, afterwards in the place of the slot of the lowest
+    accumulated weight that is not protected (position < sinks or
+    >= seen[b] - recent).  weights float32 and positions int32
+    [B, H, slots] are updated in place, as k and v are; seen int32 [B] is the
+    new token's position.  Returns (lens [B], slots [B, H]), int32."""
+    import torch
+    limit, sinks = _int32(limit, "limit", 1), _int32(sinks, "sinks", 0)
+    recent = _int32(recent, "recent", 0)
+    c = _cache_struct(k, v, table, lens)
+    if weights is None or positions is None:
+        raise ValueError("weights and positions are needed")
+    ledger = _ledger_struct(weights, positions, c, k.device,
+                            ("weights", "positions"))
+    for x, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _tensor(x, name, k.dtype, (c.batch, c.heads, c.dim), k.device,
+                dense=False)
+        if c.dim > 1 and x.stride(2) != 1:
+            raise ValueError("%s: expected unit stride in the last axis"
+                             % name)
+    if any(_stride(k_new, i) != _stride(v_new, i) for i in (0, 1)):
+        raise ValueError("k_new and v_new: expected the same strides")
+    _tensor(seen, "seen", torch.int32, (c.batch,), k.device)
+    out_lens = torch.empty_like(lens)
+    slots = torch.empty((c.batch, c.heads), dtype=torch.int32,
+                        device=k.device)
+    _cache_call("cache_append", k.device, c, _ptr(k_new), _ptr(v_new),
+                _stride(k_new, 0), _stride(k_new, 1), limit, _ptr(seen),
+                ledger, sinks, recent, _ptr(out_lens), _ptr(slots))
+    return out_lens, slots
+
+
+def cache_evict(k, v, table, lens, seen, weights, positions, keep, sinks=0,
+                recent=0, out=None):
+    """Cut each sequence's cache back to the `keep` slots of the largest
+    accumulated weight, protected ones first (see cache_evict in
+    include/libtopk.h); rows move within k and v.  Returns (weights
+    [B, H, keep], positions [B, H, keep], lens [B]); out may be given as a
+    pair of tensors for the first two (they overlap no input)."""
+    import torch
+    keep, sinks = _int32(keep, "keep", 1), _int32(sinks, "sinks", 0)
+    recent = _int32(recent, "recent", 0)
+    c = _cache_struct(k, v, table, lens)
+    if weights is None or positions is None:
+        raise ValueError("weights and positions are needed")
+    ledger = _ledger_struct(weights, positions, c, k.device,
+                            ("weights", "positions"))
+    _tensor(seen, "seen", torch.int32, (c.batch,), k.device)
+    if out is None:
+        shape = (c.batch, c.heads, keep)
+        out = (torch.empty(shape, dtype=torch.float32, device=k.device),
+               torch.empty(shape, dtype=torch.int32, device=k.device))
+    after = _ledger_struct(out[0], out[1], c, k.device,
+                           ("out[0]", "out[1]"))
+    if after.slots != keep:
+        raise ValueError("out: expected [batch, heads, %d]" % keep)
+    out_lens = torch.empty_like(lens)
+    _cache_call("cache_evict", k.device, c, _ptr(seen), ledger, keep,
+                sinks, recent, after, _ptr(out_lens))
+    return out[0], out[1], out_lens

@@ -1,10 +1,10 @@
 """Build the HIP library libtopk.so for gfx950 (in-tree, no JIT cache).
 
-One translation unit, csrc/libtopk.hip, holds the C entry points and
-includes the kernel headers.  The flags disable packed-FP32 instruction
-selection (nothing here uses floating point, but every HIP build in this
-project carries the flag), emit code for gfx950 only, and pin code object
-version 5, which both the ROCm runtime in /opt/rocm and the one bundled with
+Two translation units, compiled side by side, hold the C entry points and
+include their kernel headers: csrc/libtopk.hip (selection and reductions) and
+csrc/cache.hip (the operators on a paged key-value cache).  The flags disable
+packed-FP32 instruction selection (every HIP build in this project carries
+the flag), emit code for gfx950 only, and pin code object version 5, which both the ROCm runtime in /opt/rocm and the one bundled with
 PyTorch load.  They also turn off the compiler's atomic optimizer: every
 atomic here is issued by one lane or targets a distinct address per lane,
 and the optimizer's wave-wide combining would only add a scalar loop.
@@ -20,13 +20,13 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libtopk.so")
+UNITS = ("libtopk.hip", "cache.hip")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-mcode-object-version=5",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-mllvm", "-amdgpu-atomic-optimizer-strategy=None",
@@ -42,11 +42,23 @@ def hipcc() -> str:
 
 
 def build_libtopk(extra_flags=(), out: str = SO) -> str:
-    src = os.path.join(CSRC, "libtopk.hip")
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC,
-           src, "-o", tmp]
-    subprocess.check_call(cmd)
+    objs = [tmp + "." + os.path.splitext(u)[0] + ".o" for u in UNITS]
+    try:
+        jobs = [subprocess.Popen([hipcc(), *HIPCC_FLAGS, *extra_flags, "-I",
+                                  INCLUDE, "-I", CSRC, "-c",
+                                  os.path.join(CSRC, u), "-o", o])
+                for u, o in zip(UNITS, objs)]
+        codes = [j.wait() for j in jobs]
+        for job, code in zip(jobs, codes):
+            if code:
+                raise subprocess.CalledProcessError(code, job.args)
+        subprocess.check_call([hipcc(), "--offload-arch=gfx950", "-fPIC",
+                               "-shared", *objs, "-o", tmp])
+    finally:
+        for o in objs:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, out)
     return out
 

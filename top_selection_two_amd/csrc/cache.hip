@@ -1,0 +1,466 @@
+// Host side of the operators on a paged key-value cache (cache_attend,
+// cache_append, cache_evict of include/libtopk.h): argument checks, workspace
+// and launches.
+#include <hip/hip_runtime.h>
+
+#include <atomic>
+#include <cstdio>
+#include <cstdlib>
+#include <map>
+#include <memory>
+#include <mutex>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "libtopk.h"
+#include "cache_attend_kernel.hpp"
+#include "cache_slots_kernel.hpp"
+
+namespace {
+
+using namespace ltk;
+
+static_assert(kBf16 == LIBTOPK_BF16 && kF16 == LIBTOPK_F16 &&
+                  kE4m3 == LIBTOPK_E4M3,
+              "the kernels' types are the header's");
+
+constexpr int64_t kMaxSlots = (int64_t)1 << 30;
+constexpr int64_t kSpan = (int64_t)1 << 60;  // bytes that an array may span
+
+// ---- workspace --------------------------------------------------------------
+// Areas that a (device, stream) has used are kept until cache_release(): a
+// captured graph may hold their addresses.  Growth at least doubles, so all
+// of them together stay below twice the largest.
+struct Area {
+  char* base = nullptr;
+  size_t bytes = 0;
+  std::vector<void*> old;
+};
+
+std::mutex g_mu;
+std::map<std::pair<int, void*>, Area> g_areas;
+
+void debug_hip(const char* what, hipError_t e) {
+  static const bool on = getenv("LIBTOPK_DEBUG") != nullptr;
+  if (on) fprintf(stderr, "libtopk: %s: %s\n", what, hipGetErrorString(e));
+}
+
+int current_device(int* dev) {
+  int count = 0;
+  if (hipGetDeviceCount(&count) != hipSuccess || count < 1) {
+    (void)hipGetLastError();
+    return LIBTOPK_ERR_HIP;
+  }
+  if (hipGetDevice(dev) != hipSuccess) return LIBTOPK_ERR_HIP;
+  return LIBTOPK_OK;
+}
+
+// At least `bytes` of workspace for calls on `stream`.
+int get_area(int dev, hipStream_t stream, size_t bytes, char** out) {
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
+    Area& a = g_areas[std::make_pair(dev, (void*)stream)];
+    if (a.bytes < bytes) {
+      if (getenv("LIBTOPK_TEST_FAIL_ALLOC")) return LIBTOPK_ERR_NOMEM;
+      hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+      if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
+        (void)hipGetLastError();
+        return LIBTOPK_ERR_HIP;
+      }
+      if (st != hipStreamCaptureStatusNone) return LIBTOPK_ERR_NOMEM;
+      size_t want = 2 * a.bytes > bytes ? 2 * a.bytes : bytes;
+      if (want < ((size_t)1 << 20)) want = (size_t)1 << 20;
+      a.old.reserve(a.old.size() + 1);
+      void* p = nullptr;
+      hipError_t e = hipMalloc(&p, want);
+      if (e != hipSuccess && want > bytes) {
+        (void)hipGetLastError();
+        want = bytes;
+        e = hipMalloc(&p, want);
+      }
+      if (e != hipSuccess) {
+        debug_hip("hipMalloc(cache workspace)", e);
+        (void)hipGetLastError();
+        return LIBTOPK_ERR_NOMEM;
+      }
+      if (a.base) a.old.push_back(a.base);
+      a.base = (char*)p;
+      a.bytes = want;
+    }
+    *out = a.base;
+    return LIBTOPK_OK;
+  } catch (const std::bad_alloc&) {
+    return LIBTOPK_ERR_NOMEM;
+  } catch (...) {
+    return LIBTOPK_ERR_HIP;
+  }
+}
+
+template <class P>
+int launch(const void* fn, dim3 grid, int threads, P params, hipStream_t s) {
+  void* args[] = {&params};
+  const hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, 0, s);
+  if (e != hipSuccess) {
+    debug_hip("kernel launch", e);
+    (void)hipGetLastError();
+    return LIBTOPK_ERR_HIP;
+  }
+  return LIBTOPK_OK;
+}
+
+// ---- argument checks --------------------------------------------------------
+bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+struct Range {
+  uintptr_t lo, hi;
+  Range(const void* p, int64_t bytes)
+      : lo((uintptr_t)p), hi((uintptr_t)p + (uintptr_t)bytes) {}
+  bool meets(const Range& o) const { return lo < o.hi && o.lo < hi; }
+};
+
+// Bytes from the first element to the last of an array of sizes n[i] and
+// strides s[i] (>= 0) bytes with rows of `row` bytes; -1 if a stride is
+// negative or the span too large.
+int64_t span(const int64_t* n, const int64_t* s, int dims, int64_t row) {
+  int64_t all = row;
+  for (int i = 0; i < dims; ++i) {
+    if (n[i] < 1) return 0;
+    if (s[i] < 0) return -1;
+    if (n[i] > 1 && s[i] > (kSpan - all) / (n[i] - 1)) return -1;
+    all += (n[i] - 1) * s[i];
+  }
+  return all;
+}
+
+int elem_size(int dtype) { return dtype == LIBTOPK_E4M3 ? 1 : 2; }
+
+// Checks a cache and fills in what the kernels take of it; `k` and `v` get
+// the arrays' extents.
+int check_cache(const libtopk_cache_t* c, CacheParams* p, Range* k, Range* v,
+                Range* table, Range* lens) {
+  if (!c) return LIBTOPK_ERR_INVALID;
+  if (c->dtype != LIBTOPK_BF16 && c->dtype != LIBTOPK_F16 &&
+      c->dtype != LIBTOPK_E4M3)
+    return LIBTOPK_ERR_INVALID;
+  const int es = elem_size(c->dtype);
+  if (c->batch < 0 || c->heads < 1 || c->heads > 65535 || c->page < 1 ||
+      c->dim < 1 || c->dim > LIBTOPK_MAX_DIM || c->dim * es % 16 != 0 ||
+      c->table_width < 1 || c->pages < 0 || c->pages > INT32_MAX)
+    return LIBTOPK_ERR_INVALID;
+  if ((int64_t)c->table_width * c->page >= kMaxSlots ||
+      (int64_t)c->batch * c->heads > INT32_MAX)
+    return LIBTOPK_ERR_INVALID;
+  if (c->batch > 1 && (c->table_stride < 0 || c->table_stride > kSpan / 4))
+    return LIBTOPK_ERR_INVALID;
+  const int64_t ks[3] = {c->k_page_stride, c->k_head_stride, c->k_slot_stride};
+  const int64_t vs[3] = {c->v_page_stride, c->v_head_stride, c->v_slot_stride};
+  const int64_t n[3] = {c->pages, c->heads, c->page};
+  int64_t kb[3], vb[3];
+  for (int i = 0; i < 3; ++i) {
+    if (ks[i] < 0 || ks[i] > kSpan || vs[i] < 0 || vs[i] > kSpan)
+      return LIBTOPK_ERR_INVALID;
+    kb[i] = ks[i] * es;
+    vb[i] = vs[i] * es;
+    if (n[i] > 1 && (kb[i] % 16 || vb[i] % 16)) return LIBTOPK_ERR_INVALID;
+  }
+  const int64_t klen = span(n, kb, 3, c->dim * es);
+  const int64_t vlen = span(n, vb, 3, c->dim * es);
+  if (klen < 0 || vlen < 0) return LIBTOPK_ERR_INVALID;
+  if (c->pages > 0 && (!c->k || !c->v)) return LIBTOPK_ERR_INVALID;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return LIBTOPK_ERR_INVALID;
+  if (c->batch > 0 && (!c->table || !c->lens)) return LIBTOPK_ERR_INVALID;
+  if (!aligned(c->table, 4) || !aligned(c->lens, 4))
+    return LIBTOPK_ERR_INVALID;
+  const int64_t tn[1] = {c->batch}, ts[1] = {c->table_stride * 4};
+  const int64_t tlen = span(tn, ts, 1, (int64_t)c->table_width * 4);
+  if (tlen < 0) return LIBTOPK_ERR_INVALID;
+  *k = Range(c->k, klen);
+  *v = Range(c->v, vlen);
+  *table = Range(c->table, tlen);
+  *lens = Range(c->lens, (int64_t)c->batch * 4);
+  p->k = (const char*)c->k;
+  p->v = (const char*)c->v;
+  p->ks = RowStrides{kb[0], kb[1], kb[2]};
+  p->vs = RowStrides{vb[0], vb[1], vb[2]};
+  p->table = c->table;
+  p->table_stride = c->table_stride;
+  p->lens = c->lens;
+  p->pages = c->pages;
+  p->page = make_divisor(c->page);
+  p->batch = c->batch;
+  p->heads = c->heads;
+  p->dim = c->dim;
+  p->cap = c->table_width * c->page;
+  p->row_bytes = c->dim * es;
+  return LIBTOPK_OK;
+}
+
+// Checks a ledger; its rows must not share an entry where they are written.
+int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
+                 bool positions, bool written, LedgerParams* p, Range* w,
+                 Range* pos) {
+  if (!l || l->slots < 1) return LIBTOPK_ERR_INVALID;
+  const int64_t n[2] = {batch, heads};
+  const int64_t ws[2] = {l->weights_batch_stride, l->weights_head_stride};
+  const int64_t ps[2] = {l->positions_batch_stride, l->positions_head_stride};
+  const int64_t* st[2] = {ws, ps};
+  const void* base[2] = {l->weights, l->positions};
+  Range* out[2] = {w, pos};
+  for (int a = 0; a < (positions ? 2 : 1); ++a) {
+    if ((batch > 0 && !base[a]) || !aligned(base[a], 4))
+      return LIBTOPK_ERR_INVALID;
+    int64_t bytes[2];
+    for (int i = 0; i < 2; ++i) {
+      if (st[a][i] < 0 || st[a][i] > kSpan / 4) return LIBTOPK_ERR_INVALID;
+      bytes[i] = st[a][i] * 4;
+    }
+    if (written) {
+      // the inner of the two axes steps over whole rows, the outer over
+      // whole runs of them
+      const bool head_inner = st[a][1] <= st[a][0] || n[0] <= 1;
+      const int in = head_inner ? 1 : 0, ou = 1 - in;
+      if (n[in] > 1 && st[a][in] < l->slots) return LIBTOPK_ERR_INVALID;
+      if (n[ou] > 1 &&
+          st[a][ou] < (n[in] > 1 ? (n[in] - 1) * st[a][in] : 0) + l->slots)
+        return LIBTOPK_ERR_INVALID;
+    }
+    const int64_t len = span(n, bytes, 2, (int64_t)l->slots * 4);
+    if (len < 0) return LIBTOPK_ERR_INVALID;
+    *out[a] = Range(base[a], len);
+  }
+  p->w = l->weights;
+  p->pos = l->positions;
+  p->wb = ws[0];
+  p->wh = ws[1];
+  p->pb = ps[0];
+  p->ph = ps[1];
+  return LIBTOPK_OK;
+}
+
+const void* attend_fn(int q, int c) {
+  if (q == kBf16)
+    return c == kE4m3 ? (const void*)&attend_kernel<kBf16, kE4m3>
+                      : (const void*)&attend_kernel<kBf16, kBf16>;
+  return c == kE4m3 ? (const void*)&attend_kernel<kF16, kE4m3>
+                    : (const void*)&attend_kernel<kF16, kF16>;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
+                 int32_t q_heads, int64_t q_batch_stride,
+                 int64_t q_head_stride, float scale, const float* k_scale,
+                 const float* v_scale, const libtopk_ledger_t* ledger,
+                 void* out, float* lse, libtopk_stream_t stream) {
+  AttendParams p = {};
+  const Range none(nullptr, 0);
+  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
+  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  if (rc != LIBTOPK_OK) return rc;
+  if (q_dtype != LIBTOPK_BF16 && q_dtype != LIBTOPK_F16)
+    return LIBTOPK_ERR_INVALID;
+  if (cache->dtype != LIBTOPK_E4M3 && cache->dtype != q_dtype)
+    return LIBTOPK_ERR_INVALID;
+  if (q_heads < 1 || q_heads % cache->heads != 0) return LIBTOPK_ERR_INVALID;
+  const int64_t rows = (int64_t)cache->batch * q_heads;
+  if (rows > INT32_MAX) return LIBTOPK_ERR_INVALID;
+  if (q_batch_stride < 0 || q_head_stride < 0 || q_batch_stride > kSpan ||
+      q_head_stride > kSpan || (cache->batch > 1 && q_batch_stride % 8) ||
+      (q_heads > 1 && q_head_stride % 8))
+    return LIBTOPK_ERR_INVALID;
+  if (ledger) {
+    rc = check_ledger(ledger, cache->batch, cache->heads, false, true, &p.w,
+                      &w, &pos);
+    if (rc != LIBTOPK_OK) return rc;
+    if (ledger->slots < p.c.cap) p.c.cap = ledger->slots;
+  }
+  if (cache->batch == 0) return LIBTOPK_OK;
+  if (!q || !out || !lse || !aligned(q, 16) || !aligned(out, 16) ||
+      !aligned(lse, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4))
+    return LIBTOPK_ERR_INVALID;
+  const int64_t qn[2] = {cache->batch, q_heads};
+  const int64_t qs[2] = {q_batch_stride * 2, q_head_stride * 2};
+  const int64_t qlen = span(qn, qs, 2, (int64_t)cache->dim * 2);
+  if (qlen < 0) return LIBTOPK_ERR_INVALID;
+  const Range outs[3] = {Range(out, rows * cache->dim * 2),
+                         Range(lse, rows * 4), w};
+  const Range ins[7] = {Range(q, qlen), k, v, table, lens,
+                        Range(k_scale, k_scale ? cache->heads * 4 : 0),
+                        Range(v_scale, v_scale ? cache->heads * 4 : 0)};
+  for (int i = 0; i < 3; ++i) {
+    for (const Range& r : ins)
+      if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (outs[i].meets(outs[j])) return LIBTOPK_ERR_INVALID;
+  }
+  p.q = (const char*)q;
+  p.qb = qs[0];
+  p.qh = qs[1];
+  p.group = q_heads / cache->heads;
+  p.scale2 = scale * 1.44269504088896341f;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.out = out;
+  p.lse = lse;
+  int dev = 0;
+  rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  if (ledger) {
+    char* area = nullptr;
+    rc = get_area(dev, s, (size_t)rows * p.c.cap * 4, &area);
+    if (rc != LIBTOPK_OK) return rc;
+    p.scores = (float*)area;
+  }
+  rc = launch(attend_fn(q_dtype, cache->dtype), dim3((unsigned)rows), kBlock,
+              p, s);
+  if (rc != LIBTOPK_OK || !ledger) return rc;
+  const dim3 grid((p.c.cap + kBlock - 1) / kBlock,
+                  (unsigned)(cache->batch * cache->heads));
+  return launch((const void*)&attend_weights_kernel, grid, kBlock, p, s);
+}
+
+int cache_append(const libtopk_cache_t* cache, const void* k_new,
+                 const void* v_new, int64_t new_batch_stride,
+                 int64_t new_head_stride, int32_t limit, const int32_t* seen,
+                 const libtopk_ledger_t* ledger, int32_t sinks, int32_t recent,
+                 int32_t* out_lens, int32_t* out_slots,
+                 libtopk_stream_t stream) {
+  SlotsParams p = {};
+  const Range none(nullptr, 0);
+  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
+  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  if (rc != LIBTOPK_OK) return rc;
+  rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,
+                    &pos);
+  if (rc != LIBTOPK_OK) return rc;
+  if (limit < 1 || sinks < 0 || recent < 0) return LIBTOPK_ERR_INVALID;
+  const int es = elem_size(cache->dtype);
+  if (new_batch_stride < 0 || new_head_stride < 0 ||
+      new_batch_stride > kSpan || new_head_stride > kSpan ||
+      (cache->batch > 1 && new_batch_stride * es % 16) ||
+      (cache->heads > 1 && new_head_stride * es % 16))
+    return LIBTOPK_ERR_INVALID;
+  if (cache->batch == 0) return LIBTOPK_OK;
+  if (!k_new || !v_new || !seen || !out_lens || !out_slots ||
+      !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(seen, 4) ||
+      !aligned(out_lens, 4) || !aligned(out_slots, 4))
+    return LIBTOPK_ERR_INVALID;
+  if (ledger->slots < p.c.cap) p.c.cap = ledger->slots;
+  const int64_t nn[2] = {cache->batch, cache->heads};
+  const int64_t ns[2] = {new_batch_stride * es, new_head_stride * es};
+  const int64_t nlen = span(nn, ns, 2, (int64_t)cache->dim * es);
+  if (nlen < 0) return LIBTOPK_ERR_INVALID;
+  const int64_t rows = (int64_t)cache->batch * cache->heads;
+  const Range outs[6] = {Range(out_lens, (int64_t)cache->batch * 4),
+                         Range(out_slots, rows * 4), w, pos, k, v};
+  const Range ins[5] = {Range(k_new, nlen), Range(v_new, nlen), table, lens,
+                        Range(seen, (int64_t)cache->batch * 4)};
+  for (int i = 0; i < 6; ++i) {
+    for (const Range& r : ins)
+      if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
+    // k and v may interleave (one array of pages that holds both)
+    for (int j = 0; j < i; ++j)
+      if (!(i == 5 && j == 4) && outs[i].meets(outs[j]))
+        return LIBTOPK_ERR_INVALID;
+  }
+  p.seen = seen;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.k_new = (const char*)k_new;
+  p.v_new = (const char*)v_new;
+  p.nb = ns[0];
+  p.nh = ns[1];
+  p.limit = limit;
+  p.out_lens = out_lens;
+  p.out_slots = out_slots;
+  int dev = 0;
+  rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  return launch((const void*)&append_kernel, dim3((unsigned)rows), kBlock, p,
+                (hipStream_t)stream);
+}
+
+int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
+                const libtopk_ledger_t* ledger, int32_t keep, int32_t sinks,
+                int32_t recent, const libtopk_ledger_t* after,
+                int32_t* out_lens, libtopk_stream_t stream) {
+  SlotsParams p = {};
+  const Range none(nullptr, 0);
+  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
+  Range w2 = none, pos2 = none;
+  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  if (rc != LIBTOPK_OK) return rc;
+  rc = check_ledger(ledger, cache->batch, cache->heads, true, false, &p.w, &w,
+                    &pos);
+  if (rc != LIBTOPK_OK) return rc;
+  if (keep < 1 || sinks < 0 || recent < 0 || !after || after->slots < keep)
+    return LIBTOPK_ERR_INVALID;
+  libtopk_ledger_t used = *after;
+  used.slots = keep;
+  rc = check_ledger(&used, cache->batch, cache->heads, true, true, &p.after,
+                    &w2, &pos2);
+  if (rc != LIBTOPK_OK) return rc;
+  if (cache->batch == 0) return LIBTOPK_OK;
+  if (!seen || !out_lens || !aligned(seen, 4) || !aligned(out_lens, 4))
+    return LIBTOPK_ERR_INVALID;
+  if (ledger->slots < p.c.cap) p.c.cap = ledger->slots;
+  const int64_t rows = (int64_t)cache->batch * cache->heads;
+  const Range outs[5] = {Range(out_lens, (int64_t)cache->batch * 4), w2, pos2,
+                         k, v};
+  const Range ins[5] = {w, pos, table, lens,
+                        Range(seen, (int64_t)cache->batch * 4)};
+  for (int i = 0; i < 5; ++i) {
+    for (const Range& r : ins)
+      if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (!(i == 4 && j == 3) && outs[i].meets(outs[j]))
+        return LIBTOPK_ERR_INVALID;
+  }
+  p.seen = seen;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.keep = keep;
+  p.out_lens = out_lens;
+  // Moves of a row: at most the kept slots, and at most the slots beyond.
+  p.pair_cap = p.c.cap > keep ? (p.c.cap - keep < keep ? p.c.cap - keep : keep)
+                              : 0;
+  int dev = 0;
+  rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  hipStream_t s = (hipStream_t)stream;
+  if (p.pair_cap > 0) {
+    char* area = nullptr;
+    rc = get_area(dev, s, (size_t)rows * p.pair_cap * 8, &area);
+    if (rc != LIBTOPK_OK) return rc;
+    p.pairs = (int32_t*)area;
+  }
+  return launch((const void*)&evict_kernel, dim3((unsigned)rows), kBlock, p,
+                s);
+}
+
+void cache_release(void) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int prev = -1;
+  (void)hipGetDevice(&prev);
+  for (auto& kv : g_areas) {
+    if (hipSetDevice(kv.first.first) != hipSuccess) continue;
+    (void)hipDeviceSynchronize();
+    for (void* o : kv.second.old) (void)hipFree(o);
+    if (kv.second.base) (void)hipFree(kv.second.base);
+  }
+  g_areas.clear();
+  if (prev >= 0) (void)hipSetDevice(prev);
+  (void)hipGetLastError();
+}
+
+int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed) {
+  (void)stream;
+  (void)seed;
+  return LIBTOPK_OK;
+}
+
+}  // extern "C"
