@@ -32,14 +32,22 @@ constexpr int64_t kSpan = (int64_t)1 << 60;  // bytes that an array may span
 // Areas that a (device, stream) has used are kept until cache_release(): a
 // captured graph may hold their addresses.  Growth at least doubles, so all
 // of them together stay below twice the largest.
-struct Area {
+struct Buffer {
   char* base = nullptr;
   size_t bytes = 0;
   std::vector<void*> old;
 };
 
+struct Area {
+  Buffer work;     // partial results, scores, lists: any contents
+  Buffer tickets;  // completion tickets and nothing else (see Tagged)
+  std::shared_ptr<std::atomic<uint32_t>> epochs;
+};
+
 std::mutex g_mu;
 std::map<std::pair<int, void*>, Area> g_areas;
+std::map<int, int> g_cus;             // device -> compute units
+std::map<const void*, int> g_fit;     // kernel -> workgroups of a unit
 
 void debug_hip(const char* what, hipError_t e) {
   static const bool on = getenv("LIBTOPK_DEBUG") != nullptr;
@@ -47,53 +55,129 @@ void debug_hip(const char* what, hipError_t e) {
 }
 
 int current_device(int* dev) {
-  int count = 0;
-  if (hipGetDeviceCount(&count) != hipSuccess || count < 1) {
+  if (hipGetDevice(dev) != hipSuccess) {
     (void)hipGetLastError();
     return LIBTOPK_ERR_HIP;
   }
-  if (hipGetDevice(dev) != hipSuccess) return LIBTOPK_ERR_HIP;
   return LIBTOPK_OK;
 }
 
-// At least `bytes` of workspace for calls on `stream`.
-int get_area(int dev, hipStream_t stream, size_t bytes, char** out) {
+// The epoch of a new launch (never 0, which cleared words carry).
+uint32_t next_epoch(std::atomic<uint32_t>& c) {
+  uint32_t e = c.fetch_add(1u) + 1u;
+  while (e == 0u) e = c.fetch_add(1u) + 1u;
+  return e;
+}
+
+__global__ void fill_words(uint64_t* p, int64_t n, uint64_t seed) {
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= n) return;
+  // seed 0: clear; otherwise a SplitMix64-style mix of seed and index
+  uint64_t z = seed + 0x9e3779b97f4a7c15ull * (uint64_t)(i + 1);
+  z = (z ^ (z >> 30)) * 0xbf58476d1ce4e5b9ull;
+  z = (z ^ (z >> 27)) * 0x94d049bb133111ebull;
+  p[i] = seed ? (z ^ (z >> 31)) | 1ull : 0ull;
+}
+
+int fill(uint64_t* p, size_t words, uint64_t seed, hipStream_t s) {
+  hipLaunchKernelGGL(fill_words, dim3((unsigned)((words + 255) / 256)),
+                     dim3(256), 0, s, p, (int64_t)words, seed);
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return LIBTOPK_OK;
+  debug_hip("fill_words launch", e);
+  return LIBTOPK_ERR_HIP;
+}
+
+// Caller holds g_mu.
+int grow(Buffer* b, size_t bytes, hipStream_t stream, bool clear) {
+  if (b->bytes >= bytes) return LIBTOPK_OK;
+  if (getenv("LIBTOPK_TEST_FAIL_ALLOC")) return LIBTOPK_ERR_NOMEM;
+  hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+  if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
+    (void)hipGetLastError();
+    return LIBTOPK_ERR_HIP;
+  }
+  if (st != hipStreamCaptureStatusNone) return LIBTOPK_ERR_NOMEM;
+  size_t want = 2 * b->bytes > bytes ? 2 * b->bytes : bytes;
+  if (want < ((size_t)1 << 16)) want = (size_t)1 << 16;
+  b->old.reserve(b->old.size() + 1);
+  void* p = nullptr;
+  hipError_t e = hipMalloc(&p, want);
+  if (e != hipSuccess && want > bytes) {
+    (void)hipGetLastError();
+    want = bytes;
+    e = hipMalloc(&p, want);
+  }
+  if (e != hipSuccess) {
+    debug_hip("hipMalloc(cache workspace)", e);
+    (void)hipGetLastError();
+    return LIBTOPK_ERR_NOMEM;
+  }
+  if (clear) {
+    const int rc = fill((uint64_t*)p, want / 8, 0, stream);
+    if (rc != LIBTOPK_OK) {
+      (void)hipFree(p);
+      return rc;
+    }
+  }
+  if (b->base) b->old.push_back(b->base);
+  b->base = (char*)p;
+  b->bytes = want;
+  return LIBTOPK_OK;
+}
+
+// Workspace of a call on `stream`: `bytes` of any contents, `tickets` words,
+// and the call's epoch.
+struct Work {
+  char* base;
+  uint64_t* tickets;
+  uint32_t epoch;
+};
+
+int get_work(int dev, hipStream_t stream, size_t bytes, size_t tickets,
+             Work* out) {
   try {
     std::lock_guard<std::mutex> lock(g_mu);
     Area& a = g_areas[std::make_pair(dev, (void*)stream)];
-    if (a.bytes < bytes) {
-      if (getenv("LIBTOPK_TEST_FAIL_ALLOC")) return LIBTOPK_ERR_NOMEM;
-      hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-      if (hipStreamIsCapturing(stream, &st) != hipSuccess) {
-        (void)hipGetLastError();
-        return LIBTOPK_ERR_HIP;
-      }
-      if (st != hipStreamCaptureStatusNone) return LIBTOPK_ERR_NOMEM;
-      size_t want = 2 * a.bytes > bytes ? 2 * a.bytes : bytes;
-      if (want < ((size_t)1 << 20)) want = (size_t)1 << 20;
-      a.old.reserve(a.old.size() + 1);
-      void* p = nullptr;
-      hipError_t e = hipMalloc(&p, want);
-      if (e != hipSuccess && want > bytes) {
-        (void)hipGetLastError();
-        want = bytes;
-        e = hipMalloc(&p, want);
-      }
-      if (e != hipSuccess) {
-        debug_hip("hipMalloc(cache workspace)", e);
-        (void)hipGetLastError();
-        return LIBTOPK_ERR_NOMEM;
-      }
-      if (a.base) a.old.push_back(a.base);
-      a.base = (char*)p;
-      a.bytes = want;
-    }
-    *out = a.base;
+    if (!a.epochs) a.epochs = std::make_shared<std::atomic<uint32_t>>(0u);
+    int rc = grow(&a.work, bytes, stream, false);
+    if (rc == LIBTOPK_OK) rc = grow(&a.tickets, tickets * 8, stream, true);
+    if (rc != LIBTOPK_OK) return rc;
+    out->base = a.work.base;
+    out->tickets = (uint64_t*)a.tickets.base;
+    out->epoch = next_epoch(*a.epochs);
     return LIBTOPK_OK;
   } catch (const std::bad_alloc&) {
     return LIBTOPK_ERR_NOMEM;
   } catch (...) {
     return LIBTOPK_ERR_HIP;
+  }
+}
+
+// Workgroups of `fn` that the device holds at once.
+int resident(int dev, const void* fn, int threads, int* out) {
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
+    int& cus = g_cus[dev];
+    if (cus < 1 &&
+        (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount,
+                               dev) != hipSuccess ||
+         cus < 1)) {
+      (void)hipGetLastError();
+      cus = 256;
+    }
+    int& fit = g_fit[fn];
+    if (fit < 1 &&
+        (hipOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0) !=
+             hipSuccess ||
+         fit < 1)) {
+      (void)hipGetLastError();
+      fit = 1;
+    }
+    *out = cus * fit;
+    return LIBTOPK_OK;
+  } catch (...) {
+    return LIBTOPK_ERR_NOMEM;
   }
 }
 
@@ -238,13 +322,33 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
   return LIBTOPK_OK;
 }
 
-const void* attend_fn(int q, int c) {
-  if (q == kBf16)
-    return c == kE4m3 ? (const void*)&attend_kernel<kBf16, kE4m3>
-                      : (const void*)&attend_kernel<kBf16, kBf16>;
-  return c == kE4m3 ? (const void*)&attend_kernel<kF16, kE4m3>
-                    : (const void*)&attend_kernel<kF16, kF16>;
+// The attention kernel for a type pair, row length and page size, and the
+// columns that its partial results have.
+template <int Q, int C, int NC>
+const void* attend_fn_pages(bool pg16, int* cols) {
+  *cols = Attend<Q, C, NC, true>::COLS;
+  return pg16 ? (const void*)&attend_kernel<Q, C, NC, true>
+              : (const void*)&attend_kernel<Q, C, NC, false>;
 }
+template <int Q, int C>
+const void* attend_fn_dim(int dim, bool pg16, int* cols) {
+  return dim <= 64    ? attend_fn_pages<Q, C, 2>(pg16, cols)
+         : dim <= 96  ? attend_fn_pages<Q, C, 3>(pg16, cols)
+         : dim <= 128 ? attend_fn_pages<Q, C, 4>(pg16, cols)
+         : dim <= 192 ? attend_fn_pages<Q, C, 6>(pg16, cols)
+                      : attend_fn_pages<Q, C, 8>(pg16, cols);
+}
+const void* attend_fn(int q, int c, int dim, bool pg16, int* cols) {
+  if (q == kBf16)
+    return c == kE4m3 ? attend_fn_dim<kBf16, kE4m3>(dim, pg16, cols)
+                      : attend_fn_dim<kBf16, kBf16>(dim, pg16, cols);
+  return c == kE4m3 ? attend_fn_dim<kF16, kE4m3>(dim, pg16, cols)
+                    : attend_fn_dim<kF16, kF16>(dim, pg16, cols);
+}
+
+constexpr int kMaxRuns = 1024;  // workgroups of an attention call
+
+size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
 }  // namespace
 
@@ -305,22 +409,45 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   p.v_scale = v_scale;
   p.out = out;
   p.lse = lse;
+  p.gtiles = (p.group + 15) / 16;
+  // Units of all rows must count in 31 bits.
+  const int64_t units = ((int64_t)p.c.cap + kUnit - 1) / kUnit;
+  const int64_t att_rows = (int64_t)cache->batch * cache->heads * p.gtiles;
+  if (att_rows > INT32_MAX / units) return LIBTOPK_ERR_INVALID;
   int dev = 0;
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  if (ledger) {
-    char* area = nullptr;
-    rc = get_area(dev, s, (size_t)rows * p.c.cap * 4, &area);
-    if (rc != LIBTOPK_OK) return rc;
-    p.scores = (float*)area;
-  }
-  rc = launch(attend_fn(q_dtype, cache->dtype), dim3((unsigned)rows), kBlock,
-              p, s);
+  // Halves of a tile that lie in one page each get their addresses from
+  // scalar registers (and 16 rows must lie within 2^31 bytes).
+  const bool pg16 = cache->page % 16 == 0 && p.c.ks.slot < (1 << 27) &&
+                    p.c.vs.slot < (1 << 27);
+  int cols = 0, fit = 0;
+  const void* fn = attend_fn(q_dtype, cache->dtype, cache->dim, pg16, &cols);
+  rc = resident(dev, fn, kAttThreads, &fit);
+  if (rc != LIBTOPK_OK) return rc;
+  int64_t grid = att_rows * units;
+  if (grid > fit) grid = fit;
+  if (grid > kMaxRuns) grid = kMaxRuns;
+  p.part_rows = p.group < 16 ? p.group : 16;
+  p.score_ld = (int64_t)round_up((size_t)p.c.cap, kTileSlots);
+  const size_t part_bytes =
+      round_up((size_t)grid * 2 * p.part_rows * (cols + 2) * 4, 256);
+  const size_t score_bytes = ledger ? (size_t)rows * p.score_ld * 4 : 0;
+  Work work;
+  rc = get_work(dev, s, part_bytes + score_bytes, (size_t)att_rows, &work);
+  if (rc != LIBTOPK_OK) return rc;
+  p.part = (float*)work.base;
+  p.scores = ledger ? (float*)(work.base + part_bytes) : nullptr;
+  p.ticket = work.tickets;
+  p.epoch = work.epoch;
+  rc = launch(fn, dim3((unsigned)grid), kAttThreads, p, s);
   if (rc != LIBTOPK_OK || !ledger) return rc;
-  const dim3 grid((p.c.cap + kBlock - 1) / kBlock,
-                  (unsigned)(cache->batch * cache->heads));
-  return launch((const void*)&attend_weights_kernel, grid, kBlock, p, s);
+  const int64_t chunks =
+      (int64_t)cache->batch * cache->heads * ((p.c.cap + kBlock - 1) / kBlock);
+  return launch((const void*)&attend_weights_kernel,
+                dim3((unsigned)(chunks < 16384 ? chunks : 16384)), kBlock, p,
+                s);
 }
 
 int cache_append(const libtopk_cache_t* cache, const void* k_new,
@@ -433,10 +560,10 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
   if (p.pair_cap > 0) {
-    char* area = nullptr;
-    rc = get_area(dev, s, (size_t)rows * p.pair_cap * 8, &area);
+    Work work;
+    rc = get_work(dev, s, (size_t)rows * p.pair_cap * 8, 1, &work);
     if (rc != LIBTOPK_OK) return rc;
-    p.pairs = (int32_t*)area;
+    p.pairs = (int32_t*)work.base;
   }
   return launch((const void*)&evict_kernel, dim3((unsigned)rows), kBlock, p,
                 s);
@@ -449,8 +576,10 @@ void cache_release(void) {
   for (auto& kv : g_areas) {
     if (hipSetDevice(kv.first.first) != hipSuccess) continue;
     (void)hipDeviceSynchronize();
-    for (void* o : kv.second.old) (void)hipFree(o);
-    if (kv.second.base) (void)hipFree(kv.second.base);
+    for (Buffer* b : {&kv.second.work, &kv.second.tickets}) {
+      for (void* o : b->old) (void)hipFree(o);
+      if (b->base) (void)hipFree(b->base);
+    }
   }
   g_areas.clear();
   if (prev >= 0) (void)hipSetDevice(prev);
@@ -458,9 +587,18 @@ void cache_release(void) {
 }
 
 int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed) {
-  (void)stream;
-  (void)seed;
-  return LIBTOPK_OK;
+  int dev = 0;
+  int rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  Work work;
+  rc = get_work(dev, (hipStream_t)stream, 1, 1, &work);
+  if (rc != LIBTOPK_OK) return rc;
+  size_t words = 0;
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    words = g_areas[std::make_pair(dev, (void*)stream)].tickets.bytes / 8;
+  }
+  return fill(work.tickets, words, seed | 1u, (hipStream_t)stream);
 }
 
 }  // extern "C"
