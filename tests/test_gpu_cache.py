@@ -188,6 +188,24 @@ def test_attend_long(n, batch, heads, weights):
             weights, rng=rng)
 
 
+# Enough slots for every workgroup to take several shares of rows, whole rows
+# and split ones, and more scores than one holds: by queries a head, and with
+# a table that allows for rows too long to be finished in one launch.
+@pytest.mark.parametrize("group,heads,batch,lo,hi,extra", [
+    (1, 4, 40, 300, 3000, 1), (4, 4, 40, 300, 3000, 1),
+    (4, 4, 40, 300, 3000, 1400), (16, 2, 40, 300, 3000, 1),
+    (16, 2, 40, 300, 3000, 1400), (20, 2, 24, 300, 3000, 1),
+    (12, 1, 3, 20000, 70000, 1)])
+def test_attend_full_device(group, heads, batch, lo, hi, extra):
+    lens = [int(x) for x in
+            np.random.default_rng(group).integers(lo, hi, size=batch)]
+    lens[1], lens[-1] = 0, hi
+    rng, dev, ref = _case(group, lens, heads, 16, 16, "bf16", extra=extra)
+    print("attend full device", group, heads, batch, extra, flush=True)
+    _attend(dev, _q(rng, batch, group * heads, 16, "bf16"), ref, "bf16",
+            "bf16", rng=rng)
+
+
 def test_attend_many_sequences():
     lens = [int(x) for x in
             np.random.default_rng(5).integers(0, 90, size=700)]

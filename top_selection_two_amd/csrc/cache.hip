@@ -154,8 +154,8 @@ int get_work(int dev, hipStream_t stream, size_t bytes, size_t tickets,
   }
 }
 
-// Workgroups of `fn` that the device holds at once.
-int resident(int dev, const void* fn, int threads, int* out) {
+// Workgroups of `fn` that a compute unit holds at once, and the units.
+int resident(int dev, const void* fn, int threads, int* out, int* units) {
   try {
     std::lock_guard<std::mutex> lock(g_mu);
     int& cus = g_cus[dev];
@@ -174,7 +174,8 @@ int resident(int dev, const void* fn, int threads, int* out) {
       (void)hipGetLastError();
       fit = 1;
     }
-    *out = cus * fit;
+    *out = fit;
+    *units = cus;
     return LIBTOPK_OK;
   } catch (...) {
     return LIBTOPK_ERR_NOMEM;
@@ -182,9 +183,10 @@ int resident(int dev, const void* fn, int threads, int* out) {
 }
 
 template <class P>
-int launch(const void* fn, dim3 grid, int threads, P params, hipStream_t s) {
+int launch(const void* fn, dim3 grid, int threads, P params, hipStream_t s,
+           size_t lds = 0) {
   void* args[] = {&params};
-  const hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, 0, s);
+  const hipError_t e = hipLaunchKernel(fn, grid, dim3(threads), args, lds, s);
   if (e != hipSuccess) {
     debug_hip("kernel launch", e);
     (void)hipGetLastError();
@@ -322,23 +324,28 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
   return LIBTOPK_OK;
 }
 
-// The attention kernel for a type pair, row length and page size, and the
-// columns that its partial results have.
+// The attention kernel for a type pair, row length and page size, and what it
+// needs.
+struct AttendNeeds {
+  int cols;  // columns of a partial result
+  int lds;   // bytes of LDS besides the scores it holds
+};
 template <int Q, int C, int NC>
-const void* attend_fn_pages(bool pg16, int* cols) {
-  *cols = Attend<Q, C, NC, true>::COLS;
+const void* attend_fn_pages(bool pg16, AttendNeeds* cols) {
+  *cols = {Attend<Q, C, NC, true>::COLS,
+           (int)sizeof(typename Attend<Q, C, NC, true>::Lds)};
   return pg16 ? (const void*)&attend_kernel<Q, C, NC, true>
               : (const void*)&attend_kernel<Q, C, NC, false>;
 }
 template <int Q, int C>
-const void* attend_fn_dim(int dim, bool pg16, int* cols) {
+const void* attend_fn_dim(int dim, bool pg16, AttendNeeds* cols) {
   return dim <= 64    ? attend_fn_pages<Q, C, 2>(pg16, cols)
          : dim <= 96  ? attend_fn_pages<Q, C, 3>(pg16, cols)
          : dim <= 128 ? attend_fn_pages<Q, C, 4>(pg16, cols)
          : dim <= 192 ? attend_fn_pages<Q, C, 6>(pg16, cols)
                       : attend_fn_pages<Q, C, 8>(pg16, cols);
 }
-const void* attend_fn(int q, int c, int dim, bool pg16, int* cols) {
+const void* attend_fn(int q, int c, int dim, bool pg16, AttendNeeds* cols) {
   if (q == kBf16)
     return c == kE4m3 ? attend_fn_dim<kBf16, kE4m3>(dim, pg16, cols)
                       : attend_fn_dim<kBf16, kBf16>(dim, pg16, cols);
@@ -347,6 +354,10 @@ const void* attend_fn(int q, int c, int dim, bool pg16, int* cols) {
 }
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
+constexpr int kLdsBytes = 160 * 1024;
+// Rows of at most this many slots get their weights from their last
+// workgroup, longer ones from a second launch.
+constexpr int kDirectSlots = 16384;
 
 size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
@@ -422,32 +433,49 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   // scalar registers (and 16 rows must lie within 2^31 bytes).
   const bool pg16 = cache->page % 16 == 0 && p.c.ks.slot < (1 << 27) &&
                     p.c.vs.slot < (1 << 27);
-  int cols = 0, fit = 0;
-  const void* fn = attend_fn(q_dtype, cache->dtype, cache->dim, pg16, &cols);
-  rc = resident(dev, fn, kAttThreads, &fit);
+  AttendNeeds needs;
+  const void* fn = attend_fn(q_dtype, cache->dtype, cache->dim, pg16, &needs);
+  int fit = 0, cus = 0;
+  rc = resident(dev, fn, kAttThreads, &fit, &cus);
   if (rc != LIBTOPK_OK) return rc;
   int64_t grid = att_rows * units;
-  if (grid > fit) grid = fit;
+  if (grid > (int64_t)fit * cus) grid = (int64_t)fit * cus;
   if (grid > kMaxRuns) grid = kMaxRuns;
   p.part_rows = p.group < 16 ? p.group : 16;
-  p.score_ld = (int64_t)round_up((size_t)p.c.cap, kTileSlots);
   const size_t part_bytes =
-      round_up((size_t)grid * 2 * p.part_rows * (cols + 2) * 4, 256);
-  const size_t score_bytes = ledger ? (size_t)rows * p.score_ld * 4 : 0;
+      round_up((size_t)grid * 2 * p.part_rows * (needs.cols + 2) * 4, 256);
+  const size_t unit_bytes = (size_t)kUnit * p.part_rows * 4;
+  size_t score_bytes = 0, split_bytes = 0, lds = 0;
+  if (ledger) {
+    p.row_units = (int32_t)units;
+    p.direct = p.gtiles == 1 && p.c.cap <= kDirectSlots;
+    score_bytes = (size_t)(att_rows * units) * unit_bytes;
+    if (!p.direct) split_bytes = round_up((size_t)att_rows, 256);
+    // What LDS is left when `fit` workgroups share a unit holds scores, but
+    // no more than the longest run.
+    const int64_t run = (att_rows * units + grid - 1) / grid;
+    int64_t room = (kLdsBytes / fit - needs.lds - 256) / (int64_t)unit_bytes;
+    if (room > run) room = run;
+    p.held_units = (int32_t)room;
+    lds = (size_t)room * unit_bytes;
+  }
   Work work;
-  rc = get_work(dev, s, part_bytes + score_bytes, (size_t)att_rows, &work);
+  rc = get_work(dev, s, part_bytes + score_bytes + split_bytes,
+                (size_t)att_rows, &work);
   if (rc != LIBTOPK_OK) return rc;
   p.part = (float*)work.base;
-  p.scores = ledger ? (float*)(work.base + part_bytes) : nullptr;
+  if (ledger) p.scores = (float*)(work.base + part_bytes);
+  if (split_bytes)
+    p.split = (uint8_t*)(work.base + part_bytes + score_bytes);
   p.ticket = work.tickets;
   p.epoch = work.epoch;
-  rc = launch(fn, dim3((unsigned)grid), kAttThreads, p, s);
-  if (rc != LIBTOPK_OK || !ledger) return rc;
-  const int64_t chunks =
-      (int64_t)cache->batch * cache->heads * ((p.c.cap + kBlock - 1) / kBlock);
+  rc = launch(fn, dim3((unsigned)grid), kAttThreads, p, s, lds);
+  if (rc != LIBTOPK_OK || !ledger || p.direct) return rc;
+  const int64_t wrows = (int64_t)cache->batch * cache->heads;
   return launch((const void*)&attend_weights_kernel,
-                dim3((unsigned)(chunks < 16384 ? chunks : 16384)), kBlock, p,
-                s);
+                dim3((p.c.cap + kWeightSlots - 1) / kWeightSlots,
+                     (unsigned)(wrows < 65535 ? wrows : 65535)),
+                kBlock, p, s);
 }
 
 int cache_append(const libtopk_cache_t* cache, const void* k_new,

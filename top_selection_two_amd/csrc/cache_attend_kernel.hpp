@@ -20,6 +20,12 @@
 
 namespace ltk {
 
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kAttWaves = 8;
+constexpr int kAttThreads = kAttWaves * kWave;
+constexpr int kTileSlots = 32;                       // of one wave
+constexpr int kUnit = kTileSlots * kAttWaves;        // of a workgroup
+
 struct AttendParams {
   CacheParams c;
   LedgerParams w;
@@ -30,8 +36,13 @@ struct AttendParams {
   float scale2;         // scale * log2 e
   const float* k_scale; // NULL: 1
   const float* v_scale;
-  float* scores;        // [batch][q heads][score_ld], with a ledger
-  int64_t score_ld;     // cap rounded up to a tile
+  // With a ledger: scores of split rows, [row][unit][wave] tiles (see
+  // score_at), whether a row is split, and the units that fit in LDS.
+  float* scores;
+  uint8_t* split;
+  int32_t row_units;    // units of a row at full length
+  int32_t held_units;
+  bool direct;          // a row's last workgroup adds up its weights
   float* part;          // [grid][2][part_rows * columns + 2 * part_rows]
   int32_t part_rows;    // queries of a row, at most 16
   uint64_t* ticket;     // one per row
@@ -39,12 +50,6 @@ struct AttendParams {
   void* out;
   float* lse;
 };
-
-constexpr float kLn2 = 0.693147180559945309f;
-constexpr int kAttWaves = 8;
-constexpr int kAttThreads = kAttWaves * kWave;
-constexpr int kTileSlots = 32;                       // of one wave
-constexpr int kUnit = kTileSlots * kAttWaves;        // of a workgroup
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -114,6 +119,51 @@ __device__ __forceinline__ float quad_sum(float v) {
   return v + __shfl_xor(v, 32, kWave);
 }
 
+typedef int v2i __attribute__((ext_vector_type(2)));
+
+// K and V rows are read once a call: non-temporal.
+template <class T>
+__device__ __forceinline__ T ld_once(const char* p) {
+  return __builtin_nontemporal_load((const T*)p);
+}
+
+// Coherent at device level (sc1), as st_agent and ld_agent, four floats at a
+// time and free to be in flight together; `at` in bytes.
+__device__ __forceinline__ f32x4 ld_agent4(__amdgpu_buffer_rsrc_t r, int at) {
+  return __builtin_bit_cast(
+      f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, at, 0, 16));
+}
+__device__ __forceinline__ float ld_agent1(__amdgpu_buffer_rsrc_t r, int at) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 16));
+}
+__device__ __forceinline__ void st_agent4(__amdgpu_buffer_rsrc_t r, int at,
+                                          f32x4 x) {
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), r, at,
+                                         0, 16);
+}
+
+// Scores of a tile: `rows` queries of 32 slots, in groups of four slots.
+// The groups of a query are rotated among themselves by exclusive or, so that
+// the 16 queries that write a group each do not meet in one bank of LDS.
+__device__ __forceinline__ int score_at(int query, int group4) {
+  return query * kTileSlots + ((group4 ^ (query & 7)) * 4);
+}
+
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// weights[0 .. 4) += a, as far as they lie below the length.
+__device__ __forceinline__ void add_weights(float* w, int32_t left,
+                                            f32x4 a) {
+  if (left >= 4) {
+    *(f32x4u*)w = *(const f32x4u*)w + a;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 3; ++e)
+      if (e < left) w[e] += a[e];
+  }
+}
+
 // One wave's tile: 32 slots of a row against up to 16 queries.  With lane
 // l = 16 q + n, the 16 x 16 x 32 matrix instruction takes row (or column) n,
 // contraction indices 8 q .. 8 q + 7 of its operands, and leaves column n,
@@ -157,7 +207,7 @@ struct Attend {
     float o[kAttWaves][4][COLS];
     float m[kAttWaves][16];
     float l[kAttWaves][16];
-    float top[16], sum[16];
+    float top[16], sum[16], lse2[16];
     int32_t scan[kAttWaves];
     int32_t base;
     int32_t b;
@@ -180,7 +230,7 @@ __device__ __forceinline__ typename A::Ids find_tile(const CacheParams& c,
       s = s < len ? s : 0;
       const int32_t p = uni(quotient(c.page, s));
       r.place[tt] = s - p * c.page.d;
-      r.id[tt] = table[p];
+      r.id[tt] = ld_const(table + p);
     }
   } else {
 #pragma unroll
@@ -217,9 +267,22 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
     const int32_t len = len_of(b);
     return (len > 0 ? (len + kUnit - 1) / kUnit : 1) * hg;
   };
-  int32_t u0, u1, per, base;
-  int b;
-  {
+  // Length of a sequence that is the same in every lane.
+  auto len_uni = [&](int b) {
+    return clamp_len(ld_const(c.lens + b), top_len);
+  };
+  int32_t u0, u1, per, base = 0;
+  int b = 0;
+  auto deal = [&](int32_t all) {
+    per = (all + (int32_t)gridDim.x - 1) / (int32_t)gridDim.x;
+    u0 = (int32_t)blockIdx.x * per;
+    u1 = u0 + per < all ? u0 + per : all;
+    return u0 < all;
+  };
+  if (c.batch == 1) {
+    const int32_t len = len_uni(0);
+    if (!deal((len > 0 ? (len + kUnit - 1) / kUnit : 1) * hg)) return;
+  } else {
     // Thread i takes sequences [i * each, (i + 1) * each).
     const int each = (c.batch + kAttThreads - 1) / kAttThreads;
     int32_t mine = 0;
@@ -233,11 +296,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
       if (i < wave) before += lds.scan[i];
       all += lds.scan[i];
     }
-    all = uni(all);
-    per = (all + (int32_t)gridDim.x - 1) / (int32_t)gridDim.x;
-    u0 = (int32_t)blockIdx.x * per;
-    u1 = u0 + per < all ? u0 + per : all;
-    if (u0 >= all) return;
+    if (!deal(uni(all))) return;
     if (u0 >= before && u0 < before + mine) {
       int i = tid * each;
       for (int32_t un; before + (un = units_of(i)) <= u0; ++i) before += un;
@@ -249,16 +308,94 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
     base = uni(lds.base);
   }
 
-  int32_t len = len_of(b);
-  int32_t row_units = units_of(b) / hg;
+  int32_t len = len_uni(b);
+  auto row_units_of = [&](int32_t len) {
+    return len > 0 ? (len + kUnit - 1) / kUnit : 1;
+  };
+  int32_t row_units = row_units_of(len);
   int32_t u = u0;
+
+  // Scores of the units that this workgroup holds in LDS, as
+  // [unit][wave][part_rows][32]; `held` of them.  Those of a row that lies
+  // within the run become weights as soon as the row's sum is known.  Those
+  // of a row that other runs share go to memory, at the end of the run (or
+  // when LDS is full): a few per cent of writes strewn among the reads cost
+  // the stream more than ten times their bytes (48 sequences of 4096 slots,
+  // 8 heads of 4 queries: 165 us with each tile's scores written at once, 129
+  // us with none).
+  extern __shared__ float4 held_raw[];
+  float* const held_scores = (float*)held_raw;
+  const int tile_floats = p.part_rows * kTileSlots;
+  const int unit_floats = tile_floats * kAttWaves;
+  int32_t held = 0;
+  // A share of a row that is not finished: its row, length, runs, and the
+  // units [from, from + count) at `at` in LDS.
+  struct Share {
+    int32_t b, hi, len, first, last;
+    int32_t from, count, at;
+    bool open;
+  };
+  Share pend = {};
+  auto unit_scores = [&](const Share& r, int32_t unit) {
+    return p.scores + (((int64_t)r.b * hg + r.hi) * p.row_units + unit) *
+                          unit_floats;
+  };
+  auto flush = [&](Share& r) {
+    if (r.count > 0) {
+      const int bytes = r.count * unit_floats * 4;
+      const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(
+          uni_ptr(unit_scores(r, r.from)), (short)0, bytes, 0x00020000);
+      const f32x4* from = (const f32x4*)(held_scores + r.at * unit_floats);
+      for (int i = tid; i < bytes / 16; i += kAttThreads)
+        st_agent4(to, i * 16, from[i]);
+    }
+    r.from += r.count;
+    r.count = 0;
+  };
+  // weights += sum over queries of exp2(x - lse2), for a row whose lse2 is in
+  // LDS; scores of the share's units from LDS, the others from memory.
+  auto finish_weights = [&](const Share& r, int queries) {
+    float* w = p.w.w + r.b * p.w.wb + r.hi * p.w.wh;
+    const float* all = unit_scores(r, 0);
+    const __amdgpu_buffer_rsrc_t mem = __builtin_amdgcn_make_buffer_rsrc(
+        uni_ptr(const_cast<float*>(all)), (short)0,
+        row_units_of(r.len) * unit_floats * 4, 0x00020000);
+    for (int32_t i = tid; i * 4 < r.len; i += kAttThreads) {
+      const int32_t t = i / 8, unit = t / kAttWaves;
+      const bool here = unit >= r.from && unit < r.from + r.count;
+      const int32_t at =
+          ((here ? unit - r.from + r.at : unit) * kAttWaves + t % kAttWaves) *
+          tile_floats;
+      f32x4 a = {0, 0, 0, 0};
+      for (int g0 = 0; g0 < queries; g0 += 4) {
+        f32x4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int g = g0 + k < queries ? g0 + k : g0;
+          const int o = at + score_at(g, i % 8);
+          x[k] = here ? *(const f32x4*)(held_scores + o)
+                      : ld_agent4(mem, o * 4);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (g0 + k >= queries) continue;
+          const float z = lds.lse2[g0 + k];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            a[e] += x[k][e] == -INFINITY ? 0.0f : exp2_fast(x[k][e] - z);
+        }
+      }
+      add_weights(w + i * 4, r.len - i * 4, a);
+    }
+  };
+
   while (u < u1) {
     // ---- a row's share of the run ------------------------------------------
     while (u >= base + row_units * hg) {
       base += row_units * hg;
       ++b;
-      len = len_of(b);
-      row_units = units_of(b) / hg;
+      len = len_uni(b);
+      row_units = row_units_of(len);
     }
     const int hi = uni((u - base) / row_units);
     const int h = hi / p.gtiles, g0 = hi % p.gtiles * 16;
@@ -268,23 +405,19 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
     const int64_t qrow = (int64_t)b * c.heads * p.group + h * p.group + g0;
     const int32_t* table = c.table + b * c.table_stride;
     const int32_t tiles = (len + kTileSlots - 1) / kTileSlots;
-    int32_t t = (u - r0) * kAttWaves + wave;
-    int32_t t1 = (s1 - r0) * kAttWaves;
-    if (t1 > tiles) t1 = tiles;
     const char* kh = c.k + h * c.ks.head;
     const char* vh = c.v + h * c.vs.head;
-    float* scores =
-        p.scores ? p.scores + (qrow + n) * p.score_ld : nullptr;
-    const float scale = p.scale2 * (p.k_scale ? p.k_scale[h] : 1.0f);
+    Share cur = {b, hi, len, r0 / per, (r1 - 1) / per, u - r0, 0, held, true};
+    const float scale = p.scale2 * (p.k_scale ? ld_const(p.k_scale + h) : 1.0f);
 
     float m = -INFINITY, l = 0.0f;
     f32x4 o[NB * VE];
 #pragma unroll
     for (int i = 0; i < NB * VE; ++i) o[i] = f32x4{0, 0, 0, 0};
 
-    if (t < t1) {
-      // Query fragments: those of 8-bit rows pair up to match 16-byte loads.
-      Frag qf[QL];
+    // Query fragments: those of 8-bit rows pair up to match 16-byte loads.
+    Frag qf[QL];
+    if (len > 0) {
 #pragma unroll
       for (int f = 0; f < QL; ++f) {
         const int d = CT == kE4m3 ? f / 2 * 64 + q * 16 + f % 2 * 8
@@ -296,6 +429,30 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[f].d[e] = x[e];
       }
+    }
+
+    for (int32_t ua = u - r0, ue; ua < s1 - r0; ua = ue) {
+      // ---- units [ua, ue) of the row: all of the share, or what LDS holds
+      ue = s1 - r0;
+      float* tile_scores = nullptr;
+      if (p.scores) {
+        if (held == p.held_units) {
+          __syncthreads();
+          flush(pend);
+          flush(cur);
+          drain_memory_ops();  // finish_weights may read them back
+          __syncthreads();
+          held = 0;
+          cur.at = 0;
+        }
+        if (ue - ua > p.held_units - held) ue = ua + p.held_units - held;
+        tile_scores = held_scores + held * unit_floats + wave * tile_floats;
+        held += ue - ua;
+        cur.count += ue - ua;
+      }
+      int32_t t = ua * kAttWaves + wave;
+      const int32_t t1 = ue * kAttWaves < tiles ? ue * kAttWaves : tiles;
+      if (t >= t1) continue;
 
       v4i kr[2][KL];
       int vr[NB][8][VD];
@@ -313,7 +470,7 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
           for (int k = 0; k < KL; ++k) {
             const int at = k * 64 + q * 16;
             const bool in = A::last_chunk(k) < A::SHORT || at < c.row_bytes;
-            kr[tt][k] = *(const v4i*)(row + (in ? at : 0));
+            kr[tt][k] = ld_once<v4i>(row + (in ? at : 0));
           }
         }
       };
@@ -334,15 +491,15 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
             const int col = (nb * 16 + n) * VE * ES;
             const char* src = row + (col < c.row_bytes ? col : 0);
             if constexpr (VD == 4) {
-              const v4i x = *(const v4i*)src;
+              const v4i x = ld_once<v4i>(src);
 #pragma unroll
               for (int e = 0; e < 4; ++e) vr[nb][j][e] = x[e];
             } else if constexpr (VD == 2) {
-              const int2 x = *(const int2*)src;
-              vr[nb][j][0] = x.x;
-              vr[nb][j][1] = x.y;
+              const v2i x = ld_once<v2i>(src);
+              vr[nb][j][0] = x[0];
+              vr[nb][j][1] = x[1];
             } else {
-              vr[nb][j][0] = *(const int*)src;
+              vr[nb][j][0] = ld_once<int>(src);
             }
           }
         }
@@ -419,18 +576,15 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
           x[j] = ok[j] ? s[j / 4][j % 4] * scale : -INFINITY;
           hi_x = fmaxf(hi_x, x[j]);
         }
-        if (scores && n < queries) {
+        if (tile_scores) {
+          if (n < queries) {
 #pragma unroll
-          for (int tt = 0; tt < 2; ++tt) {
-            uint64_t* dst = (uint64_t*)(scores + t * kTileSlots + tt * 16 +
-                                        q * 4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              st_agent(dst + e,
-                       (uint64_t)__float_as_uint(x[4 * tt + 2 * e]) |
-                           (uint64_t)__float_as_uint(x[4 * tt + 2 * e + 1])
-                               << 32);
+            for (int tt = 0; tt < 2; ++tt)
+              *(f32x4*)(tile_scores + score_at(n, tt * 4 + q)) =
+                  f32x4{x[4 * tt], x[4 * tt + 1], x[4 * tt + 2],
+                        x[4 * tt + 3]};
           }
+          tile_scores += unit_floats;
         }
         // The reference m of a query only moves when a score passes it by
         // 2^8: until then exp2(x - m) stays below 2^8 and nothing has to be
@@ -503,14 +657,16 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
       };
       for (; t + kAttWaves < t1; t += kAttWaves) step(std::true_type());
       step(std::false_type());
-      l = quad_sum(l);
     }
+    l = quad_sum(l);
 
     // ---- the workgroup's waves joined ---------------------------------------
     const bool whole = u == r0 && s1 == r1;
-    const int32_t first = r0 / per, last = (r1 - 1) / per;
-    const int64_t part_size = (int64_t)p.part_rows * (COLS + 2);
-    float* part = p.part + ((int64_t)blockIdx.x * 2 + (u == r0)) * part_size;
+    // Bytes of a run's result, and where this one lies.
+    const int32_t part_size = p.part_rows * (COLS + 2) * 4;
+    const int32_t part = ((int)blockIdx.x * 2 + (u == r0)) * part_size;
+    const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
+        p.part, (short)0, (int)gridDim.x * 2 * part_size, 0x00020000);
     if (q == 0) {
       lds.m[wave][n] = m;
       lds.l[wave][n] = l;
@@ -527,24 +683,28 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
       }
       lds.top[tid] = top;
       lds.sum[tid] = sum;
+      lds.lse2[tid] = sum == 0.0f ? -INFINITY : top + log2f(sum);
       if (tid < queries) {
         if (whole) {
-          p.lse[qrow + tid] =
-              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          p.lse[qrow + tid] = lds.lse2[tid] * kLn2;
         } else {
-          st_agent(part + p.part_rows * COLS + tid, top);
-          st_agent(part + p.part_rows * (COLS + 1) + tid, sum);
+          st_agent(p.part + part / 4 + p.part_rows * COLS + tid, top);
+          st_agent(p.part + part / 4 + p.part_rows * (COLS + 1) + tid, sum);
         }
       }
     }
-    const float vs = p.v_scale ? p.v_scale[h] : 1.0f;
-    auto store = [&](int g, int col, float x) {
-      const int64_t at = (qrow + g) * c.dim + col;
-      if constexpr (QT == kBf16)
-        ((__bf16*)p.out)[at] = (__bf16)x;
-      else
-        ((_Float16*)p.out)[at] = (_Float16)x;
+    auto store = [&](int64_t row, int g, int col, float vs, f32x4 x) {
+      const float sum = lds.sum[g];
+      const float f = vs / sum;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] * f;
+      *(int2*)((char*)p.out + ((row + g) * c.dim + col) * 2) =
+          make_int2(pack2<QT>(x[0], x[1]), pack2<QT>(x[2], x[3]));
     };
+    auto v_factor = [&](int h) {
+      return p.v_scale ? ld_const(p.v_scale + h) : 1.0f;
+    };
+    const float vs = v_factor(h);
     for (int g4 = 0; g4 < queries; g4 += 4) {
       if (q == g4 / 4) {
 #pragma unroll
@@ -560,91 +720,166 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
             }
       }
       __syncthreads();
-      for (int at = tid; at < 4 * COLS; at += kAttThreads) {
-        const int i = at / COLS, col = at % COLS, g = g4 + i;
-        if (g >= queries || col >= c.dim) continue;
-        float x = 0.0f;
+      if (tid < COLS) {
+        const int i = tid / (COLS / 4), col = tid % (COLS / 4) * 4, g = g4 + i;
+        if (g < queries && col < c.dim) {
+          f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kAttWaves; ++w) x += lds.o[w][i][col] * lds.m[w][g];
-        if (whole)
-          store(g, col, lds.sum[g] == 0.0f ? 0.0f : x * vs / lds.sum[g]);
-        else
-          st_agent(part + g * COLS + col, x);
+          for (int w = 0; w < kAttWaves; ++w)
+            x += *(const f32x4*)&lds.o[w][i][col] * lds.m[w][g];
+          if (whole)
+            store(qrow, g, col, vs, x);
+          else
+            st_agent4(parts, part + (g * COLS + col) * 4, x);
+        }
       }
       __syncthreads();
     }
 
-    // ---- the row's runs joined, by the last of them --------------------------
-    if (!whole &&
-        last_to_finish(p.ticket + (int64_t)b * hg + hi, last - first + 1,
-                       p.epoch, &lds.flag)) {
+    if (p.scores) {
+      const bool added = whole && p.gtiles == 1;
+      if (p.split && u == r0 && tid == 0)
+        p.split[(int64_t)b * hg + hi] = !added;
+      if (added) {
+        finish_weights(cur, queries);
+        held -= cur.count;
+        __syncthreads();
+      }
+      // (The rows of a head with more than 16 queries share its weights, and
+      // leave them to the second kernel.)
+      if (whole && !added) {
+        flush(cur);
+        held = cur.at;
+        __syncthreads();
+      }
+    }
+    const bool at_end = s1 == u1;
+    if (!whole && p.scores && !at_end) pend = cur;
+
+    // ---- shares of split rows joined, by the last workgroup of each ----------
+    if (p.scores && at_end) {
+      flush(pend);
+      if (!whole) flush(cur);
+    }
+    for (int which = 0; which < 2; ++which) {
+      Share& r = which ? cur : pend;
+      if (which ? whole || (p.scores && !at_end) : !at_end || !pend.open)
+        continue;
+      const int32_t first = r.first, last = r.last;
+      if (!last_to_finish(p.ticket + (int64_t)r.b * hg + r.hi,
+                          last - first + 1, p.epoch, &lds.flag))
+        continue;
+      const int h = r.hi / p.gtiles, g0 = r.hi % p.gtiles * 16;
+      const int queries = p.group - g0 < 16 ? p.group - g0 : 16;
+      const int64_t qrow =
+          (int64_t)r.b * c.heads * p.group + h * p.group + g0;
+      const float vs = v_factor(h);
       auto part_of = [&](int32_t w) {
-        return p.part + ((int64_t)w * 2 + (w == first)) * part_size;
+        return (w * 2 + (w == first)) * part_size;
       };
-      const int g = tid / 32;  // 16 queries by 32 threads
+      const int32_t at_m = p.part_rows * COLS * 4;
+      constexpr int TG = kAttThreads / 16;  // threads of a query
+      const int g = tid / TG;
       float top = -INFINITY, sum = 0.0f;
       if (g < queries) {
-        for (int32_t w = first + tid % 32; w <= last; w += 32)
-          top = fmaxf(top, ld_agent(part_of(w) + p.part_rows * COLS + g));
+        for (int32_t w = first + tid % TG; w <= last; w += TG)
+          top = fmaxf(top, ld_agent1(parts, part_of(w) + at_m + g * 4));
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1)
+        for (int k = TG / 2; k > 0; k >>= 1)
           top = fmaxf(top, __shfl_xor(top, k, kWave));
-        for (int32_t w = first + tid % 32; w <= last; w += 32) {
-          const float* pm = part_of(w) + p.part_rows * COLS + g;
-          const float mw = ld_agent(pm);
-          sum += ld_agent(pm + p.part_rows) *
+        for (int32_t w = first + tid % TG; w <= last; w += TG) {
+          const int32_t at = part_of(w) + at_m + g * 4;
+          const float mw = ld_agent1(parts, at);
+          sum += ld_agent1(parts, at + p.part_rows * 4) *
                  (mw == top ? 1.0f : exp2_fast(mw - top));
         }
 #pragma unroll
-        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor(sum, k, kWave);
-        if (tid % 32 == 0) {
+        for (int k = TG / 2; k > 0; k >>= 1) sum += __shfl_xor(sum, k, kWave);
+        if (tid % TG == 0) {
           lds.top[g] = top;
           lds.sum[g] = sum;
-          p.lse[qrow + g] =
-              sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+          lds.lse2[g] = sum == 0.0f ? -INFINITY : top + log2f(sum);
+          p.lse[qrow + g] = lds.lse2[g] * kLn2;
         }
       }
       __syncthreads();
-      for (int at = tid; at < queries * COLS; at += kAttThreads) {
-        const int gg = at / COLS, col = at % COLS;
-        if (col >= c.dim) continue;
-        const float tg = lds.top[gg];
-        float x = 0.0f;
-#pragma unroll 8
-        for (int32_t w = first; w <= last; ++w) {
-          const float* pw = part_of(w);
-          const float mw = ld_agent(pw + p.part_rows * COLS + gg);
-          x += ld_agent(pw + gg * COLS + col) *
-               (mw == tg ? 1.0f : exp2_fast(mw - tg));
+      // Four columns a thread; with threads to spare, the runs are split
+      // over `subs` of them.
+      const int vecs = queries * (COLS / 4);
+      const int subs = vecs < kAttThreads ? kAttThreads / vecs : 1;
+      for (int o0 = 0; o0 < vecs; o0 += kAttThreads) {
+        const int sub = subs > 1 ? tid / vecs : 0;
+        const int at = subs > 1 ? tid % vecs : o0 + tid;
+        const int gg = at / (COLS / 4), col = at % (COLS / 4) * 4;
+        f32x4 x = {0, 0, 0, 0};
+        if (at < vecs && sub < subs) {
+          const float tg = lds.top[gg];
+          constexpr int J = 8;  // loads in flight
+          for (int32_t w = first + sub; w <= last; w += J * subs) {
+            f32x4 d[J];
+            float mw[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              const int32_t wj = w + j * subs;
+              const int32_t pj = part_of(wj <= last ? wj : w);
+              d[j] = ld_agent4(parts, pj + (gg * COLS + col) * 4);
+              mw[j] = ld_agent1(parts, pj + at_m + gg * 4);
+            }
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+              const float f = mw[j] == tg ? 1.0f : exp2_fast(mw[j] - tg);
+              x += d[j] * (w + j * subs <= last ? f : 0.0f);
+            }
+          }
         }
-        store(gg, col, lds.sum[gg] == 0.0f ? 0.0f : x * vs / lds.sum[gg]);
+        if (subs > 1) {
+          f32x4* sums = (f32x4*)&lds.o[0][0][0];
+          if (sub < subs) sums[sub * vecs + at] = x;
+          __syncthreads();
+          if (sub == 0)
+            for (int i = 1; i < subs; ++i) x += sums[i * vecs + at];
+        }
+        if (sub == 0 && at < vecs && col < c.dim)
+          store(qrow, gg, col, vs, x);
       }
+      if (p.scores && p.direct) finish_weights(r, queries);
+      __syncthreads();
     }
     u = s1;
   }
 }
 
-// weights[t] += sum over the head's queries of exp(x - lse).  One workgroup
-// per chunk of kBlock slots of a sequence and head, round robin.
+// weights[t] += sum over the head's queries of exp(x - lse), for the rows that
+// attend_kernel left: four slots a thread, a workgroup for every kWeightSlots
+// slots of a sequence and head.
+constexpr int kWeightSlots = 4 * kBlock;
+
 __global__ __launch_bounds__(kBlock) void attend_weights_kernel(
     AttendParams p) {
   const CacheParams& c = p.c;
-  const int32_t chunks = (c.cap + kBlock - 1) / kBlock;
-  const int64_t all = (int64_t)c.batch * c.heads * chunks;
-  for (int64_t i = blockIdx.x; i < all; i += gridDim.x) {
-    const int row = (int)(i / chunks);  // sequence and head
+  const int32_t i = blockIdx.x * kBlock + threadIdx.x, t = i / 8;
+  const int tile_floats = p.part_rows * kTileSlots;
+  for (int row = blockIdx.y; row < c.batch * c.heads; row += gridDim.y) {
     const int b = row / c.heads, h = row % c.heads;
-    const int32_t len = clamp_len(c.lens[b], c.pages > 0 ? c.cap : 0);
-    const int32_t t = (int32_t)(i % chunks) * kBlock + threadIdx.x;
-    if (t >= len) continue;
-    const int64_t first = (int64_t)row * p.group;
-    float a = 0.0f;
-    for (int g = 0; g < p.group; ++g) {
-      const float lse2 = p.lse[first + g] * (1.0f / kLn2);
-      const float x = p.scores[(first + g) * p.score_ld + t];
-      a += x == -INFINITY ? 0.0f : exp2_fast(x - lse2);
+    const int32_t len =
+        clamp_len(ld_const(c.lens + b), c.pages > 0 ? c.cap : 0);
+    if (i * 4 >= len || !p.split[(int64_t)row * p.gtiles]) continue;
+    f32x4 a = {0, 0, 0, 0};
+    for (int gt = 0; gt < p.gtiles; ++gt) {
+      const float* x0 =
+          p.scores + (((int64_t)row * p.gtiles + gt) * p.row_units *
+                          kAttWaves + t) * tile_floats;
+      for (int g = 0; g < 16 && gt * 16 + g < p.group; ++g) {
+        const float lse2 =
+            ld_const(p.lse + (int64_t)row * p.group + gt * 16 + g) *
+            (1.0f / kLn2);
+        const f32x4 x = *(const f32x4*)(x0 + score_at(g, i % 8));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          a[e] += x[e] == -INFINITY ? 0.0f : exp2_fast(x[e] - lse2);
+      }
     }
-    p.w.w[b * p.w.wb + h * p.w.wh + t] += a;
+    add_weights(p.w.w + b * p.w.wb + h * p.w.wh + i * 4, len - i * 4, a);
   }
 }
 

@@ -30,6 +30,16 @@ struct LedgerParams {
   int64_t wb, wh, pb, ph;  // elements
 };
 
+// Load, through the scalar cache, of a value that no kernel in flight writes
+// (tables, lengths, scales), from an address that is the same in every lane.
+// Scalar loads have a counter of their own: waiting for one leaves the vector
+// loads before and after it in flight.
+template <class T>
+__device__ __forceinline__ T ld_const(const T* p) {
+  typedef const __attribute__((address_space(4))) T ConstT;
+  return *(ConstT*)(uintptr_t)p;
+}
+
 // Page of slot t of a sequence whose table row is `table` (-1: none), and the
 // slot's place within the page.
 __device__ __forceinline__ int32_t find_page(const CacheParams& c,
