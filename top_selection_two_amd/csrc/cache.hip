@@ -79,13 +79,17 @@ __global__ void fill_words(uint64_t* p, int64_t n, uint64_t seed) {
   p[i] = seed ? (z ^ (z >> 31)) | 1ull : 0ull;
 }
 
+int launched(const char* what) {
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) return LIBTOPK_OK;
+  debug_hip(what, e);
+  return LIBTOPK_ERR_HIP;
+}
+
 int fill(uint64_t* p, size_t words, uint64_t seed, hipStream_t s) {
   hipLaunchKernelGGL(fill_words, dim3((unsigned)((words + 255) / 256)),
                      dim3(256), 0, s, p, (int64_t)words, seed);
-  const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) return LIBTOPK_OK;
-  debug_hip("fill_words launch", e);
-  return LIBTOPK_ERR_HIP;
+  return launched("fill_words");
 }
 
 // Caller holds g_mu.
@@ -358,6 +362,8 @@ constexpr int kLdsBytes = 160 * 1024;
 // Rows of at most this many slots get their weights from their last
 // workgroup, longer ones from a second launch.
 constexpr int kDirectSlots = 16384;
+static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
+              "a thread searches two bins");
 
 size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
@@ -587,14 +593,58 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  if (p.pair_cap > 0) {
-    Work work;
-    rc = get_work(dev, s, (size_t)rows * p.pair_cap * 8, 1, &work);
-    if (rc != LIBTOPK_OK) return rc;
-    p.pairs = (int32_t*)work.base;
+  const bool is_long = p.c.cap > kShortSlots;
+  p.chunks = is_long ? (p.c.cap + kChunkSlots - 1) / kChunkSlots : 1;
+  if (rows > INT32_MAX / p.chunks) return LIBTOPK_ERR_INVALID;
+  if (p.pair_cap == 0) {  // every row is short enough as it is
+    return launch((const void*)&evict_short_kernel<1>, dim3((unsigned)rows),
+                  kEvThreads, p, s);
   }
-  return launch((const void*)&evict_kernel, dim3((unsigned)rows), kBlock, p,
-                s);
+  p.row_units = make_divisor(2 * p.c.row_bytes / 16);
+  if ((int64_t)p.pair_cap * p.row_units.d > INT32_MAX - kBlock * kMoves)
+    return LIBTOPK_ERR_INVALID;
+  const size_t pair_bytes = round_up((size_t)rows * p.pair_cap * 8, 256);
+  const size_t move_bytes = round_up((size_t)rows * 4, 256);
+  const size_t hist_words = is_long ? (size_t)rows * 3 * kBins / 2 : 0;
+  const size_t count_bytes = is_long ? (size_t)rows * p.chunks * 16 : 0;
+  Work work;
+  rc = get_work(dev, s, pair_bytes + move_bytes + hist_words * 8 + count_bytes,
+                1, &work);
+  if (rc != LIBTOPK_OK) return rc;
+  char* at = work.base;
+  p.pairs = (int32_t*)at;
+  p.moves = (int32_t*)(at += pair_bytes);
+  p.hist = (uint32_t*)(at += move_bytes);
+  p.counts = (int32_t*)(at += hist_words * 8);
+  const unsigned wide = (unsigned)(rows * p.chunks);
+  if (is_long) {
+    rc = fill((uint64_t*)p.hist, hist_words, 0, s);
+    for (int pass = 0; pass < 3 && rc == LIBTOPK_OK; ++pass) {
+      hipLaunchKernelGGL(evict_digit_kernel, dim3(wide), dim3(kEvThreads), 0,
+                         s, p, pass);
+      rc = launched("evict_digit_kernel");
+    }
+    if (rc == LIBTOPK_OK)
+      rc = launch((const void*)&evict_count_kernel, dim3(wide), kEvThreads, p,
+                  s);
+    if (rc == LIBTOPK_OK)
+      rc = launch((const void*)&evict_list_kernel, dim3(wide), kEvThreads, p,
+                  s);
+  } else {
+    const int keys = (p.c.cap + kEvThreads - 1) / kEvThreads;
+    const void* fn = keys <= 2   ? (const void*)&evict_short_kernel<2>
+                     : keys <= 4 ? (const void*)&evict_short_kernel<4>
+                     : keys <= 8 ? (const void*)&evict_short_kernel<8>
+                                 : (const void*)&evict_short_kernel<16>;
+    rc = launch(fn, dim3(wide), kEvThreads, p, s);
+  }
+  if (rc != LIBTOPK_OK) return rc;
+  const int64_t units = (int64_t)p.pair_cap * p.row_units.d;
+  return launch((const void*)&evict_move_kernel,
+                dim3((unsigned)((units + kBlock * kMoves - 1) /
+                                (kBlock * kMoves)),
+                     (unsigned)(rows < 65535 ? rows : 65535)),
+                kBlock, p, s);
 }
 
 void cache_release(void) {

@@ -10,6 +10,9 @@
 
 namespace ltk {
 
+typedef float f32x4s __attribute__((ext_vector_type(4), aligned(4)));
+typedef int i32x4s __attribute__((ext_vector_type(4), aligned(4)));
+
 struct SlotsParams {
   CacheParams c;
   LedgerParams w;
@@ -25,7 +28,12 @@ struct SlotsParams {
   int32_t keep;
   LedgerParams after;
   int32_t* pairs;     // [rows][2][pair_cap]: holes, then movers
+  int32_t* moves;     // [rows]: pairs of the row
   int32_t pair_cap;
+  Divisor row_units;  // 16-byte units of a K and a V row
+  uint32_t* hist;     // [rows][3][kBins], long rows
+  int32_t* counts;    // [rows][chunks][4], long rows
+  int32_t chunks;
   int32_t* out_lens;
 };
 
@@ -33,163 +41,507 @@ __device__ __forceinline__ uint64_t min64(uint64_t a, uint64_t b) {
   return a < b ? a : b;
 }
 
-// Key of slot t of a ledger row.
-__device__ __forceinline__ int32_t slot_key(const float* w, const int32_t* pos,
-                                            int32_t t, int32_t seen,
-                                            int32_t sinks, int32_t recent) {
-  return rank_key(__float_as_int(w[t]), pos[t], seen, sinks, recent);
+// A row (sequence and head) of the ledger as the kernels read it.
+struct LedgerRow {
+  int b, h;
+  int32_t len, seen;
+  const float* w;
+  const int32_t* pos;
+};
+
+__device__ __forceinline__ LedgerRow ledger_row(const SlotsParams& p,
+                                                int row) {
+  LedgerRow r;
+  r.b = row / p.c.heads;
+  r.h = row % p.c.heads;
+  r.len = clamp_len(ld_const(p.c.lens + r.b), p.c.cap);
+  r.seen = ld_const(p.seen + r.b);
+  r.w = p.w.w + r.b * p.w.wb + r.h * p.w.wh;
+  r.pos = p.w.pos + r.b * p.w.pb + r.h * p.w.ph;
+  return r;
 }
 
-// One workgroup per sequence and head.
+// ---- append ------------------------------------------------------------------
+// One workgroup per sequence and head.  A full row is read once, four slots a
+// thread at a time, for the least (key, slot) word; the reads of a row of some
+// thousand slots are all in flight together.
 __global__ __launch_bounds__(kBlock) void append_kernel(SlotsParams p) {
   const CacheParams& c = p.c;
   const int row = blockIdx.x;
-  const int b = row / c.heads, h = row % c.heads;
-  const int32_t len = clamp_len(c.lens[b], c.cap);
-  const int32_t seen = p.seen[b];
-  float* w = p.w.w + b * p.w.wb + h * p.w.wh;
-  int32_t* pos = p.w.pos + b * p.w.pb + h * p.w.ph;
+  const LedgerRow r = ledger_row(p, row);
+  const int32_t len = r.len;
+  // The new row's bytes, loaded ahead of the search.
+  const int units = c.row_bytes / 16;
+  const int tid = threadIdx.x;
+  const bool is_k = tid < units, mover = tid < 2 * units;
+  const int off = (is_k ? tid : tid - units) * 16;
+  v4i bytes = {0, 0, 0, 0};
+  if (mover)
+    bytes = *(const v4i*)((is_k ? p.k_new : p.v_new) + r.b * p.nb +
+                          r.h * p.nh + off);
   __shared__ uint64_t low[kWaves];
   int32_t slot;
   if (len < p.limit) {
     slot = len < c.cap ? len : -1;
   } else {
     uint64_t last = ~0ull;
-    for (int32_t t = threadIdx.x; t < len; t += kBlock)
-      last = min64(last, rank_word(slot_key(w, pos, t, seen, p.sinks,
-                                            p.recent), t));
+    const int32_t whole = len & ~3;
+    constexpr int J = 4;
+    for (int32_t t0 = tid * 4; t0 < whole; t0 += J * 4 * kBlock) {
+      f32x4s w[J];
+      i32x4s at[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int32_t t = t0 + j * 4 * kBlock;
+        const int32_t in = t < whole ? t : t0;  // a repeat changes nothing
+        w[j] = *(const f32x4s*)(r.w + in);
+        at[j] = *(const i32x4s*)(r.pos + in);
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int32_t t = t0 + j * 4 * kBlock;
+        const int32_t in = t < whole ? t : t0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          last = min64(last, rank_word(rank_key(__float_as_int(w[j][e]),
+                                                at[j][e], r.seen, p.sinks,
+                                                p.recent),
+                                       in + e));
+      }
+    }
+    const int32_t t = whole + tid;
+    if (t < len)
+      last = min64(last, rank_word(rank_key(__float_as_int(r.w[t]), r.pos[t],
+                                            r.seen, p.sinks, p.recent),
+                                   t));
     last = wave_fold(last, min64);
-    if (threadIdx.x % kWave == 0) low[threadIdx.x / kWave] = last;
+    if (tid % kWave == 0) low[tid / kWave] = last;
     __syncthreads();
     for (int i = 0; i < kWaves; ++i) last = min64(last, low[i]);
     slot = (int32_t)~(uint32_t)last;
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     p.out_slots[row] = slot;
-    if (h == 0) p.out_lens[b] = len < p.limit && slot >= 0 ? len + 1 : len;
+    if (r.h == 0) p.out_lens[r.b] = len < p.limit && slot >= 0 ? len + 1 : len;
     if (slot >= 0) {
-      w[slot] = 0.0f;
-      pos[slot] = seen;
+      const_cast<float*>(r.w)[slot] = 0.0f;
+      const_cast<int32_t*>(r.pos)[slot] = r.seen;
     }
   }
   if (slot < 0) return;
   int32_t place;
   const int32_t id =
-      find_page(c, c.table + b * c.table_stride, slot, &place);
+      find_page(c, c.table + r.b * c.table_stride, slot, &place);
   if (id < 0) return;
-  const int units = c.row_bytes / 16;
-  const int u = threadIdx.x;
-  if (u < 2 * units) {
-    const bool is_k = u < units;
-    const int off = (is_k ? u : u - units) * 16;
-    const char* src = (is_k ? p.k_new : p.v_new) + b * p.nb + h * p.nh + off;
-    const char* dst = is_k ? c.k + row_offset(c.ks, id, h, place)
-                           : c.v + row_offset(c.vs, id, h, place);
-    *(v4i*)(const_cast<char*>(dst) + off) = *(const v4i*)src;
+  if (mover) {
+    const char* dst = is_k ? c.k + row_offset(c.ks, id, r.h, place)
+                           : c.v + row_offset(c.vs, id, r.h, place);
+    *(v4i*)(const_cast<char*>(dst) + off) = bytes;
   }
 }
 
-// Sum over the workgroup, in every thread.
-__device__ __forceinline__ int block_sum(int v, int* lds) {
-  v = wave_fold(v, [](int a, int e) { return a + e; });
-  __syncthreads();
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = v;
-  __syncthreads();
-  int s = 0;
-  for (int i = 0; i < kWaves; ++i) s += lds[i];
-  return s;
+// ---- eviction ----------------------------------------------------------------
+// The key of the last kept slot is found digit by digit (11, 11 and 10 bits)
+// from histograms of the keys; ties at it are kept in slot order.  Holes
+// (slots below `keep` that are not kept) and movers (kept slots at or beyond
+// it) are listed in slot order by counting, and a second kernel moves the
+// rows, which is most of the bytes.
+//
+// Rows of up to kShortSlots slots are selected by one workgroup that holds
+// their keys in registers.  Longer rows are cut into chunks of kChunkSlots,
+// a workgroup each, and the digits, the ties and the lists become launches.
+constexpr int kEvThreads = 1024;
+constexpr int kEvWaves = kEvThreads / kWave;
+constexpr int kBins = 2048;
+constexpr int kShortSlots = 16 * kEvThreads;
+constexpr int kChunkKeys = 8;
+constexpr int kChunkSlots = kChunkKeys * kEvThreads;
+
+struct Digit {
+  int shift, bits;
+};
+__device__ __forceinline__ Digit digit(int pass) {
+  return pass == 0 ? Digit{21, 11} : pass == 1 ? Digit{10, 11} : Digit{0, 10};
 }
 
-// Threads below this one for which f is true; *total of the workgroup.
-__device__ __forceinline__ int block_rank(bool f, int* lds, int* total) {
-  const uint64_t m = ballot(f);
+// Exclusive prefix sum of v over the workgroup, and the total.
+__device__ __forceinline__ int block_scan(int v, int* lds, int* total) {
+  const int incl = wave_scan_incl(v);
   __syncthreads();
-  if (threadIdx.x % kWave == 0) lds[threadIdx.x / kWave] = popc(m);
+  if (threadIdx.x % kWave == kWave - 1) lds[threadIdx.x / kWave] = incl;
   __syncthreads();
   int before = 0, all = 0;
-  for (int i = 0; i < kWaves; ++i) {
-    if (i < (int)threadIdx.x / kWave) before += lds[i];
-    all += lds[i];
+#pragma unroll
+  for (int i = 0; i < kEvWaves; ++i) {
+    const int x = lds[i];
+    if (i < (int)threadIdx.x / kWave) before += x;
+    all += x;
   }
   *total = all;
-  return before + lanes_below(m);
+  return before + incl - v;
 }
 
-// One workgroup per sequence and head: the key of the last kept slot by
-// bitwise search, the lists of holes and movers by ordered counting, then the
-// moves.
-__global__ __launch_bounds__(kBlock) void evict_kernel(SlotsParams p) {
-  const CacheParams& c = p.c;
-  const int row = blockIdx.x;
-  const int b = row / c.heads, h = row % c.heads;
-  const int32_t len = clamp_len(c.lens[b], c.cap);
-  const int32_t seen = p.seen[b], keep = p.keep;
-  const float* w = p.w.w + b * p.w.wb + h * p.w.wh;
-  const int32_t* pos = p.w.pos + b * p.w.pb + h * p.w.ph;
-  float* w2 = p.after.w + b * p.after.wb + h * p.after.wh;
-  int32_t* pos2 = p.after.pos + b * p.after.pb + h * p.after.ph;
-  if (h == 0 && threadIdx.x == 0) p.out_lens[b] = len < keep ? len : keep;
-  for (int32_t t = threadIdx.x; t < keep; t += kBlock) {
-    w2[t] = t < len ? w[t] : 0.0f;
-    pos2[t] = t < len ? pos[t] : -1;
-  }
-  if (len <= keep) return;
-  __shared__ int lds[kWaves];
-  // The largest u with at least `keep` keys >= u (keys biased to unsigned).
-  uint32_t cut = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t u = cut | (1u << bit);
-    int n = 0;
-    for (int32_t t = threadIdx.x; t < len; t += kBlock)
-      n += bias(slot_key(w, pos, t, seen, p.sinks, p.recent)) >= u;
-    if (block_sum(n, lds) >= keep) cut = u;
-  }
-  int above = 0;
-  for (int32_t t = threadIdx.x; t < len; t += kBlock)
-    above += bias(slot_key(w, pos, t, seen, p.sinks, p.recent)) > cut;
-  int ties = keep - block_sum(above, lds);  // of the slots with key = cut
-  int32_t* holes = p.pairs + (int64_t)row * 2 * p.pair_cap;
-  int32_t* movers = holes + p.pair_cap;
-  int nh = 0, nm = 0;
-  for (int32_t t0 = 0; t0 < len; t0 += kBlock) {
-    const int32_t t = t0 + threadIdx.x;
-    const bool in = t < len;
-    const uint32_t u =
-        in ? bias(slot_key(w, pos, t, seen, p.sinks, p.recent)) : 0u;
-    int total;
-    const int r = block_rank(in && u == cut, lds, &total);
-    const bool kept = in && (u > cut || (u == cut && r < ties));
-    ties -= total;
-    const bool hole = in && t < keep && !kept, mover = kept && t >= keep;
-    int i = nh + block_rank(hole, lds, &total);
-    if (hole && i < p.pair_cap) holes[i] = t;
-    nh += total;
-    i = nm + block_rank(mover, lds, &total);
-    if (mover && i < p.pair_cap) movers[i] = t;
-    nm += total;
-  }
+// The bin that holds the `want`-th largest key of a histogram, and how many
+// keys lie in the bins above it.  Thread i takes bins 2 i and 2 i + 1 counted
+// from the top.
+struct Found {
+  int bin, above;
+};
+__device__ __forceinline__ Found find_bin(const uint32_t* hist, int want,
+                                          int* lds, Found* out) {
+  const int b = kBins - 1 - 2 * (int)threadIdx.x;
+  const int c0 = (int)hist[b], c1 = (int)hist[b - 1];
+  int total;
+  const int before = block_scan(c0 + c1, lds, &total);
+  if (before < want && want <= before + c0) *out = Found{b, before};
+  if (before + c0 < want && want <= before + c0 + c1)
+    *out = Found{b - 1, before + c0};
   __syncthreads();
-  const int32_t* table = c.table + b * c.table_stride;
-  const int units = c.row_bytes / 16;
-  for (int i = threadIdx.x / kWave; i < nm && i < p.pair_cap; i += kWaves) {
-    const int32_t to = holes[i], from = movers[i];
-    if (threadIdx.x % kWave == 0) {
-      w2[to] = w[from];
-      pos2[to] = pos[from];
+  return *out;
+}
+
+// Keys of KPT slots a thread: wave w holds slots first + (w KPT + j) 64 + lane,
+// so that slot order is wave, j, lane.
+template <int KPT>
+__device__ __forceinline__ int32_t key_slot(int32_t first, int j) {
+  return first + ((int)threadIdx.x / kWave * KPT + j) * kWave +
+         (int)threadIdx.x % kWave;
+}
+
+template <int KPT>
+__device__ __forceinline__ void load_keys(const SlotsParams& p,
+                                          const LedgerRow& r, int32_t first,
+                                          uint32_t (&u)[KPT]) {
+  float w[KPT];
+  int32_t at[KPT];
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int32_t t = key_slot<KPT>(first, j);
+    const int32_t in = t < r.len ? t : 0;
+    w[j] = r.w[in];
+    at[j] = r.pos[in];
+  }
+#pragma unroll
+  for (int j = 0; j < KPT; ++j)
+    u[j] = bias(rank_key(__float_as_int(w[j]), at[j], r.seen, p.sinks,
+                         p.recent));
+}
+
+// Adds the digits of the keys that begin with `prefix` (all bits above the
+// digit) to a histogram in LDS.  A wave whose keys all fall into one bin
+// (protected slots, equal weights) adds once: its lanes would queue there.
+template <int KPT>
+__device__ __forceinline__ void count_digits(const uint32_t (&u)[KPT],
+                                             int32_t first, int32_t len,
+                                             uint32_t prefix, Digit d,
+                                             uint32_t* hist) {
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int32_t t = key_slot<KPT>(first, j);
+    const uint32_t head = d.shift + d.bits == 32
+                              ? 0u
+                              : u[j] >> (d.shift + d.bits) <<
+                                    (d.shift + d.bits);
+    const bool in = t < len && head == prefix;
+    const uint32_t bin = (u[j] >> d.shift) & ((1u << d.bits) - 1u);
+    const uint64_t all = ballot(in);
+    if (all == 0) continue;
+    const uint32_t bin0 = (uint32_t)__builtin_amdgcn_readlane(
+        (int)bin, __builtin_ctzll(all));
+    if (ballot(in && bin == bin0) == all) {
+      if (lane() == 0) atomicAdd(&hist[bin0], (uint32_t)popc(all));
+    } else if (in) {
+      atomicAdd(&hist[bin], 1u);
     }
-    int32_t zt, zf;
-    const int32_t it = find_page(c, table, to, &zt);
-    const int32_t jf = find_page(c, table, from, &zf);
-    if (it < 0 || jf < 0) continue;
-    const int u = threadIdx.x % kWave;
-    if (u < 2 * units) {
-      const bool is_k = u < units;
-      const int off = (is_k ? u : u - units) * 16;
+  }
+}
+
+__device__ __forceinline__ void clear_bins(uint32_t* hist) {
+  for (int i = threadIdx.x; i < kBins; i += kEvThreads) hist[i] = 0u;
+}
+
+// Lists a chunk's holes and movers and writes what stays in place; before the
+// chunk lie `ties` slots with key = cut, `holes` holes and `movers` movers.
+// `need` ties are kept in all.  Returns (in every thread) holes and movers
+// up to and with this chunk.
+template <int KPT>
+__device__ __forceinline__ int2 list_chunk(const SlotsParams& p,
+                                           const LedgerRow& r, int row,
+                                           int32_t first,
+                                           const uint32_t (&u)[KPT],
+                                           uint32_t cut, int need, int ties,
+                                           int holes, int movers, int* lds) {
+  const int keep = p.keep;
+  int n_tie = 0;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j)
+    n_tie += popc(ballot(key_slot<KPT>(first, j) < r.len && u[j] == cut));
+  // Of each wave: its ties, then its holes and movers (counts that are the
+  // same in every lane).
+  int total;
+  int tie = ties + uni(block_scan(lane() == 0 ? n_tie : 0, lds, &total));
+  uint64_t hole_m[KPT], move_m[KPT];
+  int nh = 0, nm = 0;
+  float* w2 = p.after.w + r.b * p.after.wb + r.h * p.after.wh;
+  int32_t* pos2 = p.after.pos + r.b * p.after.pb + r.h * p.after.ph;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int32_t t = key_slot<KPT>(first, j);
+    const bool in = t < r.len;
+    const uint64_t eq = ballot(in && u[j] == cut);
+    const bool kept = in && (u[j] > cut || (u[j] == cut &&
+                                            tie + lanes_below(eq) < need));
+    tie += popc(eq);
+    hole_m[j] = ballot(in && t < keep && !kept);
+    move_m[j] = ballot(kept && t >= keep);
+    nh += popc(hole_m[j]);
+    nm += popc(move_m[j]);
+    if (kept && t < keep) {
+      w2[t] = r.w[t];
+      pos2[t] = r.pos[t];
+    }
+  }
+  int th, tm;
+  int ih = holes + uni(block_scan(lane() == 0 ? nh : 0, lds, &th));
+  int im = movers + uni(block_scan(lane() == 0 ? nm : 0, lds, &tm));
+  int32_t* list = p.pairs + (int64_t)row * 2 * p.pair_cap;
+#pragma unroll
+  for (int j = 0; j < KPT; ++j) {
+    const int32_t t = key_slot<KPT>(first, j);
+    const int a = ih + lanes_below(hole_m[j]), b = im + lanes_below(move_m[j]);
+    if (hole_m[j] >> lane() & 1 && a < p.pair_cap) list[a] = t;
+    if (move_m[j] >> lane() & 1 && b < p.pair_cap) list[p.pair_cap + b] = t;
+    ih += popc(hole_m[j]);
+    im += popc(move_m[j]);
+  }
+  return make_int2(holes + th, movers + tm);
+}
+
+// Rows that are short enough to stay as they are: copied, and padded.
+__device__ __forceinline__ void copy_row(const SlotsParams& p,
+                                         const LedgerRow& r, int from,
+                                         int step) {
+  float* w2 = p.after.w + r.b * p.after.wb + r.h * p.after.wh;
+  int32_t* pos2 = p.after.pos + r.b * p.after.pb + r.h * p.after.ph;
+  for (int32_t t = from; t < p.keep; t += step) {
+    w2[t] = t < r.len ? r.w[t] : 0.0f;
+    pos2[t] = t < r.len ? r.pos[t] : -1;
+  }
+}
+
+template <int KPT>
+__global__ __launch_bounds__(kEvThreads) void evict_short_kernel(
+    SlotsParams p) {
+  __shared__ uint32_t hist[kBins];
+  __shared__ int lds[kEvWaves];
+  __shared__ Found found;
+  const int row = blockIdx.x, keep = p.keep;
+  const LedgerRow r = ledger_row(p, row);
+  if (threadIdx.x == 0) {
+    if (r.h == 0) p.out_lens[r.b] = r.len < keep ? r.len : keep;
+    if (p.moves && r.len <= keep) p.moves[row] = 0;
+  }
+  if (r.len <= keep) {
+    copy_row(p, r, threadIdx.x, kEvThreads);
+    return;
+  }
+  uint32_t u[KPT];
+  load_keys<KPT>(p, r, 0, u);
+  uint32_t cut = 0;
+  int want = keep;
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const Digit d = digit(pass);
+    clear_bins(hist);
+    __syncthreads();
+    count_digits<KPT>(u, 0, r.len, cut, d, hist);
+    __syncthreads();
+    const Found f = find_bin(hist, want, lds, &found);
+    cut |= (uint32_t)f.bin << d.shift;
+    want -= f.above;
+  }
+  const int2 n = list_chunk<KPT>(p, r, row, 0, u, cut, want, 0, 0, 0, lds);
+  if (threadIdx.x == 0) p.moves[row] = n.y;
+}
+
+// ---- long rows ---------------------------------------------------------------
+// hist[row][pass] collects the digits of all chunks; every later launch finds
+// the digits so far from it again.
+__device__ __forceinline__ void find_cut(const SlotsParams& p, int row,
+                                         int passes, int* lds, Found* found,
+                                         uint32_t* cut, int* want) {
+  *cut = 0;
+  *want = p.keep;
+  for (int i = 0; i < passes; ++i) {
+    const Found f = find_bin(p.hist + ((int64_t)row * 3 + i) * kBins, *want,
+                             lds, found);
+    __syncthreads();
+    *cut |= (uint32_t)f.bin << digit(i).shift;
+    *want -= f.above;
+  }
+}
+
+__global__ __launch_bounds__(kEvThreads) void evict_digit_kernel(
+    SlotsParams p, int pass) {
+  __shared__ uint32_t hist[kBins];
+  __shared__ int lds[kEvWaves];
+  __shared__ Found found;
+  const int row = blockIdx.x / p.chunks;
+  const int32_t first = blockIdx.x % p.chunks * kChunkSlots;
+  const LedgerRow r = ledger_row(p, row);
+  if (r.len <= p.keep || first >= r.len) return;
+  uint32_t u[kChunkKeys];
+  load_keys<kChunkKeys>(p, r, first, u);
+  uint32_t cut;
+  int want;
+  find_cut(p, row, pass, lds, &found, &cut, &want);
+  clear_bins(hist);
+  __syncthreads();
+  count_digits<kChunkKeys>(u, first, r.len, cut, digit(pass), hist);
+  __syncthreads();
+  uint32_t* all = p.hist + ((int64_t)row * 3 + pass) * kBins;
+  for (int i = threadIdx.x; i < kBins; i += kEvThreads)
+    if (hist[i]) atomicAdd(all + i, hist[i]);
+}
+
+// Of each chunk: slots with key above the cut and at it, below `keep` and
+// from it on.
+__global__ __launch_bounds__(kEvThreads) void evict_count_kernel(
+    SlotsParams p) {
+  __shared__ int lds[kEvWaves];
+  __shared__ Found found;
+  __shared__ int sums[4];
+  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int32_t first = chunk * kChunkSlots;
+  const LedgerRow r = ledger_row(p, row);
+  if (r.len <= p.keep || first >= r.len) return;
+  uint32_t u[kChunkKeys];
+  load_keys<kChunkKeys>(p, r, first, u);
+  if (threadIdx.x < 4) sums[threadIdx.x] = 0;
+  uint32_t cut;
+  int want;
+  find_cut(p, row, 3, lds, &found, &cut, &want);
+  int n[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < kChunkKeys; ++j) {
+    const int32_t t = key_slot<kChunkKeys>(first, j);
+    const bool in = t < r.len, low = t < p.keep;
+    n[0] += popc(ballot(in && low && u[j] > cut));
+    n[1] += popc(ballot(in && low && u[j] == cut));
+    n[2] += popc(ballot(in && !low && u[j] > cut));
+    n[3] += popc(ballot(in && !low && u[j] == cut));
+  }
+  if (lane() == 0)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n[i]) atomicAdd(&sums[i], n[i]);
+  __syncthreads();
+  if (threadIdx.x < 4)
+    p.counts[((int64_t)row * p.chunks + chunk) * 4 + threadIdx.x] =
+        sums[threadIdx.x];
+}
+
+__global__ __launch_bounds__(kEvThreads) void evict_list_kernel(
+    SlotsParams p) {
+  __shared__ int lds[kEvWaves];
+  __shared__ Found found;
+  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int32_t first = chunk * kChunkSlots;
+  const LedgerRow r = ledger_row(p, row);
+  if (chunk == 0 && r.h == 0 && threadIdx.x == 0)
+    p.out_lens[r.b] = r.len < p.keep ? r.len : p.keep;
+  if (r.len <= p.keep) {
+    if (chunk == 0 && threadIdx.x == 0) p.moves[row] = 0;
+    copy_row(p, r, chunk * kEvThreads + threadIdx.x, p.chunks * kEvThreads);
+    return;
+  }
+  if (first >= r.len) return;
+  uint32_t u[kChunkKeys];
+  load_keys<kChunkKeys>(p, r, first, u);
+  uint32_t cut;
+  int want;
+  find_cut(p, row, 3, lds, &found, &cut, &want);
+  // Ties, kept slots below `keep` and kept slots from it on, before this
+  // chunk: kept = above + what is left of `want` for the ties.
+  const int32_t* counts = p.counts + (int64_t)row * p.chunks * 4;
+  int ties = 0, low = 0, high = 0;
+  for (int i = 0; i < chunk; ++i) {
+    int left = want > ties ? want - ties : 0;
+    const int t1 = ld_const(counts + i * 4 + 1);
+    low += ld_const(counts + i * 4) + (t1 < left ? t1 : left);
+    ties += t1;
+    left = want > ties ? want - ties : 0;
+    const int t3 = ld_const(counts + i * 4 + 3);
+    high += ld_const(counts + i * 4 + 2) + (t3 < left ? t3 : left);
+    ties += t3;
+  }
+  const int below = first < p.keep ? first : p.keep;
+  const int2 n = list_chunk<kChunkKeys>(p, r, row, first, u, cut, want, ties,
+                                        below - low, high, lds);
+  if (r.len - first <= kChunkSlots && threadIdx.x == 0) p.moves[row] = n.y;
+}
+
+// ---- moves -------------------------------------------------------------------
+// Pair i of a row: slot movers[i] goes to slot holes[i].  A thread moves 16
+// bytes of kMoves pairs' K or V rows, all loaded before the first is stored;
+// the first thread of a pair takes its weight and position along.
+constexpr int kMoves = 4;
+
+__global__ __launch_bounds__(kBlock) void evict_move_kernel(SlotsParams p) {
+  const CacheParams& c = p.c;
+  const int row = blockIdx.y;
+  for (int rr = row; rr < c.batch * c.heads; rr += gridDim.y) {
+    const int32_t n = ld_const(p.moves + rr);
+    const int32_t per = p.row_units.d;
+    if ((int64_t)blockIdx.x * kBlock * kMoves >= (int64_t)n * per) continue;
+    const int b = rr / c.heads, h = rr % c.heads;
+    const int32_t* table = c.table + b * c.table_stride;
+    const int32_t* holes = p.pairs + (int64_t)rr * 2 * p.pair_cap;
+    const int32_t* movers = holes + p.pair_cap;
+    const float* w = p.w.w + b * p.w.wb + h * p.w.wh;
+    const int32_t* pos = p.w.pos + b * p.w.pb + h * p.w.ph;
+    float* w2 = p.after.w + b * p.after.wb + h * p.after.wh;
+    int32_t* pos2 = p.after.pos + b * p.after.pb + h * p.after.ph;
+    int32_t to[kMoves], from[kMoves], unit[kMoves];
+    bool in[kMoves];
+#pragma unroll
+    for (int j = 0; j < kMoves; ++j) {
+      const int32_t i = (blockIdx.x * kMoves + j) * kBlock + threadIdx.x;
+      const int32_t pair = quotient(p.row_units, i);
+      unit[j] = i - pair * per;
+      in[j] = pair < n;
+      to[j] = in[j] ? holes[pair] : 0;
+      from[j] = in[j] ? movers[pair] : 0;
+    }
+    char* dst[kMoves];
+    v4i x[kMoves];
+#pragma unroll
+    for (int j = 0; j < kMoves; ++j) {
+      int32_t zt, zf;
+      const int32_t it = find_page(c, table, to[j], &zt);
+      const int32_t jf = find_page(c, table, from[j], &zf);
+      const bool is_k = unit[j] * 16 < c.row_bytes;
       const RowStrides& s = is_k ? c.ks : c.vs;
-      const char* base = (is_k ? c.k : c.v) + off;
-      *(v4i*)const_cast<char*>(base + row_offset(s, it, h, zt)) =
-          *(const v4i*)(base + row_offset(s, jf, h, zf));
+      const char* base =
+          (is_k ? c.k : c.v - c.row_bytes) + unit[j] * 16;
+      dst[j] = in[j] && it >= 0 && jf >= 0
+                   ? const_cast<char*>(base) + row_offset(s, it, h, zt)
+                   : nullptr;
+      x[j] = v4i{0, 0, 0, 0};
+      if (dst[j])
+        x[j] = __builtin_nontemporal_load(
+            (const v4i*)(base + row_offset(s, jf, h, zf)));
     }
+#pragma unroll
+    for (int j = 0; j < kMoves; ++j) {
+      if (in[j] && unit[j] == 0) {
+        w2[to[j]] = w[from[j]];
+        pos2[to[j]] = pos[from[j]];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kMoves; ++j)
+      if (dst[j]) __builtin_nontemporal_store(x[j], (v4i*)dst[j]);
   }
 }
 
