@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libtopk.so, whose C interface is include/libtopk.h.  PyTorch
-supplies device memory and the current stream.  There is no CPU fallback:
+supplies device memory and the current stream.  (The cache_* calls, made once
+a layer and token, are marshalled in C++: csrc/binding.cpp.)  There is no CPU fallback:
 if the library is not built, importing this package raises.
 
     topk(x, k)      -> int32 tensor [k], the k largest of x, descending
@@ -150,6 +151,14 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+try:
+    from . import _binding  # noqa: E402  (native; needs torch and lib)
+except ImportError as e:
+    raise ImportError(
+        "_binding.so is not built; run `python -c 'import __graft_entry__ as "
+        "g; g.build()'` from the repository root") from e
+_binding.set_error(LibtopkError)
 
 
 def strerror(status: int) -> str:
@@ -502,119 +511,9 @@ def histogram(x, lo: int, shift: int, nbins: int, out=None):
 
 
 # ------------------------------------------------- paged key-value cache
-# Checked on the host, from metadata alone: shapes, types, strides, and last
-# that the tensors are a GPU's.  (Length, table and position values stay on
-# the device; the kernels bound what they read there.)
-def _tensor(x, name, dtype, shape, device, dense=True):
-    import torch
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("%s: expected a torch.Tensor" % name)
-    if x.dtype != dtype:
-        raise TypeError("%s: expected %s, got %s" % (name, dtype, x.dtype))
-    if x.device != device:
-        raise ValueError("%s: expected a tensor on %s, got %s"
-                         % (name, device, x.device))
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError("%s: expected shape %s, got %s"
-                         % (name, tuple(shape), tuple(x.shape)))
-    if dense and not x.is_contiguous():
-        raise ValueError("%s: expected a contiguous tensor" % name)
-
-
-def _ptr(x):
-    return None if x is None else x.data_ptr() or None
-
-
-def _stride(x, i):
-    return x.stride(i) if x.size(i) > 1 else 0
-
-
-def _cache_struct(k, v, table, lens):
-    import torch
-    dtypes = {torch.bfloat16: BF16, torch.float16: F16,
-              torch.float8_e4m3fn: E4M3}
-    for x, name in ((k, "k"), (v, "v")):
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("%s: expected a torch.Tensor" % name)
-        if x.dtype not in dtypes:
-            raise TypeError("%s: expected bfloat16, float16 or float8_e4m3fn,"
-                            " got %s" % (name, x.dtype))
-        if x.dim() != 4:
-            raise ValueError("%s: expected [pages, heads, page, dim]" % name)
-        if x.size(1) < 1 or x.size(2) < 1 or x.size(3) < 1:
-            raise ValueError("%s: no axis but the pages may be empty" % name)
-        if x.size(3) > 1 and x.stride(3) != 1:
-            raise ValueError("%s: expected unit stride in the last axis"
-                             % name)
-    _tensor(v, "v", k.dtype, k.shape, k.device, dense=False)
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table: expected [batch, pages of a sequence]")
-    batch, width = table.shape
-    _tensor(table, "table", torch.int32, (batch, width), k.device,
-            dense=False)
-    if width < 1 or (width > 1 and table.stride(1) != 1):
-        raise ValueError("table: expected at least one column, unit stride")
-    _tensor(lens, "lens", torch.int32, (batch,), k.device)
-    if k.size(3) > MAX_DIM or k.size(3) * k.element_size() % 16:
-        raise ValueError("rows of %d elements of %s: expected at most %d and "
-                         "a multiple of 16 bytes"
-                         % (k.size(3), k.dtype, MAX_DIM))
-    return CacheStruct(
-        k=_ptr(k), v=_ptr(v),
-        k_page_stride=_stride(k, 0), k_head_stride=_stride(k, 1),
-        k_slot_stride=_stride(k, 2),
-        v_page_stride=_stride(v, 0), v_head_stride=_stride(v, 1),
-        v_slot_stride=_stride(v, 2),
-        pages=k.size(0), table_stride=_stride(table, 0), table=_ptr(table),
-        lens=_ptr(lens), batch=batch, table_width=width, heads=k.size(1),
-        page=k.size(2), dim=k.size(3), dtype=dtypes[k.dtype])
-
-
-def _ledger_struct(weights, positions, c, device, names):
-    """weights (and positions) [batch, heads, slots], unit stride in slots."""
-    import torch
-    slots = None
-    for x, name, dtype in ((weights, names[0], torch.float32),
-                           (positions, names[1], torch.int32)):
-        if x is None:
-            continue
-        if not isinstance(x, torch.Tensor) or x.dim() != 3:
-            raise ValueError("%s: expected [batch, heads, slots]" % name)
-        slots = x.size(2) if slots is None else slots
-        _tensor(x, name, dtype, (c.batch, c.heads, slots), device,
-                dense=False)
-        if slots < 1 or (slots > 1 and x.stride(2) != 1):
-            raise ValueError("%s: expected at least one slot, unit stride"
-                             % name)
-    p = positions
-    return LedgerStruct(
-        weights=_ptr(weights), positions=_ptr(p),
-        weights_batch_stride=_stride(weights, 0),
-        weights_head_stride=_stride(weights, 1),
-        positions_batch_stride=_stride(p, 0) if p is not None else 0,
-        positions_head_stride=_stride(p, 1) if p is not None else 0,
-        slots=slots)
-
-
-def _int32(x, name, least):
-    x = int(x)
-    if not least <= x < 2 ** 31:
-        raise ValueError("%s: expected %d .. 2^31 - 1, got %d"
-                         % (name, least, x))
-    return x
-
-
-def _cache_call(name, device, *args):
-    import torch
-    if device.type != "cuda":
-        raise ValueError("expected device tensors, got %s" % device)
-    with torch.cuda.device(device):
-        stream = torch.cuda.current_stream(device).cuda_stream
-        rc = getattr(lib, name)(*args, stream or None)
-    if rc != OK:
-        raise LibtopkError(rc, name)
-
-
+# Tensors are checked by csrc/binding.cpp, on the host, from metadata alone:
+# shapes, types, strides, and last that they are a GPU's.  (Length, table and
+# position values stay on the device; the kernels bound what they read there.)
 def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
                  v_scale=None, out=None):
     """Attention of one new token a sequence over its slots in a paged cache
@@ -629,42 +528,8 @@ def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
     attention weights, summed over the Hq / H queries of its head, added in
     place.  Returns (out [B, Hq, D] of q's type, lse float32 [B, Hq]); out
     may be given as that pair of tensors."""
-    import torch
-    c = _cache_struct(k, v, table, lens)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q: expected [batch, query heads, dim]")
-    heads = q.size(1)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError("q: expected bfloat16 or float16, got %s" % q.dtype)
-    if c.dtype != E4M3 and q.dtype != k.dtype:
-        raise TypeError("q is %s, the cache %s" % (q.dtype, k.dtype))
-    _tensor(q, "q", q.dtype, (c.batch, heads, c.dim), k.device, dense=False)
-    if heads < 1 or heads % c.heads:
-        raise ValueError("q: %d query heads over %d heads" % (heads, c.heads))
-    if c.dim > 1 and q.stride(2) != 1:
-        raise ValueError("q: expected unit stride in the last axis")
-    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if x is not None:
-            _tensor(x, name, torch.float32, (c.heads,), k.device)
-    ledger = None
-    if weights is not None:
-        ledger = _ledger_struct(weights, None, c, k.device,
-                                ("weights", "positions"))
-    if out is None:
-        o = torch.empty((c.batch, heads, c.dim), dtype=q.dtype,
-                        device=k.device)
-        lse = torch.empty((c.batch, heads), dtype=torch.float32,
-                          device=k.device)
-    else:
-        o, lse = out
-        _tensor(o, "out", q.dtype, (c.batch, heads, c.dim), k.device)
-        _tensor(lse, "lse", torch.float32, (c.batch, heads), k.device)
-    _cache_call("cache_attend", k.device, c, _ptr(q),
-                BF16 if q.dtype == torch.bfloat16 else F16, heads,
-                _stride(q, 0), _stride(q, 1),
-                c.dim ** -0.5 if scale is None else float(scale),
-                _ptr(k_scale), _ptr(v_scale), ledger, _ptr(o), _ptr(lse))
-    return o, lse
+    return _binding.attend(q, k, v, table, lens, scale, weights, k_scale,
+                           v_scale, out)
 
 
 def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
@@ -676,30 +541,8 @@ def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
     >= seen[b] - recent).  weights float32 and positions int32
     [B, H, slots] are updated in place, as k and v are; seen int32 [B] is the
     new token's position.  Returns (lens [B], slots [B, H]), int32."""
-    import torch
-    limit, sinks = _int32(limit, "limit", 1), _int32(sinks, "sinks", 0)
-    recent = _int32(recent, "recent", 0)
-    c = _cache_struct(k, v, table, lens)
-    if weights is None or positions is None:
-        raise ValueError("weights and positions are needed")
-    ledger = _ledger_struct(weights, positions, c, k.device,
-                            ("weights", "positions"))
-    for x, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _tensor(x, name, k.dtype, (c.batch, c.heads, c.dim), k.device,
-                dense=False)
-        if c.dim > 1 and x.stride(2) != 1:
-            raise ValueError("%s: expected unit stride in the last axis"
-                             % name)
-    if any(_stride(k_new, i) != _stride(v_new, i) for i in (0, 1)):
-        raise ValueError("k_new and v_new: expected the same strides")
-    _tensor(seen, "seen", torch.int32, (c.batch,), k.device)
-    out_lens = torch.empty_like(lens)
-    slots = torch.empty((c.batch, c.heads), dtype=torch.int32,
-                        device=k.device)
-    _cache_call("cache_append", k.device, c, _ptr(k_new), _ptr(v_new),
-                _stride(k_new, 0), _stride(k_new, 1), limit, _ptr(seen),
-                ledger, sinks, recent, _ptr(out_lens), _ptr(slots))
-    return out_lens, slots
+    return _binding.append(k_new, v_new, k, v, table, lens, limit, seen,
+                           weights, positions, sinks, recent)
 
 
 def cache_evict(k, v, table, lens, seen, weights, positions, keep, sinks=0,
@@ -709,24 +552,5 @@ def cache_evict(k, v, table, lens, seen, weights, positions, keep, sinks=0,
     include/libtopk.h); rows move within k and v.  Returns (weights
     [B, H, keep], positions [B, H, keep], lens [B]); out may be given as a
     pair of tensors for the first two (they overlap no input)."""
-    import torch
-    keep, sinks = _int32(keep, "keep", 1), _int32(sinks, "sinks", 0)
-    recent = _int32(recent, "recent", 0)
-    c = _cache_struct(k, v, table, lens)
-    if weights is None or positions is None:
-        raise ValueError("weights and positions are needed")
-    ledger = _ledger_struct(weights, positions, c, k.device,
-                            ("weights", "positions"))
-    _tensor(seen, "seen", torch.int32, (c.batch,), k.device)
-    if out is None:
-        shape = (c.batch, c.heads, keep)
-        out = (torch.empty(shape, dtype=torch.float32, device=k.device),
-               torch.empty(shape, dtype=torch.int32, device=k.device))
-    after = _ledger_struct(out[0], out[1], c, k.device,
-                           ("out[0]", "out[1]"))
-    if after.slots != keep:
-        raise ValueError("out: expected [batch, heads, %d]" % keep)
-    out_lens = torch.empty_like(lens)
-    _cache_call("cache_evict", k.device, c, _ptr(seen), ledger, keep,
-                sinks, recent, after, _ptr(out_lens))
-    return out[0], out[1], out_lens
+    return _binding.evict(k, v, table, lens, seen, weights, positions, keep,
+                          sinks, recent, out)

@@ -8,6 +8,10 @@ the flag), emit code for gfx950 only, and pin code object version 5, which both 
 PyTorch load.  They also turn off the compiler's atomic optimizer: every
 atomic here is issued by one lane or targets a distinct address per lane,
 and the optimizer's wave-wide combining would only add a scalar loop.
+
+_binding.so, the native part of the Python binding (csrc/binding.cpp), is
+plain C++ against PyTorch's and Python's headers; it finds libtopk.so beside
+itself and PyTorch's libraries in the process that imports it.
 """
 from __future__ import annotations
 
@@ -20,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libtopk.so")
+BINDING = os.path.join(PKG, "_binding.so")
 UNITS = ("libtopk.hip", "cache.hip")
 
 HIPCC_FLAGS = [
@@ -63,5 +68,26 @@ def build_libtopk(extra_flags=(), out: str = SO) -> str:
     return out
 
 
+def build_binding(out: str = BINDING) -> str:
+    """After build_libtopk()."""
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [INCLUDE, os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"]]
+    tmp = out + ".tmp%d" % os.getpid()
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+         *(x for i in inc for x in ("-isystem" if i != INCLUDE else "-I", i)),
+         os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+         "-L", PKG, "-l:" + os.path.basename(SO),
+         "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu",
+         "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, out)
+    return out
+
+
 if __name__ == "__main__":
     print(build_libtopk())
+    print(build_binding())
