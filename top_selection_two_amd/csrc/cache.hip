@@ -332,12 +332,14 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
 // needs.
 struct AttendNeeds {
   int cols;  // columns of a partial result
+  int unit;  // slots of a unit
+  int threads;
   int lds;   // bytes of LDS besides the scores it holds
 };
 template <int Q, int C, int NC>
 const void* attend_fn_pages(bool pg16, AttendNeeds* cols) {
-  *cols = {Attend<Q, C, NC, true>::COLS,
-           (int)sizeof(typename Attend<Q, C, NC, true>::Lds)};
+  typedef Attend<Q, C, NC, true> A;
+  *cols = {A::COLS, A::UNIT, A::THREADS, (int)sizeof(typename A::Lds)};
   return pg16 ? (const void*)&attend_kernel<Q, C, NC, true>
               : (const void*)&attend_kernel<Q, C, NC, false>;
 }
@@ -359,9 +361,11 @@ const void* attend_fn(int q, int c, int dim, bool pg16, AttendNeeds* cols) {
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
 constexpr int kLdsBytes = 160 * 1024;
-// Rows of at most this many slots get their weights from their last
+// Rows of at most this many scores get their weights from their last
 // workgroup, longer ones from a second launch.
-constexpr int kDirectSlots = 16384;
+constexpr int kDirectScores = 32768;
+// Least share of a row (see the dealing in attend_kernel).
+constexpr int kMinUnits = 2;
 static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
               "a thread searches two bins");
 
@@ -428,9 +432,9 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   p.lse = lse;
   p.gtiles = (p.group + 15) / 16;
   // Units of all rows must count in 31 bits.
-  const int64_t units = ((int64_t)p.c.cap + kUnit - 1) / kUnit;
   const int64_t att_rows = (int64_t)cache->batch * cache->heads * p.gtiles;
-  if (att_rows > INT32_MAX / units) return LIBTOPK_ERR_INVALID;
+  if (att_rows > INT32_MAX / ((p.c.cap + 127) / 128))
+    return LIBTOPK_ERR_INVALID;
   int dev = 0;
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
@@ -442,24 +446,27 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   AttendNeeds needs;
   const void* fn = attend_fn(q_dtype, cache->dtype, cache->dim, pg16, &needs);
   int fit = 0, cus = 0;
-  rc = resident(dev, fn, kAttThreads, &fit, &cus);
+  rc = resident(dev, fn, needs.threads, &fit, &cus);
   if (rc != LIBTOPK_OK) return rc;
+  const int64_t units = ((int64_t)p.c.cap + needs.unit - 1) / needs.unit;
   int64_t grid = att_rows * units;
   if (grid > (int64_t)fit * cus) grid = (int64_t)fit * cus;
   if (grid > kMaxRuns) grid = kMaxRuns;
   p.part_rows = p.group < 16 ? p.group : 16;
+  p.min_units = kMinUnits;
   const size_t part_bytes =
       round_up((size_t)grid * 2 * p.part_rows * (needs.cols + 2) * 4, 256);
-  const size_t unit_bytes = (size_t)kUnit * p.part_rows * 4;
+  const size_t unit_bytes = (size_t)needs.unit * p.part_rows * 4;
   size_t score_bytes = 0, split_bytes = 0, lds = 0;
   if (ledger) {
-    p.row_units = (int32_t)units;
-    p.direct = p.gtiles == 1 && p.c.cap <= kDirectSlots;
+    p.row_tiles = (int32_t)(units * (needs.unit / kTileSlots));
+    p.direct = p.gtiles == 1 && (int64_t)p.c.cap * p.group <= kDirectScores;
     score_bytes = (size_t)(att_rows * units) * unit_bytes;
     if (!p.direct) split_bytes = round_up((size_t)att_rows, 256);
     // What LDS is left when `fit` workgroups share a unit holds scores, but
     // no more than the longest run.
-    const int64_t run = (att_rows * units + grid - 1) / grid;
+    int64_t run = (att_rows * units + grid - 1) / grid;
+    if (run < kMinUnits) run = kMinUnits;
     int64_t room = (kLdsBytes / fit - needs.lds - 256) / (int64_t)unit_bytes;
     if (room > run) room = run;
     p.held_units = (int32_t)room;
@@ -475,7 +482,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
     p.split = (uint8_t*)(work.base + part_bytes + score_bytes);
   p.ticket = work.tickets;
   p.epoch = work.epoch;
-  rc = launch(fn, dim3((unsigned)grid), kAttThreads, p, s, lds);
+  rc = launch(fn, dim3((unsigned)grid), needs.threads, p, s, lds);
   if (rc != LIBTOPK_OK || !ledger || p.direct) return rc;
   const int64_t wrows = (int64_t)cache->batch * cache->heads;
   return launch((const void*)&attend_weights_kernel,

@@ -21,10 +21,7 @@
 namespace ltk {
 
 constexpr float kLn2 = 0.693147180559945309f;
-constexpr int kAttWaves = 8;
-constexpr int kAttThreads = kAttWaves * kWave;
-constexpr int kTileSlots = 32;                       // of one wave
-constexpr int kUnit = kTileSlots * kAttWaves;        // of a workgroup
+constexpr int kTileSlots = 32;  // of one wave
 
 struct AttendParams {
   CacheParams c;
@@ -40,11 +37,12 @@ struct AttendParams {
   // score_at), whether a row is split, and the units that fit in LDS.
   float* scores;
   uint8_t* split;
-  int32_t row_units;    // units of a row at full length
+  int32_t row_tiles;    // tiles of a row at full length, whole units
   int32_t held_units;
   bool direct;          // a row's last workgroup adds up its weights
   float* part;          // [grid][2][part_rows * columns + 2 * part_rows]
   int32_t part_rows;    // queries of a row, at most 16
+  int32_t min_units;    // least share of a row
   uint64_t* ticket;     // one per row
   uint32_t epoch;
   void* out;
@@ -184,6 +182,11 @@ __device__ __forceinline__ void add_weights(float* w, int32_t left,
 // of a multiple of 16 slots, so that each half of a tile lies in one page.
 template <int QT, int CT, int NC, bool PG16>
 struct Attend {
+  // Rows of more than 128 elements need more than 256 registers a lane: one
+  // wave to a SIMD instead of two, with twice the bytes in flight each.
+  static constexpr int WAVES = NC > 4 ? 4 : 8;
+  static constexpr int THREADS = WAVES * kWave;
+  static constexpr int UNIT = WAVES * kTileSlots;  // slots
   static constexpr int ES = CT == kE4m3 ? 1 : 2;
   static constexpr int KL = CT == kE4m3 ? (NC + 1) / 2 : NC;  // K loads a half
   static constexpr int VE = NC == 2 ? 4 : 8;
@@ -204,11 +207,11 @@ struct Attend {
   };
 
   struct Lds {
-    float o[kAttWaves][4][COLS];
-    float m[kAttWaves][16];
-    float l[kAttWaves][16];
+    float o[WAVES][4][COLS];
+    float m[WAVES][16];
+    float l[WAVES][16];
     float top[16], sum[16], lse2[16];
-    int32_t scan[kAttWaves];
+    int32_t scan[2][WAVES];
     int32_t base;
     int32_t b;
     int32_t flag;
@@ -248,9 +251,12 @@ __device__ __forceinline__ typename A::Ids find_tile(const CacheParams& c,
 }
 
 template <int QT, int CT, int NC, bool PG16>
-__global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
-    AttendParams p) {
+__global__ __launch_bounds__((Attend<QT, CT, NC, PG16>::THREADS),
+                             (Attend<QT, CT, NC, PG16>::WAVES / 4)) void
+attend_kernel(AttendParams p) {
   typedef Attend<QT, CT, NC, PG16> A;
+  constexpr int kAttWaves = A::WAVES, kAttThreads = A::THREADS;
+  constexpr int kUnit = A::UNIT;
   constexpr int ES = A::ES, KL = A::KL, VE = A::VE, VD = A::VD, NB = A::NB;
   constexpr int COLS = A::COLS, QL = A::QL;
   __shared__ typename A::Lds lds;
@@ -263,55 +269,104 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
   // Units of a sequence, at least one a row: an empty row has an output too.
   const int32_t top_len = c.pages > 0 ? c.cap : 0;
   auto len_of = [&](int b) { return clamp_len(c.lens[b], top_len); };
-  auto units_of = [&](int b) {
-    const int32_t len = len_of(b);
-    return (len > 0 ? (len + kUnit - 1) / kUnit : 1) * hg;
-  };
   // Length of a sequence that is the same in every lane.
   auto len_uni = [&](int b) {
     return clamp_len(ld_const(c.lens + b), top_len);
   };
-  int32_t u0, u1, per, base = 0;
+  // Two ways of dealing.  Shares: a row of n units is cut into ceil(n / per)
+  // equal shares, one to a workgroup, as long as there are no more shares than
+  // workgroups.  A workgroup then has one row, and few rows are split: joining
+  // one costs as much as several tiles.  Runs: with more rows, every workgroup
+  // takes `per` consecutive units of whatever rows.
+  int32_t u0 = 0, u1 = 0, per = 1, base = 0, share = -1, cuts = 1;
   int b = 0;
+  const int32_t grid = (int32_t)gridDim.x, wg = (int32_t)blockIdx.x;
+  auto cuts_of = [&](int32_t units) { return (units + per - 1) / per; };
+  // Share `i` of the sequence whose units begin at `base`.  (None is empty:
+  // the shares before the last hold at most (cuts - 1) per < n units.)
+  auto take_share = [&](int32_t i, int32_t units) {
+    cuts = cuts_of(units);
+    const int32_t hi = i / cuts;
+    share = i % cuts;
+    const int32_t each = (units + cuts - 1) / cuts, r0 = base + hi * units;
+    const int32_t end = (share + 1) * each < units ? (share + 1) * each : units;
+    u0 = r0 + share * each;
+    u1 = r0 + end;
+  };
+  auto row_units_of = [&](int32_t len) {
+    return len > 0 ? (len + kUnit - 1) / kUnit : 1;
+  };
   auto deal = [&](int32_t all) {
-    per = (all + (int32_t)gridDim.x - 1) / (int32_t)gridDim.x;
-    u0 = (int32_t)blockIdx.x * per;
-    u1 = u0 + per < all ? u0 + per : all;
-    return u0 < all;
+    per = (all + grid - 1) / grid;
+    if (per < p.min_units) per = p.min_units;
   };
   if (c.batch == 1) {
-    const int32_t len = len_uni(0);
-    if (!deal((len > 0 ? (len + kUnit - 1) / kUnit : 1) * hg)) return;
+    const int32_t units = row_units_of(len_uni(0));
+    deal(units * hg);
+    if (cuts_of(units) * hg <= grid) {
+      if (wg >= cuts_of(units) * hg) return;
+      take_share(wg, units);
+    } else {
+      u0 = wg * per;
+      u1 = u0 + per < units * hg ? u0 + per : units * hg;
+      if (u0 >= u1) return;
+    }
   } else {
     // Thread i takes sequences [i * each, (i + 1) * each).
     const int each = (c.batch + kAttThreads - 1) / kAttThreads;
     int32_t mine = 0;
     for (int i = tid * each; i < (tid + 1) * each && i < c.batch; ++i)
-      mine += units_of(i);
+      mine += row_units_of(len_of(i)) * hg;
     const int32_t incl = wave_scan_incl(mine);
-    if (ln == kWave - 1) lds.scan[wave] = incl;
+    if (ln == kWave - 1) lds.scan[0][wave] = incl;
     __syncthreads();
     int32_t before = incl - mine, all = 0;
     for (int i = 0; i < kAttWaves; ++i) {
-      if (i < wave) before += lds.scan[i];
-      all += lds.scan[i];
+      if (i < wave) before += lds.scan[0][i];
+      all += lds.scan[0][i];
     }
-    if (!deal(uni(all))) return;
-    if (u0 >= before && u0 < before + mine) {
+    deal(uni(all));
+    int32_t mine_s = 0;
+    for (int i = tid * each; i < (tid + 1) * each && i < c.batch; ++i)
+      mine_s += cuts_of(row_units_of(len_of(i))) * hg;
+    const int32_t incl_s = wave_scan_incl(mine_s);
+    if (ln == kWave - 1) lds.scan[1][wave] = incl_s;
+    __syncthreads();
+    int32_t before_s = incl_s - mine_s, all_s = 0;
+    for (int i = 0; i < kAttWaves; ++i) {
+      if (i < wave) before_s += lds.scan[1][i];
+      all_s += lds.scan[1][i];
+    }
+    const bool shares = uni(all_s) <= grid;
+    const int32_t at = shares ? wg : wg * per;
+    if (at >= uni(shares ? all_s : all)) return;
+    const int32_t from = shares ? before_s : before;
+    if (at >= from && at < from + (shares ? mine_s : mine)) {
       int i = tid * each;
-      for (int32_t un; before + (un = units_of(i)) <= u0; ++i) before += un;
+      int32_t f = from;
+      for (;; ++i) {
+        const int32_t units = row_units_of(len_of(i));
+        const int32_t n = (shares ? cuts_of(units) : units) * hg;
+        if (f + n > at) break;
+        f += n;
+        before += units * hg;
+      }
       lds.b = i;
       lds.base = before;
+      lds.flag = at - f;
     }
     __syncthreads();
     b = uni(lds.b);
     base = uni(lds.base);
+    if (shares) {
+      take_share(uni(lds.flag), row_units_of(len_uni(b)));
+    } else {
+      u0 = at;
+      u1 = u0 + per < uni(all) ? u0 + per : uni(all);
+    }
   }
 
   int32_t len = len_uni(b);
-  auto row_units_of = [&](int32_t len) {
-    return len > 0 ? (len + kUnit - 1) / kUnit : 1;
-  };
   int32_t row_units = row_units_of(len);
   int32_t u = u0;
 
@@ -337,8 +392,8 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
   };
   Share pend = {};
   auto unit_scores = [&](const Share& r, int32_t unit) {
-    return p.scores + (((int64_t)r.b * hg + r.hi) * p.row_units + unit) *
-                          unit_floats;
+    return p.scores + (((int64_t)r.b * hg + r.hi) * p.row_tiles +
+                       (int64_t)unit * kAttWaves) * tile_floats;
   };
   auto flush = [&](Share& r) {
     if (r.count > 0) {
@@ -407,7 +462,9 @@ __global__ __launch_bounds__(kAttThreads, 2) void attend_kernel(
     const int32_t tiles = (len + kTileSlots - 1) / kTileSlots;
     const char* kh = c.k + h * c.ks.head;
     const char* vh = c.v + h * c.vs.head;
-    Share cur = {b, hi, len, r0 / per, (r1 - 1) / per, u - r0, 0, held, true};
+    Share cur = {b, hi, len, share < 0 ? r0 / per : wg - share,
+                 share < 0 ? (r1 - 1) / per : wg - share + cuts - 1,
+                 u - r0, 0, held, true};
     const float scale = p.scale2 * (p.k_scale ? ld_const(p.k_scale + h) : 1.0f);
 
     float m = -INFINITY, l = 0.0f;
@@ -867,8 +924,8 @@ __global__ __launch_bounds__(kBlock) void attend_weights_kernel(
     f32x4 a = {0, 0, 0, 0};
     for (int gt = 0; gt < p.gtiles; ++gt) {
       const float* x0 =
-          p.scores + (((int64_t)row * p.gtiles + gt) * p.row_units *
-                          kAttWaves + t) * tile_floats;
+          p.scores + (((int64_t)row * p.gtiles + gt) * p.row_tiles + t) *
+                         tile_floats;
       for (int g = 0; g < 16 && gt * 16 + g < p.group; ++g) {
         const float lse2 =
             ld_const(p.lse + (int64_t)row * p.group + gt * 16 + g) *
