@@ -332,14 +332,14 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
 // needs.
 struct AttendNeeds {
   int cols;  // columns of a partial result
-  int unit;  // slots of a unit
   int threads;
-  int lds;   // bytes of LDS besides the scores it holds
+  int lds;   // bytes of static LDS
+  int join;  // floats of dynamic LDS at least
 };
 template <int Q, int C, int NC>
 const void* attend_fn_pages(bool pg16, AttendNeeds* cols) {
   typedef Attend<Q, C, NC, true> A;
-  *cols = {A::COLS, A::UNIT, A::THREADS, (int)sizeof(typename A::Lds)};
+  *cols = {A::COLS, A::THREADS, (int)sizeof(typename A::Lds), A::JOIN};
   return pg16 ? (const void*)&attend_kernel<Q, C, NC, true>
               : (const void*)&attend_kernel<Q, C, NC, false>;
 }
@@ -365,7 +365,10 @@ constexpr int kLdsBytes = 160 * 1024;
 // workgroup, longer ones from a second launch.
 constexpr int kDirectScores = 32768;
 // Least share of a row (see the dealing in attend_kernel).
-constexpr int kMinUnits = 2;
+#ifndef MINT
+#define MINT 24
+#endif
+constexpr int kMinTiles = MINT;
 static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
               "a thread searches two bins");
 
@@ -431,9 +434,15 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   p.out = out;
   p.lse = lse;
   p.gtiles = (p.group + 15) / 16;
-  // Units of all rows must count in 31 bits.
+  // A share that is dealt out costs about as much, besides its tiles, as
+  // 128 KiB of them (loading the queries, joining the waves), a split row
+  // some four times that.
+  p.row_cost = 2048 / p.c.row_bytes;
+  p.min_tiles = 2 * p.row_cost < kMinTiles ? 2 * p.row_cost : kMinTiles;
+  // Tiles of all rows must count in 31 bits.
   const int64_t att_rows = (int64_t)cache->batch * cache->heads * p.gtiles;
-  if (att_rows > INT32_MAX / ((p.c.cap + 127) / 128))
+  const int64_t tiles = ((int64_t)p.c.cap + kTileSlots - 1) / kTileSlots;
+  if (att_rows > INT32_MAX / (tiles + p.row_cost + kMinTiles))
     return LIBTOPK_ERR_INVALID;
   int dev = 0;
   rc = current_device(&dev);
@@ -448,29 +457,33 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   int fit = 0, cus = 0;
   rc = resident(dev, fn, needs.threads, &fit, &cus);
   if (rc != LIBTOPK_OK) return rc;
-  const int64_t units = ((int64_t)p.c.cap + needs.unit - 1) / needs.unit;
-  int64_t grid = att_rows * units;
+  int64_t grid = att_rows * tiles;
   if (grid > (int64_t)fit * cus) grid = (int64_t)fit * cus;
   if (grid > kMaxRuns) grid = kMaxRuns;
   p.part_rows = p.group < 16 ? p.group : 16;
-  p.min_units = kMinUnits;
+  p.lds_rows = (p.part_rows + 3) / 4 * 4;
   const size_t part_bytes =
       round_up((size_t)grid * 2 * p.part_rows * (needs.cols + 2) * 4, 256);
-  const size_t unit_bytes = (size_t)needs.unit * p.part_rows * 4;
-  size_t score_bytes = 0, split_bytes = 0, lds = 0;
+  const int waves = needs.threads / kWave;
+  int join = waves * p.lds_rows * needs.cols;
+  if (join < needs.join) join = needs.join;
+  size_t lds = (size_t)join * 4;
+  const size_t tile_bytes = (size_t)kTileSlots * p.part_rows * 4;
+  size_t score_bytes = 0, split_bytes = 0;
   if (ledger) {
-    p.row_tiles = (int32_t)(units * (needs.unit / kTileSlots));
+    p.row_tiles = (int32_t)tiles;
     p.direct = p.gtiles == 1 && (int64_t)p.c.cap * p.group <= kDirectScores;
-    score_bytes = (size_t)(att_rows * units) * unit_bytes;
+    score_bytes = (size_t)(att_rows * tiles) * tile_bytes;
     if (!p.direct) split_bytes = round_up((size_t)att_rows, 256);
     // What LDS is left when `fit` workgroups share a unit holds scores, but
     // no more than the longest run.
-    int64_t run = (att_rows * units + grid - 1) / grid;
-    if (run < kMinUnits) run = kMinUnits;
-    int64_t room = (kLdsBytes / fit - needs.lds - 256) / (int64_t)unit_bytes;
+    int64_t run = (att_rows * (tiles + p.row_cost) + grid - 1) / grid;
+    if (run < kMinTiles) run = kMinTiles;
+    int64_t room = (kLdsBytes / fit - needs.lds - 256 - (int64_t)lds) /
+                   (int64_t)tile_bytes;
     if (room > run) room = run;
-    p.held_units = (int32_t)room;
-    lds = (size_t)room * unit_bytes;
+    p.held_tiles = (int32_t)room;
+    lds += (size_t)room * tile_bytes;
   }
   Work work;
   rc = get_work(dev, s, part_bytes + score_bytes + split_bytes,

@@ -7,11 +7,11 @@
 //
 // The kernel reads every K and V row once and should run at the rate of that
 // read.  Work: the slots of a row (a sequence, a cache head and up to 16 of
-// its queries) are cut into units of kUnit slots; the units of all rows, in
-// order, are dealt out in equal runs to as many workgroups as the chip holds
-// at once, so that sequences of any mix of lengths load it evenly.  A row that
-// lies within one run is finished there; of the others each run leaves its
-// (m, l, o), and the row's last workgroup to finish joins them.
+// its queries) are cut into tiles of 32 slots, one wave's step; the tiles of
+// all rows are dealt out evenly to as many workgroups as the chip holds at
+// once, whatever the mix of lengths.  A row that one workgroup has alone is
+// finished there; of the others each leaves its (m, l, o), and the row's last
+// workgroup to finish joins them.
 #pragma once
 
 #include <type_traits>
@@ -33,16 +33,18 @@ struct AttendParams {
   float scale2;         // scale * log2 e
   const float* k_scale; // NULL: 1
   const float* v_scale;
-  // With a ledger: scores of split rows, [row][unit][wave] tiles (see
-  // score_at), whether a row is split, and the units that fit in LDS.
+  // With a ledger: scores of split rows, [row][tile] (see score_at), whether
+  // a row is split, and the tiles that fit in LDS.
   float* scores;
   uint8_t* split;
-  int32_t row_tiles;    // tiles of a row at full length, whole units
-  int32_t held_units;
+  int32_t row_tiles;    // tiles of a row at full length
+  int32_t held_tiles;
   bool direct;          // a row's last workgroup adds up its weights
   float* part;          // [grid][2][part_rows * columns + 2 * part_rows]
   int32_t part_rows;    // queries of a row, at most 16
-  int32_t min_units;    // least share of a row
+  int32_t min_tiles;    // least share of a row
+  int32_t row_cost;     // what a row costs besides its tiles, in tiles
+  int32_t lds_rows;     // part_rows, to a multiple of 4
   uint64_t* ticket;     // one per row
   uint32_t epoch;
   void* out;
@@ -134,6 +136,10 @@ __device__ __forceinline__ f32x4 ld_agent4(__amdgpu_buffer_rsrc_t r, int at) {
 __device__ __forceinline__ float ld_agent1(__amdgpu_buffer_rsrc_t r, int at) {
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 16));
 }
+__device__ __forceinline__ void st_agent1(__amdgpu_buffer_rsrc_t r, int at,
+                                          float x) {
+  __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, at, 0, 16);
+}
 __device__ __forceinline__ void st_agent4(__amdgpu_buffer_rsrc_t r, int at,
                                           f32x4 x) {
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
@@ -186,7 +192,6 @@ struct Attend {
   // wave to a SIMD instead of two, with twice the bytes in flight each.
   static constexpr int WAVES = NC > 4 ? 4 : 8;
   static constexpr int THREADS = WAVES * kWave;
-  static constexpr int UNIT = WAVES * kTileSlots;  // slots
   static constexpr int ES = CT == kE4m3 ? 1 : 2;
   static constexpr int KL = CT == kE4m3 ? (NC + 1) / 2 : NC;  // K loads a half
   static constexpr int VE = NC == 2 ? 4 : 8;
@@ -206,11 +211,13 @@ struct Attend {
     int32_t place[PG16 ? 2 : 10];
   };
 
+  // Static LDS; besides it [WAVES][lds_rows][COLS] floats in which the waves
+  // (and a row's shares) are joined, at least JOIN of them, and the scores.
+  static constexpr int JOIN = 6 * THREADS;
   struct Lds {
-    float o[WAVES][4][COLS];
     float m[WAVES][16];
     float l[WAVES][16];
-    float top[16], sum[16], lse2[16];
+    float lse2[16];
     int32_t scan[2][WAVES];
     int32_t base;
     int32_t b;
@@ -256,7 +263,6 @@ __global__ __launch_bounds__((Attend<QT, CT, NC, PG16>::THREADS),
 attend_kernel(AttendParams p) {
   typedef Attend<QT, CT, NC, PG16> A;
   constexpr int kAttWaves = A::WAVES, kAttThreads = A::THREADS;
-  constexpr int kUnit = A::UNIT;
   constexpr int ES = A::ES, KL = A::KL, VE = A::VE, VD = A::VD, NB = A::NB;
   constexpr int COLS = A::COLS, QL = A::QL;
   __shared__ typename A::Lds lds;
@@ -266,49 +272,53 @@ attend_kernel(AttendParams p) {
   const int hg = c.heads * p.gtiles;  // rows of a sequence
 
   // ---- this workgroup's run of units -------------------------------------
-  // Units of a sequence, at least one a row: an empty row has an output too.
   const int32_t top_len = c.pages > 0 ? c.cap : 0;
   auto len_of = [&](int b) { return clamp_len(c.lens[b], top_len); };
   // Length of a sequence that is the same in every lane.
   auto len_uni = [&](int b) {
     return clamp_len(ld_const(c.lens + b), top_len);
   };
-  // Two ways of dealing.  Shares: a row of n units is cut into ceil(n / per)
+  // Two ways of dealing.  Shares: a row of n tiles is cut into ceil(n / per)
   // equal shares, one to a workgroup, as long as there are no more shares than
   // workgroups.  A workgroup then has one row, and few rows are split: joining
-  // one costs as much as several tiles.  Runs: with more rows, every workgroup
-  // takes `per` consecutive units of whatever rows.
+  // one costs as much as many tiles.  Runs: with more rows, every workgroup
+  // takes `per` consecutive tiles of whatever rows; what a row costs besides
+  // its tiles (loading the queries, joining the waves) counts as row_cost
+  // tiles before its first.
   int32_t u0 = 0, u1 = 0, per = 1, base = 0, share = -1, cuts = 1;
+  int32_t cost = p.row_cost;
   int b = 0;
   const int32_t grid = (int32_t)gridDim.x, wg = (int32_t)blockIdx.x;
-  auto cuts_of = [&](int32_t units) { return (units + per - 1) / per; };
-  // Share `i` of the sequence whose units begin at `base`.  (None is empty:
-  // the shares before the last hold at most (cuts - 1) per < n units.)
-  auto take_share = [&](int32_t i, int32_t units) {
-    cuts = cuts_of(units);
+  auto tiles_of = [&](int32_t len) {  // an empty row has an output too
+    return len > 0 ? (len + kTileSlots - 1) / kTileSlots : 1;
+  };
+  auto cuts_of = [&](int32_t tiles) { return (tiles + per - 1) / per; };
+  // Share `i` of a sequence.  (None is empty: the shares before the last hold
+  // at most (cuts - 1) per < n tiles.)
+  auto take_share = [&](int32_t i, int32_t tiles) {
+    cuts = cuts_of(tiles);
     const int32_t hi = i / cuts;
     share = i % cuts;
-    const int32_t each = (units + cuts - 1) / cuts, r0 = base + hi * units;
-    const int32_t end = (share + 1) * each < units ? (share + 1) * each : units;
+    const int32_t each = (tiles + cuts - 1) / cuts, r0 = hi * tiles;
+    const int32_t end = (share + 1) * each < tiles ? (share + 1) * each : tiles;
+    base = 0;
+    cost = 0;
     u0 = r0 + share * each;
     u1 = r0 + end;
   };
-  auto row_units_of = [&](int32_t len) {
-    return len > 0 ? (len + kUnit - 1) / kUnit : 1;
-  };
   auto deal = [&](int32_t all) {
     per = (all + grid - 1) / grid;
-    if (per < p.min_units) per = p.min_units;
+    if (per < p.min_tiles) per = p.min_tiles;
   };
   if (c.batch == 1) {
-    const int32_t units = row_units_of(len_uni(0));
-    deal(units * hg);
-    if (cuts_of(units) * hg <= grid) {
-      if (wg >= cuts_of(units) * hg) return;
-      take_share(wg, units);
+    const int32_t tiles = tiles_of(len_uni(0)), all = (tiles + cost) * hg;
+    deal(all);
+    if (cuts_of(tiles) * hg <= grid) {
+      if (wg >= cuts_of(tiles) * hg) return;
+      take_share(wg, tiles);
     } else {
       u0 = wg * per;
-      u1 = u0 + per < units * hg ? u0 + per : units * hg;
+      u1 = u0 + per < all ? u0 + per : all;
       if (u0 >= u1) return;
     }
   } else {
@@ -316,7 +326,7 @@ attend_kernel(AttendParams p) {
     const int each = (c.batch + kAttThreads - 1) / kAttThreads;
     int32_t mine = 0;
     for (int i = tid * each; i < (tid + 1) * each && i < c.batch; ++i)
-      mine += row_units_of(len_of(i)) * hg;
+      mine += (tiles_of(len_of(i)) + cost) * hg;
     const int32_t incl = wave_scan_incl(mine);
     if (ln == kWave - 1) lds.scan[0][wave] = incl;
     __syncthreads();
@@ -325,10 +335,11 @@ attend_kernel(AttendParams p) {
       if (i < wave) before += lds.scan[0][i];
       all += lds.scan[0][i];
     }
-    deal(uni(all));
+    all = uni(all);
+    deal(all);
     int32_t mine_s = 0;
     for (int i = tid * each; i < (tid + 1) * each && i < c.batch; ++i)
-      mine_s += cuts_of(row_units_of(len_of(i))) * hg;
+      mine_s += cuts_of(tiles_of(len_of(i))) * hg;
     const int32_t incl_s = wave_scan_incl(mine_s);
     if (ln == kWave - 1) lds.scan[1][wave] = incl_s;
     __syncthreads();
@@ -337,70 +348,68 @@ attend_kernel(AttendParams p) {
       if (i < wave) before_s += lds.scan[1][i];
       all_s += lds.scan[1][i];
     }
-    const bool shares = uni(all_s) <= grid;
+    all_s = uni(all_s);
+    const bool shares = all_s <= grid;
     const int32_t at = shares ? wg : wg * per;
-    if (at >= uni(shares ? all_s : all)) return;
-    const int32_t from = shares ? before_s : before;
-    if (at >= from && at < from + (shares ? mine_s : mine)) {
+    if (at >= (shares ? all_s : all)) return;
+    int32_t f = shares ? before_s : before;
+    if (at >= f && at < f + (shares ? mine_s : mine)) {
       int i = tid * each;
-      int32_t f = from;
       for (;; ++i) {
-        const int32_t units = row_units_of(len_of(i));
-        const int32_t n = (shares ? cuts_of(units) : units) * hg;
+        const int32_t tiles = tiles_of(len_of(i));
+        const int32_t n = (shares ? cuts_of(tiles) : tiles + cost) * hg;
         if (f + n > at) break;
         f += n;
-        before += units * hg;
       }
       lds.b = i;
-      lds.base = before;
-      lds.flag = at - f;
+      lds.base = f;
     }
     __syncthreads();
     b = uni(lds.b);
     base = uni(lds.base);
     if (shares) {
-      take_share(uni(lds.flag), row_units_of(len_uni(b)));
+      take_share(at - base, tiles_of(len_uni(b)));
     } else {
       u0 = at;
-      u1 = u0 + per < uni(all) ? u0 + per : uni(all);
+      u1 = u0 + per < all ? u0 + per : all;
     }
   }
 
   int32_t len = len_uni(b);
-  int32_t row_units = row_units_of(len);
+  int32_t row_tiles = tiles_of(len);
   int32_t u = u0;
 
-  // Scores of the units that this workgroup holds in LDS, as
-  // [unit][wave][part_rows][32]; `held` of them.  Those of a row that lies
-  // within the run become weights as soon as the row's sum is known.  Those
-  // of a row that other runs share go to memory, at the end of the run (or
-  // when LDS is full): a few per cent of writes strewn among the reads cost
-  // the stream more than ten times their bytes (48 sequences of 4096 slots,
-  // 8 heads of 4 queries: 165 us with each tile's scores written at once, 129
-  // us with none).
-  extern __shared__ float4 held_raw[];
-  float* const held_scores = (float*)held_raw;
+  // Scores of the tiles that this workgroup holds in LDS; `held` of them.
+  // Those of a row that it has alone become weights as soon as the row's sum
+  // is known.  Those of a row that others share go to memory, at the end of
+  // the run (or when LDS is full): a few per cent of writes strewn among the
+  // reads cost the stream more than ten times their bytes (48 sequences of
+  // 4096 slots, 8 heads of 4 queries: 165 us with each tile's scores written
+  // at once, 129 us with none).
+  extern __shared__ float4 dynamic_lds[];
+  float* const join = (float*)dynamic_lds;
+  const int join_floats = max(kAttWaves * p.lds_rows * COLS, A::JOIN);
+  float* const held_scores = join + join_floats;
   const int tile_floats = p.part_rows * kTileSlots;
-  const int unit_floats = tile_floats * kAttWaves;
   int32_t held = 0;
-  // A share of a row that is not finished: its row, length, runs, and the
-  // units [from, from + count) at `at` in LDS.
+  // A share of a row that is not finished: its row, length, workgroups, and
+  // the tiles [from, from + count) at `at` in LDS.
   struct Share {
     int32_t b, hi, len, first, last;
     int32_t from, count, at;
     bool open;
   };
   Share pend = {};
-  auto unit_scores = [&](const Share& r, int32_t unit) {
-    return p.scores + (((int64_t)r.b * hg + r.hi) * p.row_tiles +
-                       (int64_t)unit * kAttWaves) * tile_floats;
+  auto row_scores = [&](const Share& r) {
+    return p.scores + ((int64_t)r.b * hg + r.hi) * p.row_tiles * tile_floats;
   };
   auto flush = [&](Share& r) {
     if (r.count > 0) {
-      const int bytes = r.count * unit_floats * 4;
+      const int bytes = r.count * tile_floats * 4;
       const __amdgpu_buffer_rsrc_t to = __builtin_amdgcn_make_buffer_rsrc(
-          uni_ptr(unit_scores(r, r.from)), (short)0, bytes, 0x00020000);
-      const f32x4* from = (const f32x4*)(held_scores + r.at * unit_floats);
+          uni_ptr(row_scores(r) + (int64_t)r.from * tile_floats), (short)0,
+          bytes, 0x00020000);
+      const f32x4* from = (const f32x4*)(held_scores + r.at * tile_floats);
       for (int i = tid; i < bytes / 16; i += kAttThreads)
         st_agent4(to, i * 16, from[i]);
     }
@@ -408,19 +417,16 @@ attend_kernel(AttendParams p) {
     r.count = 0;
   };
   // weights += sum over queries of exp2(x - lse2), for a row whose lse2 is in
-  // LDS; scores of the share's units from LDS, the others from memory.
+  // LDS; scores of the share's tiles from LDS, the others from memory.
   auto finish_weights = [&](const Share& r, int queries) {
     float* w = p.w.w + r.b * p.w.wb + r.hi * p.w.wh;
-    const float* all = unit_scores(r, 0);
     const __amdgpu_buffer_rsrc_t mem = __builtin_amdgcn_make_buffer_rsrc(
-        uni_ptr(const_cast<float*>(all)), (short)0,
-        row_units_of(r.len) * unit_floats * 4, 0x00020000);
+        uni_ptr(row_scores(r)), (short)0, tiles_of(r.len) * tile_floats * 4,
+        0x00020000);
     for (int32_t i = tid; i * 4 < r.len; i += kAttThreads) {
-      const int32_t t = i / 8, unit = t / kAttWaves;
-      const bool here = unit >= r.from && unit < r.from + r.count;
-      const int32_t at =
-          ((here ? unit - r.from + r.at : unit) * kAttWaves + t % kAttWaves) *
-          tile_floats;
+      const int32_t t = i / 8;
+      const bool here = t >= r.from && t < r.from + r.count;
+      const int32_t at = (here ? t - r.from + r.at : t) * tile_floats;
       f32x4 a = {0, 0, 0, 0};
       for (int g0 = 0; g0 < queries; g0 += 4) {
         f32x4 x[4];
@@ -445,17 +451,20 @@ attend_kernel(AttendParams p) {
   };
 
   while (u < u1) {
-    // ---- a row's share of the run ------------------------------------------
-    while (u >= base + row_units * hg) {
-      base += row_units * hg;
+    // ---- a row's share ------------------------------------------------------
+    while (u >= base + (row_tiles + cost) * hg) {
+      base += (row_tiles + cost) * hg;
       ++b;
       len = len_uni(b);
-      row_units = row_units_of(len);
+      row_tiles = tiles_of(len);
     }
-    const int hi = uni((u - base) / row_units);
+    const int hi = uni((u - base) / (row_tiles + cost));
+    // The row's tiles count as [r0, r1), after its cost.
+    const int32_t r0 = base + hi * (row_tiles + cost) + cost;
+    const int32_t r1 = r0 + row_tiles;
+    const int32_t s0 = u > r0 ? u : r0, s1 = r1 < u1 ? r1 : u1;
+    if (s0 >= s1) break;  // the run ends before the row's first tile
     const int h = hi / p.gtiles, g0 = hi % p.gtiles * 16;
-    const int32_t r0 = base + hi * row_units, r1 = r0 + row_units;
-    const int32_t s1 = r1 < u1 ? r1 : u1;
     const int queries = p.group - g0 < 16 ? p.group - g0 : 16;
     const int64_t qrow = (int64_t)b * c.heads * p.group + h * p.group + g0;
     const int32_t* table = c.table + b * c.table_stride;
@@ -464,7 +473,7 @@ attend_kernel(AttendParams p) {
     const char* vh = c.v + h * c.vs.head;
     Share cur = {b, hi, len, share < 0 ? r0 / per : wg - share,
                  share < 0 ? (r1 - 1) / per : wg - share + cuts - 1,
-                 u - r0, 0, held, true};
+                 s0 - r0, 0, held, true};
     const float scale = p.scale2 * (p.k_scale ? ld_const(p.k_scale + h) : 1.0f);
 
     float m = -INFINITY, l = 0.0f;
@@ -473,27 +482,27 @@ attend_kernel(AttendParams p) {
     for (int i = 0; i < NB * VE; ++i) o[i] = f32x4{0, 0, 0, 0};
 
     // Query fragments: those of 8-bit rows pair up to match 16-byte loads.
+    // Columns past the row's queries repeat the last and are not used.
     Frag qf[QL];
-    if (len > 0) {
+    {
+      const char* from = p.q + b * p.qb +
+                         (h * p.group + g0 + min(n, queries - 1)) * p.qh;
 #pragma unroll
       for (int f = 0; f < QL; ++f) {
         const int d = CT == kE4m3 ? f / 2 * 64 + q * 16 + f % 2 * 8
                                   : f * 32 + q * 8;
-        v4i x = {0, 0, 0, 0};
-        if (n < queries && d < c.dim)
-          x = *(const v4i*)(p.q + b * p.qb + (h * p.group + g0 + n) * p.qh +
-                            d * 2);
+        const v4i x = *(const v4i*)(from + (d < c.dim ? d * 2 : 0));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) qf[f].d[e] = x[e];
+        for (int e = 0; e < 4; ++e) qf[f].d[e] = d < c.dim ? x[e] : 0;
       }
     }
 
-    for (int32_t ua = u - r0, ue; ua < s1 - r0; ua = ue) {
-      // ---- units [ua, ue) of the row: all of the share, or what LDS holds
-      ue = s1 - r0;
+    for (int32_t ta = s0 - r0, te; ta < s1 - r0; ta = te) {
+      // ---- tiles [ta, te) of the row: all of the share, or what LDS holds
+      te = s1 - r0;
       float* tile_scores = nullptr;
       if (p.scores) {
-        if (held == p.held_units) {
+        if (held == p.held_tiles) {
           __syncthreads();
           flush(pend);
           flush(cur);
@@ -502,13 +511,13 @@ attend_kernel(AttendParams p) {
           held = 0;
           cur.at = 0;
         }
-        if (ue - ua > p.held_units - held) ue = ua + p.held_units - held;
-        tile_scores = held_scores + held * unit_floats + wave * tile_floats;
-        held += ue - ua;
-        cur.count += ue - ua;
+        if (te - ta > p.held_tiles - held) te = ta + p.held_tiles - held;
+        tile_scores = held_scores + (held + wave) * tile_floats;
+        held += te - ta;
+        cur.count += te - ta;
       }
-      int32_t t = ua * kAttWaves + wave;
-      const int32_t t1 = ue * kAttWaves < tiles ? ue * kAttWaves : tiles;
+      int32_t t = ta + wave;
+      const int32_t t1 = te < tiles ? te : tiles;
       if (t >= t1) continue;
 
       v4i kr[2][KL];
@@ -641,7 +650,7 @@ attend_kernel(AttendParams p) {
                   f32x4{x[4 * tt], x[4 * tt + 1], x[4 * tt + 2],
                         x[4 * tt + 3]};
           }
-          tile_scores += unit_floats;
+          tile_scores += kAttWaves * tile_floats;
         }
         // The reference m of a query only moves when a score passes it by
         // 2^8: until then exp2(x - m) stays below 2^8 and nothing has to be
@@ -718,84 +727,82 @@ attend_kernel(AttendParams p) {
     l = quad_sum(l);
 
     // ---- the workgroup's waves joined ---------------------------------------
-    const bool whole = u == r0 && s1 == r1;
-    // Bytes of a run's result, and where this one lies.
+    const bool whole = s0 == r0 && s1 == r1;
+    // Bytes of a share's result, and where this one lies: a workgroup can
+    // have a row's end and, last, another's beginning.
     const int32_t part_size = p.part_rows * (COLS + 2) * 4;
-    const int32_t part = ((int)blockIdx.x * 2 + (u == r0)) * part_size;
+    const int32_t part = (wg * 2 + (s0 == r0)) * part_size;
+    const int32_t at_m = p.part_rows * COLS * 4, at_l = at_m + p.part_rows * 4;
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
-        p.part, (short)0, (int)gridDim.x * 2 * part_size, 0x00020000);
-    if (q == 0) {
-      lds.m[wave][n] = m;
-      lds.l[wave][n] = l;
-    }
-    __syncthreads();
-    if (tid < 16) {
-      float top = -INFINITY, sum = 0.0f;
-      for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, lds.m[w][tid]);
-      for (int w = 0; w < kAttWaves; ++w) {
-        const float f =
-            lds.m[w][tid] == top ? 1.0f : exp2_fast(lds.m[w][tid] - top);
-        lds.m[w][tid] = f;
-        sum += lds.l[w][tid] * f;
+        p.part, (short)0, grid * 2 * part_size, 0x00020000);
+    auto v_factor = [&](int h) {
+      return p.v_scale ? ld_const(p.v_scale + h) : 1.0f;
+    };
+    // Four columns of query g: out, and with the first of them lse.
+    auto store = [&](int64_t row, int g, int col, float vs, float top,
+                     float sum, f32x4 x) {
+      if (col == 0) {
+        const float z = sum == 0.0f ? -INFINITY : top + log2f(sum);
+        lds.lse2[g] = z;
+        p.lse[row + g] = z * kLn2;
       }
-      lds.top[tid] = top;
-      lds.sum[tid] = sum;
-      lds.lse2[tid] = sum == 0.0f ? -INFINITY : top + log2f(sum);
-      if (tid < queries) {
-        if (whole) {
-          p.lse[qrow + tid] = lds.lse2[tid] * kLn2;
-        } else {
-          st_agent(p.part + part / 4 + p.part_rows * COLS + tid, top);
-          st_agent(p.part + part / 4 + p.part_rows * (COLS + 1) + tid, sum);
-        }
-      }
-    }
-    auto store = [&](int64_t row, int g, int col, float vs, f32x4 x) {
-      const float sum = lds.sum[g];
+      if (col >= c.dim) return;
       const float f = vs / sum;
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] * f;
       *(int2*)((char*)p.out + ((row + g) * c.dim + col) * 2) =
           make_int2(pack2<QT>(x[0], x[1]), pack2<QT>(x[2], x[3]));
     };
-    auto v_factor = [&](int h) {
-      return p.v_scale ? ld_const(p.v_scale + h) : 1.0f;
+    auto weight = [](float m, float top) {
+      return m == top ? 1.0f : exp2_fast(m - top);
     };
     const float vs = v_factor(h);
-    for (int g4 = 0; g4 < queries; g4 += 4) {
-      if (q == g4 / 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int e = 0; e < VE; e += 4) {
-              f32x4 x;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = o[nb * VE + e + k][i];
-              *(f32x4*)&lds.o[wave][i][(nb * 16 + n) * VE + e] = x;
-            }
-      }
-      __syncthreads();
-      if (tid < COLS) {
-        const int i = tid / (COLS / 4), col = tid % (COLS / 4) * 4, g = g4 + i;
-        if (g < queries && col < c.dim) {
-          f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-          for (int w = 0; w < kAttWaves; ++w)
-            x += *(const f32x4*)&lds.o[w][i][col] * lds.m[w][g];
-          if (whole)
-            store(qrow, g, col, vs, x);
-          else
-            st_agent4(parts, part + (g * COLS + col) * 4, x);
-        }
-      }
-      __syncthreads();
+    if (q == 0) {
+      lds.m[wave][n] = m;
+      lds.l[wave][n] = l;
     }
+    if (q * 4 < queries) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int e = 0; e < VE; e += 4) {
+            f32x4 x;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = o[nb * VE + e + k][i];
+            *(f32x4*)&join[(wave * p.lds_rows + q * 4 + i) * COLS +
+                           (nb * 16 + n) * VE + e] = x;
+          }
+    }
+    __syncthreads();
+    for (int at = tid; at < queries * (COLS / 4); at += kAttThreads) {
+      const int g = at / (COLS / 4), col = at % (COLS / 4) * 4;
+      float top = -INFINITY, sum = 0.0f;
+      f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, lds.m[w][g]);
+#pragma unroll
+      for (int w = 0; w < kAttWaves; ++w) {
+        const float f = weight(lds.m[w][g], top);
+        sum += lds.l[w][g] * f;
+        x += *(const f32x4*)&join[(w * p.lds_rows + g) * COLS + col] * f;
+      }
+      if (whole) {
+        store(qrow, g, col, vs, top, sum, x);
+      } else {
+        if (col == 0) {
+          st_agent1(parts, part + at_m + g * 4, top);
+          st_agent1(parts, part + at_l + g * 4, sum);
+        }
+        st_agent4(parts, part + (g * COLS + col) * 4, x);
+      }
+    }
+    __syncthreads();
 
     if (p.scores) {
       const bool added = whole && p.gtiles == 1;
-      if (p.split && u == r0 && tid == 0)
+      if (p.split && s0 == r0 && tid == 0)
         p.split[(int64_t)b * hg + hi] = !added;
       if (added) {
         finish_weights(cur, queries);
@@ -810,7 +817,8 @@ attend_kernel(AttendParams p) {
         __syncthreads();
       }
     }
-    const bool at_end = s1 == u1;
+    // Nothing left to this workgroup but, perhaps, the next row's cost.
+    const bool at_end = s1 == u1 || r1 + cost >= u1;
     if (!whole && p.scores && !at_end) pend = cur;
 
     // ---- shares of split rows joined, by the last workgroup of each ----------
@@ -834,71 +842,95 @@ attend_kernel(AttendParams p) {
       auto part_of = [&](int32_t w) {
         return (w * 2 + (w == first)) * part_size;
       };
-      const int32_t at_m = p.part_rows * COLS * 4;
-      constexpr int TG = kAttThreads / 16;  // threads of a query
-      const int g = tid / TG;
-      float top = -INFINITY, sum = 0.0f;
-      if (g < queries) {
-        for (int32_t w = first + tid % TG; w <= last; w += TG)
-          top = fmaxf(top, ld_agent1(parts, part_of(w) + at_m + g * 4));
-#pragma unroll
-        for (int k = TG / 2; k > 0; k >>= 1)
-          top = fmaxf(top, __shfl_xor(top, k, kWave));
-        for (int32_t w = first + tid % TG; w <= last; w += TG) {
-          const int32_t at = part_of(w) + at_m + g * 4;
-          const float mw = ld_agent1(parts, at);
-          sum += ld_agent1(parts, at + p.part_rows * 4) *
-                 (mw == top ? 1.0f : exp2_fast(mw - top));
-        }
-#pragma unroll
-        for (int k = TG / 2; k > 0; k >>= 1) sum += __shfl_xor(sum, k, kWave);
-        if (tid % TG == 0) {
-          lds.top[g] = top;
-          lds.sum[g] = sum;
-          lds.lse2[g] = sum == 0.0f ? -INFINITY : top + log2f(sum);
-          p.lse[qrow + g] = lds.lse2[g] * kLn2;
-        }
-      }
-      __syncthreads();
-      // Four columns a thread; with threads to spare, the runs are split
-      // over `subs` of them.
+      // Four columns a thread, VP times over; with threads to spare, the
+      // shares are split over `subs` of them.
+      constexpr int VP = NC > 4 ? 4 : 1;  // 16 queries at once
+      constexpr int J = NC > 4 ? 4 : 8;   // shares whose loads are in flight
+      static_assert(16 * (COLS / 4) <= VP * kAttThreads, "one round");
       const int vecs = queries * (COLS / 4);
-      const int subs = vecs < kAttThreads ? kAttThreads / vecs : 1;
-      for (int o0 = 0; o0 < vecs; o0 += kAttThreads) {
-        const int sub = subs > 1 ? tid / vecs : 0;
-        const int at = subs > 1 ? tid % vecs : o0 + tid;
-        const int gg = at / (COLS / 4), col = at % (COLS / 4) * 4;
-        f32x4 x = {0, 0, 0, 0};
-        if (at < vecs && sub < subs) {
-          const float tg = lds.top[gg];
-          constexpr int J = 8;  // loads in flight
-          for (int32_t w = first + sub; w <= last; w += J * subs) {
-            f32x4 d[J];
-            float mw[J];
+      const int subs =
+          min(vecs < kAttThreads ? kAttThreads / vecs : 1, last - first + 1);
+      const int sub = subs > 1 ? tid / vecs : 0;
+      const int at0 = subs > 1 ? tid % vecs : tid;
+      float top[VP], sum[VP];
+      f32x4 x[VP];
+#pragma unroll
+      for (int v = 0; v < VP; ++v) {
+        top[v] = -INFINITY;
+        sum[v] = 0.0f;
+        x[v] = f32x4{0, 0, 0, 0};
+      }
+      if (sub < subs) {
+        for (int32_t w = first + sub; w <= last; w += J * subs) {
+          f32x4 d[VP][J];
+          float mw[VP][J], lw[VP][J];
+#pragma unroll
+          for (int v = 0; v < VP; ++v) {
+            const int at = at0 + v * kAttThreads;
+            const int g = at / (COLS / 4), col = at % (COLS / 4) * 4;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
+              // past the last: beyond the buffer, which reads nothing
               const int32_t wj = w + j * subs;
-              const int32_t pj = part_of(wj <= last ? wj : w);
-              d[j] = ld_agent4(parts, pj + (gg * COLS + col) * 4);
-              mw[j] = ld_agent1(parts, pj + at_m + gg * 4);
+              const int32_t pj =
+                  wj <= last && at < vecs ? part_of(wj) : 0x40000000;
+              d[v][j] = ld_agent4(parts, pj + (g * COLS + col) * 4);
+              mw[v][j] = ld_agent1(parts, pj + at_m + g * 4);
+              lw[v][j] = ld_agent1(parts, pj + at_l + g * 4);
             }
+          }
+#pragma unroll
+          for (int v = 0; v < VP; ++v) {
+            float next = top[v];
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+              if (w + j * subs <= last) next = fmaxf(next, mw[v][j]);
+            const float f0 = weight(top[v], next);
+            top[v] = next;
+            sum[v] *= f0;
+            x[v] *= f0;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
-              const float f = mw[j] == tg ? 1.0f : exp2_fast(mw[j] - tg);
-              x += d[j] * (w + j * subs <= last ? f : 0.0f);
+              const float f =
+                  w + j * subs <= last ? weight(mw[v][j], next) : 0.0f;
+              sum[v] += lw[v][j] * f;
+              x[v] += d[v][j] * f;
             }
           }
         }
-        if (subs > 1) {
-          f32x4* sums = (f32x4*)&lds.o[0][0][0];
-          if (sub < subs) sums[sub * vecs + at] = x;
-          __syncthreads();
-          if (sub == 0)
-            for (int i = 1; i < subs; ++i) x += sums[i * vecs + at];
-        }
-        if (sub == 0 && at < vecs && col < c.dim)
-          store(qrow, gg, col, vs, x);
       }
+      if (subs > 1) {  // then a thread has v = 0 alone
+        f32x4* xs = (f32x4*)join;
+        float2* ts = (float2*)(join + 4 * kAttThreads);
+        if (sub < subs) {
+          xs[sub * vecs + at0] = x[0];
+          ts[sub * vecs + at0] = make_float2(top[0], sum[0]);
+        }
+        __syncthreads();
+        if (sub == 0) {
+          float next = top[0];
+          for (int i = 1; i < subs; ++i)
+            next = fmaxf(next, ts[i * vecs + at0].x);
+          const float f0 = weight(top[0], next);
+          sum[0] *= f0;
+          x[0] *= f0;
+          for (int i = 1; i < subs; ++i) {
+            const float2 z = ts[i * vecs + at0];
+            const float f = weight(z.x, next);
+            sum[0] += z.y * f;
+            x[0] += xs[i * vecs + at0] * f;
+          }
+          top[0] = next;
+        }
+      }
+#pragma unroll
+      for (int v = 0; v < VP; ++v) {
+        const int at = at0 + v * kAttThreads;
+        if (sub == 0 && at < vecs)
+          store(qrow, at / (COLS / 4), at % (COLS / 4) * 4, vs, top[v],
+                sum[v], x[v]);
+      }
+      __syncthreads();
       if (p.scores && p.direct) finish_weights(r, queries);
       __syncthreads();
     }
