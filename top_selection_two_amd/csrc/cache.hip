@@ -158,8 +158,8 @@ int get_work(int dev, hipStream_t stream, size_t bytes, size_t tickets,
   }
 }
 
-// Workgroups of `fn` that a compute unit holds at once, and the units.
-int resident(int dev, const void* fn, int threads, int* out, int* units) {
+// Compute units of a device.
+int units_of(int dev, int* out) {
   try {
     std::lock_guard<std::mutex> lock(g_mu);
     int& cus = g_cus[dev];
@@ -170,6 +170,17 @@ int resident(int dev, const void* fn, int threads, int* out, int* units) {
       (void)hipGetLastError();
       cus = 256;
     }
+    *out = cus;
+    return LIBTOPK_OK;
+  } catch (...) {
+    return LIBTOPK_ERR_NOMEM;
+  }
+}
+
+// Workgroups of `fn` that a compute unit holds at once.
+int resident(const void* fn, int threads, int* out) {
+  try {
+    std::lock_guard<std::mutex> lock(g_mu);
     int& fit = g_fit[fn];
     if (fit < 1 &&
         (hipOccupancyMaxActiveBlocksPerMultiprocessor(&fit, fn, threads, 0) !=
@@ -179,7 +190,6 @@ int resident(int dev, const void* fn, int threads, int* out, int* units) {
       fit = 1;
     }
     *out = fit;
-    *units = cus;
     return LIBTOPK_OK;
   } catch (...) {
     return LIBTOPK_ERR_NOMEM;
@@ -337,26 +347,30 @@ struct AttendNeeds {
   int join;  // floats of dynamic LDS at least
 };
 template <int Q, int C, int NC>
-const void* attend_fn_pages(bool pg16, AttendNeeds* cols) {
+const void* attend_fn_nc(bool pg16, bool heads, AttendNeeds* needs) {
   typedef Attend<Q, C, NC, true> A;
-  *cols = {A::COLS, A::THREADS, (int)sizeof(typename A::Lds), A::JOIN};
-  return pg16 ? (const void*)&attend_kernel<Q, C, NC, true>
-              : (const void*)&attend_kernel<Q, C, NC, false>;
+  *needs = {A::COLS, A::THREADS, (int)sizeof(typename A::Lds), A::JOIN};
+  if (heads)
+    return pg16 ? (const void*)&attend_kernel<Q, C, NC, true, kHeadRun>
+                : (const void*)&attend_kernel<Q, C, NC, false, kHeadRun>;
+  return pg16 ? (const void*)&attend_kernel<Q, C, NC, true, 1>
+              : (const void*)&attend_kernel<Q, C, NC, false, 1>;
 }
 template <int Q, int C>
-const void* attend_fn_dim(int dim, bool pg16, AttendNeeds* cols) {
-  return dim <= 64    ? attend_fn_pages<Q, C, 2>(pg16, cols)
-         : dim <= 96  ? attend_fn_pages<Q, C, 3>(pg16, cols)
-         : dim <= 128 ? attend_fn_pages<Q, C, 4>(pg16, cols)
-         : dim <= 192 ? attend_fn_pages<Q, C, 6>(pg16, cols)
-                      : attend_fn_pages<Q, C, 8>(pg16, cols);
+const void* attend_fn_dim(int dim, bool pg16, bool heads, AttendNeeds* n) {
+  return dim <= 64    ? attend_fn_nc<Q, C, 2>(pg16, heads, n)
+         : dim <= 96  ? attend_fn_nc<Q, C, 3>(pg16, heads, n)
+         : dim <= 128 ? attend_fn_nc<Q, C, 4>(pg16, heads, n)
+         : dim <= 192 ? attend_fn_nc<Q, C, 6>(pg16, heads, n)
+                      : attend_fn_nc<Q, C, 8>(pg16, heads, n);
 }
-const void* attend_fn(int q, int c, int dim, bool pg16, AttendNeeds* cols) {
+const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
+                      AttendNeeds* n) {
   if (q == kBf16)
-    return c == kE4m3 ? attend_fn_dim<kBf16, kE4m3>(dim, pg16, cols)
-                      : attend_fn_dim<kBf16, kBf16>(dim, pg16, cols);
-  return c == kE4m3 ? attend_fn_dim<kF16, kE4m3>(dim, pg16, cols)
-                    : attend_fn_dim<kF16, kF16>(dim, pg16, cols);
+    return c == kE4m3 ? attend_fn_dim<kBf16, kE4m3>(dim, pg16, heads, n)
+                      : attend_fn_dim<kBf16, kBf16>(dim, pg16, heads, n);
+  return c == kE4m3 ? attend_fn_dim<kF16, kE4m3>(dim, pg16, heads, n)
+                    : attend_fn_dim<kF16, kF16>(dim, pg16, heads, n);
 }
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
@@ -434,16 +448,6 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   p.out = out;
   p.lse = lse;
   p.gtiles = (p.group + 15) / 16;
-  // A share that is dealt out costs about as much, besides its tiles, as
-  // 128 KiB of them (loading the queries, joining the waves), a split row
-  // some four times that.
-  p.row_cost = 2048 / p.c.row_bytes;
-  p.min_tiles = 2 * p.row_cost < kMinTiles ? 2 * p.row_cost : kMinTiles;
-  // Tiles of all rows must count in 31 bits.
-  const int64_t att_rows = (int64_t)cache->batch * cache->heads * p.gtiles;
-  const int64_t tiles = ((int64_t)p.c.cap + kTileSlots - 1) / kTileSlots;
-  if (att_rows > INT32_MAX / (tiles + p.row_cost + kMinTiles))
-    return LIBTOPK_ERR_INVALID;
   int dev = 0;
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
@@ -452,33 +456,61 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   // scalar registers (and 16 rows must lie within 2^31 bytes).
   const bool pg16 = cache->page % 16 == 0 && p.c.ks.slot < (1 << 27) &&
                     p.c.vs.slot < (1 << 27);
-  AttendNeeds needs;
-  const void* fn = attend_fn(q_dtype, cache->dtype, cache->dim, pg16, &needs);
-  int fit = 0, cus = 0;
-  rc = resident(dev, fn, needs.threads, &fit, &cus);
+  int dev_units = 0;
+  rc = units_of(dev, &dev_units);
   if (rc != LIBTOPK_OK) return rc;
+  // Heads side by side within a slot, and work enough (at full lengths) that
+  // a workgroup's waves need not share one head's tiles: several heads a
+  // workgroup.
+  const int64_t tiles = ((int64_t)p.c.cap + kTileSlots - 1) / kTileSlots;
+  const bool heads =
+      p.c.ks.head < p.c.ks.slot && p.c.vs.head < p.c.vs.slot &&
+      cache->heads % kHeadRun == 0 &&
+      (int64_t)cache->batch * cache->heads * p.gtiles * tiles >=
+          (int64_t)dev_units * 2 * kMinTiles;
+  p.hs = heads ? kHeadRun : 1;
+  AttendNeeds needs;
+  const void* fn =
+      attend_fn(q_dtype, cache->dtype, cache->dim, pg16, heads, &needs);
+  int fit = 0;
+  rc = resident(fn, needs.threads, &fit);
+  if (rc != LIBTOPK_OK) return rc;
+  const int64_t slots = (int64_t)fit * dev_units < kMaxRuns
+                            ? (int64_t)fit * dev_units
+                            : kMaxRuns;
+  // A share that is dealt out costs about as much, besides its tiles, as
+  // 128 KiB of them (loading the queries, joining the waves), a split row
+  // some twice that.
+  p.row_cost = 2048 / p.c.row_bytes;
+  p.min_tiles = 2 * p.row_cost < kMinTiles ? 2 * p.row_cost : kMinTiles;
+  p.row_cost = p.row_cost / p.hs > 1 ? p.row_cost / p.hs : 1;
+  p.min_tiles = p.min_tiles / p.hs > 1 ? p.min_tiles / p.hs : 1;
+  // Tiles of all rows must count in 31 bits.
+  const int64_t att_rows =
+      (int64_t)cache->batch * (cache->heads / p.hs) * p.gtiles;
+  if (att_rows > INT32_MAX / (tiles + p.row_cost + kMinTiles))
+    return LIBTOPK_ERR_INVALID;
   int64_t grid = att_rows * tiles;
-  if (grid > (int64_t)fit * cus) grid = (int64_t)fit * cus;
-  if (grid > kMaxRuns) grid = kMaxRuns;
+  if (grid > slots) grid = slots;
   p.part_rows = p.group < 16 ? p.group : 16;
   p.lds_rows = (p.part_rows + 3) / 4 * 4;
-  const size_t part_bytes =
-      round_up((size_t)grid * 2 * p.part_rows * (needs.cols + 2) * 4, 256);
+  const size_t part_bytes = round_up(
+      (size_t)grid * 2 * p.hs * p.part_rows * (needs.cols + 2) * 4, 256);
   const int waves = needs.threads / kWave;
   int join = waves * p.lds_rows * needs.cols;
   if (join < needs.join) join = needs.join;
   size_t lds = (size_t)join * 4;
-  const size_t tile_bytes = (size_t)kTileSlots * p.part_rows * 4;
+  const size_t tile_bytes = (size_t)kTileSlots * p.hs * p.part_rows * 4;
   size_t score_bytes = 0, split_bytes = 0;
   if (ledger) {
     p.row_tiles = (int32_t)tiles;
-    p.direct = p.gtiles == 1 && (int64_t)p.c.cap * p.group <= kDirectScores;
+    p.direct = p.gtiles == 1 && (int64_t)p.c.cap * p.group * p.hs <= kDirectScores;
     score_bytes = (size_t)(att_rows * tiles) * tile_bytes;
     if (!p.direct) split_bytes = round_up((size_t)att_rows, 256);
     // What LDS is left when `fit` workgroups share a unit holds scores, but
     // no more than the longest run.
     int64_t run = (att_rows * (tiles + p.row_cost) + grid - 1) / grid;
-    if (run < kMinTiles) run = kMinTiles;
+    if (run < p.min_tiles) run = p.min_tiles;
     int64_t room = (kLdsBytes / fit - needs.lds - 256 - (int64_t)lds) /
                    (int64_t)tile_bytes;
     if (room > run) room = run;

@@ -6,12 +6,17 @@
 // are taken to base 2 (scale is multiplied by log2 e on the host).
 //
 // The kernel reads every K and V row once and should run at the rate of that
-// read.  Work: the slots of a row (a sequence, a cache head and up to 16 of
-// its queries) are cut into tiles of 32 slots, one wave's step; the tiles of
-// all rows are dealt out evenly to as many workgroups as the chip holds at
-// once, whatever the mix of lengths.  A row that one workgroup has alone is
-// finished there; of the others each leaves its (m, l, o), and the row's last
-// workgroup to finish joins them.
+// read.  Work: the slots of a row (a sequence, `hs` of its cache heads and up
+// to 16 queries of each) are cut into tiles of 32 slots, a step of one wave for
+// each head; the tiles of all rows are dealt out evenly to as many workgroups
+// as the chip holds at once, whatever the mix of lengths.  A row that one
+// workgroup has alone is finished there; of the others each leaves its
+// (m, l, o), and the row's last workgroup to finish joins them.
+//
+// hs is 1 where a head's slots lie together.  Where slots lie outside heads,
+// a head's rows are short pieces far apart, and a workgroup that reads one
+// head alone keeps to few of the memory's channels: there the waves of a
+// workgroup take kHeadRun heads of the same slots.
 #pragma once
 
 #include <type_traits>
@@ -22,6 +27,7 @@ namespace ltk {
 
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kTileSlots = 32;  // of one wave
+constexpr int kHeadRun = 4;
 
 struct AttendParams {
   CacheParams c;
@@ -29,7 +35,8 @@ struct AttendParams {
   const char* q;
   int64_t qb, qh;       // bytes
   int32_t group;        // query heads of a cache head
-  int32_t gtiles;       // rows of a cache head: ceil(group / 16)
+  int32_t gtiles;       // ceil(group / 16)
+  int32_t hs;           // cache heads of a row: 1 or kHeadRun
   float scale2;         // scale * log2 e
   const float* k_scale; // NULL: 1
   const float* v_scale;
@@ -217,7 +224,7 @@ struct Attend {
   struct Lds {
     float m[WAVES][16];
     float l[WAVES][16];
-    float lse2[16];
+    float lse2[WAVES * 16];
     int32_t scan[2][WAVES];
     int32_t base;
     int32_t b;
@@ -257,7 +264,7 @@ __device__ __forceinline__ typename A::Ids find_tile(const CacheParams& c,
   return r;
 }
 
-template <int QT, int CT, int NC, bool PG16>
+template <int QT, int CT, int NC, bool PG16, int HS>
 __global__ __launch_bounds__((Attend<QT, CT, NC, PG16>::THREADS),
                              (Attend<QT, CT, NC, PG16>::WAVES / 4)) void
 attend_kernel(AttendParams p) {
@@ -269,7 +276,10 @@ attend_kernel(AttendParams p) {
   const CacheParams& c = p.c;
   const int tid = threadIdx.x, wave = uni(tid / kWave), ln = tid % kWave;
   const int q = ln / 16, n = ln % 16;
-  const int hg = c.heads * p.gtiles;  // rows of a sequence
+  const int hg = c.heads / HS * p.gtiles;  // rows of a sequence
+  // Waves: head hsub of the row's, every ts-th tile from tsub on.
+  constexpr int ts = kAttWaves / HS;
+  const int hsub = wave % HS, tsub = wave / HS;
 
   // ---- this workgroup's run of units -------------------------------------
   const int32_t top_len = c.pages > 0 ? c.cap : 0;
@@ -390,7 +400,8 @@ attend_kernel(AttendParams p) {
   float* const join = (float*)dynamic_lds;
   const int join_floats = max(kAttWaves * p.lds_rows * COLS, A::JOIN);
   float* const held_scores = join + join_floats;
-  const int tile_floats = p.part_rows * kTileSlots;
+  const int head_floats = p.part_rows * kTileSlots;
+  const int tile_floats = HS * head_floats;  // scores of a tile
   int32_t held = 0;
   // A share of a row that is not finished: its row, length, workgroups, and
   // the tiles [from, from + count) at `at` in LDS.
@@ -419,34 +430,38 @@ attend_kernel(AttendParams p) {
   // weights += sum over queries of exp2(x - lse2), for a row whose lse2 is in
   // LDS; scores of the share's tiles from LDS, the others from memory.
   auto finish_weights = [&](const Share& r, int queries) {
-    float* w = p.w.w + r.b * p.w.wb + r.hi * p.w.wh;
+    const int h0 = r.hi / p.gtiles * HS;
     const __amdgpu_buffer_rsrc_t mem = __builtin_amdgcn_make_buffer_rsrc(
         uni_ptr(row_scores(r)), (short)0, tiles_of(r.len) * tile_floats * 4,
         0x00020000);
-    for (int32_t i = tid; i * 4 < r.len; i += kAttThreads) {
-      const int32_t t = i / 8;
-      const bool here = t >= r.from && t < r.from + r.count;
-      const int32_t at = (here ? t - r.from + r.at : t) * tile_floats;
-      f32x4 a = {0, 0, 0, 0};
-      for (int g0 = 0; g0 < queries; g0 += 4) {
-        f32x4 x[4];
+    for (int s = 0; s < HS; ++s) {
+      float* w = p.w.w + r.b * p.w.wb + (h0 + s) * p.w.wh;
+      for (int32_t i = tid; i * 4 < r.len; i += kAttThreads) {
+        const int32_t t = i / 8;
+        const bool here = t >= r.from && t < r.from + r.count;
+        const int32_t at =
+            (here ? t - r.from + r.at : t) * tile_floats + s * head_floats;
+        f32x4 a = {0, 0, 0, 0};
+        for (int g0 = 0; g0 < queries; g0 += 4) {
+          f32x4 x[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int g = g0 + k < queries ? g0 + k : g0;
-          const int o = at + score_at(g, i % 8);
-          x[k] = here ? *(const f32x4*)(held_scores + o)
-                      : ld_agent4(mem, o * 4);
+          for (int k = 0; k < 4; ++k) {
+            const int g = g0 + k < queries ? g0 + k : g0;
+            const int o = at + score_at(g, i % 8);
+            x[k] = here ? *(const f32x4*)(held_scores + o)
+                        : ld_agent4(mem, o * 4);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (g0 + k >= queries) continue;
+            const float z = lds.lse2[s * 16 + g0 + k];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              a[e] += x[k][e] == -INFINITY ? 0.0f : exp2_fast(x[k][e] - z);
+          }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if (g0 + k >= queries) continue;
-          const float z = lds.lse2[g0 + k];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            a[e] += x[k][e] == -INFINITY ? 0.0f : exp2_fast(x[k][e] - z);
-        }
+        add_weights(w + i * 4, r.len - i * 4, a);
       }
-      add_weights(w + i * 4, r.len - i * 4, a);
     }
   };
 
@@ -464,9 +479,9 @@ attend_kernel(AttendParams p) {
     const int32_t r1 = r0 + row_tiles;
     const int32_t s0 = u > r0 ? u : r0, s1 = r1 < u1 ? r1 : u1;
     if (s0 >= s1) break;  // the run ends before the row's first tile
-    const int h = hi / p.gtiles, g0 = hi % p.gtiles * 16;
+    const int h0 = hi / p.gtiles * HS, g0 = hi % p.gtiles * 16;
+    const int h = h0 + hsub;
     const int queries = p.group - g0 < 16 ? p.group - g0 : 16;
-    const int64_t qrow = (int64_t)b * c.heads * p.group + h * p.group + g0;
     const int32_t* table = c.table + b * c.table_stride;
     const int32_t tiles = (len + kTileSlots - 1) / kTileSlots;
     const char* kh = c.k + h * c.ks.head;
@@ -512,11 +527,12 @@ attend_kernel(AttendParams p) {
           cur.at = 0;
         }
         if (te - ta > p.held_tiles - held) te = ta + p.held_tiles - held;
-        tile_scores = held_scores + (held + wave) * tile_floats;
+        tile_scores =
+            held_scores + (held + tsub) * tile_floats + hsub * head_floats;
         held += te - ta;
         cur.count += te - ta;
       }
-      int32_t t = ta + wave;
+      int32_t t = ta + tsub;
       const int32_t t1 = te < tiles ? te : tiles;
       if (t >= t1) continue;
 
@@ -575,7 +591,7 @@ attend_kernel(AttendParams p) {
       load_k(cur);
       load_v(cur);
       typename A::Ids next =
-          find_tile<A, PG16>(c, table, t + kAttWaves, len, q, n);
+          find_tile<A, PG16>(c, table, t + ts, len, q, n);
 
       auto step = [&](auto more) {
         // Scores of 2 x 16 slots.
@@ -612,7 +628,7 @@ attend_kernel(AttendParams p) {
         sched_fence();
         if constexpr (decltype(more)::value) {
           load_k(next);
-          after = find_tile<A, PG16>(c, table, t + 2 * kAttWaves, len, q, n);
+          after = find_tile<A, PG16>(c, table, t + 2 * ts, len, q, n);
         }
         sched_fence();
         // Slots that count.
@@ -650,7 +666,7 @@ attend_kernel(AttendParams p) {
                   f32x4{x[4 * tt], x[4 * tt + 1], x[4 * tt + 2],
                         x[4 * tt + 3]};
           }
-          tile_scores += kAttWaves * tile_floats;
+          tile_scores += ts * tile_floats;
         }
         // The reference m of a query only moves when a score passes it by
         // 2^8: until then exp2(x - m) stays below 2^8 and nothing has to be
@@ -721,7 +737,7 @@ attend_kernel(AttendParams p) {
           sched_fence();
         }
       };
-      for (; t + kAttWaves < t1; t += kAttWaves) step(std::true_type());
+      for (; t + ts < t1; t += ts) step(std::true_type());
       step(std::false_type());
     }
     l = quad_sum(l);
@@ -730,33 +746,34 @@ attend_kernel(AttendParams p) {
     const bool whole = s0 == r0 && s1 == r1;
     // Bytes of a share's result, and where this one lies: a workgroup can
     // have a row's end and, last, another's beginning.
-    const int32_t part_size = p.part_rows * (COLS + 2) * 4;
+    const int32_t part_rows = HS * p.part_rows;
+    const int32_t part_size = part_rows * (COLS + 2) * 4;
     const int32_t part = (wg * 2 + (s0 == r0)) * part_size;
-    const int32_t at_m = p.part_rows * COLS * 4, at_l = at_m + p.part_rows * 4;
+    const int32_t at_m = part_rows * COLS * 4, at_l = at_m + part_rows * 4;
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(
         p.part, (short)0, grid * 2 * part_size, 0x00020000);
-    auto v_factor = [&](int h) {
-      return p.v_scale ? ld_const(p.v_scale + h) : 1.0f;
-    };
-    // Four columns of query g: out, and with the first of them lse.
-    auto store = [&](int64_t row, int g, int col, float vs, float top,
+    // Four columns of query g of head s of a row: out, and with the first of
+    // them lse.
+    auto store = [&](const Share& r, int s, int g, int col, float top,
                      float sum, f32x4 x) {
+      const int h = r.hi / p.gtiles * HS + s;
+      const int64_t row = ((int64_t)r.b * c.heads + h) * p.group +
+                          r.hi % p.gtiles * 16 + g;
       if (col == 0) {
         const float z = sum == 0.0f ? -INFINITY : top + log2f(sum);
-        lds.lse2[g] = z;
-        p.lse[row + g] = z * kLn2;
+        lds.lse2[s * 16 + g] = z;
+        p.lse[row] = z * kLn2;
       }
       if (col >= c.dim) return;
-      const float f = vs / sum;
+      const float f = (p.v_scale ? p.v_scale[h] : 1.0f) / sum;
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = sum == 0.0f ? 0.0f : x[e] * f;
-      *(int2*)((char*)p.out + ((row + g) * c.dim + col) * 2) =
+      *(int2*)((char*)p.out + (row * c.dim + col) * 2) =
           make_int2(pack2<QT>(x[0], x[1]), pack2<QT>(x[2], x[3]));
     };
     auto weight = [](float m, float top) {
       return m == top ? 1.0f : exp2_fast(m - top);
     };
-    const float vs = v_factor(h);
     if (q == 0) {
       lds.m[wave][n] = m;
       lds.l[wave][n] = l;
@@ -776,26 +793,30 @@ attend_kernel(AttendParams p) {
           }
     }
     __syncthreads();
-    for (int at = tid; at < queries * (COLS / 4); at += kAttThreads) {
-      const int g = at / (COLS / 4), col = at % (COLS / 4) * 4;
+    for (int at = tid; at < HS * queries * (COLS / 4); at += kAttThreads) {
+      const int col = at % (COLS / 4) * 4, sg = at / (COLS / 4);
+      const int s = HS > 1 ? sg / queries : 0, g = sg - s * queries;
       float top = -INFINITY, sum = 0.0f;
       f32x4 x = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kAttWaves; ++w) top = fmaxf(top, lds.m[w][g]);
+      for (int i = 0; i < ts; ++i)
+        top = fmaxf(top, lds.m[i * HS + s][g]);
 #pragma unroll
-      for (int w = 0; w < kAttWaves; ++w) {
+      for (int i = 0; i < ts; ++i) {
+        const int w = i * HS + s;
         const float f = weight(lds.m[w][g], top);
         sum += lds.l[w][g] * f;
         x += *(const f32x4*)&join[(w * p.lds_rows + g) * COLS + col] * f;
       }
       if (whole) {
-        store(qrow, g, col, vs, top, sum, x);
+        store(cur, s, g, col, top, sum, x);
       } else {
+        const int row = s * p.part_rows + g;
         if (col == 0) {
-          st_agent1(parts, part + at_m + g * 4, top);
-          st_agent1(parts, part + at_l + g * 4, sum);
+          st_agent1(parts, part + at_m + row * 4, top);
+          st_agent1(parts, part + at_l + row * 4, sum);
         }
-        st_agent4(parts, part + (g * COLS + col) * 4, x);
+        st_agent4(parts, part + (row * COLS + col) * 4, x);
       }
     }
     __syncthreads();
@@ -834,24 +855,21 @@ attend_kernel(AttendParams p) {
       if (!last_to_finish(p.ticket + (int64_t)r.b * hg + r.hi,
                           last - first + 1, p.epoch, &lds.flag))
         continue;
-      const int h = r.hi / p.gtiles, g0 = r.hi % p.gtiles * 16;
+      const int g0 = r.hi % p.gtiles * 16;
       const int queries = p.group - g0 < 16 ? p.group - g0 : 16;
-      const int64_t qrow =
-          (int64_t)r.b * c.heads * p.group + h * p.group + g0;
-      const float vs = v_factor(h);
       auto part_of = [&](int32_t w) {
         return (w * 2 + (w == first)) * part_size;
       };
       // Four columns a thread, VP times over; with threads to spare, the
       // shares are split over `subs` of them.
-      constexpr int VP = NC > 4 ? 4 : 1;  // 16 queries at once
-      constexpr int J = NC > 4 ? 4 : 8;   // shares whose loads are in flight
-      static_assert(16 * (COLS / 4) <= VP * kAttThreads, "one round");
-      const int vecs = queries * (COLS / 4);
+      constexpr int VP = NC > 4 ? 4 : 1;
+      constexpr int J = NC > 4 ? 4 : 8;  // shares whose loads are in flight
+      const int vecs = HS * queries * (COLS / 4);
       const int subs =
           min(vecs < kAttThreads ? kAttThreads / vecs : 1, last - first + 1);
       const int sub = subs > 1 ? tid / vecs : 0;
-      const int at0 = subs > 1 ? tid % vecs : tid;
+      for (int at0 = subs > 1 ? tid % vecs : tid; at0 < vecs;
+           at0 += VP * kAttThreads) {
       float top[VP], sum[VP];
       f32x4 x[VP];
 #pragma unroll
@@ -867,16 +885,18 @@ attend_kernel(AttendParams p) {
 #pragma unroll
           for (int v = 0; v < VP; ++v) {
             const int at = at0 + v * kAttThreads;
-            const int g = at / (COLS / 4), col = at % (COLS / 4) * 4;
+            const int sg = at / (COLS / 4), col = at % (COLS / 4) * 4;
+            const int s = HS > 1 ? sg / queries : 0;
+            const int row = s * p.part_rows + sg - s * queries;
 #pragma unroll
             for (int j = 0; j < J; ++j) {
               // past the last: beyond the buffer, which reads nothing
               const int32_t wj = w + j * subs;
               const int32_t pj =
                   wj <= last && at < vecs ? part_of(wj) : 0x40000000;
-              d[v][j] = ld_agent4(parts, pj + (g * COLS + col) * 4);
-              mw[v][j] = ld_agent1(parts, pj + at_m + g * 4);
-              lw[v][j] = ld_agent1(parts, pj + at_l + g * 4);
+              d[v][j] = ld_agent4(parts, pj + (row * COLS + col) * 4);
+              mw[v][j] = ld_agent1(parts, pj + at_m + row * 4);
+              lw[v][j] = ld_agent1(parts, pj + at_l + row * 4);
             }
           }
 #pragma unroll
@@ -925,10 +945,12 @@ attend_kernel(AttendParams p) {
       }
 #pragma unroll
       for (int v = 0; v < VP; ++v) {
-        const int at = at0 + v * kAttThreads;
+        const int at = at0 + v * kAttThreads, sg = at / (COLS / 4);
+        const int s = HS > 1 ? sg / queries : 0;
         if (sub == 0 && at < vecs)
-          store(qrow, at / (COLS / 4), at % (COLS / 4) * 4, vs, top[v],
-                sum[v], x[v]);
+          store(r, s, sg - s * queries, at % (COLS / 4) * 4, top[v], sum[v],
+                x[v]);
+      }
       }
       __syncthreads();
       if (p.scores && p.direct) finish_weights(r, queries);
@@ -947,17 +969,18 @@ __global__ __launch_bounds__(kBlock) void attend_weights_kernel(
     AttendParams p) {
   const CacheParams& c = p.c;
   const int32_t i = blockIdx.x * kBlock + threadIdx.x, t = i / 8;
-  const int tile_floats = p.part_rows * kTileSlots;
+  const int head_floats = p.part_rows * kTileSlots;
   for (int row = blockIdx.y; row < c.batch * c.heads; row += gridDim.y) {
     const int b = row / c.heads, h = row % c.heads;
     const int32_t len =
         clamp_len(ld_const(c.lens + b), c.pages > 0 ? c.cap : 0);
-    if (i * 4 >= len || !p.split[(int64_t)row * p.gtiles]) continue;
+    // The rows of its head's queries.
+    const int64_t row0 = ((int64_t)b * (c.heads / p.hs) + h / p.hs) * p.gtiles;
+    if (i * 4 >= len || !p.split[row0]) continue;
     f32x4 a = {0, 0, 0, 0};
     for (int gt = 0; gt < p.gtiles; ++gt) {
-      const float* x0 =
-          p.scores + (((int64_t)row * p.gtiles + gt) * p.row_tiles + t) *
-                         tile_floats;
+      const float* x0 = p.scores + (((row0 + gt) * p.row_tiles + t) * p.hs +
+                                    h % p.hs) * head_floats;
       for (int g = 0; g < 16 && gt * 16 + g < p.group; ++g) {
         const float lse2 =
             ld_const(p.lse + (int64_t)row * p.group + gt * 16 + g) *
