@@ -652,22 +652,25 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
     return launch((const void*)&evict_short_kernel<1>, dim3((unsigned)rows),
                   kEvThreads, p, s);
   }
-  p.row_units = make_divisor(2 * p.c.row_bytes / 16);
-  if ((int64_t)p.pair_cap * p.row_units.d > INT32_MAX - kBlock * kMoves)
+  p.row_units = make_divisor(p.c.row_bytes / 16);
+  if ((int64_t)p.pair_cap * p.row_units.d > INT32_MAX - kBlock)
     return LIBTOPK_ERR_INVALID;
   const size_t pair_bytes = round_up((size_t)rows * p.pair_cap * 8, 256);
   const size_t move_bytes = round_up((size_t)rows * 4, 256);
   const size_t hist_words = is_long ? (size_t)rows * 3 * kBins / 2 : 0;
   const size_t count_bytes = is_long ? (size_t)rows * p.chunks * 16 : 0;
+  const size_t state_bytes = is_long ? (size_t)rows * 32 : 0;
   Work work;
-  rc = get_work(dev, s, pair_bytes + move_bytes + hist_words * 8 + count_bytes,
+  rc = get_work(dev, s, pair_bytes + move_bytes + hist_words * 8 + count_bytes +
+                       state_bytes,
                 1, &work);
   if (rc != LIBTOPK_OK) return rc;
   char* at = work.base;
   p.pairs = (int32_t*)at;
   p.moves = (int32_t*)(at += pair_bytes);
   p.hist = (uint32_t*)(at += move_bytes);
-  p.counts = (int32_t*)(at += hist_words * 8);
+  p.counts = (int4*)(at += hist_words * 8);
+  p.state = (int2*)(at += count_bytes);
   const unsigned wide = (unsigned)(rows * p.chunks);
   if (is_long) {
     rc = fill((uint64_t*)p.hist, hist_words, 0, s);
@@ -693,8 +696,7 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   if (rc != LIBTOPK_OK) return rc;
   const int64_t units = (int64_t)p.pair_cap * p.row_units.d;
   return launch((const void*)&evict_move_kernel,
-                dim3((unsigned)((units + kBlock * kMoves - 1) /
-                                (kBlock * kMoves)),
+                dim3((unsigned)((units + kBlock - 1) / kBlock),
                      (unsigned)(rows < 65535 ? rows : 65535)),
                 kBlock, p, s);
 }

@@ -30,9 +30,10 @@ struct SlotsParams {
   int32_t* pairs;     // [rows][2][pair_cap]: holes, then movers
   int32_t* moves;     // [rows]: pairs of the row
   int32_t pair_cap;
-  Divisor row_units;  // 16-byte units of a K and a V row
+  Divisor row_units;  // 16-byte units of a row
   uint32_t* hist;     // [rows][3][kBins], long rows
-  int32_t* counts;    // [rows][chunks][4], long rows
+  int4* counts;       // [rows][chunks], long rows
+  int2* state;        // [rows][4]: cut and want before each digit, long rows
   int32_t chunks;
   int32_t* out_lens;
 };
@@ -154,7 +155,7 @@ constexpr int kEvThreads = 1024;
 constexpr int kEvWaves = kEvThreads / kWave;
 constexpr int kBins = 2048;
 constexpr int kShortSlots = 16 * kEvThreads;
-constexpr int kChunkKeys = 8;
+constexpr int kChunkKeys = 4;
 constexpr int kChunkSlots = kChunkKeys * kEvThreads;
 
 struct Digit {
@@ -162,6 +163,22 @@ struct Digit {
 };
 __device__ __forceinline__ Digit digit(int pass) {
   return pass == 0 ? Digit{21, 11} : pass == 1 ? Digit{10, 11} : Digit{0, 10};
+}
+
+// Sum of the counts v (the same in a wave's lanes) of the waves before this
+// one, and of all.  `lds` is the caller's for this one call.
+__device__ __forceinline__ int wave_offset(int v, int* lds, int* total) {
+  if (lane() == 0) lds[threadIdx.x / kWave] = v;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kEvWaves; ++i) {
+    const int x = lds[i];
+    if (i < (int)threadIdx.x / kWave) before += x;
+    all += x;
+  }
+  *total = uni(all);
+  return uni(before);
 }
 
 // Exclusive prefix sum of v over the workgroup, and the total.
@@ -211,9 +228,8 @@ __device__ __forceinline__ int32_t key_slot(int32_t first, int j) {
 template <int KPT>
 __device__ __forceinline__ void load_keys(const SlotsParams& p,
                                           const LedgerRow& r, int32_t first,
-                                          uint32_t (&u)[KPT]) {
-  float w[KPT];
-  int32_t at[KPT];
+                                          uint32_t (&u)[KPT], float (&w)[KPT],
+                                          int32_t (&at)[KPT]) {
 #pragma unroll
   for (int j = 0; j < KPT; ++j) {
     const int32_t t = key_slot<KPT>(first, j);
@@ -225,6 +241,15 @@ __device__ __forceinline__ void load_keys(const SlotsParams& p,
   for (int j = 0; j < KPT; ++j)
     u[j] = bias(rank_key(__float_as_int(w[j]), at[j], r.seen, p.sinks,
                          p.recent));
+}
+
+template <int KPT>
+__device__ __forceinline__ void load_keys(const SlotsParams& p,
+                                          const LedgerRow& r, int32_t first,
+                                          uint32_t (&u)[KPT]) {
+  float w[KPT];
+  int32_t at[KPT];
+  load_keys<KPT>(p, r, first, u, w, at);
 }
 
 // Adds the digits of the keys that begin with `prefix` (all bits above the
@@ -269,19 +294,21 @@ __device__ __forceinline__ int2 list_chunk(const SlotsParams& p,
                                            const LedgerRow& r, int row,
                                            int32_t first,
                                            const uint32_t (&u)[KPT],
+                                           const float (&w)[KPT],
+                                           const int32_t (&at)[KPT],
                                            uint32_t cut, int need, int ties,
-                                           int holes, int movers, int* lds) {
+                                           int holes, int movers,
+                                           int (*lds)[kEvWaves]) {
+  static_assert(KPT * kEvThreads < 1 << 16, "two counts in a word");
   const int keep = p.keep;
   int n_tie = 0;
 #pragma unroll
   for (int j = 0; j < KPT; ++j)
     n_tie += popc(ballot(key_slot<KPT>(first, j) < r.len && u[j] == cut));
-  // Of each wave: its ties, then its holes and movers (counts that are the
-  // same in every lane).
   int total;
-  int tie = ties + uni(block_scan(lane() == 0 ? n_tie : 0, lds, &total));
+  int tie = ties + wave_offset(n_tie, lds[0], &total);
   uint64_t hole_m[KPT], move_m[KPT];
-  int nh = 0, nm = 0;
+  int n = 0;  // holes, and 2^16 times movers
   float* w2 = p.after.w + r.b * p.after.wb + r.h * p.after.wh;
   int32_t* pos2 = p.after.pos + r.b * p.after.pb + r.h * p.after.ph;
 #pragma unroll
@@ -294,16 +321,14 @@ __device__ __forceinline__ int2 list_chunk(const SlotsParams& p,
     tie += popc(eq);
     hole_m[j] = ballot(in && t < keep && !kept);
     move_m[j] = ballot(kept && t >= keep);
-    nh += popc(hole_m[j]);
-    nm += popc(move_m[j]);
+    n += popc(hole_m[j]) + (popc(move_m[j]) << 16);
     if (kept && t < keep) {
-      w2[t] = r.w[t];
-      pos2[t] = r.pos[t];
+      w2[t] = w[j];
+      pos2[t] = at[j];
     }
   }
-  int th, tm;
-  int ih = holes + uni(block_scan(lane() == 0 ? nh : 0, lds, &th));
-  int im = movers + uni(block_scan(lane() == 0 ? nm : 0, lds, &tm));
+  const int before = wave_offset(n, lds[1], &total);
+  int ih = holes + (before & 0xffff), im = movers + (before >> 16);
   int32_t* list = p.pairs + (int64_t)row * 2 * p.pair_cap;
 #pragma unroll
   for (int j = 0; j < KPT; ++j) {
@@ -314,7 +339,7 @@ __device__ __forceinline__ int2 list_chunk(const SlotsParams& p,
     ih += popc(hole_m[j]);
     im += popc(move_m[j]);
   }
-  return make_int2(holes + th, movers + tm);
+  return make_int2(holes + (total & 0xffff), movers + (total >> 16));
 }
 
 // Rows that are short enough to stay as they are: copied, and padded.
@@ -333,7 +358,7 @@ template <int KPT>
 __global__ __launch_bounds__(kEvThreads) void evict_short_kernel(
     SlotsParams p) {
   __shared__ uint32_t hist[kBins];
-  __shared__ int lds[kEvWaves];
+  __shared__ int lds[kEvWaves], sums[2][kEvWaves];
   __shared__ Found found;
   const int row = blockIdx.x, keep = p.keep;
   const LedgerRow r = ledger_row(p, row);
@@ -346,7 +371,9 @@ __global__ __launch_bounds__(kEvThreads) void evict_short_kernel(
     return;
   }
   uint32_t u[KPT];
-  load_keys<KPT>(p, r, 0, u);
+  float w[KPT];
+  int32_t at[KPT];
+  load_keys<KPT>(p, r, 0, u, w, at);
   uint32_t cut = 0;
   int want = keep;
 #pragma unroll
@@ -360,25 +387,31 @@ __global__ __launch_bounds__(kEvThreads) void evict_short_kernel(
     cut |= (uint32_t)f.bin << d.shift;
     want -= f.above;
   }
-  const int2 n = list_chunk<KPT>(p, r, row, 0, u, cut, want, 0, 0, 0, lds);
+  const int2 n =
+      list_chunk<KPT>(p, r, row, 0, u, w, at, cut, want, 0, 0, 0, sums);
   if (threadIdx.x == 0) p.moves[row] = n.y;
 }
 
 // ---- long rows ---------------------------------------------------------------
-// hist[row][pass] collects the digits of all chunks; every later launch finds
-// the digits so far from it again.
-__device__ __forceinline__ void find_cut(const SlotsParams& p, int row,
-                                         int passes, int* lds, Found* found,
-                                         uint32_t* cut, int* want) {
-  *cut = 0;
-  *want = p.keep;
-  for (int i = 0; i < passes; ++i) {
-    const Found f = find_bin(p.hist + ((int64_t)row * 3 + i) * kBins, *want,
-                             lds, found);
-    __syncthreads();
-    *cut |= (uint32_t)f.bin << digit(i).shift;
-    *want -= f.above;
+// hist[row][i] collects digit i of all chunks.  state[row][i] holds the cut's
+// bits above digit i and the rank looked for below them; the launch after a
+// digit's finds it from the histogram, in every workgroup, and the first chunk
+// writes it down for the launch after that.
+__device__ __forceinline__ void next_state(const SlotsParams& p, int row,
+                                           int chunk, int done, int* lds,
+                                           Found* found, uint32_t* cut,
+                                           int* want) {
+  int2 z = make_int2(0, p.keep);
+  if (done > 0) {
+    if (done > 1) z = p.state[(int64_t)row * 4 + done - 1];
+    const Found f = find_bin(p.hist + ((int64_t)row * 3 + done - 1) * kBins,
+                             z.y, lds, found);
+    z.x |= (int)((uint32_t)f.bin << digit(done - 1).shift);
+    z.y -= f.above;
+    if (chunk == 0 && threadIdx.x == 0) p.state[(int64_t)row * 4 + done] = z;
   }
+  *cut = (uint32_t)z.x;
+  *want = z.y;
 }
 
 __global__ __launch_bounds__(kEvThreads) void evict_digit_kernel(
@@ -386,16 +419,16 @@ __global__ __launch_bounds__(kEvThreads) void evict_digit_kernel(
   __shared__ uint32_t hist[kBins];
   __shared__ int lds[kEvWaves];
   __shared__ Found found;
-  const int row = blockIdx.x / p.chunks;
-  const int32_t first = blockIdx.x % p.chunks * kChunkSlots;
+  const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
+  const int32_t first = chunk * kChunkSlots;
   const LedgerRow r = ledger_row(p, row);
   if (r.len <= p.keep || first >= r.len) return;
   uint32_t u[kChunkKeys];
   load_keys<kChunkKeys>(p, r, first, u);
+  clear_bins(hist);
   uint32_t cut;
   int want;
-  find_cut(p, row, pass, lds, &found, &cut, &want);
-  clear_bins(hist);
+  next_state(p, row, chunk, pass, lds, &found, &cut, &want);
   __syncthreads();
   count_digits<kChunkKeys>(u, first, r.len, cut, digit(pass), hist);
   __syncthreads();
@@ -404,8 +437,8 @@ __global__ __launch_bounds__(kEvThreads) void evict_digit_kernel(
     if (hist[i]) atomicAdd(all + i, hist[i]);
 }
 
-// Of each chunk: slots with key above the cut and at it, below `keep` and
-// from it on.
+// Of each chunk: slots with key above the cut and at it, below `keep` (x, y)
+// and from it on (z, w).
 __global__ __launch_bounds__(kEvThreads) void evict_count_kernel(
     SlotsParams p) {
   __shared__ int lds[kEvWaves];
@@ -420,7 +453,7 @@ __global__ __launch_bounds__(kEvThreads) void evict_count_kernel(
   if (threadIdx.x < 4) sums[threadIdx.x] = 0;
   uint32_t cut;
   int want;
-  find_cut(p, row, 3, lds, &found, &cut, &want);
+  next_state(p, row, chunk, 3, lds, &found, &cut, &want);
   int n[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int j = 0; j < kChunkKeys; ++j) {
@@ -436,15 +469,14 @@ __global__ __launch_bounds__(kEvThreads) void evict_count_kernel(
     for (int i = 0; i < 4; ++i)
       if (n[i]) atomicAdd(&sums[i], n[i]);
   __syncthreads();
-  if (threadIdx.x < 4)
-    p.counts[((int64_t)row * p.chunks + chunk) * 4 + threadIdx.x] =
-        sums[threadIdx.x];
+  if (threadIdx.x == 0)
+    p.counts[(int64_t)row * p.chunks + chunk] =
+        make_int4(sums[0], sums[1], sums[2], sums[3]);
 }
 
 __global__ __launch_bounds__(kEvThreads) void evict_list_kernel(
     SlotsParams p) {
-  __shared__ int lds[kEvWaves];
-  __shared__ Found found;
+  __shared__ int sums[2][kEvWaves];
   const int row = blockIdx.x / p.chunks, chunk = blockIdx.x % p.chunks;
   const int32_t first = chunk * kChunkSlots;
   const LedgerRow r = ledger_row(p, row);
@@ -457,91 +489,71 @@ __global__ __launch_bounds__(kEvThreads) void evict_list_kernel(
   }
   if (first >= r.len) return;
   uint32_t u[kChunkKeys];
-  load_keys<kChunkKeys>(p, r, first, u);
-  uint32_t cut;
-  int want;
-  find_cut(p, row, 3, lds, &found, &cut, &want);
+  float w[kChunkKeys];
+  int32_t at[kChunkKeys];
+  load_keys<kChunkKeys>(p, r, first, u, w, at);
+  const int2 z = p.state[(int64_t)row * 4 + 3];
+  const uint32_t cut = (uint32_t)z.x;
+  const int want = z.y;
   // Ties, kept slots below `keep` and kept slots from it on, before this
-  // chunk: kept = above + what is left of `want` for the ties.
-  const int32_t* counts = p.counts + (int64_t)row * p.chunks * 4;
+  // chunk (every wave for itself, a chunk a lane): of a chunk's ties those are
+  // kept that come before the want-th.
+  const int4* counts = p.counts + (int64_t)row * p.chunks;
   int ties = 0, low = 0, high = 0;
-  for (int i = 0; i < chunk; ++i) {
-    int left = want > ties ? want - ties : 0;
-    const int t1 = ld_const(counts + i * 4 + 1);
-    low += ld_const(counts + i * 4) + (t1 < left ? t1 : left);
-    ties += t1;
-    left = want > ties ? want - ties : 0;
-    const int t3 = ld_const(counts + i * 4 + 3);
-    high += ld_const(counts + i * 4 + 2) + (t3 < left ? t3 : left);
-    ties += t3;
+  for (int i0 = 0; i0 < chunk; i0 += kWave) {
+    const int i = i0 + lane();
+    const int4 n = i < chunk ? counts[i] : make_int4(0, 0, 0, 0);
+    const int incl = wave_scan_incl(n.y + n.w);
+    const int before = ties + incl - n.y - n.w;
+    const int left = max(want - before, 0), left2 = max(want - before - n.y, 0);
+    low += __builtin_amdgcn_readlane(wave_scan_incl(n.x + min(n.y, left)), 63);
+    high +=
+        __builtin_amdgcn_readlane(wave_scan_incl(n.z + min(n.w, left2)), 63);
+    ties += __builtin_amdgcn_readlane(incl, 63);
   }
   const int below = first < p.keep ? first : p.keep;
-  const int2 n = list_chunk<kChunkKeys>(p, r, row, first, u, cut, want, ties,
-                                        below - low, high, lds);
+  const int2 n = list_chunk<kChunkKeys>(p, r, row, first, u, w, at, cut, want,
+                                        ties, below - low, high, sums);
   if (r.len - first <= kChunkSlots && threadIdx.x == 0) p.moves[row] = n.y;
 }
 
 // ---- moves -------------------------------------------------------------------
 // Pair i of a row: slot movers[i] goes to slot holes[i].  A thread moves 16
-// bytes of kMoves pairs' K or V rows, all loaded before the first is stored;
-// the first thread of a pair takes its weight and position along.
-constexpr int kMoves = 4;
-
+// bytes of a pair's K row and of its V row; the first thread of a pair takes
+// its weight and position along.  One pair a thread and as many workgroups as
+// it takes: the chain pair -> pages -> bytes is hidden by other waves, and two
+// or four pairs a thread were slower (16 prompts of up to 8192 slots cut to
+// 2048, slots outside heads: 33 us against 35 and 41), as were separate
+// threads for K and V, which find the same pages twice (46 us).
 __global__ __launch_bounds__(kBlock) void evict_move_kernel(SlotsParams p) {
   const CacheParams& c = p.c;
-  const int row = blockIdx.y;
-  for (int rr = row; rr < c.batch * c.heads; rr += gridDim.y) {
-    const int32_t n = ld_const(p.moves + rr);
-    const int32_t per = p.row_units.d;
-    if ((int64_t)blockIdx.x * kBlock * kMoves >= (int64_t)n * per) continue;
-    const int b = rr / c.heads, h = rr % c.heads;
+  const int32_t i = blockIdx.x * kBlock + threadIdx.x;
+  const int32_t pair = quotient(p.row_units, i);
+  const int32_t off = (i - pair * p.row_units.d) * 16;
+  for (int row = blockIdx.y; row < c.batch * c.heads; row += gridDim.y) {
+    if (pair >= ld_const(p.moves + row)) continue;
+    const int b = row / c.heads, h = row % c.heads;
     const int32_t* table = c.table + b * c.table_stride;
-    const int32_t* holes = p.pairs + (int64_t)rr * 2 * p.pair_cap;
-    const int32_t* movers = holes + p.pair_cap;
-    const float* w = p.w.w + b * p.w.wb + h * p.w.wh;
-    const int32_t* pos = p.w.pos + b * p.w.pb + h * p.w.ph;
-    float* w2 = p.after.w + b * p.after.wb + h * p.after.wh;
-    int32_t* pos2 = p.after.pos + b * p.after.pb + h * p.after.ph;
-    int32_t to[kMoves], from[kMoves], unit[kMoves];
-    bool in[kMoves];
-#pragma unroll
-    for (int j = 0; j < kMoves; ++j) {
-      const int32_t i = (blockIdx.x * kMoves + j) * kBlock + threadIdx.x;
-      const int32_t pair = quotient(p.row_units, i);
-      unit[j] = i - pair * per;
-      in[j] = pair < n;
-      to[j] = in[j] ? holes[pair] : 0;
-      from[j] = in[j] ? movers[pair] : 0;
+    const int32_t* holes = p.pairs + (int64_t)row * 2 * p.pair_cap;
+    const int32_t to = holes[pair], from = holes[p.pair_cap + pair];
+    if (off == 0) {
+      p.after.w[b * p.after.wb + h * p.after.wh + to] =
+          p.w.w[b * p.w.wb + h * p.w.wh + from];
+      p.after.pos[b * p.after.pb + h * p.after.ph + to] =
+          p.w.pos[b * p.w.pb + h * p.w.ph + from];
     }
-    char* dst[kMoves];
-    v4i x[kMoves];
-#pragma unroll
-    for (int j = 0; j < kMoves; ++j) {
-      int32_t zt, zf;
-      const int32_t it = find_page(c, table, to[j], &zt);
-      const int32_t jf = find_page(c, table, from[j], &zf);
-      const bool is_k = unit[j] * 16 < c.row_bytes;
-      const RowStrides& s = is_k ? c.ks : c.vs;
-      const char* base =
-          (is_k ? c.k : c.v - c.row_bytes) + unit[j] * 16;
-      dst[j] = in[j] && it >= 0 && jf >= 0
-                   ? const_cast<char*>(base) + row_offset(s, it, h, zt)
-                   : nullptr;
-      x[j] = v4i{0, 0, 0, 0};
-      if (dst[j])
-        x[j] = __builtin_nontemporal_load(
-            (const v4i*)(base + row_offset(s, jf, h, zf)));
-    }
-#pragma unroll
-    for (int j = 0; j < kMoves; ++j) {
-      if (in[j] && unit[j] == 0) {
-        w2[to[j]] = w[from[j]];
-        pos2[to[j]] = pos[from[j]];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < kMoves; ++j)
-      if (dst[j]) __builtin_nontemporal_store(x[j], (v4i*)dst[j]);
+    int32_t zt, zf;
+    const int32_t it = find_page(c, table, to, &zt);
+    const int32_t jf = find_page(c, table, from, &zf);
+    if (it < 0 || jf < 0) continue;
+    const v4i x = __builtin_nontemporal_load(
+        (const v4i*)(c.k + row_offset(c.ks, jf, h, zf) + off));
+    const v4i y = __builtin_nontemporal_load(
+        (const v4i*)(c.v + row_offset(c.vs, jf, h, zf) + off));
+    __builtin_nontemporal_store(
+        x, (v4i*)const_cast<char*>(c.k + row_offset(c.ks, it, h, zt) + off));
+    __builtin_nontemporal_store(
+        y, (v4i*)const_cast<char*>(c.v + row_offset(c.vs, it, h, zt) + off));
   }
 }
 
