@@ -375,8 +375,8 @@ const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
 constexpr int kLdsBytes = 160 * 1024;
-// Rows of at most this many scores get their weights from their last
-// workgroup, longer ones from a second launch.
+// Rows of at most this many scores are joined and get their weights from
+// their last workgroup, longer ones from a second launch.
 constexpr int kDirectScores = 32768;
 // Least share of a row (see the dealing in attend_kernel).
 #ifndef MINT
@@ -501,12 +501,12 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   if (join < needs.join) join = needs.join;
   size_t lds = (size_t)join * 4;
   const size_t tile_bytes = (size_t)kTileSlots * p.hs * p.part_rows * 4;
-  size_t score_bytes = 0, split_bytes = 0;
+  size_t score_bytes = 0, share_bytes = 0;
   if (ledger) {
     p.row_tiles = (int32_t)tiles;
     p.direct = p.gtiles == 1 && (int64_t)p.c.cap * p.group * p.hs <= kDirectScores;
     score_bytes = (size_t)(att_rows * tiles) * tile_bytes;
-    if (!p.direct) split_bytes = round_up((size_t)att_rows, 256);
+    if (!p.direct) share_bytes = round_up((size_t)att_rows * 8, 256);
     // What LDS is left when `fit` workgroups share a unit holds scores, but
     // no more than the longest run.
     int64_t run = (att_rows * (tiles + p.row_cost) + grid - 1) / grid;
@@ -518,19 +518,21 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
     lds += (size_t)room * tile_bytes;
   }
   Work work;
-  rc = get_work(dev, s, part_bytes + score_bytes + split_bytes,
+  rc = get_work(dev, s, part_bytes + score_bytes + share_bytes,
                 (size_t)att_rows, &work);
   if (rc != LIBTOPK_OK) return rc;
   p.part = (float*)work.base;
   if (ledger) p.scores = (float*)(work.base + part_bytes);
-  if (split_bytes)
-    p.split = (uint8_t*)(work.base + part_bytes + score_bytes);
+  if (share_bytes)
+    p.shares = (int2*)(work.base + part_bytes + score_bytes);
+  p.cols = needs.cols;
+  p.q_type = q_dtype;
   p.ticket = work.tickets;
   p.epoch = work.epoch;
   rc = launch(fn, dim3((unsigned)grid), needs.threads, p, s, lds);
   if (rc != LIBTOPK_OK || !ledger || p.direct) return rc;
   const int64_t wrows = (int64_t)cache->batch * cache->heads;
-  return launch((const void*)&attend_weights_kernel,
+  return launch((const void*)&attend_join_kernel,
                 dim3((p.c.cap + kWeightSlots - 1) / kWeightSlots,
                      (unsigned)(wrows < 65535 ? wrows : 65535)),
                 kBlock, p, s);
