@@ -532,8 +532,12 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   rc = launch(fn, dim3((unsigned)grid), needs.threads, p, s, lds);
   if (rc != LIBTOPK_OK || !ledger || p.direct) return rc;
   const int64_t wrows = (int64_t)cache->batch * cache->heads;
+  // Few rows: workgroups enough to share out the joining, too.
+  int64_t chunks = (p.c.cap + kWeightSlots - 1) / kWeightSlots;
+  const int64_t joiners = 1024 / wrows < kJoiners ? 1024 / wrows : kJoiners;
+  if (chunks < joiners) chunks = joiners;
   return launch((const void*)&attend_join_kernel,
-                dim3((p.c.cap + kWeightSlots - 1) / kWeightSlots,
+                dim3((unsigned)chunks,
                      (unsigned)(wrows < 65535 ? wrows : 65535)),
                 kBlock, p, s);
 }

@@ -987,9 +987,10 @@ attend_kernel(AttendParams p) {
 // What attend_kernel left: for the rows that several workgroups share, lse and
 // out from the shares' results, and weights[t] += sum over the head's queries
 // of exp(x - lse).  A workgroup for every kWeightSlots slots of a sequence and
-// head, four slots a thread; the columns of out are dealt to the row's
-// workgroups, so that a row of many shares is joined by many.
+// head, four slots a thread; the columns of out are dealt to the row's first
+// kJoiners workgroups, so that a row of many shares is joined by many.
 constexpr int kWeightSlots = 4 * kBlock;
+constexpr int kJoiners = 16;
 
 __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
   const CacheParams& c = p.c;
@@ -1005,8 +1006,8 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
     const int b = row / c.heads, h = row % c.heads, hsub = h % p.hs;
     const int32_t len =
         clamp_len(ld_const(c.lens + b), c.pages > 0 ? c.cap : 0);
-    if ((int32_t)blockIdx.x * kWeightSlots >= len) continue;
-    const int workers = (len + kWeightSlots - 1) / kWeightSlots;
+    const int workers = min((int)gridDim.x, kJoiners), wg = (int)blockIdx.x;
+    if (wg >= workers && wg * kWeightSlots >= len) continue;
     // The rows of its head's queries.
     const int64_t row0 = ((int64_t)b * (c.heads / p.hs) + h / p.hs) * p.gtiles;
     f32x4 a = {0, 0, 0, 0};
@@ -1080,7 +1081,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
       // over `subs` threads.
       const int vecs = queries * vecs_of_row;
       const int each = (vecs + workers - 1) / workers;
-      const int v0 = blockIdx.x * each;
+      const int v0 = wg < workers ? wg * each : vecs;
       const int v1 = v0 + each < vecs ? v0 + each : vecs;
       for (int va = v0; va < v1; va += kBlock) {
         const int nv = v1 - va < kBlock ? v1 - va : kBlock;
