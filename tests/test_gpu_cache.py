@@ -206,6 +206,25 @@ def test_attend_full_device(group, heads, batch, lo, hi, extra):
             "bf16", rng=rng)
 
 
+# The same with slots outside heads, where a workgroup takes four heads.
+@pytest.mark.parametrize("group,heads,dim,page,dtype,extra", [
+    (1, 4, 16, 16, "bf16", 1), (4, 4, 16, 20, "f16", 1),
+    (3, 8, 80, 16, "bf16", 1), (20, 4, 16, 16, "bf16", 1),
+    (16, 4, 16, 16, "e4m3", 600), (2, 4, 256, 16, "bf16", 1),
+    (2, 4, 136, 3, "bf16", 1), (6, 12, 16, 16, "bf16", 1)])
+def test_attend_full_device_slots_first(group, heads, dim, page, dtype,
+                                        extra):
+    lens = [int(x) for x in
+            np.random.default_rng(group).integers(100, 3000, size=40)]
+    lens[1], lens[-1] = 0, 3000
+    rng, dev, ref = _case(group, lens, heads, dim, page, dtype, True, extra)
+    q = "f16" if dtype == "f16" else "bf16"
+    print("attend slots first", group, heads, dim, page, dtype, flush=True)
+    _attend(dev, _q(rng, 40, group * heads, dim, q), ref, q, dtype, rng=rng)
+    _attend(dev, _q(rng, 40, group * heads, dim, q), ref, q, dtype,
+            weights=False, rng=rng)
+
+
 def test_attend_many_sequences():
     lens = [int(x) for x in
             np.random.default_rng(5).integers(0, 90, size=700)]
@@ -640,3 +659,25 @@ def test_evict_into_given_arrays_and_repeat():
     got = ltk.cache_evict(dev["k"], dev["v"], dev["table"], dev["lens"],
                           seen, dw, dp, 100)
     assert all(_same(x, y) for x, y in zip(got, r[0]))
+
+
+def test_example_keeps_a_bounded_cache():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(
+        os.path.abspath(__file__))), "examples", "bounded_cache.py")
+    spec = importlib.util.spec_from_file_location("bounded_cache", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    r = mod.decode(batch=2, heads=2, group=4, dim=64, prompt=300, budget=128,
+                   tokens=20)
+    # the budget holds, the sinks and the recent tokens are in the cache, and
+    # its positions are distinct
+    assert r["lens"].tolist() == [128, 128]
+    for row in r["positions"].cpu().numpy().reshape(-1, 128):
+        have = set(row.tolist())
+        assert len(have) == 128 and {0, 1, 2, 3} <= have
+        assert set(range(320 - 16, 320)) <= have
+    assert r["out"].isfinite().all()
+    # what the cache's rows say: every row is its position's
+    assert mod.rows_match(r)

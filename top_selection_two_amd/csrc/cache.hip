@@ -378,11 +378,9 @@ constexpr int kLdsBytes = 160 * 1024;
 // Rows of at most this many scores are joined and get their weights from
 // their last workgroup, longer ones from a second launch.
 constexpr int kDirectScores = 32768;
-// Least share of a row (see the dealing in attend_kernel).
-#ifndef MINT
-#define MINT 24
-#endif
-constexpr int kMinTiles = MINT;
+// Least share of a row, in tiles (see the dealing in attend_kernel): below
+// it, joining costs more than the tiles that others take over.
+constexpr int kMinTiles = 24;
 static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
               "a thread searches two bins");
 
