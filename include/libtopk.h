@@ -446,10 +446,14 @@ typedef struct libtopk_ledger {
  *   lse      device, float32[batch][q_heads], contiguous
  *
  * Workspace: partial results of at most 1024 workgroups, and with a ledger
- * one float32 a query head and slot of the table's width.
+ * one float32 a query head and slot of the table's width (rounded up to 32).
+ * One launch, or two with a ledger and long rows (more than 32768 scores a
+ * row) or more than 16 queries a head.
  *
  * Errors: LIBTOPK_ERR_INVALID for a NULL or misaligned pointer, a size,
- * stride or type outside the above, or outputs that overlap an input.
+ * stride or type outside the above, outputs that overlap an input, or more
+ * than 2^31 tiles of 32 slots over all sequences, heads and 16-query groups;
+ * LIBTOPK_ERR_NOMEM if the workspace cannot grow.
  */
 int cache_attend(const libtopk_cache_t *cache, const void *q, int32_t q_dtype,
                  int32_t q_heads, int64_t q_batch_stride,
@@ -503,7 +507,8 @@ int cache_append(const libtopk_cache_t *cache, const void *k_new,
  *
  * weights and positions of `after` get the `keep` entries of every row
  * (entries past the new length: 0 and -1); out_lens[b] = min(lens[b], keep).
- * `ledger` is only read.
+ * `ledger` is only read.  Two launches, seven when the table (or the ledger)
+ * can name more than 16384 slots.
  *
  *   keep     1 <= keep <= after->slots
  *   after    device arrays that overlap neither the ledger nor each other

@@ -376,10 +376,13 @@ const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
 constexpr int kLdsBytes = 160 * 1024;
 // Rows of at most this many scores are joined and get their weights from
-// their last workgroup, longer ones from a second launch.
+// their last workgroup, longer ones from a second launch.  (211 slots of 8
+// heads of 4 queries: 9.5 us in one launch, 11.2 in two; 16 sequences of 5000
+// slots, one head of 16 queries: 37 us in one launch, 29 in two.)
 constexpr int kDirectScores = 32768;
 // Least share of a row, in tiles (see the dealing in attend_kernel): below
-// it, joining costs more than the tiles that others take over.
+// it, joining costs more than the tiles that others take over (about 6 us
+// against 0.6 us a tile of 128 elements).
 constexpr int kMinTiles = 24;
 static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
               "a thread searches two bins");
@@ -459,7 +462,8 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   if (rc != LIBTOPK_OK) return rc;
   // Heads side by side within a slot, and work enough (at full lengths) that
   // a workgroup's waves need not share one head's tiles: several heads a
-  // workgroup.
+  // workgroup (48 ragged sequences of 8 heads: 132 us against 151 with one
+  // head a workgroup and 135 with eight).
   const int64_t tiles = ((int64_t)p.c.cap + kTileSlots - 1) / kTileSlots;
   const bool heads =
       p.c.ks.head < p.c.ks.slot && p.c.vs.head < p.c.vs.slot &&

@@ -17,6 +17,13 @@
 // a head's rows are short pieces far apart, and a workgroup that reads one
 // head alone keeps to few of the memory's channels: there the waves of a
 // workgroup take kHeadRun heads of the same slots.
+//
+// Measured (MI355X; a large read reaches 7.2 TB/s): 48 sequences of 4096
+// slots, 8 heads of 4 queries of 128 elements, bfloat16, 0.81 GB: 129 us
+// (6.3 TB/s), 142 us with the weights; 32 sequences of 8192 slots in pages of
+// 256: 160 us (6.7 TB/s); a document of 131072 slots, 4 heads of 8 queries:
+// 50 us, of which the rows' stream is 40 (6.7 TB/s) and joining 64 shares a
+// row 7.  Matrix instructions are busy about a twentieth of the time.
 #pragma once
 
 #include <type_traits>
