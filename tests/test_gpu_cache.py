@@ -358,7 +358,7 @@ def test_attend_is_reproducible_on_any_stream():
 
     want = call()
     for i in range(4):
-        ltk.debug_scramble(2, i + 1)
+        ltk.cache_debug_scramble(i + 1)
         assert all(torch.equal(a, b) for a, b in zip(call(), want))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -649,7 +649,7 @@ def test_evict_into_given_arrays_and_repeat():
     r = []
     for i in range(3):
         k, v = dev["k"].clone(), dev["v"].clone()
-        ltk.debug_scramble(2, i)
+        ltk.cache_debug_scramble(i)
         a = ltk.cache_evict(k, v, dev["table"], dev["lens"], seen, dw, dp,
                             100, out=(ow[:, :, 20:120], op[:, :, 28:]))
         r.append((a[0].clone(), a[1].clone(), a[2], k, v))

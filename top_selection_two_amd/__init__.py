@@ -189,16 +189,23 @@ def release() -> None:
 def debug_scramble(which: int = 0, seed: int = 1, stream: int | None = None):
     """Overwrite the tickets and histogram counters that later calls on the
     current stream (which=0) or topk_i32_noalloc (which=1) use with
-    pseudo-random words: no result may depend on them (a test hook).
-    which=2: the tickets of the cache_* calls on the current stream."""
+    pseudo-random words: no result may depend on them (a test hook)."""
     import torch
     if stream is None:
         stream = torch.cuda.current_stream().cuda_stream
-    seed &= 2 ** 64 - 1
-    rc = (lib.cache_debug_scramble(stream or None, seed) if which == 2 else
-          lib.libtopk_debug_scramble(stream or None, which, seed))
+    rc = lib.libtopk_debug_scramble(stream or None, which,
+                                    seed & (2 ** 64 - 1))
     if rc != OK:
         raise LibtopkError(rc, "libtopk_debug_scramble")
+
+
+def cache_debug_scramble(seed: int = 1):
+    """The same for the tickets of the cache_* calls on the current stream."""
+    import torch
+    rc = lib.cache_debug_scramble(
+        torch.cuda.current_stream().cuda_stream or None, seed & (2 ** 64 - 1))
+    if rc != OK:
+        raise LibtopkError(rc, "cache_debug_scramble")
 
 
 # ---------------------------------------------------------------- raw calls
