@@ -1,8 +1,9 @@
 """Build the HIP library libtopk.so for gfx950 (in-tree, no JIT cache).
 
-Two translation units, compiled side by side, hold the C entry points and
-include their kernel headers: csrc/libtopk.hip (selection and reductions) and
-csrc/cache.hip (the operators on a paged key-value cache).  The flags disable
+The translation units, compiled side by side, hold the C entry points and
+include their kernel headers: csrc/libtopk.hip (selection and reductions),
+csrc/cache.hip (the operators on a paged key-value cache) and
+csrc/cache_attend.hip (its attention kernels, once for each pair of types).  The flags disable
 packed-FP32 instruction selection (every HIP build in this project carries
 the flag), emit code for gfx950 only, and pin code object version 5, which both the ROCm runtime in /opt/rocm and the one bundled with
 PyTorch load.  They also turn off the compiler's atomic optimizer: every
@@ -25,7 +26,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 SO = os.path.join(PKG, "libtopk.so")
 BINDING = os.path.join(PKG, "_binding.so")
-UNITS = ("libtopk.hip", "cache.hip")
+# Sources with their definitions: LTK_Q, LTK_C are types of include/libtopk.h.
+UNITS = (("libtopk.hip",), ("cache.hip",),
+         *(("cache_attend.hip", "-DLTK_Q=%d" % q, "-DLTK_C=%d" % c)
+           for q, c in ((0, 0), (0, 2), (1, 1), (1, 2))))
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -48,11 +52,11 @@ def hipcc() -> str:
 
 def build_libtopk(extra_flags=(), out: str = SO) -> str:
     tmp = out + ".tmp%d" % os.getpid()
-    objs = [tmp + "." + os.path.splitext(u)[0] + ".o" for u in UNITS]
+    objs = ["%s.%d.o" % (tmp, i) for i in range(len(UNITS))]
     try:
         jobs = [subprocess.Popen([hipcc(), *HIPCC_FLAGS, *extra_flags, "-I",
                                   INCLUDE, "-I", CSRC, "-c",
-                                  os.path.join(CSRC, u), "-o", o])
+                                  os.path.join(CSRC, u[0]), *u[1:], "-o", o])
                 for u, o in zip(UNITS, objs)]
         codes = [j.wait() for j in jobs]
         for job, code in zip(jobs, codes):

@@ -14,7 +14,7 @@
 #include <vector>
 
 #include "libtopk.h"
-#include "cache_attend_kernel.hpp"
+#include "cache_join_kernel.hpp"
 #include "cache_slots_kernel.hpp"
 
 namespace {
@@ -338,32 +338,6 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
   return LIBTOPK_OK;
 }
 
-// The attention kernel for a type pair, row length and page size, and what it
-// needs.
-struct AttendNeeds {
-  int cols;  // columns of a partial result
-  int threads;
-  int lds;   // bytes of static LDS
-  int join;  // floats of dynamic LDS at least
-};
-template <int Q, int C, int NC>
-const void* attend_fn_nc(bool pg16, bool heads, AttendNeeds* needs) {
-  typedef Attend<Q, C, NC, true> A;
-  *needs = {A::COLS, A::THREADS, (int)sizeof(typename A::Lds), A::JOIN};
-  if (heads)
-    return pg16 ? (const void*)&attend_kernel<Q, C, NC, true, kHeadRun>
-                : (const void*)&attend_kernel<Q, C, NC, false, kHeadRun>;
-  return pg16 ? (const void*)&attend_kernel<Q, C, NC, true, 1>
-              : (const void*)&attend_kernel<Q, C, NC, false, 1>;
-}
-template <int Q, int C>
-const void* attend_fn_dim(int dim, bool pg16, bool heads, AttendNeeds* n) {
-  return dim <= 64    ? attend_fn_nc<Q, C, 2>(pg16, heads, n)
-         : dim <= 96  ? attend_fn_nc<Q, C, 3>(pg16, heads, n)
-         : dim <= 128 ? attend_fn_nc<Q, C, 4>(pg16, heads, n)
-         : dim <= 192 ? attend_fn_nc<Q, C, 6>(pg16, heads, n)
-                      : attend_fn_nc<Q, C, 8>(pg16, heads, n);
-}
 const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
                       AttendNeeds* n) {
   if (q == kBf16)
