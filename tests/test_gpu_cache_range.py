@@ -1,0 +1,107 @@
+"""Attention over a paged cache where the range of the numbers counts: slots of
+tiny probability that alone decide an output, infinite V rows, and sums that
+cancel.
+
+Bounds, with u = 2^-24: as for finite rows in test_gpu_cache.py (a score's
+error is dx, a probability's 2 dx + (n + 8) u relative, the sum over V another
+(n + 8) u), but with probabilities that enter the sum as float32: out is off by
+those times sum p |V|, and by its one rounding.  The bounds are relative to the
+probabilities, however small these are.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.cache as oc
+import top_selection_two_amd as ltk
+from test_gpu_cache import TINY, TYPES, U, _case
+
+pytestmark = pytest.mark.gpu
+
+PAIRS = [("bf16", "bf16"), ("f16", "f16"), ("bf16", "e4m3"), ("f16", "e4m3")]
+
+
+def _put(dev, ref, name, b, t, row, head=slice(None)):
+    """Row(s) of slot t of a sequence, on both sides, rounded to the type."""
+    page = ref["k"].shape[2]
+    p, z = int(ref["table"][b, t // page]), t % page
+    x = torch.as_tensor(row, dtype=torch.float32).to(dev[name].dtype)
+    if x.element_size() == 1:
+        dev[name].view(torch.uint8)[p, head, z] = x.view(torch.uint8).cuda()
+    else:
+        dev[name][p, head, z] = x.cuda()
+    ref[name][p, head, z] = x.double().numpy()
+
+
+def _run(dev, q, ref, scale, weights, seed):
+    b, dim = q.shape[0], q.shape[2]
+    heads, page = ref["k"].shape[1], ref["k"].shape[2]
+    w = torch.zeros(b, heads, dev["table"].shape[1] * page,
+                    device="cuda") if weights else None
+    out, lse = ltk.cache_attend(q, dev["k"], dev["v"], dev["table"],
+                                dev["lens"], scale=scale, weights=w)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        want = oc.attend(q.double().cpu().numpy(), ref, scale)
+    return out.double().cpu().numpy(), want
+
+
+def _bound(want, n, dim, qtype):
+    o, z, _, spread, size = want
+    dx = (dim + 12) * U * size + 4 * U * np.abs(z)
+    dp = 2 * dx + (n + 8) * U
+    eps = torch.finfo(TYPES[qtype]).eps / 2
+    return eps * np.abs(o) + TINY[qtype] + \
+        (1 + eps) * (dp[:, :, None] + (n + 8) * U) * spread
+
+
+@pytest.mark.parametrize("qtype,ctype", PAIRS)
+@pytest.mark.parametrize("gap", [8.0, 12.0, 16.0, 18.0, 26.0])
+@pytest.mark.parametrize("heads,slots_first", [(2, False), (4, True)])
+def test_attend_outputs_of_tiny_probabilities(qtype, ctype, gap, heads,
+                                              slots_first):
+    """A slot that takes nearly all weight and whose V row is zero: what is
+    left of out comes from slots exp(gap) times less probable."""
+    lens = [2, 31, 70, 1000, 9000]
+    rng, dev, ref = _case(int(gap), lens, heads, 64, 16, ctype, slots_first)
+    print("tiny probabilities", qtype, ctype, gap, heads, flush=True)
+    # scores: elements 0 and 1 of K times ones, the others times zero
+    for b, n in enumerate(lens):
+        for t in range(n):
+            at = ref["table"][b, t // 16], slice(None), t % 16
+            ref["k"][at][:, 0] = 0.0
+            ref["k"][at][:, 1] *= 0.25
+            ref["v"][at] = rng.choice([96.0, 288.0, 448.0], (heads, 64))
+    for name in ("k", "v"):
+        x = torch.from_numpy(ref[name]).to(TYPES[ctype])
+        ref[name] = x.double().numpy()
+        dev[name] = x.transpose(1, 2).contiguous().cuda().transpose(1, 2) \
+            if slots_first else x.cuda()
+    for b, t in enumerate((0, 17, 69, 500, 8000)):
+        row = np.zeros((heads, 64))
+        row[:, 0] = gap
+        _put(dev, ref, "k", b, t, row)
+        _put(dev, ref, "v", b, t, np.zeros((heads, 64)))
+    q = torch.zeros(len(lens), heads * 2, 64)
+    q[:, :, :2] = 1.0
+    for weights in (True, False):
+        out, want = _run(dev, q.to(TYPES[qtype]).cuda(), ref, 1.0, weights, 1)
+        tol = _bound(want, max(lens), 64, qtype)
+        bad = np.abs(out - want[0]) > tol
+        assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5],
+                               want[0][bad][:5], tol[bad][:5])
+
+
+def test_attend_two_slots_far_apart():
+    """Scores 0 and -25 ln 2, V 0 and 1000: out is 1000 / (2^25 + 1)."""
+    _, dev, ref = _case(1, [2], 1, 64, 16, "f16")
+    for t, (x, v) in enumerate(((0.0, 0.0), (-17.328125, 1000.0))):
+        k = np.zeros(64)
+        k[0] = x
+        _put(dev, ref, "k", 0, t, k)
+        _put(dev, ref, "v", 0, t, np.full(64, v))
+    q = torch.zeros(1, 1, 64)
+    q[..., 0] = 1.0
+    out, want = _run(dev, q.to(torch.float16).cuda(), ref, 1.0, False, 1)
+    assert want[0][0, 0, 0] > 2.9e-5
+    assert (np.abs(out - want[0]) <= _bound(want, 2, 64, "f16")).all()

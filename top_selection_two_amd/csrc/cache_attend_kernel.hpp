@@ -96,6 +96,11 @@ __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
         0);
 }
 
+// 16 x 16 x 4: lane 16 q + n takes row (or column) n, contraction index q.
+__device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
 // Two floats rounded to the operand's type, and back.
 template <int QT>
 __device__ __forceinline__ int pack2(float a, float b) {
@@ -708,49 +713,74 @@ attend_kernel(AttendParams p) {
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        // A weight enters the product as two numbers of the operand's type,
-        // its rounding and what that lost (2^-17 relative left in bfloat16):
-        // out is then rounded once, at the end, as if the weights had stayed
-        // in float32.
-        Frag hi, lo;
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          const float e0 = exp2_fast(x[j] - ref), e1 = exp2_fast(x[j + 1] - ref);
-          l += e0 + e1;
-          hi.d[j / 2] = pack2<QT>(e0, e1);
-          float a0, a1;
-          unpack2<QT>(hi.d[j / 2], &a0, &a1);
-          lo.d[j / 2] = pack2<QT>(e0 - a0, e1 - a1);
-        }
+        for (int j = 0; j < 8; ++j) w[j] = exp2_fast(x[j] - ref);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          int w[8][VE / 2];  // 8 slots of VE elements
+        for (int j = 0; j < 8; j += 2) l += w[j] + w[j + 1];
+        if constexpr (CT == kF16) {
+          // Product in float32: a weight counts however small it is, where the
+          // rows of the larger ones are zero, and below 2^-14 float16 has not
+          // the bits, below 2^-25 not the range.  Instruction j of a column
+          // block contracts over the j-th slot of the four lane groups.
+          // Against 16-bit operands these are eight times the matrix cycles:
+          // 133 us against 132 for 48 sequences of up to 8000 slots, 8 heads
+          // of 4 queries of 128 elements, 11.0 against 9.4 for 211 slots.
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if constexpr (CT == kE4m3) {
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int e = 0; e < VD; ++e) {
-                w[j][2 * e] = widen2<QT, false>(vr[nb][j][e]);
-                w[j][2 * e + 1] = widen2<QT, true>(vr[nb][j][e]);
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int e = 0; e < VE; e += 2) {
+                float y0, y1;
+                unpack2<kF16>(vr[nb][j][e / 2], &y0, &y1);
+                f32x4* acc = &o[nb * VE + e];
+                acc[0] = mma4(w[j], y0, acc[0]);
+                acc[1] = mma4(w[j], y1, acc[1]);
               }
-            } else {
+        } else {
+          // A weight enters the product as two bfloat16 numbers, its rounding
+          // and what that lost (2^-17 relative left): out is then rounded
+          // once, at the end, as if the weights had stayed in float32.
+          // bfloat16 has the range of float32, and holds e4m3 rows exactly.
+          Frag hi, lo;
 #pragma unroll
-              for (int e = 0; e < VD; ++e) w[j][e] = vr[nb][j][e];
-            }
+          for (int j = 0; j < 8; j += 2) {
+            hi.d[j / 2] = pack2<kBf16>(w[j], w[j + 1]);
+            float a0, a1;
+            unpack2<kBf16>(hi.d[j / 2], &a0, &a1);
+            lo.d[j / 2] = pack2<kBf16>(w[j] - a0, w[j + 1] - a1);
           }
 #pragma unroll
-          for (int e = 0; e < VE; ++e) {
-            // element e of the 8 slots: low or high halves, in pairs
-            const unsigned sel = e % 2 ? 0x07060302u : 0x05040100u;
-            Frag v;
+          for (int nb = 0; nb < NB; ++nb) {
+            int y[8][VE / 2];  // 8 slots of VE elements
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              v.d[j] = (int)__builtin_amdgcn_perm((unsigned)w[2 * j + 1][e / 2],
-                                                  (unsigned)w[2 * j][e / 2],
-                                                  sel);
-            f32x4& acc = o[nb * VE + e];
-            acc = mma<QT>(hi, v, acc);
-            acc = mma<QT>(lo, v, acc);
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (CT == kE4m3) {
+#pragma unroll
+                for (int e = 0; e < VD; ++e) {
+                  y[j][2 * e] = widen2<kBf16, false>(vr[nb][j][e]);
+                  y[j][2 * e + 1] = widen2<kBf16, true>(vr[nb][j][e]);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < VD; ++e) y[j][e] = vr[nb][j][e];
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+              // element e of the 8 slots: low or high halves, in pairs
+              const unsigned sel = e % 2 ? 0x07060302u : 0x05040100u;
+              Frag v;
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                v.d[j] = (int)__builtin_amdgcn_perm((unsigned)y[2 * j + 1][e / 2],
+                                                    (unsigned)y[2 * j][e / 2],
+                                                    sel);
+              f32x4& acc = o[nb * VE + e];
+              acc = mma<kBf16>(hi, v, acc);
+              acc = mma<kBf16>(lo, v, acc);
+            }
           }
         }
         sched_fence();
