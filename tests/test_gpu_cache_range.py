@@ -105,3 +105,43 @@ def test_attend_two_slots_far_apart():
     out, want = _run(dev, q.to(torch.float16).cuda(), ref, 1.0, False, 1)
     assert want[0][0, 0, 0] > 2.9e-5
     assert (np.abs(out - want[0]) <= _bound(want, 2, 64, "f16")).all()
+
+
+@pytest.mark.parametrize("qtype,ctype", PAIRS)
+@pytest.mark.parametrize("weights", [True, False])
+def test_attend_sums_that_cancel(qtype, ctype, weights):
+    """Pairs of slots with V rows of opposite signs whose scores differ by
+    2^-13: out is about 2^-14 of sum p |V| and its rounding at most 2^-22 of
+    it, so that probabilities held in fewer bits than float32 show.
+
+    Scores are sums of few exact products: off by the rounding of scale *
+    log2 e and of the product with it, 2 u |x|; the exponential by 2 u, sums
+    of n terms by n u each, the division by 4 u and the products by u."""
+    lens = [3, 5, 7] * 8
+    rng, dev, ref = _case(5, lens, 2, 64, 16, ctype)
+    print("cancelling", qtype, ctype, weights, flush=True)
+    for b, n in enumerate(lens):
+        # slot 0: the largest score, 0, and no V
+        _put(dev, ref, "k", b, 0, np.zeros((2, 64)))
+        _put(dev, ref, "v", b, 0, np.zeros((2, 64)))
+        for t in range(1, n, 2):
+            v = rng.choice([-1.75, -1.0, 1.0, 1.5], (2, 64))
+            base = -rng.integers(1, 9) / 8
+            for i in range(2):
+                k = np.zeros((2, 64))
+                k[:, 0] = base
+                k[:, 1] = float(i)
+                _put(dev, ref, "k", b, t + i, k)
+                _put(dev, ref, "v", b, t + i, v if i else -v)
+    q = torch.zeros(len(lens), 6, 64)
+    q[:, :, 0] = torch.tensor([0.5, 1.0, 0.625, 0.75, 0.875, 0.25])
+    q[:, :, 1] = 2.0 ** -13
+    out, want = _run(dev, q.to(TYPES[qtype]).cuda(), ref, 1.0, weights, 2)
+    n = np.asarray(lens)[:, None, None]
+    eps = torch.finfo(TYPES[qtype]).eps / 2
+    tol = eps * np.abs(want[0]) + TINY[qtype] + \
+        (2 * 1.0 + 2 + 2 * n + 4 + 1) * U * want[3]
+    assert (np.abs(want[0]) < 2.0 ** -12 * want[3].max()).all()
+    bad = np.abs(out - want[0]) > tol
+    assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5],
+                           want[0][bad][:5], tol[bad][:5])

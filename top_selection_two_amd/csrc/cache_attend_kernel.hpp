@@ -739,17 +739,22 @@ attend_kernel(AttendParams p) {
                 acc[1] = mma4(w[j], y1, acc[1]);
               }
         } else {
-          // A weight enters the product as two bfloat16 numbers, its rounding
-          // and what that lost (2^-17 relative left): out is then rounded
-          // once, at the end, as if the weights had stayed in float32.
-          // bfloat16 has the range of float32, and holds e4m3 rows exactly.
-          Frag hi, lo;
+          // A weight enters the product as three bfloat16 numbers, its
+          // rounding and what that and the next lost: 3 x 8 bits hold a
+          // float32 number, whose range bfloat16 has, so that out is rounded
+          // once, at the end.  (bfloat16 holds e4m3 rows exactly.)
+          Frag part[3];
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            hi.d[j / 2] = pack2<kBf16>(w[j], w[j + 1]);
-            float a0, a1;
-            unpack2<kBf16>(hi.d[j / 2], &a0, &a1);
-            lo.d[j / 2] = pack2<kBf16>(w[j] - a0, w[j + 1] - a1);
+            float a0 = w[j], a1 = w[j + 1];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+              part[i].d[j / 2] = pack2<kBf16>(a0, a1);
+              float b0, b1;
+              unpack2<kBf16>(part[i].d[j / 2], &b0, &b1);
+              a0 -= b0;
+              a1 -= b1;
+            }
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
@@ -778,8 +783,8 @@ attend_kernel(AttendParams p) {
                                                     (unsigned)y[2 * j][e / 2],
                                                     sel);
               f32x4& acc = o[nb * VE + e];
-              acc = mma<kBf16>(hi, v, acc);
-              acc = mma<kBf16>(lo, v, acc);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) acc = mma<kBf16>(part[i], v, acc);
             }
           }
         }
