@@ -145,3 +145,69 @@ def test_attend_sums_that_cancel(qtype, ctype, weights):
     bad = np.abs(out - want[0]) > tol
     assert not bad.any(), (np.argwhere(bad)[:5], out[bad][:5],
                            want[0][bad][:5], tol[bad][:5])
+
+
+INF = float("inf")
+
+
+@pytest.mark.parametrize("ctype", ["bf16", "f16"])
+@pytest.mark.parametrize("weights", [True, False])
+@pytest.mark.parametrize("heads,dim,slots_first", [(2, 64, False),
+                                                   (4, 136, True)])
+def test_attend_infinite_v(ctype, weights, heads, dim, slots_first):
+    """Infinities of V, at the largest score, at ordinary ones and at scores
+    down to 80 below it, make their columns infinite (NaN where both signs or
+    a NaN meet), and no others."""
+    lens = [1, 2, 33, 100, 700, 5000]
+    rng, dev, ref = _case(7, lens, heads, dim, 16, ctype, slots_first)
+    print("infinite v", ctype, weights, heads, dim, flush=True)
+    for b, n in enumerate(lens):
+        for t in (0, n // 2, n - 1):
+            k = np.zeros((heads, dim))
+            # 0 the largest, and far below it
+            k[:, 0] = 40.0 if t == 0 else -40.0 if t == n - 1 else 0.0
+            _put(dev, ref, "k", b, t, k)
+            v = rng.standard_normal((heads, dim))
+            v[:, 3 + (t == 0)] = INF
+            v[:, 6 + (t == n - 1)] = -INF
+            v[:, 9] = -INF if t == 0 else 1.0
+            v[:, 10] = INF if t == n - 1 else 1.0
+            v[:, 11] = INF if t == n // 2 else 1.0
+            v[:, 12] = float("nan") if t == n - 1 else 2.0
+            v[:, dim - 1] = INF if t == n - 1 else 1.0
+            _put(dev, ref, "v", b, t, v)
+    q = torch.zeros(len(lens), heads * 3, dim)
+    q[:, :, 0] = 1.0
+    q[:, 1::3, 1] = 0.5
+    out, want = _run(dev, q.to(TYPES[ctype]).cuda(), ref, 1.0, weights, 3)
+    o = want[0]
+    assert np.isposinf(o).any() and np.isneginf(o).any() and np.isnan(o).any()
+    assert np.array_equal(np.isnan(out), np.isnan(o))
+    assert np.array_equal(np.isposinf(out), np.isposinf(o))
+    assert np.array_equal(np.isneginf(out), np.isneginf(o))
+    fin = np.isfinite(o)
+    with np.errstate(invalid="ignore"):
+        tol = _bound(want, max(lens), dim, ctype)
+        bad = fin & (np.abs(out - o) > tol)
+    assert not bad.any()
+
+
+@pytest.mark.parametrize("ctype", ["bf16", "f16"])
+def test_attend_infinite_v_under_every_weight(ctype):
+    """Weights over the whole range, powers of two and others, each before an
+    infinity of its own column."""
+    n, dim = 128, 128
+    _, dev, ref = _case(8, [n], 1, dim, 16, ctype)
+    for t in range(n):
+        k = np.zeros((1, dim))
+        k[:, 0] = -t * 0.625
+        _put(dev, ref, "k", 0, t, k)
+        v = np.ones((1, dim))
+        v[:, t] = INF if t % 3 else -INF
+        _put(dev, ref, "v", 0, t, v)
+    q = torch.zeros(1, 4, dim)
+    # steps of 0.625 and 0.3 nats, of one and of half a power of two
+    q[0, :, 0] = torch.tensor([1.0, 0.5, 1.109375, 0.5546875])
+    out, want = _run(dev, q.to(TYPES[ctype]).cuda(), ref, 1.0, False, 3)
+    assert np.isinf(want[0]).all()
+    assert np.array_equal(out, want[0])

@@ -133,6 +133,24 @@ __device__ __forceinline__ int widen2(int v) {
         int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, HI));
 }
 
+// A weight (>= 0 or NaN) as the sum of three bfloat16 numbers, the upper
+// halves of p; 2^-22 of it is left.  Each but the last is the largest number
+// below what is left to hold, so that none is negative and none is 0 unless
+// the weight is: their products with an infinity of V add up to it.  (Rounded
+// parts are some instructions less, 150.6 us against 151.3 for 48 ragged
+// sequences, 111.6 against 112.2 for 8-bit rows, and give NaN there.)
+__device__ __forceinline__ void split3(float w, unsigned (&p)[3]) {
+  const unsigned u = __float_as_uint(w);
+  const unsigned least = u < 0x10000u ? u : 0x10000u;
+  p[0] = __builtin_elementwise_sub_sat(u, 1u);
+  const float r = w - __uint_as_float(p[0] & 0xffff0000u);
+  p[1] = __builtin_elementwise_sub_sat(__float_as_uint(r), 1u);
+  p[1] = p[1] > least ? p[1] : least;
+  const float s = fmaxf(r - __uint_as_float(p[1] & 0xffff0000u), 0.0f);
+  p[2] = __float_as_uint(s) + 0x8000u;
+  p[2] = p[2] > least ? p[2] : least;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
   return __builtin_amdgcn_exp2f(x);
 }
@@ -739,22 +757,19 @@ attend_kernel(AttendParams p) {
                 acc[1] = mma4(w[j], y1, acc[1]);
               }
         } else {
-          // A weight enters the product as three bfloat16 numbers, its
-          // rounding and what that and the next lost: 3 x 8 bits hold a
-          // float32 number, whose range bfloat16 has, so that out is rounded
-          // once, at the end.  (bfloat16 holds e4m3 rows exactly.)
+          // Weights enter the product as three bfloat16 numbers each (see
+          // split3), which has the range of float32: out is rounded once, at
+          // the end.  (bfloat16 holds e4m3 rows exactly.)
           Frag part[3];
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            float a0 = w[j], a1 = w[j + 1];
+            unsigned a[3], b[3];
+            split3(w[j], a);
+            split3(w[j + 1], b);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-              part[i].d[j / 2] = pack2<kBf16>(a0, a1);
-              float b0, b1;
-              unpack2<kBf16>(part[i].d[j / 2], &b0, &b1);
-              a0 -= b0;
-              a1 -= b1;
-            }
+            for (int i = 0; i < 3; ++i)
+              part[i].d[j / 2] =
+                  (int)__builtin_amdgcn_perm(b[i], a[i], 0x07060302u);
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
