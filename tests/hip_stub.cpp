@@ -1,0 +1,191 @@
+// A host without a GPU, for tests of what the C entry points of a call do on
+// the host: the HIP calls that libtopk.so makes, answered here (a symbol of
+// the program comes before the library's), with a log of the launches.
+//
+// usage: hip_stub <test>; prints what the test looks at.
+#include <hip/hip_runtime_api.h>
+
+#include <stdint.h>
+#include <stdio.h>
+#include <string.h>
+#include <unistd.h>
+
+#include <mutex>
+#include <string>
+#include <thread>
+#include <vector>
+
+#include "libtopk.h"
+
+struct Launch {
+  int thread, call;
+  dim3 grid, block;
+  size_t lds;
+};
+static std::mutex log_mu;
+static std::vector<Launch> launches;
+static thread_local int this_thread = 0, this_call = 0;
+static int pause_us = 0, fit = 1;
+static uintptr_t next_address = (uintptr_t)1 << 40;
+
+extern "C" {
+hipError_t hipGetDevice(int* d) { return *d = 0, hipSuccess; }
+hipError_t hipGetDeviceCount(int* n) { return *n = 1, hipSuccess; }
+hipError_t hipSetDevice(int) { return hipSuccess; }
+hipError_t hipDeviceSynchronize() { return hipSuccess; }
+hipError_t hipGetLastError() { return hipSuccess; }
+const char* hipGetErrorString(hipError_t) { return "stub"; }
+hipError_t hipFree(void*) { return hipSuccess; }
+hipError_t hipMalloc(void** p, size_t n) {
+  std::lock_guard<std::mutex> lock(log_mu);
+  *p = (void*)next_address;
+  next_address += (n + 4095) / 4096 * 4096;
+  return hipSuccess;
+}
+hipError_t hipDeviceGetAttribute(int* v, hipDeviceAttribute_t, int) {
+  return *v = 256, hipSuccess;
+}
+hipError_t hipStreamIsCapturing(hipStream_t, hipStreamCaptureStatus* s) {
+  return *s = hipStreamCaptureStatusNone, hipSuccess;
+}
+hipError_t hipOccupancyMaxActiveBlocksPerMultiprocessor(int* n, const void*,
+                                                        int, size_t) {
+  return *n = fit, hipSuccess;
+}
+// What kernel<<<grid, block, lds, stream>>>(...) becomes.
+struct Config {
+  dim3 grid, block;
+  size_t lds;
+  hipStream_t stream;
+};
+static thread_local Config config;
+hipError_t __hipPushCallConfiguration(dim3 grid, dim3 block, size_t lds,
+                                      hipStream_t s) {
+  config = {grid, block, lds, s};
+  return hipSuccess;
+}
+hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds,
+                                     hipStream_t* s) {
+  *grid = config.grid;
+  *block = config.block;
+  *lds = config.lds;
+  *s = config.stream;
+  return hipSuccess;
+}
+hipError_t hipLaunchKernel(const void*, dim3 grid, dim3 block, void**,
+                           size_t lds, hipStream_t) {
+  {
+    std::lock_guard<std::mutex> lock(log_mu);
+    launches.push_back({this_thread, this_call, grid, block, lds});
+  }
+  if (pause_us) usleep(pause_us);
+  return hipSuccess;
+}
+}
+
+// Addresses that are never dereferenced.
+static char* const kFake = (char*)0x10000000;
+template <class T>
+static T* fake(int i) {
+  return (T*)(kFake + (size_t)i * 0x40000000);
+}
+
+static libtopk_cache_t cache_of(int batch, int heads, int width, int dim) {
+  libtopk_cache_t c = {};
+  c.k = fake<char>(0);
+  c.v = fake<char>(64);
+  c.k_slot_stride = c.v_slot_stride = dim;
+  c.k_head_stride = c.v_head_stride = 16 * dim;
+  c.k_page_stride = c.v_page_stride = (int64_t)heads * 16 * dim;
+  c.pages = (int64_t)batch * width;
+  c.table_stride = width;
+  c.table = fake<int32_t>(128);
+  c.lens = fake<int32_t>(129);
+  c.batch = batch;
+  c.table_width = width;
+  c.heads = heads;
+  c.page = 16;
+  c.dim = dim;
+  c.dtype = LIBTOPK_BF16;
+  return c;
+}
+
+static libtopk_ledger_t ledger_of(int i, int heads, int slots) {
+  libtopk_ledger_t l = {};
+  l.weights = fake<float>(i);
+  l.positions = fake<int32_t>(i + 16);
+  l.weights_head_stride = l.positions_head_stride = slots;
+  l.weights_batch_stride = l.positions_batch_stride = (int64_t)heads * slots;
+  l.slots = slots;
+  return l;
+}
+
+static int attend(const libtopk_cache_t& c, int group,
+                  const libtopk_ledger_t* l, libtopk_stream_t s) {
+  return cache_attend(&c, fake<char>(130), LIBTOPK_BF16, c.heads * group,
+                      (int64_t)c.heads * group * c.dim, c.dim, 1.0f, nullptr,
+                      nullptr, l, fake<char>(132), fake<float>(134), s);
+}
+
+static int evict(const libtopk_cache_t& c, const libtopk_ledger_t& l,
+                 int keep, libtopk_stream_t s) {
+  const libtopk_ledger_t after = ledger_of(200, c.heads, keep);
+  return cache_evict(&c, fake<int32_t>(136), &l, keep, 0, 0, &after,
+                     fake<int32_t>(137), s);
+}
+
+static int append(const libtopk_cache_t& c, const libtopk_ledger_t& l,
+                  libtopk_stream_t s) {
+  return cache_append(&c, fake<char>(140), fake<char>(142),
+                      (int64_t)c.heads * c.dim, c.dim, 64, fake<int32_t>(136),
+                      &l, 0, 0, fake<int32_t>(137), fake<int32_t>(138), s);
+}
+
+// Threads that each make calls of several launches on one stream: are a
+// call's launches next to one another?
+static int threads_test() {
+  pause_us = 300;
+  const libtopk_cache_t c = cache_of(2, 4, 256, 64);  // 4096 slots a head
+  const libtopk_cache_t wide = cache_of(1, 2, 2048, 64);  // 32768
+  const libtopk_ledger_t l = ledger_of(160, 4, 4096);
+  const libtopk_ledger_t wl = ledger_of(160, 2, 32768);
+  std::vector<std::thread> t;
+  int failed = 0;
+  for (int i = 0; i < 3; ++i)
+    t.emplace_back([&, i] {
+      this_thread = i;
+      for (this_call = 0; this_call < 12; ++this_call) {
+        const int rc = i == 0   ? evict(c, l, 512, nullptr)
+                       : i == 1 ? evict(wide, wl, 512, nullptr)
+                                : attend(c, 16, &l, nullptr);
+        if (rc != LIBTOPK_OK) {
+          std::lock_guard<std::mutex> lock(log_mu);
+          ++failed;
+        }
+      }
+    });
+  for (std::thread& x : t) x.join();
+  int torn = 0, most = 0, run = 0;
+  std::vector<std::string> seen;
+  for (size_t i = 0; i < launches.size(); ++i) {
+    const Launch &a = launches[i];
+    const bool same = i > 0 && launches[i - 1].thread == a.thread &&
+                      launches[i - 1].call == a.call;
+    run = same ? run + 1 : 1;
+    most = run > most ? run : most;
+    if (same) continue;
+    const std::string id =
+        std::to_string(a.thread) + "." + std::to_string(a.call);
+    for (const std::string& x : seen) torn += x == id;
+    seen.push_back(id);
+  }
+  printf("failed %d torn %d calls %zu most %d\n", failed, torn, seen.size(),
+         most);
+  return 0;
+}
+
+int main(int n, char** a) {
+  const std::string what = n > 1 ? a[1] : "";
+  if (what == "threads") return threads_test();
+  return 2;
+}

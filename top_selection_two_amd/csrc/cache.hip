@@ -3,11 +3,9 @@
 // and launches.
 #include <hip/hip_runtime.h>
 
-#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <map>
-#include <memory>
 #include <mutex>
 #include <new>
 #include <utility>
@@ -38,10 +36,14 @@ struct Buffer {
   std::vector<void*> old;
 };
 
+// A call holds its area from here to its last launch: the launches of a call
+// hand results to one another in the area, and another thread's on the same
+// stream must not come between them.
 struct Area {
+  std::mutex mu;
   Buffer work;     // partial results, scores, lists: any contents
   Buffer tickets;  // completion tickets and nothing else (see Tagged)
-  std::shared_ptr<std::atomic<uint32_t>> epochs;
+  uint32_t epoch = 0;
 };
 
 std::mutex g_mu;
@@ -60,13 +62,6 @@ int current_device(int* dev) {
     return LIBTOPK_ERR_HIP;
   }
   return LIBTOPK_OK;
-}
-
-// The epoch of a new launch (never 0, which cleared words carry).
-uint32_t next_epoch(std::atomic<uint32_t>& c) {
-  uint32_t e = c.fetch_add(1u) + 1u;
-  while (e == 0u) e = c.fetch_add(1u) + 1u;
-  return e;
 }
 
 __global__ void fill_words(uint64_t* p, int64_t n, uint64_t seed) {
@@ -92,7 +87,7 @@ int fill(uint64_t* p, size_t words, uint64_t seed, hipStream_t s) {
   return launched("fill_words");
 }
 
-// Caller holds g_mu.
+// Caller holds the area.
 int grow(Buffer* b, size_t bytes, hipStream_t stream, bool clear) {
   if (b->bytes >= bytes) return LIBTOPK_OK;
   if (getenv("LIBTOPK_TEST_FAIL_ALLOC")) return LIBTOPK_ERR_NOMEM;
@@ -131,25 +126,32 @@ int grow(Buffer* b, size_t bytes, hipStream_t stream, bool clear) {
 }
 
 // Workspace of a call on `stream`: `bytes` of any contents, `tickets` words,
-// and the call's epoch.
+// and the call's epoch (never 0, which cleared words carry).
 struct Work {
   char* base;
   uint64_t* tickets;
+  size_t ticket_words;  // all there are
   uint32_t epoch;
+  std::unique_lock<std::mutex> hold;  // of the area, while this lives
 };
 
 int get_work(int dev, hipStream_t stream, size_t bytes, size_t tickets,
              Work* out) {
   try {
-    std::lock_guard<std::mutex> lock(g_mu);
-    Area& a = g_areas[std::make_pair(dev, (void*)stream)];
-    if (!a.epochs) a.epochs = std::make_shared<std::atomic<uint32_t>>(0u);
-    int rc = grow(&a.work, bytes, stream, false);
-    if (rc == LIBTOPK_OK) rc = grow(&a.tickets, tickets * 8, stream, true);
+    Area* a;
+    {
+      std::lock_guard<std::mutex> lock(g_mu);
+      a = &g_areas[std::make_pair(dev, (void*)stream)];  // stays where it is
+    }
+    out->hold = std::unique_lock<std::mutex>(a->mu);
+    int rc = grow(&a->work, bytes, stream, false);
+    if (rc == LIBTOPK_OK) rc = grow(&a->tickets, tickets * 8, stream, true);
     if (rc != LIBTOPK_OK) return rc;
-    out->base = a.work.base;
-    out->tickets = (uint64_t*)a.tickets.base;
-    out->epoch = next_epoch(*a.epochs);
+    if (++a->epoch == 0) ++a->epoch;
+    out->base = a->work.base;
+    out->tickets = (uint64_t*)a->tickets.base;
+    out->ticket_words = a->tickets.bytes / 8;
+    out->epoch = a->epoch;
     return LIBTOPK_OK;
   } catch (const std::bad_alloc&) {
     return LIBTOPK_ERR_NOMEM;
@@ -707,12 +709,7 @@ int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed) {
   Work work;
   rc = get_work(dev, (hipStream_t)stream, 1, 1, &work);
   if (rc != LIBTOPK_OK) return rc;
-  size_t words = 0;
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    words = g_areas[std::make_pair(dev, (void*)stream)].tickets.bytes / 8;
-  }
-  return fill(work.tickets, words, seed | 1u, (hipStream_t)stream);
+  return fill(work.tickets, work.ticket_words, seed | 1u, (hipStream_t)stream);
 }
 
 }  // extern "C"
