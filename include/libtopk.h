@@ -371,7 +371,8 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
  *    read nor write rows there.  Nothing outside the given arrays is ever
  *    read or written.
  *  - Pages that append or evict write to must belong to one sequence alone;
- *    attention may share them.
+ *    attention may share them.  For these two calls each axis of k, and of v,
+ *    steps over all that the axes within it span (no stride of 0).
  *
  * Workspace: per (device, stream), grown on demand by doubling; an area is
  * kept until cache_release() (or process exit) once it has been used, so a

@@ -6,6 +6,7 @@ import subprocess
 
 import pytest
 
+import test_cache_host as host
 import top_selection_two_amd as ltk
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,3 +40,39 @@ def test_a_call_s_launches_stay_together(stub):
     r = stub("threads")
     assert r["failed"] == 0 and r["torn"] == 0
     assert r["calls"] == 36 and r["most"] >= 7
+
+
+# 4 heads of 16 slots of 64 elements (k and v have 32 pages)
+@pytest.mark.parametrize("strides", [
+    (4096, 0, 64), (4096, 1024, 0), (0, 1024, 64), (2048, 1024, 64),
+    (4096, 1024, 32), (4096, 512, 64), (4096, 8, 64), (4096 - 64, 1024, 64),
+    (64, 64 * 32, 64 * 32)], ids=str)
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_append_and_evict_refuse_rows_that_overlap(name, strides):
+    kw = {name + "_%s_stride" % a: x
+          for a, x in zip(("page", "head", "slot"), strides)}
+    assert host._append(host._c(**kw)) == ltk.ERR_INVALID
+    assert host._evict(host._c(**kw)) == ltk.ERR_INVALID
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="a GPU is visible")
+@pytest.mark.parametrize("kw", [
+    # slots outside heads, and with padding
+    dict(k_head_stride=64, k_slot_stride=256),
+    dict(k_head_stride=72, k_slot_stride=296, k_page_stride=8192),
+    # pages inside heads
+    dict(k_page_stride=1024, k_head_stride=32 * 1024),
+    # an axis of one does not step at all
+    dict(heads=1, k_head_stride=0, v_head_stride=0),
+    dict(page=1, k_slot_stride=0, v_slot_stride=8),
+    dict(pages=1, k_page_stride=0, v_page_stride=0)], ids=str)
+def test_rows_that_lie_apart_are_taken(kw):
+    """(Without a device a valid call ends at the device.)"""
+    assert host._append(host._c(**kw)) == ltk.ERR_HIP
+    assert host._evict(host._c(**kw)) == ltk.ERR_HIP
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="a GPU is visible")
+def test_attend_reads_rows_that_overlap():
+    assert host._attend(host._c(k_head_stride=0, v_head_stride=0,
+                                v_page_stride=0)) == ltk.ERR_HIP

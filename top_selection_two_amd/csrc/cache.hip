@@ -237,10 +237,27 @@ int64_t span(const int64_t* n, const int64_t* s, int dims, int64_t row) {
 
 int elem_size(int dtype) { return dtype == LIBTOPK_E4M3 ? 1 : 2; }
 
+// Do the rows of an array (as for span, strides >= 0) lie apart: does each
+// axis, from the innermost on, step over all that the ones within it span?
+bool apart(const int64_t* n, const int64_t* s, int dims, int64_t row) {
+  int64_t all = row;
+  bool done[4] = {};
+  for (int k = 0; k < dims; ++k) {
+    int in = -1;
+    for (int i = 0; i < dims; ++i)
+      if (!done[i] && (in < 0 || s[i] < s[in])) in = i;
+    done[in] = true;
+    if (n[in] <= 1) continue;
+    if (s[in] < all) return false;
+    all += (n[in] - 1) * s[in];
+  }
+  return true;
+}
+
 // Checks a cache and fills in what the kernels take of it; `k` and `v` get
-// the arrays' extents.
-int check_cache(const libtopk_cache_t* c, CacheParams* p, Range* k, Range* v,
-                Range* table, Range* lens) {
+// the arrays' extents.  Rows that are written must not share a byte.
+int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
+                Range* k, Range* v, Range* table, Range* lens) {
   if (!c) return LIBTOPK_ERR_INVALID;
   if (c->dtype != LIBTOPK_BF16 && c->dtype != LIBTOPK_F16 &&
       c->dtype != LIBTOPK_E4M3)
@@ -269,6 +286,8 @@ int check_cache(const libtopk_cache_t* c, CacheParams* p, Range* k, Range* v,
   const int64_t klen = span(n, kb, 3, c->dim * es);
   const int64_t vlen = span(n, vb, 3, c->dim * es);
   if (klen < 0 || vlen < 0) return LIBTOPK_ERR_INVALID;
+  if (written && !(apart(n, kb, 3, c->dim * es) && apart(n, vb, 3, c->dim * es)))
+    return LIBTOPK_ERR_INVALID;
   if (c->pages > 0 && (!c->k || !c->v)) return LIBTOPK_ERR_INVALID;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return LIBTOPK_ERR_INVALID;
   if (c->batch > 0 && (!c->table || !c->lens)) return LIBTOPK_ERR_INVALID;
@@ -377,7 +396,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   AttendParams p = {};
   const Range none(nullptr, 0);
   Range k = none, v = none, table = none, lens = none, w = none, pos = none;
-  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  int rc = check_cache(cache, false, &p.c, &k, &v, &table, &lens);
   if (rc != LIBTOPK_OK) return rc;
   if (q_dtype != LIBTOPK_BF16 && q_dtype != LIBTOPK_F16)
     return LIBTOPK_ERR_INVALID;
@@ -529,7 +548,7 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
   SlotsParams p = {};
   const Range none(nullptr, 0);
   Range k = none, v = none, table = none, lens = none, w = none, pos = none;
-  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  int rc = check_cache(cache, true, &p.c, &k, &v, &table, &lens);
   if (rc != LIBTOPK_OK) return rc;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,
                     &pos);
@@ -589,7 +608,7 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   const Range none(nullptr, 0);
   Range k = none, v = none, table = none, lens = none, w = none, pos = none;
   Range w2 = none, pos2 = none;
-  int rc = check_cache(cache, &p.c, &k, &v, &table, &lens);
+  int rc = check_cache(cache, true, &p.c, &k, &v, &table, &lens);
   if (rc != LIBTOPK_OK) return rc;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, false, &p.w, &w,
                     &pos);
