@@ -489,7 +489,8 @@ int cache_attend(const libtopk_cache_t *cache, const void *q, int32_t q_dtype,
  *   out_lens   device, int32[batch]; may not be cache->lens
  *   out_slots  device, int32[batch][heads]
  *
- * Errors: as cache_attend.
+ * Errors: as cache_attend, and LIBTOPK_ERR_INVALID for 2^24 rows (batch *
+ * heads) or more.
  */
 int cache_append(const libtopk_cache_t *cache, const void *k_new,
                  const void *v_new, int64_t new_batch_stride,
@@ -509,13 +510,15 @@ int cache_append(const libtopk_cache_t *cache, const void *k_new,
  * weights and positions of `after` get the `keep` entries of every row
  * (entries past the new length: 0 and -1); out_lens[b] = min(lens[b], keep).
  * `ledger` is only read.  Two launches, seven when the table (or the ledger)
- * can name more than 16384 slots.
+ * can name more than 16384 slots, one when it can name no more than `keep`.
  *
  *   keep     1 <= keep <= after->slots
  *   after    device arrays that overlap neither the ledger nor each other
  *   out_lens device, int32[batch]; may not be cache->lens
  *
- * Errors: as cache_attend.
+ * Errors: as cache_attend, and LIBTOPK_ERR_INVALID for 2^22 rows (batch *
+ * heads) or more, where rows in the seven launches count once for every 4096
+ * slots that the table (or the ledger) can name.
  */
 int cache_evict(const libtopk_cache_t *cache, const int32_t *seen,
                 const libtopk_ledger_t *ledger, int32_t keep, int32_t sinks,

@@ -7,6 +7,7 @@
 
 #include <stdint.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 #include <unistd.h>
 
@@ -184,8 +185,49 @@ static int threads_test() {
   return 0;
 }
 
+// Batches of many rows: status and launches of each call, and the most
+// threads along an axis of a launch.
+static int many_rows_test(int batch, int heads, int width) {
+  const libtopk_cache_t c = cache_of(batch, heads, width, 16);
+  libtopk_ledger_t l = ledger_of(160, heads, width * 16);
+  // (arrays of so many rows span more than the fake addresses are apart)
+  l.weights = (float*)((uintptr_t)1 << 50);
+  l.positions = (int32_t*)((uintptr_t)1 << 51);
+  libtopk_cache_t big = c;
+  big.k = (void*)((uintptr_t)1 << 52);
+  big.v = (void*)((uintptr_t)1 << 53);
+  big.table = (int32_t*)((uintptr_t)1 << 54);
+  for (int i = 0; i < 2; ++i) {
+    launches.clear();
+    int rc;
+    if (i == 0) {
+      rc = cache_append(&big, (char*)((uintptr_t)1 << 55),
+                        (char*)((uintptr_t)1 << 56), (int64_t)heads * 16, 16,
+                        4, fake<int32_t>(136), &l, 0, 0, fake<int32_t>(138),
+                        (int32_t*)((uintptr_t)1 << 57), nullptr);
+    } else {
+      libtopk_ledger_t after = ledger_of(160, heads, 4);
+      after.weights = (float*)((uintptr_t)1 << 55);
+      after.positions = (int32_t*)((uintptr_t)1 << 56);
+      rc = cache_evict(&big, fake<int32_t>(136), &l, 4, 0, 0, &after,
+                       fake<int32_t>(138), nullptr);
+    }
+    uint64_t threads = 0;
+    for (const Launch& x : launches) {
+      const uint64_t t = (uint64_t)x.grid.x * x.block.x;
+      threads = t > threads ? t : threads;
+    }
+    const char* name = i ? "evict" : "append";
+    printf("%s %d %s_launches %zu %s_wide %d\n", name, rc, name,
+           launches.size(), name, threads >> 32 != 0);
+  }
+  return 0;
+}
+
 int main(int n, char** a) {
   const std::string what = n > 1 ? a[1] : "";
   if (what == "threads") return threads_test();
+  if (what == "rows" && n > 4)
+    return many_rows_test(atoi(a[2]), atoi(a[3]), atoi(a[4]));
   return 2;
 }

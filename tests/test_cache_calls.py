@@ -76,3 +76,20 @@ def test_rows_that_lie_apart_are_taken(kw):
 def test_attend_reads_rows_that_overlap():
     assert host._attend(host._c(k_head_stride=0, v_head_stride=0,
                                 v_page_stride=0)) == ltk.ERR_HIP
+
+
+def test_launches_of_too_many_threads_are_refused(stub):
+    """2^32 threads or more along an axis cannot be launched: such calls are
+    refused before anything is."""
+    for batch, heads, width, append, evict in (
+            (1 << 12, 1 << 10, 1, 0, 1),          # 2^22 rows
+            ((1 << 22) - 1, 1, 1, 0, 0),
+            (1 << 14, 1 << 10, 1, 1, 1),          # 2^24 rows
+            ((1 << 24) - 1, 1, 1, 0, 1),
+            (1 << 19, 1, 2048, 0, 1),             # of 8 chunks each
+            ((1 << 19) - 1, 1, 2048, 0, 0)):
+        r = stub("rows", str(batch), str(heads), str(width))
+        assert (r["append"], r["evict"]) == (append, evict), (batch, r)
+        assert r["append_wide"] == r["evict_wide"] == 0, (batch, r)
+        for name in ("append", "evict"):
+            assert (r[name + "_launches"] == 0) == (r[name] != 0), (batch, r)

@@ -382,6 +382,12 @@ constexpr int kMinTiles = 24;
 static_assert(kBins % 2 == 0 && kBins == 2 * kEvThreads,
               "a thread searches two bins");
 
+// Can this many workgroups be launched along an axis?  (Fewer than 2^32
+// threads can.)
+bool launchable(int64_t groups, int threads) {
+  return groups <= (int64_t)(UINT32_MAX / (uint32_t)threads);
+}
+
 size_t round_up(size_t n, size_t to) { return (n + to - 1) / to * to; }
 
 }  // namespace
@@ -571,6 +577,7 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
   const int64_t nlen = span(nn, ns, 2, (int64_t)cache->dim * es);
   if (nlen < 0) return LIBTOPK_ERR_INVALID;
   const int64_t rows = (int64_t)cache->batch * cache->heads;
+  if (!launchable(rows, kBlock)) return LIBTOPK_ERR_INVALID;
   const Range outs[6] = {Range(out_lens, (int64_t)cache->batch * 4),
                          Range(out_slots, rows * 4), w, pos, k, v};
   const Range ins[5] = {Range(k_new, nlen), Range(v_new, nlen), table, lens,
@@ -644,20 +651,20 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   // Moves of a row: at most the kept slots, and at most the slots beyond.
   p.pair_cap = p.c.cap > keep ? (p.c.cap - keep < keep ? p.c.cap - keep : keep)
                               : 0;
+  const bool is_long = p.pair_cap > 0 && p.c.cap > kShortSlots;
+  p.chunks = is_long ? (p.c.cap + kChunkSlots - 1) / kChunkSlots : 1;
+  if (!launchable(rows * p.chunks, kEvThreads)) return LIBTOPK_ERR_INVALID;
+  p.row_units = make_divisor(p.c.row_bytes / 16);
+  if ((int64_t)p.pair_cap * p.row_units.d > INT32_MAX - kBlock)
+    return LIBTOPK_ERR_INVALID;
   int dev = 0;
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  const bool is_long = p.c.cap > kShortSlots;
-  p.chunks = is_long ? (p.c.cap + kChunkSlots - 1) / kChunkSlots : 1;
-  if (rows > INT32_MAX / p.chunks) return LIBTOPK_ERR_INVALID;
   if (p.pair_cap == 0) {  // every row is short enough as it is
     return launch((const void*)&evict_short_kernel<1>, dim3((unsigned)rows),
                   kEvThreads, p, s);
   }
-  p.row_units = make_divisor(p.c.row_bytes / 16);
-  if ((int64_t)p.pair_cap * p.row_units.d > INT32_MAX - kBlock)
-    return LIBTOPK_ERR_INVALID;
   const size_t pair_bytes = round_up((size_t)rows * p.pair_cap * 8, 256);
   const size_t move_bytes = round_up((size_t)rows * 4, 256);
   const size_t hist_words = is_long ? (size_t)rows * 3 * kBins / 2 : 0;
