@@ -224,10 +224,31 @@ static int many_rows_test(int batch, int heads, int width) {
   return 0;
 }
 
+// LDS that attention with weights asks for, when the device says that `per_cu`
+// workgroups fit a compute unit.
+static int lds_test(int dim, bool slots_first, int per_cu) {
+  fit = per_cu;
+  libtopk_cache_t c = cache_of(8, 4, 1024, dim);
+  if (slots_first) {
+    c.k_head_stride = c.v_head_stride = dim;
+    c.k_slot_stride = c.v_slot_stride = 4 * dim;
+  }
+  const libtopk_ledger_t l = ledger_of(160, 4, 16384);
+  const int rc = attend(c, 16, &l, nullptr);
+  const Launch* a = &launches[0];  // the one that takes LDS at the launch
+  for (const Launch& x : launches)
+    if (x.lds > a->lds) a = &x;
+  printf("rc %d lds %zu threads %u groups %u\n", rc, a->lds, a->block.x,
+         a->grid.x);
+  return 0;
+}
+
 int main(int n, char** a) {
   const std::string what = n > 1 ? a[1] : "";
   if (what == "threads") return threads_test();
   if (what == "rows" && n > 4)
     return many_rows_test(atoi(a[2]), atoi(a[3]), atoi(a[4]));
+  if (what == "lds" && n > 4)
+    return lds_test(atoi(a[2]), atoi(a[3]) != 0, atoi(a[4]));
   return 2;
 }

@@ -93,3 +93,19 @@ def test_launches_of_too_many_threads_are_refused(stub):
         assert r["append_wide"] == r["evict_wide"] == 0, (batch, r)
         for name in ("append", "evict"):
             assert (r[name + "_launches"] == 0) == (r[name] != 0), (batch, r)
+
+
+@pytest.mark.parametrize("fit", [1, 2, 3, 4, 5, 8])
+@pytest.mark.parametrize("dim,cols,waves", [
+    (64, 64, 8), (96, 128, 8), (128, 128, 8), (192, 256, 4), (256, 256, 4)])
+def test_attention_has_room_for_scores(stub, dim, cols, waves, fit):
+    """However many workgroups the device would hold at once, each gets room
+    for the waves' results of 16 queries and the scores of a tile at least (of
+    32 slots, and of 4 heads where slots lie outside heads): with none the
+    kernel would not advance."""
+    for slots_first in (0, 1):
+        r = stub("lds", str(dim), str(slots_first), str(fit))
+        tile = 32 * 16 * 4 * (4 if slots_first else 1)
+        assert r["rc"] == 0 and r["threads"] == 64 * waves
+        join = waves * 16 * cols * 4
+        assert join + tile <= r["lds"] <= 160 * 1024, (slots_first, r)

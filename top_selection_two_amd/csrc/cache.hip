@@ -369,7 +369,6 @@ const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
 }
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
-constexpr int kLdsBytes = 160 * 1024;
 // Rows of at most this many scores are joined and get their weights from
 // their last workgroup, longer ones from a second launch.  (211 slots of 8
 // heads of 4 queries: 9.5 us in one launch, 11.2 in two; 16 sequences of 5000
@@ -478,6 +477,19 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   int fit = 0;
   rc = resident(fn, needs.threads, &fit);
   if (rc != LIBTOPK_OK) return rc;
+  p.part_rows = p.group < 16 ? p.group : 16;
+  p.lds_rows = (p.part_rows + 3) / 4 * 4;
+  const int waves = needs.threads / kWave;
+  int join = waves * p.lds_rows * needs.cols;
+  if (join < needs.join) join = needs.join;
+  size_t lds = (size_t)join * 4;
+  const size_t tile_bytes = (size_t)kTileSlots * p.hs * p.part_rows * 4;
+  // Workgroups that share a unit share its LDS: with a ledger each needs room
+  // for the scores of a tile (one alone has it, see kScoresFit).
+  const int64_t fixed = needs.lds + 256 + (int64_t)lds;
+  while (ledger && fit > 1 &&
+         kLdsBytes / fit < fixed + (int64_t)tile_bytes)
+    --fit;
   const int64_t slots = (int64_t)fit * dev_units < kMaxRuns
                             ? (int64_t)fit * dev_units
                             : kMaxRuns;
@@ -495,15 +507,8 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
     return LIBTOPK_ERR_INVALID;
   int64_t grid = att_rows * tiles;
   if (grid > slots) grid = slots;
-  p.part_rows = p.group < 16 ? p.group : 16;
-  p.lds_rows = (p.part_rows + 3) / 4 * 4;
   const size_t part_bytes = round_up(
       (size_t)grid * 2 * p.hs * p.part_rows * (needs.cols + 2) * 4, 256);
-  const int waves = needs.threads / kWave;
-  int join = waves * p.lds_rows * needs.cols;
-  if (join < needs.join) join = needs.join;
-  size_t lds = (size_t)join * 4;
-  const size_t tile_bytes = (size_t)kTileSlots * p.hs * p.part_rows * 4;
   size_t score_bytes = 0, share_bytes = 0;
   if (ledger) {
     p.row_tiles = (int32_t)tiles;
@@ -514,8 +519,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
     // no more than the longest run.
     int64_t run = (att_rows * (tiles + p.row_cost) + grid - 1) / grid;
     if (run < p.min_tiles) run = p.min_tiles;
-    int64_t room = (kLdsBytes / fit - needs.lds - 256 - (int64_t)lds) /
-                   (int64_t)tile_bytes;
+    int64_t room = (kLdsBytes / fit - fixed) / (int64_t)tile_bytes;
     if (room > run) room = run;
     p.held_tiles = (int32_t)room;
     lds += (size_t)room * tile_bytes;

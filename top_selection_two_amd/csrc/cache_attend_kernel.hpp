@@ -35,6 +35,7 @@ namespace ltk {
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr int kTileSlots = 32;  // of one wave
 constexpr int kHeadRun = 4;
+constexpr int kLdsBytes = 160 * 1024;  // of a compute unit
 
 // What attend_kernel leaves to attend_join_kernel of a row: the workgroups
 // that share it, or one of these.
@@ -268,6 +269,13 @@ struct Attend {
     int32_t b;
     int32_t flag;
   };
+  // A workgroup alone on a unit has room for the scores of a tile (with 256
+  // bytes for the allocation's steps).
+  static constexpr bool kScoresFit =
+      (int)sizeof(Lds) + 256 + 4 * (WAVES * 16 * COLS) +
+          4 * (kHeadRun * 16 * kTileSlots) <=
+      kLdsBytes;
+  static_assert(kScoresFit && JOIN <= WAVES * 16 * COLS);
 };
 
 // Pages of tile `t`'s slots.  Slots past the length repeat the last one;
