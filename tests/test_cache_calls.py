@@ -1,6 +1,7 @@
 """What the cache_* entry points do on the host: a program of its own with
 HIP's calls answered by a stub (hip_stub.cpp), so that no GPU is needed and
 every launch is seen."""
+import ctypes
 import os
 import subprocess
 
@@ -109,3 +110,20 @@ def test_attention_has_room_for_scores(stub, dim, cols, waves, fit):
         assert r["rc"] == 0 and r["threads"] == 64 * waves
         join = waves * 16 * cols * 4
         assert join + tile <= r["lds"] <= 160 * 1024, (slots_first, r)
+
+
+def test_shares_lie_in_whole_vectors(tmp_path):
+    """Results of shares follow one another in units of 16 bytes, in which
+    they are read, also those of an odd number of queries."""
+    src, so = str(tmp_path / "share.cpp"), str(tmp_path / "share.so")
+    with open(src, "w") as f:
+        f.write('#include "cache_layout.hpp"\nextern "C" int floats(int rows, '
+                'int cols) { return ltk::share_floats(rows, cols); }\n')
+    subprocess.check_call(["g++", "-std=c++17", "-shared", "-fPIC", "-I",
+                           host.CSRC, src, "-o", so])
+    floats = ctypes.CDLL(so).floats
+    for cols in (64, 128, 256):
+        for rows in range(1, 65):
+            need = rows * (cols + 2)
+            assert floats(rows, cols) % 4 == 0
+            assert need <= floats(rows, cols) < need + 4

@@ -508,7 +508,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   int64_t grid = att_rows * tiles;
   if (grid > slots) grid = slots;
   const size_t part_bytes = round_up(
-      (size_t)grid * 2 * p.hs * p.part_rows * (needs.cols + 2) * 4, 256);
+      (size_t)grid * 2 * share_floats(p.hs * p.part_rows, needs.cols) * 4, 256);
   size_t score_bytes = 0, share_bytes = 0;
   if (ledger) {
     p.row_tiles = (int32_t)tiles;

@@ -63,7 +63,7 @@ struct AttendParams {
                         // weights; otherwise attend_join_kernel does
   int32_t cols;         // columns of a share's result
   int32_t q_type;
-  float* part;          // [grid][2][part_rows * columns + 2 * part_rows]
+  float* part;          // [grid][2][share_floats]: sums, maxima, weights' sums
   int32_t part_rows;    // queries of a row, at most 16
   int32_t min_tiles;    // least share of a row
   int32_t row_cost;     // what a row costs besides its tiles, in tiles
@@ -829,7 +829,7 @@ attend_kernel(AttendParams p) {
     // Bytes of a share's result, and where this one lies: a workgroup can
     // have a row's end and, last, another's beginning.
     const int32_t part_rows = HS * p.part_rows;
-    const int32_t part_size = part_rows * (COLS + 2) * 4;
+    const int32_t part_size = share_floats(part_rows, COLS) * 4;
     const int32_t part = (wg * 2 + (s0 == r0)) * part_size;
     const int32_t at_m = part_rows * COLS * 4, at_l = at_m + part_rows * 4;
     const __amdgpu_buffer_rsrc_t parts = __builtin_amdgcn_make_buffer_rsrc(

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(kBlock) void attend_join_kernel(AttendParams p) {
   const int32_t i = blockIdx.x * kBlock + tid, t = i / 8;
   const int head_floats = p.part_rows * kTileSlots;
   const int part_rows = p.hs * p.part_rows;
-  const int64_t part_size = (int64_t)part_rows * (p.cols + 2);  // floats
+  const int64_t part_size = share_floats(part_rows, p.cols);
   const int vecs_of_row = p.cols / 4;
   for (int row = blockIdx.y; row < c.batch * c.heads; row += gridDim.y) {
     const int b = row / c.heads, h = row % c.heads, hsub = h % p.hs;

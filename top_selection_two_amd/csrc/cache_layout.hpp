@@ -49,6 +49,13 @@ constexpr int64_t row_offset(const RowStrides& s, int32_t id, int32_t head,
          (int64_t)place * s.slot;
 }
 
+// Floats of a share's result of an attention row: `cols` sums, a maximum and a
+// weight's sum for each of `rows` queries, in whole 16-byte units, in which
+// the next share's result is read too.
+constexpr int32_t share_floats(int32_t rows, int32_t cols) {
+  return (rows * (cols + 2) + 3) / 4 * 4;
+}
+
 // The largest key: protected slots.
 constexpr int32_t kKeySafe = 0x7fffffff;
 
