@@ -15,3 +15,14 @@ def test_attend_long_rows_of_odd_groups(group, n, dim):
     print("attend odd group", group, n, dim, flush=True)
     t._attend(dev, t._q(rng, 2, group, dim, "bf16"), ref, "bf16", "bf16",
               rng=rng)
+
+
+@pytest.mark.parametrize("lens,keep,extra", [
+    ([2000, 0, 1, 1024], 2000, 80), ([500, 20000, 3000, 4096], 4096, 1),
+    ([100, 90], 64, 80)])
+@pytest.mark.parametrize("kind", ["plain", "special"])
+def test_evict_short_rows_in_a_wide_table(lens, keep, extra, kind):
+    """Rows of at most `keep` slots, and short rows that are cut, where the
+    table can name more slots than one workgroup selects from."""
+    print("evict in a wide table", lens, keep, kind, flush=True)
+    t._check_evict(lens, 2, 8, 256, keep, 4, 20, kind, extra=extra)
