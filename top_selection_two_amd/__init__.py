@@ -534,7 +534,11 @@ def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
     factors of the rows.  weights float32 [B, H, slots] gets each slot's
     attention weights, summed over the Hq / H queries of its head, added in
     place.  Returns (out [B, Hq, D] of q's type, lse float32 [B, Hq]); out
-    may be given as that pair of tensors."""
+    may be given as that pair of tensors.
+
+    There is no backward pass: with inputs that require gradients, a gradient
+    through the outputs is an error (through outputs given as `out` there is
+    none)."""
     return _binding.attend(q, k, v, table, lens, scale, weights, k_scale,
                            v_scale, out)
 
@@ -547,7 +551,8 @@ def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
     accumulated weight that is not protected (position < sinks or
     >= seen[b] - recent).  weights float32 and positions int32
     [B, H, slots] are updated in place, as k and v are; seen int32 [B] is the
-    new token's position.  Returns (lens [B], slots [B, H]), int32."""
+    new token's position.  Returns (lens [B], slots [B, H]), int32.  No
+    gradient passes through the rows written."""
     return _binding.append(k_new, v_new, k, v, table, lens, limit, seen,
                            weights, positions, sinks, recent)
 
@@ -558,6 +563,7 @@ def cache_evict(k, v, table, lens, seen, weights, positions, keep, sinks=0,
     accumulated weight, protected ones first (see cache_evict in
     include/libtopk.h); rows move within k and v.  Returns (weights
     [B, H, keep], positions [B, H, keep], lens [B]); out may be given as a
-    pair of tensors for the first two (they overlap no input)."""
+    pair of tensors for the first two (they overlap no input).  No gradient
+    passes through the rows moved."""
     return _binding.evict(k, v, table, lens, seen, weights, positions, keep,
                           sinks, recent, out)

@@ -5,6 +5,8 @@
 // In C++ because these calls are made once a layer and token: the same checks
 // through Python attributes and ctypes took 20 us a call, several times what
 // the kernels of a short sequence take.
+#include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
@@ -74,7 +76,7 @@ void expect_unit(const Tensor& x, const char* name) {
     value_error(std::string(name) + ": expected unit stride in the last axis");
 }
 
-int64_t stride(const Tensor& x, int64_t i) {
+int64_t step_of(const Tensor& x, int64_t i) {
   return x.size(i) > 1 ? x.stride(i) : 0;
 }
 
@@ -139,14 +141,14 @@ Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
   libtopk_cache_t& c = r.c;
   c.k = pointer(k);
   c.v = pointer(v);
-  c.k_page_stride = stride(k, 0);
-  c.k_head_stride = stride(k, 1);
-  c.k_slot_stride = stride(k, 2);
-  c.v_page_stride = stride(v, 0);
-  c.v_head_stride = stride(v, 1);
-  c.v_slot_stride = stride(v, 2);
+  c.k_page_stride = step_of(k, 0);
+  c.k_head_stride = step_of(k, 1);
+  c.k_slot_stride = step_of(k, 2);
+  c.v_page_stride = step_of(v, 0);
+  c.v_head_stride = step_of(v, 1);
+  c.v_slot_stride = step_of(v, 2);
   c.pages = k.size(0);
-  c.table_stride = stride(table, 0);
+  c.table_stride = step_of(table, 0);
   c.table = (const int32_t*)pointer(table);
   c.lens = (const int32_t*)pointer(lens);
   for (int64_t n : {table.size(0), table.size(1), k.size(1), k.size(2)})
@@ -180,8 +182,8 @@ libtopk_ledger_t ledger(const Cache& r, PyObject* wo, const char* wname,
     if (slots < 1 || slots > INT32_MAX)
       value_error(std::string(name) + ": expected 1 .. 2^31 - 1 slots");
     expect_unit(x, name);
-    (i ? l.positions_batch_stride : l.weights_batch_stride) = stride(x, 0);
-    (i ? l.positions_head_stride : l.weights_head_stride) = stride(x, 1);
+    (i ? l.positions_batch_stride : l.weights_batch_stride) = step_of(x, 0);
+    (i ? l.positions_head_stride : l.weights_head_stride) = step_of(x, 1);
     if (i)
       l.positions = (int32_t*)pointer(x);
     else
@@ -217,6 +219,12 @@ void check(int rc, const char* name) {
     PyErr_Format(PyExc_RuntimeError, "%s failed (status %d)", name, rc);
   }
   throw PythonError{};
+}
+
+// A tensor that a call has changed: gradients that need what it held are
+// refused from here on.  (Inference tensors count no changes.)
+void changed(const Tensor& x) {
+  if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
 }
 
 void expect_args(Py_ssize_t n, Py_ssize_t want) {
@@ -278,10 +286,31 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n) {
   const c10::DeviceGuard guard(r.device);
   check(cache_attend(&r.c, pointer(q),
                      t == at::kBFloat16 ? LIBTOPK_BF16 : LIBTOPK_F16,
-                     (int32_t)heads, stride(q, 0), stride(q, 1), (float)scale,
+                     (int32_t)heads, step_of(q, 0), step_of(q, 1), (float)scale,
                      scales[0], scales[1], weights ? &l : nullptr,
                      pointer(out), (float*)pointer(lse), stream),
         "cache_attend");
+  if (weights) changed(tensor(a[6], "weights"));
+  if (a[9] != Py_None) {
+    changed(out);
+    changed(lse);
+  } else if (at::GradMode::is_enabled()) {
+    // There is no backward pass: one that is asked for is an error, and not a
+    // gradient of zero.
+    torch::autograd::edge_list edges;
+    for (int i : {0, 1, 2, 6, 7, 8}) {
+      if (a[i] == Py_None) continue;
+      const Tensor& x = tensor(a[i], "");
+      if (x.requires_grad())
+        edges.push_back(torch::autograd::impl::gradient_edge(x));
+    }
+    if (!edges.empty()) {
+      const auto node = std::make_shared<torch::autograd::NotImplemented>(
+          "cache_attend", std::move(edges));
+      torch::autograd::set_history(out, node);
+      torch::autograd::set_history(lse, node);
+    }
+  }
   PyObject* o = THPVariable_Wrap(std::move(out));
   PyObject* z = THPVariable_Wrap(std::move(lse));
   return Py_BuildValue("(NN)", o, z);
@@ -305,7 +334,7 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
     expect_unit(*both[i], name);
   }
   for (int i = 0; i < 2; ++i)
-    if (stride(kn, i) != stride(vn, i))
+    if (step_of(kn, i) != step_of(vn, i))
       value_error("k_new and v_new: expected the same strides");
   const Tensor& seen = tensor(a[7], "seen");
   expect(seen, "seen", at::kInt, {r.c.batch}, r.device);
@@ -313,11 +342,12 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   Tensor lens = at::empty({r.c.batch}, seen.options());
   Tensor slots = at::empty({r.c.batch, r.c.heads}, seen.options());
   const c10::DeviceGuard guard(r.device);
-  check(cache_append(&r.c, pointer(kn), pointer(vn), stride(kn, 0),
-                     stride(kn, 1), limit, (const int32_t*)pointer(seen), &l,
+  check(cache_append(&r.c, pointer(kn), pointer(vn), step_of(kn, 0),
+                     step_of(kn, 1), limit, (const int32_t*)pointer(seen), &l,
                      sinks, recent, (int32_t*)pointer(lens),
                      (int32_t*)pointer(slots), stream),
         "cache_append");
+  for (int i : {2, 3, 8, 9}) changed(tensor(a[i], ""));
   PyObject* x = THPVariable_Wrap(std::move(lens));
   PyObject* y = THPVariable_Wrap(std::move(slots));
   return Py_BuildValue("(NN)", x, y);
@@ -349,8 +379,8 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
     pos = at::empty({r.c.batch, r.c.heads, keep}, seen.options());
     w = at::empty({r.c.batch, r.c.heads, keep},
                   seen.options().dtype(at::kFloat));
-    after = {(float*)pointer(w), (int32_t*)pointer(pos), stride(w, 0),
-             stride(w, 1), stride(pos, 0), stride(pos, 1), keep};
+    after = {(float*)pointer(w), (int32_t*)pointer(pos), step_of(w, 0),
+             step_of(w, 1), step_of(pos, 0), step_of(pos, 1), keep};
   } else {
     w = THPVariable_Unpack(PyTuple_GET_ITEM(a[10], 0));
     pos = THPVariable_Unpack(PyTuple_GET_ITEM(a[10], 1));
@@ -360,6 +390,11 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   check(cache_evict(&r.c, (const int32_t*)pointer(seen), &l, keep, sinks,
                     recent, &after, (int32_t*)pointer(lens), stream),
         "cache_evict");
+  for (int i : {0, 1}) changed(tensor(a[i], ""));
+  if (a[10] != Py_None) {
+    changed(w);
+    changed(pos);
+  }
   PyObject* x = THPVariable_Wrap(std::move(w));
   PyObject* y = THPVariable_Wrap(std::move(pos));
   PyObject* z = THPVariable_Wrap(std::move(lens));
