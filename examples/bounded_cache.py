@@ -49,7 +49,7 @@ def decode(batch, heads, group, dim, prompt, budget, tokens):
         return torch.randn(batch, heads * group, dim, generator=g,
                            device=dev).to(torch.bfloat16)
 
-    # the last prompt tokens' attention says which slots matter
+    # the last prompt tokens' attention, a call each, says which slots matter
     for _ in range(4):
         ltk.cache_attend(query(), k, v, table, lens, weights=weights)
     weights, positions, lens = ltk.cache_evict(

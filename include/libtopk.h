@@ -432,9 +432,18 @@ typedef struct libtopk_ledger {
  *     out[b][j] = v_scale[h] * sum_t exp(x[j][t] - lse[b][j]) V[b][h][t]
  *     weights[b][h][t] += sum_{j of h} exp(x[j][t] - lse[b][j])
  *
- * A sequence with no slot gets out = 0 and lse = -infinity.  Scores, sums and
- * the running output are float32; only out is rounded, once.  Results do not
- * depend on the order in which workgroups run.
+ * A sequence with no slot gets out = 0 and lse = -infinity.  Scores, weights,
+ * sums and the running output are float32 (the weights that multiply bfloat16
+ * and 8-bit rows to 2^-22); only out is rounded, once.  Results do not depend
+ * on the order in which workgroups run.
+ *
+ * Every weight counts that float32 can hold next to the largest (scores down
+ * to 87 below it); an infinite V element under one makes its column infinite
+ * (NaN with one of the other sign, or a NaN).  Before the division by their
+ * sum weights reach up to 2^8, so that V elements beyond 2^119 / len can
+ * overflow.  A sequence has one query token; the weights that a prompt's
+ * slots have drawn come from a call a token, or from the caller's own
+ * attention over the prompt.
  *
  *   q        device, q_dtype (LIBTOPK_BF16 or LIBTOPK_F16; the cache's own,
  *            or either over an LIBTOPK_E4M3 cache), 16-byte aligned, element
@@ -447,9 +456,12 @@ typedef struct libtopk_ledger {
  *   lse      device, float32[batch][q_heads], contiguous
  *
  * Workspace: partial results of at most 1024 workgroups, and with a ledger
- * one float32 a query head and slot of the table's width (rounded up to 32).
+ * one float32 a query head and slot of the table's width (rounded up to 32):
+ * 4.3 GB for 256 sequences of 32 query heads and a table of 131072 slots.
  * One launch, or two with a ledger and long rows (more than 32768 scores a
- * row) or more than 16 queries a head.
+ * row) or more than 16 queries a head.  Lengths being on the device, a row
+ * counts as long as the table (or the ledger) lets it be: a table no wider
+ * than needed is faster, here and in cache_evict.
  *
  * Errors: LIBTOPK_ERR_INVALID for a NULL or misaligned pointer, a size,
  * stride or type outside the above, outputs that overlap an input, or more

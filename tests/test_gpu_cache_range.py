@@ -211,3 +211,27 @@ def test_attend_infinite_v_under_every_weight(ctype):
     out, want = _run(dev, q.to(TYPES[ctype]).cuda(), ref, 1.0, False, 3)
     assert np.isinf(want[0]).all()
     assert np.array_equal(out, want[0])
+
+
+@pytest.mark.parametrize("ctype", ["bf16", "f16"])
+def test_attend_infinite_v_in_joined_rows(ctype):
+    """Long rows with weights, whose shares the second launch joins."""
+    lens, dim = [12000, 7001], 64
+    rng, dev, ref = _case(9, lens, 1, dim, 16, ctype)
+    print("infinite v, joined", ctype, flush=True)
+    for b, n in enumerate(lens):
+        for i, t in enumerate((0, 31, n // 2, n - 1)):
+            v = rng.standard_normal((1, dim))
+            v[:, 5 + i] = -INF if i % 2 else INF
+            v[:, 20] = INF
+            v[:, 21] = -INF if i == 2 else INF
+            _put(dev, ref, "v", b, t, v)
+    q = torch.from_numpy(rng.standard_normal((2, 5, dim)).astype(np.float32))
+    out, want = _run(dev, q.to(TYPES[ctype]).cuda(), ref, dim ** -0.5, True, 3)
+    o = want[0]
+    for f in (np.isnan, np.isposinf, np.isneginf):
+        assert f(o).any() and np.array_equal(f(out), f(o))
+    fin = np.isfinite(o)
+    with np.errstate(invalid="ignore"):
+        bad = fin & (np.abs(out - o) > _bound(want, max(lens), dim, ctype))
+    assert not bad.any()
