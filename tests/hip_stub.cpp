@@ -34,6 +34,7 @@ hipError_t hipGetDevice(int* d) { return *d = 0, hipSuccess; }
 hipError_t hipGetDeviceCount(int* n) { return *n = 1, hipSuccess; }
 hipError_t hipSetDevice(int) { return hipSuccess; }
 hipError_t hipDeviceSynchronize() { return hipSuccess; }
+hipError_t hipStreamSynchronize(hipStream_t) { return hipSuccess; }
 hipError_t hipGetLastError() { return hipSuccess; }
 const char* hipGetErrorString(hipError_t) { return "stub"; }
 hipError_t hipFree(void*) { return hipSuccess; }
@@ -142,27 +143,20 @@ static int append(const libtopk_cache_t& c, const libtopk_ledger_t& l,
                       &l, 0, 0, fake<int32_t>(137), fake<int32_t>(138), s);
 }
 
-// Threads that each make calls of several launches on one stream: are a
-// call's launches next to one another?
-static int threads_test() {
+// Threads that each make calls on one stream, `call(thread)`: are a call's
+// launches next to one another?
+template <class F>
+static int threads_test(int threads, F call) {
   pause_us = 300;
-  const libtopk_cache_t c = cache_of(2, 4, 256, 64);  // 4096 slots a head
-  const libtopk_cache_t wide = cache_of(1, 2, 2048, 64);  // 32768
-  const libtopk_ledger_t l = ledger_of(160, 4, 4096);
-  const libtopk_ledger_t wl = ledger_of(160, 2, 32768);
   std::vector<std::thread> t;
   int failed = 0;
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < threads; ++i)
     t.emplace_back([&, i] {
       this_thread = i;
       for (this_call = 0; this_call < 12; ++this_call) {
-        const int rc = i == 0   ? evict(c, l, 512, nullptr)
-                       : i == 1 ? evict(wide, wl, 512, nullptr)
-                                : attend(c, 16, &l, nullptr);
-        if (rc != LIBTOPK_OK) {
-          std::lock_guard<std::mutex> lock(log_mu);
-          ++failed;
-        }
+        if (call(i) == LIBTOPK_OK) continue;
+        std::lock_guard<std::mutex> lock(log_mu);
+        ++failed;
       }
     });
   for (std::thread& x : t) x.join();
@@ -183,6 +177,34 @@ static int threads_test() {
   printf("failed %d torn %d calls %zu most %d\n", failed, torn, seen.size(),
          most);
   return 0;
+}
+
+static int cache_threads_test() {
+  const libtopk_cache_t c = cache_of(2, 4, 256, 64);  // 4096 slots a head
+  const libtopk_cache_t wide = cache_of(1, 2, 2048, 64);  // 32768
+  const libtopk_ledger_t l = ledger_of(160, 4, 4096);
+  const libtopk_ledger_t wl = ledger_of(160, 2, 32768);
+  return threads_test(3, [&](int i) {
+    return i == 0   ? evict(c, l, 512, nullptr)
+           : i == 1 ? evict(wide, wl, 512, nullptr)
+                    : attend(c, 16, &l, nullptr);
+  });
+}
+
+static int selection_threads_test() {
+  const int32_t* in = fake<int32_t>(0);
+  return threads_test(4, [&](int i) {
+    if (i == 0)
+      return topk_i32(in, 1 << 20, 1000, fake<int32_t>(64), nullptr);
+    if (i == 1)  // a longer input each time: the segments' scratch grows
+      return topk_segmented_i32(in, (int64_t)(this_call + 1) << 21,
+                                fake<int64_t>(65), 100, 20, fake<int32_t>(66),
+                                nullptr, nullptr);
+    if (i == 2)
+      return topk_segmented_i32(in, 1 << 20, fake<int64_t>(65), 100, 20,
+                                fake<int32_t>(67), nullptr, nullptr);
+    return histogram_i32(in, 1 << 20, 0, 0, 256, fake<int64_t>(68), nullptr);
+  });
 }
 
 // Batches of many rows: status and launches of each call, and the most
@@ -245,7 +267,8 @@ static int lds_test(int dim, bool slots_first, int per_cu) {
 
 int main(int n, char** a) {
   const std::string what = n > 1 ? a[1] : "";
-  if (what == "threads") return threads_test();
+  if (what == "threads") return cache_threads_test();
+  if (what == "selection_threads") return selection_threads_test();
   if (what == "rows" && n > 4)
     return many_rows_test(atoi(a[2]), atoi(a[3]), atoi(a[4]));
   if (what == "lds" && n > 4)

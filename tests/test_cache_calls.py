@@ -43,6 +43,14 @@ def test_a_call_s_launches_stay_together(stub):
     assert r["calls"] == 36 and r["most"] >= 7
 
 
+def test_selections_of_several_launches_stay_together(stub):
+    """The same for top-k above 128 and of segments, with a histogram, which
+    counts in the same words, between them."""
+    r = stub("selection_threads")
+    assert r["failed"] == 0 and r["torn"] == 0
+    assert r["calls"] == 48 and r["most"] >= 6
+
+
 # 4 heads of 16 slots of 64 elements (k and v have 32 pages)
 @pytest.mark.parametrize("strides", [
     (4096, 0, 64), (4096, 1024, 0), (0, 1024, 64), (2048, 1024, 64),

@@ -70,6 +70,15 @@ struct Scratch {
   // Segmented top-k calls so far: each call's tag for the counters its two
   // launches share (the next call arms them).
   std::shared_ptr<std::atomic<uint32_t>> seg_calls;
+  std::shared_ptr<std::mutex> turn;
+};
+
+// A call's scratch, and its turn on it until the call returns: calls of
+// several launches hand results from one to the next in the scratch, and
+// another thread's launches on the same stream must not come between them
+// (nor may it grow the segments' scratch meanwhile).
+struct Held : Scratch {
+  std::unique_lock<std::mutex> hold;
 };
 
 // The epoch of a new launch on a scratch (never 0, which freshly cleared
@@ -158,8 +167,8 @@ int groups_per_cu(const void* fn) {
   return nb;
 }
 
-int get_scratch(int dev, hipStream_t stream, Scratch* out) {
-  std::lock_guard<std::mutex> lock(g_mu);
+// Caller holds g_mu.
+int find_scratch(int dev, hipStream_t stream, Scratch* out) {
   const auto key = std::make_pair(dev, (void*)stream);
   auto it = g_cache.find(key);
   if (it != g_cache.end()) {
@@ -198,6 +207,7 @@ int get_scratch(int dev, hipStream_t stream, Scratch* out) {
   s.ticket = (uint64_t*)b;
   s.epochs = std::make_shared<std::atomic<uint32_t>>(0u);
   s.seg_calls = std::make_shared<std::atomic<uint32_t>>(0u);
+  s.turn = std::make_shared<std::mutex>();
   // A kernel (not a memset) clears the histogram counters, the selection
   // state and the tickets (contiguous), ordered on the caller's stream
   // before the first real launch.  (Any value would do for the counters and
@@ -213,6 +223,16 @@ int get_scratch(int dev, hipStream_t stream, Scratch* out) {
   }
   g_cache[key] = s;
   *out = s;
+  return LIBTOPK_OK;
+}
+
+int get_scratch(int dev, hipStream_t stream, Held* out) {
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    const int rc = find_scratch(dev, stream, out);
+    if (rc != LIBTOPK_OK) return rc;
+  }
+  out->hold = std::unique_lock<std::mutex>(*out->turn);
   return LIBTOPK_OK;
 }
 
@@ -350,7 +370,7 @@ int topk_kv(const int32_t* in, int64_t n, int32_t k, int32_t* out_v,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   // With 128-key lists (k > 64) the kernel's registers leave room for one
@@ -792,7 +812,7 @@ int topk_i32(const int32_t* in, int64_t n, int32_t k, int32_t* out,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   int cus;
@@ -832,7 +852,7 @@ int reduce_i32(const int32_t* in, int64_t n, int32_t op, int64_t* out_i64,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   int cus;
@@ -880,7 +900,7 @@ int reduce_stats_i32(const int32_t* in, int64_t n, int64_t* out,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   int cus;
@@ -927,7 +947,7 @@ int topk_batched_i32(const int32_t* in, int64_t rows, int64_t cols,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   int cus;
@@ -990,7 +1010,7 @@ int topk_merge_i32(const int32_t* lists, int64_t m, int32_t len, int32_t k,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   MergeParams p;
@@ -1031,7 +1051,7 @@ int topk_segmented_i32(const int32_t* in, int64_t n, const int64_t* offsets,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   SegScratch ss;
@@ -1106,7 +1126,7 @@ int histogram_i32(const int32_t* in, int64_t n, int32_t lo, int32_t shift,
   int rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   hipStream_t s = (hipStream_t)stream;
-  Scratch sc;
+  Held sc;
   rc = get_scratch(dev, s, &sc);
   if (rc != LIBTOPK_OK) return rc;
   int cus;
@@ -1145,7 +1165,7 @@ int libtopk_debug_scramble(libtopk_stream_t stream, int32_t which,
   int counts[3];
   int parts = 0;
   if (which == 0) {
-    Scratch sc;
+    Held sc;
     rc = get_scratch(dev, s, &sc);
     if (rc != LIBTOPK_OK) return rc;
     words[0] = sc.ticket;
