@@ -37,7 +37,9 @@
  *    (completion tickets, histogram counters) carry that launch's epoch,
  *    so no result depends on what an earlier call, finished or not, left
  *    in the scratch.
- *  - Calls on different streams may run concurrently.  Thread-safe.
+ *  - Calls on different streams may run concurrently.  Thread-safe: a call's
+ *    launches follow one another on its stream, also when other host threads
+ *    call on it.
  *  - No C++ exception crosses this interface.  The library prints nothing
  *    unless LIBTOPK_DEBUG is set in the environment (then HIP failures are
  *    described on stderr).
