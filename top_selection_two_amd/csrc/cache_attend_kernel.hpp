@@ -103,24 +103,13 @@ __device__ __forceinline__ f32x4 mma4(float a, float b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
-// Two floats rounded to the operand's type, and back.
+// Two floats rounded to a 16-bit type.
 template <int QT>
 __device__ __forceinline__ int pack2(float a, float b) {
   if constexpr (QT == kBf16)
     return __builtin_bit_cast(int, bf16x2{(__bf16)a, (__bf16)b});
   else
     return __builtin_bit_cast(int, f16x2{(_Float16)a, (_Float16)b});
-}
-template <int QT>
-__device__ __forceinline__ void unpack2(int v, float* a, float* b) {
-  if constexpr (QT == kBf16) {
-    *a = __int_as_float(v << 16);
-    *b = __int_as_float(v & (int)0xffff0000);
-  } else {
-    const f16x2 h = __builtin_bit_cast(f16x2, v);
-    *a = (float)h[0];
-    *b = (float)h[1];
-  }
 }
 
 // Two of the four e4m3 values of a dword in the operand's type (exact: both
@@ -229,7 +218,9 @@ __device__ __forceinline__ void add_weights(float* w, int32_t left,
 //    the V operand supplies the same slots.  Weights never leave the lane.
 //  * V operand: a lane reads VE consecutive elements (n VE ..) of its 8
 //    slots and transposes the 8 x VE block in registers; instruction e takes
-//    element e, so its column n is the row's element n VE + e.
+//    element e, so its column n is the row's element n VE + e.  (float16 rows
+//    need no transposition: a 16 x 16 x 4 float32 instruction takes one slot
+//    of each lane group, with the weights in the lanes that hold them.)
 //
 // QT: query type, CT: cache type, NC: 32-element chunks of a row, PG16: pages
 // of a multiple of 16 slots, so that each half of a tile lies in one page.
@@ -759,11 +750,10 @@ attend_kernel(AttendParams p) {
             for (int j = 0; j < 8; ++j)
 #pragma unroll
               for (int e = 0; e < VE; e += 2) {
-                float y0, y1;
-                unpack2<kF16>(vr[nb][j][e / 2], &y0, &y1);
+                const f16x2 y = __builtin_bit_cast(f16x2, vr[nb][j][e / 2]);
                 f32x4* acc = &o[nb * VE + e];
-                acc[0] = mma4(w[j], y0, acc[0]);
-                acc[1] = mma4(w[j], y1, acc[1]);
+                acc[0] = mma4(w[j], (float)y[0], acc[0]);
+                acc[1] = mma4(w[j], (float)y[1], acc[1]);
               }
         } else {
           // Weights enter the product as three bfloat16 numbers each (see
