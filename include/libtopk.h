@@ -354,7 +354,8 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
 
 /* ---------------------------------------------------------------------------
  * Operators on a paged key-value cache of a decoder: attention of one new
- * token, append, and eviction by accumulated attention weight.
+ * token, append, eviction by accumulated attention weight, and extension by
+ * new tokens.
  *
  * The cache holds K and V rows of `dim` elements in pages of `page` slots.
  * Sequence b's slot t (0 <= t < lens[b]) of head h is the row at
@@ -372,8 +373,8 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
  *    slots out (score -infinity, weight unchanged), append and evict neither
  *    read nor write rows there.  Nothing outside the given arrays is ever
  *    read or written.
- *  - Pages that append or evict write to must belong to one sequence alone;
- *    attention may share them.  For these two calls each axis of k, and of v,
+ *  - Pages that append, evict or extend write to must belong to one sequence
+ *    alone; attention may share them.  For these calls each axis of k, and of v,
  *    steps over all that the axes within it span (no stride of 0).
  *
  * Workspace: per (device, stream), grown on demand by doubling; an area is
@@ -389,8 +390,16 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
 enum {
     LIBTOPK_BF16 = 0,
     LIBTOPK_F16 = 1,
-    LIBTOPK_E4M3 = 2 /* 8-bit float, 4 exponent bits, no infinity; cache only */
+    LIBTOPK_E4M3 = 2, /* 8-bit float, 4 exponent bits, no infinity; cache only */
+    LIBTOPK_F32 = 3,  /* logits and norm weights only */
+    LIBTOPK_E2M1 = 4  /* 4-bit float (0 .5 1 1.5 2 3 4 6 and their negatives),
+                         cache only: two to a byte, the even element in the low
+                         half, and a scale 2^(byte - 127) for each
+                         LIBTOPK_BLOCK_ELEMS of a row (255: NaN) */
 };
+
+/* Elements of a 4-bit row that share a scale. */
+#define LIBTOPK_BLOCK_ELEMS 32
 
 /* Largest row length of a cache. */
 #define LIBTOPK_MAX_DIM 256
@@ -410,7 +419,16 @@ typedef struct libtopk_cache {
     int32_t page;         /* slots of a page, 1 <= page                   */
     int32_t dim;          /* 1 <= dim <= LIBTOPK_MAX_DIM, rows of a whole
                              number of 16-byte units                      */
-    int32_t dtype;        /* LIBTOPK_BF16, LIBTOPK_F16 or LIBTOPK_E4M3    */
+    int32_t dtype;        /* LIBTOPK_BF16, _F16, _E4M3 or _E2M1           */
+    /* With LIBTOPK_E2M1 alone (otherwise not read, so that they may be left
+     * out of an older caller's struct): strides of k and v count bytes, dim is
+     * a multiple of 32, and the scales of slot t's row are the dim / 32 bytes
+     * at k_blocks + table[..] * k_block_page_stride + h * k_block_head_stride
+     * + (t % page) * k_block_slot_stride, at any alignment; likewise v's. */
+    void *k_blocks; /* device */
+    void *v_blocks;
+    int64_t k_block_page_stride, k_block_head_stride, k_block_slot_stride;
+    int64_t v_block_page_stride, v_block_head_stride, v_block_slot_stride;
 } libtopk_cache_t;
 
 /* What is kept for every slot besides its rows: the attention weight that it
@@ -448,7 +466,7 @@ typedef struct libtopk_ledger {
  * attention over the prompt.
  *
  *   q        device, q_dtype (LIBTOPK_BF16 or LIBTOPK_F16; the cache's own,
- *            or either over an LIBTOPK_E4M3 cache), 16-byte aligned, element
+ *            or either over an LIBTOPK_E4M3 or LIBTOPK_E2M1 cache), 16-byte aligned, element
  *            strides q_batch_stride and q_head_stride (multiples of 8)
  *   q_heads  a positive multiple of cache->heads
  *   k_scale, v_scale   device, float32[heads], or NULL for 1
@@ -494,6 +512,8 @@ int cache_attend(const libtopk_cache_t *cache, const void *q, int32_t q_dtype,
  * A replaced slot whose table entry names no page loses weight and position
  * as any other; only its rows are written nowhere.
  *
+ *   cache    of a type other than LIBTOPK_E2M1 (rows enter a 4-bit cache by
+ *            cache_extend)
  *   k_new, v_new   device, the cache's type, 16-byte aligned, element strides
  *                  new_batch_stride and new_head_stride (multiples of 16 B)
  *   limit    >= 1 slots
@@ -538,6 +558,72 @@ int cache_evict(const libtopk_cache_t *cache, const int32_t *seen,
                 const libtopk_ledger_t *ledger, int32_t keep, int32_t sinks,
                 int32_t recent, const libtopk_ledger_t *after,
                 int32_t *out_lens, libtopk_stream_t stream);
+
+/*
+ * cache_extend -- the heads of new tokens enter the cache, several tokens a
+ * sequence.  Token i of the tokens [starts[b], starts[b + 1]) is sequence b's
+ * at slot t = lens[b] + i - starts[b] and position s = seen[b] + i -
+ * starts[b].  Its rows x of k (and q, where given) become
+ *
+ *     y = x * (mean of x^2 + eps)^(-1/2) * k_norm      (or q_norm; if given)
+ *
+ * and then each of the rot / 2 pairs (y[c], y[d]) of its first rot elements
+ *
+ *     (y[c] cos a - y[d] sin a, y[d] cos a + y[c] sin a),  a = s * freqs[j]
+ *
+ * with (c, d) = (j, j + rot / 2), or (2 j, 2 j + 1) if `interleaved`.  Rows of
+ * k and v are divided by k_scale[h], v_scale[h] (as cache_attend multiplies)
+ * and stored in the cache's type; q goes to q_out in its own.  All of it is
+ * computed in 64 bits and rounded at the end, through float32 where the type
+ * has 16 or 8 bits.  Numbers beyond an LIBTOPK_E4M3 cache's range become its
+ * largest.  In an LIBTOPK_E2M1 cache a block of 32 elements, the largest of
+ * magnitude m, gets the scale s = 2^(byte - 127), the least (of 0 <= byte <=
+ * 254) with m < 7 s, and each element the nearest 4-bit number to x / s, of
+ * two the even code; a block with an infinity or NaN gets 255.
+ *
+ * With a ledger, weight and position of the new slots become 0 and s.
+ * out_lens[b] is the length with the new slots.  Where a slot would lie beyond
+ * the table or the ledger, nothing is written for it (q_out is) and the length
+ * stops there; where the table names no page, no row is written.  Tokens that
+ * belong to no sequence (from starts[batch] on) are left alone, in q_out too.
+ *
+ *   starts   device, int32[batch + 1], non-decreasing within [0, tokens]: the
+ *            caller's promise; otherwise which rows are written is
+ *            unspecified (none outside the arrays)
+ *   out_lens device, int32[batch]; may not be cache->lens
+ *
+ * One launch, no workspace.  Errors: LIBTOPK_ERR_INVALID for a NULL or
+ * misaligned pointer, a size, stride or type outside the above, an output that
+ * overlaps an input or another output (k and v may interleave; q_out may be
+ * q), or more than 2^24 workgroups (a token each, or with few tokens several).
+ */
+typedef struct libtopk_tokens {
+    const void *q;       /* device, dtype[tokens][q_heads][dim]; NULL: none */
+    const void *k, *v;   /* device, dtype[tokens][heads][dim]               */
+    void *q_out;         /* device, as q; with q's strides it may be q      */
+    /* elements, multiples of 8; all of these arrays 16-byte aligned */
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride;
+    int64_t q_out_token_stride, q_out_head_stride;
+    const int32_t *starts;
+    const int32_t *seen;  /* device, int32[batch]; NULL: the lengths         */
+    const void *q_norm;   /* device, norm_dtype[dim], or NULL                */
+    const void *k_norm;
+    const float *freqs;   /* device, float32[rot / 2]                        */
+    const float *k_scale; /* device, float32[heads], or NULL for 1           */
+    const float *v_scale;
+    int32_t tokens, q_heads;
+    int32_t dtype;        /* LIBTOPK_BF16 or LIBTOPK_F16; the cache's type is
+                             this, LIBTOPK_E4M3 or LIBTOPK_E2M1              */
+    int32_t norm_dtype;   /* dtype or LIBTOPK_F32                            */
+    int32_t rot;          /* 0 <= rot <= dim, a multiple of 16               */
+    int32_t interleaved;
+    float eps;            /* >= 0                                            */
+} libtopk_tokens_t;
+
+int cache_extend(const libtopk_cache_t *cache, const libtopk_tokens_t *tokens,
+                 const libtopk_ledger_t *ledger, int32_t *out_lens,
+                 libtopk_stream_t stream);
 
 /* Free the workspaces of the cache_* calls after synchronising their
  * devices.  Must not race with other calls, nor precede the replay of a graph

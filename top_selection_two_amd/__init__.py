@@ -34,6 +34,9 @@ if the library is not built, importing this package raises.
                     -> (lens [B], slots [B, H]): the new token's rows enter
                        the cache, in a full one in the place of the slot of
                        the lowest accumulated attention weight
+    cache_extend(k_new, v_new, k, v, table, lens, starts, ...)
+                    -> (lens [B], q [N, Hq, D]): new tokens' heads, normed
+                       and rotated, enter the cache in its type
     cache_evict(k, v, table, lens, seen, weights, positions, keep, ...)
                     -> (weights [B, H, keep], positions, lens [B]): the cache
                        cut back to the slots of the largest weight
@@ -51,7 +54,7 @@ MAX_K_SELECT = 16384   # LIBTOPK_MAX_K_SELECT: largest k of topk()
 MAX_BINS = 4096        # LIBTOPK_MAX_BINS
 SUM, MAX, MIN = 0, 1, 2
 OPS = {"sum": SUM, "max": MAX, "min": MIN}
-BF16, F16, E4M3 = 0, 1, 2   # element types of a cache
+BF16, F16, E4M3, F32, E2M1 = 0, 1, 2, 3, 4   # element types
 MAX_DIM = 256               # LIBTOPK_MAX_DIM
 
 _VP = ctypes.c_void_p
@@ -67,7 +70,12 @@ class CacheStruct(ctypes.Structure):
                 + [("table", _VP), ("lens", _VP)]
                 + [(n, ctypes.c_int32) for n in
                    ("batch", "table_width", "heads", "page", "dim",
-                    "dtype")])
+                    "dtype")]
+                + [("k_blocks", _VP), ("v_blocks", _VP)]
+                + [(n, ctypes.c_int64) for n in
+                   ("k_block_page_stride", "k_block_head_stride",
+                    "k_block_slot_stride", "v_block_page_stride",
+                    "v_block_head_stride", "v_block_slot_stride")])
 
 
 class LedgerStruct(ctypes.Structure):
@@ -77,6 +85,20 @@ class LedgerStruct(ctypes.Structure):
                    ("weights_batch_stride", "weights_head_stride",
                     "positions_batch_stride", "positions_head_stride")]
                 + [("slots", ctypes.c_int32)])
+
+
+class TokensStruct(ctypes.Structure):
+    """libtopk_tokens_t of include/libtopk.h."""
+    _fields_ = ([(n, _VP) for n in ("q", "k", "v", "q_out")]
+                + [(n + "_stride", ctypes.c_int64) for n in
+                   ("q_token", "q_head", "k_token", "k_head", "v_token",
+                    "v_head", "q_out_token", "q_out_head")]
+                + [(n, _VP) for n in ("starts", "seen", "q_norm", "k_norm",
+                                      "freqs", "k_scale", "v_scale")]
+                + [(n, ctypes.c_int32) for n in
+                   ("tokens", "q_heads", "dtype", "norm_dtype", "rot",
+                    "interleaved")]
+                + [("eps", ctypes.c_float)])
 
 
 _CACHE = ctypes.POINTER(CacheStruct)
@@ -112,6 +134,8 @@ SIGNATURES = {
                       ctypes.c_int32, _VP, _VP, _VP], ctypes.c_int),
     "cache_evict": ([_CACHE, _VP, _LEDGER, ctypes.c_int32, ctypes.c_int32,
                      ctypes.c_int32, _LEDGER, _VP, _VP], ctypes.c_int),
+    "cache_extend": ([_CACHE, ctypes.POINTER(TokensStruct), _LEDGER, _VP,
+                      _VP], ctypes.c_int),
     "cache_release": ([], None),
     "cache_debug_scramble": ([_VP, ctypes.c_uint64], ctypes.c_int),
     "libtopk_strerror": ([ctypes.c_int], ctypes.c_char_p),
@@ -522,7 +546,7 @@ def histogram(x, lo: int, shift: int, nbins: int, out=None):
 # shapes, types, strides, and last that they are a GPU's.  (Length, table and
 # position values stay on the device; the kernels bound what they read there.)
 def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
-                 v_scale=None, out=None):
+                 v_scale=None, out=None, k_blocks=None, v_blocks=None):
     """Attention of one new token a sequence over its slots in a paged cache
     (see cache_attend in include/libtopk.h).
 
@@ -533,14 +557,17 @@ def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
     scale of the scores (default D ** -0.5); k_scale, v_scale float32 [H]
     factors of the rows.  weights float32 [B, H, slots] gets each slot's
     attention weights, summed over the Hq / H queries of its head, added in
-    place.  Returns (out [B, Hq, D] of q's type, lse float32 [B, Hq]); out
+    place.  A cache held in 4 bits is k, v of float4_e2m1fn_x2
+    [pages, H, page, D / 2] (the even element in a byte's low half) with
+    k_blocks, v_blocks float8_e8m0fnu [pages, H, page, D / 32], the scales of
+    32 elements each.  Returns (out [B, Hq, D] of q's type, lse float32 [B, Hq]); out
     may be given as that pair of tensors.
 
     There is no backward pass: with inputs that require gradients, a gradient
     through the outputs is an error (through outputs given as `out` there is
     none)."""
     return _binding.attend(q, k, v, table, lens, scale, weights, k_scale,
-                           v_scale, out)
+                           v_scale, out, k_blocks, v_blocks)
 
 
 def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
@@ -552,18 +579,50 @@ def cache_append(k_new, v_new, k, v, table, lens, limit, seen, weights,
     >= seen[b] - recent).  weights float32 and positions int32
     [B, H, slots] are updated in place, as k and v are; seen int32 [B] is the
     new token's position.  Returns (lens [B], slots [B, H]), int32.  No
-    gradient passes through the rows written."""
+    gradient passes through the rows written.  (Rows enter a cache held in
+    4 bits by cache_extend.)"""
     return _binding.append(k_new, v_new, k, v, table, lens, limit, seen,
                            weights, positions, sinks, recent)
 
 
 def cache_evict(k, v, table, lens, seen, weights, positions, keep, sinks=0,
-                recent=0, out=None):
+                recent=0, out=None, k_blocks=None, v_blocks=None):
     """Cut each sequence's cache back to the `keep` slots of the largest
     accumulated weight, protected ones first (see cache_evict in
     include/libtopk.h); rows move within k and v.  Returns (weights
     [B, H, keep], positions [B, H, keep], lens [B]); out may be given as a
-    pair of tensors for the first two (they overlap no input).  No gradient
-    passes through the rows moved."""
+    pair of tensors for the first two (they overlap no input).  The scales
+    k_blocks, v_blocks of a cache held in 4 bits (see cache_attend) move with
+    the rows.  No gradient passes through the rows moved."""
     return _binding.evict(k, v, table, lens, seen, weights, positions, keep,
-                          sinks, recent, out)
+                          sinks, recent, out, k_blocks, v_blocks)
+
+
+def cache_extend(k_new, v_new, k, v, table, lens, starts, seen=None, q=None,
+                 freqs=None, interleaved=False, q_norm=None, k_norm=None,
+                 eps=1e-6, k_scale=None, v_scale=None, weights=None,
+                 positions=None, k_blocks=None, v_blocks=None, out=None):
+    """The heads of new tokens, several a sequence, enter the cache (see
+    cache_extend in include/libtopk.h).
+
+    k_new, v_new [N, H, D] and, where given, q [N, Hq, D] (bfloat16 or
+    float16, any strides that are multiples of 16 bytes: slices of one
+    projection's output will do); starts [B + 1] int32: sequence b's tokens
+    are starts[b] .. starts[b + 1), which go to the slots from lens[b] on and
+    have the positions from seen[b] on (default: lens).  k_norm, q_norm [D]
+    (that type or float32) are weights of a root-mean-square norm of each
+    head; freqs float32 [pairs] turns that many pairs of a head's first
+    elements by position * freqs, (j, j + pairs) or (2 j, 2 j + 1) if
+    interleaved.  Then k / k_scale[h] and v / v_scale[h] are stored in the
+    cache's type: k_new's, float8_e4m3fn, or float4_e2m1fn_x2 with k_blocks
+    and v_blocks (see cache_attend).  weights and positions [B, H, slots] of
+    the new slots become 0 and their position.
+
+    Returns (lens [B], q [N, Hq, D] or None); out may be given for the
+    latter, and may be q itself.  Tokens of no sequence are left as they were.
+    No gradient passes through the rows written; one through the queries
+    returned is an error."""
+    return _binding.extend(k_new, v_new, k, v, table, lens, starts, seen, q,
+                           freqs, interleaved, q_norm, k_norm, eps, k_scale,
+                           v_scale, weights, positions, k_blocks, v_blocks,
+                           out)

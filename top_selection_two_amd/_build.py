@@ -29,7 +29,7 @@ BINDING = os.path.join(PKG, "_binding.so")
 # Sources with their definitions: LTK_Q, LTK_C are types of include/libtopk.h.
 UNITS = (("libtopk.hip",), ("cache.hip",),
          *(("cache_attend.hip", "-DLTK_Q=%d" % q, "-DLTK_C=%d" % c)
-           for q, c in ((0, 0), (0, 2), (1, 1), (1, 2))))
+           for q, c in ((0, 0), (0, 2), (0, 4), (1, 1), (1, 2), (1, 4))))
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -102,7 +102,32 @@ struct Cache {
   at::ScalarType type{};
 };
 
-Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
+// The scales of 4-bit rows, where the cache has such.
+void blocks(const Tensor& x, PyObject* o, const char* name,
+            const at::Device& device, void** p, int64_t* page, int64_t* head,
+            int64_t* slot) {
+  if (x.scalar_type() != at::kFloat4_e2m1fn_x2) {
+    if (o != Py_None)
+      value_error(std::string(name) + ": only with a float4_e2m1fn_x2 cache");
+    return;
+  }
+  if (o == Py_None)
+    value_error(std::string(name) + ": needed with a float4_e2m1fn_x2 cache");
+  const Tensor& b = tensor(o, name);
+  if (x.size(3) % 16)
+    value_error("rows of " + std::to_string(2 * x.size(3)) +
+                " elements of 4 bits: expected a multiple of 32");
+  expect(b, name, at::kFloat8_e8m0fnu,
+         {x.size(0), x.size(1), x.size(2), x.size(3) / 16}, device, false);
+  expect_unit(b, name);
+  *p = pointer(b);
+  *page = step_of(b, 0);
+  *head = step_of(b, 1);
+  *slot = step_of(b, 2);
+}
+
+Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo,
+            PyObject* kbo = Py_None, PyObject* vbo = Py_None) {
   const Tensor &k = tensor(ko, "k"), &v = tensor(vo, "v");
   Cache r;
   r.device = k.device();
@@ -112,9 +137,10 @@ Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
   for (int i = 0; i < 2; ++i) {
     const Tensor& x = *both[i];
     const at::ScalarType t = x.scalar_type();
-    if (t != at::kBFloat16 && t != at::kHalf && t != at::kFloat8_e4m3fn)
-      type_error(std::string(names[i]) + ": expected bfloat16, float16 or "
-                 "float8_e4m3fn, got " + c10::toString(t));
+    if (t != at::kBFloat16 && t != at::kHalf && t != at::kFloat8_e4m3fn &&
+        t != at::kFloat4_e2m1fn_x2)
+      type_error(std::string(names[i]) + ": expected bfloat16, float16, "
+                 "float8_e4m3fn or float4_e2m1fn_x2, got " + c10::toString(t));
     if (x.dim() != 4)
       value_error(std::string(names[i]) +
                   ": expected [pages, heads, page, dim]");
@@ -133,12 +159,18 @@ Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
   const Tensor& lens = tensor(lo, "lens");
   expect(lens, "lens", at::kInt, {table.size(0)}, r.device);
   const int64_t bytes = k.size(3) * (int64_t)k.element_size();
-  if (k.size(3) > LIBTOPK_MAX_DIM || bytes % 16)
-    value_error("rows of " + std::to_string(k.size(3)) + " elements of " +
+  const int64_t dim = k.size(3) * (r.type == at::kFloat4_e2m1fn_x2 ? 2 : 1);
+  if (dim > LIBTOPK_MAX_DIM || bytes % 16)
+    value_error("rows of " + std::to_string(dim) + " elements of " +
                 c10::toString(r.type) + ": expected at most " +
                 std::to_string(LIBTOPK_MAX_DIM) +
                 " and a multiple of 16 bytes");
   libtopk_cache_t& c = r.c;
+  c = {};
+  blocks(k, kbo, "k_blocks", r.device, &c.k_blocks, &c.k_block_page_stride,
+         &c.k_block_head_stride, &c.k_block_slot_stride);
+  blocks(v, vbo, "v_blocks", r.device, &c.v_blocks, &c.v_block_page_stride,
+         &c.v_block_head_stride, &c.v_block_slot_stride);
   c.k = pointer(k);
   c.v = pointer(v);
   c.k_page_stride = step_of(k, 0);
@@ -157,10 +189,11 @@ Cache cache(PyObject* ko, PyObject* vo, PyObject* to, PyObject* lo) {
   c.table_width = (int32_t)table.size(1);
   c.heads = (int32_t)k.size(1);
   c.page = (int32_t)k.size(2);
-  c.dim = (int32_t)k.size(3);
-  c.dtype = r.type == at::kBFloat16 ? LIBTOPK_BF16
-            : r.type == at::kHalf   ? LIBTOPK_F16
-                                    : LIBTOPK_E4M3;
+  c.dim = (int32_t)dim;
+  c.dtype = r.type == at::kBFloat16            ? LIBTOPK_BF16
+            : r.type == at::kHalf              ? LIBTOPK_F16
+            : r.type == at::kFloat4_e2m1fn_x2 ? LIBTOPK_E2M1
+                                               : LIBTOPK_E4M3;
   return r;
 }
 
@@ -231,17 +264,26 @@ void expect_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) type_error("wrong number of arguments");
 }
 
-// (q, k, v, table, lens, scale, weights, k_scale, v_scale, out)
+// Factors of the heads' rows: float32 [heads], or None.
+const float* head_scale(const Cache& r, PyObject* o, const char* name) {
+  if (o == Py_None) return nullptr;
+  const Tensor& x = tensor(o, name);
+  expect(x, name, at::kFloat, {r.c.heads}, r.device);
+  return (const float*)pointer(x);
+}
+
+// (q, k, v, table, lens, scale, weights, k_scale, v_scale, out, k_blocks,
+// v_blocks)
 PyObject* attend(PyObject* const* a, Py_ssize_t n) {
-  expect_args(n, 10);
-  const Cache r = cache(a[1], a[2], a[3], a[4]);
+  expect_args(n, 12);
+  const Cache r = cache(a[1], a[2], a[3], a[4], a[10], a[11]);
   const Tensor& q = tensor(a[0], "q");
   const at::ScalarType t = q.scalar_type();
   if (q.dim() != 3) value_error("q: expected [batch, query heads, dim]");
   if (t != at::kBFloat16 && t != at::kHalf)
     type_error(std::string("q: expected bfloat16 or float16, got ") +
                c10::toString(t));
-  if (r.c.dtype != LIBTOPK_E4M3 && t != r.type)
+  if (r.c.dtype != LIBTOPK_E4M3 && r.c.dtype != LIBTOPK_E2M1 && t != r.type)
     type_error(std::string("q is ") + c10::toString(t) + ", the cache " +
                c10::toString(r.type));
   const int64_t heads = q.size(1);
@@ -257,14 +299,8 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n) {
     scale = PyFloat_AsDouble(a[5]);
     if (PyErr_Occurred()) throw PythonError{};
   }
-  const float* scales[2] = {nullptr, nullptr};
-  for (int i = 0; i < 2; ++i) {
-    if (a[7 + i] == Py_None) continue;
-    const char* name = i ? "v_scale" : "k_scale";
-    const Tensor& x = tensor(a[7 + i], name);
-    expect(x, name, at::kFloat, {r.c.heads}, r.device);
-    scales[i] = (const float*)pointer(x);
-  }
+  const float* scales[2] = {head_scale(r, a[7], "k_scale"),
+                            head_scale(r, a[8], "v_scale")};
   libtopk_ledger_t l = {};
   const bool weights = a[6] != Py_None;
   if (weights) l = ledger(r, a[6], "weights", nullptr, nullptr);
@@ -323,7 +359,7 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   const int32_t limit = integer(a[6], "limit", 1);
   const int32_t sinks = integer(a[10], "sinks", 0);
   const int32_t recent = integer(a[11], "recent", 0);
-  const Cache r = cache(a[2], a[3], a[4], a[5]);
+  const Cache r = cache(a[2], a[3], a[4], a[5]);  // (of no 4-bit type)
   const libtopk_ledger_t l = ledger(r, a[8], "weights", a[9], "positions");
   const Tensor &kn = tensor(a[0], "k_new"), &vn = tensor(a[1], "v_new");
   const Tensor* both[2] = {&kn, &vn};
@@ -353,13 +389,14 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NN)", x, y);
 }
 
-// (k, v, table, lens, seen, weights, positions, keep, sinks, recent, out)
+// (k, v, table, lens, seen, weights, positions, keep, sinks, recent, out,
+// k_blocks, v_blocks)
 PyObject* evict(PyObject* const* a, Py_ssize_t n) {
-  expect_args(n, 11);
+  expect_args(n, 13);
   const int32_t keep = integer(a[7], "keep", 1);
   const int32_t sinks = integer(a[8], "sinks", 0);
   const int32_t recent = integer(a[9], "recent", 0);
-  const Cache r = cache(a[0], a[1], a[2], a[3]);
+  const Cache r = cache(a[0], a[1], a[2], a[3], a[11], a[12]);
   const libtopk_ledger_t l = ledger(r, a[5], "weights", a[6], "positions");
   const Tensor& seen = tensor(a[4], "seen");
   expect(seen, "seen", at::kInt, {r.c.batch}, r.device);
@@ -390,7 +427,8 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   check(cache_evict(&r.c, (const int32_t*)pointer(seen), &l, keep, sinks,
                     recent, &after, (int32_t*)pointer(lens), stream),
         "cache_evict");
-  for (int i : {0, 1}) changed(tensor(a[i], ""));
+  for (int i : {0, 1, 11, 12})
+    if (a[i] != Py_None) changed(tensor(a[i], ""));
   if (a[10] != Py_None) {
     changed(w);
     changed(pos);
@@ -399,6 +437,150 @@ PyObject* evict(PyObject* const* a, Py_ssize_t n) {
   PyObject* y = THPVariable_Wrap(std::move(pos));
   PyObject* z = THPVariable_Wrap(std::move(lens));
   return Py_BuildValue("(NNN)", x, y, z);
+}
+
+// (k_new, v_new, k, v, table, lens, starts, seen, q, freqs, interleaved,
+// q_norm, k_norm, eps, k_scale, v_scale, weights, positions, k_blocks,
+// v_blocks, out)
+PyObject* extend(PyObject* const* a, Py_ssize_t n) {
+  expect_args(n, 21);
+  const Cache r = cache(a[2], a[3], a[4], a[5], a[18], a[19]);
+  libtopk_tokens_t t = {};
+  const Tensor& kn = tensor(a[0], "k_new");
+  const at::ScalarType type = kn.scalar_type();
+  if (type != at::kBFloat16 && type != at::kHalf)
+    type_error(std::string("k_new: expected bfloat16 or float16, got ") +
+               c10::toString(type));
+  if (r.c.dtype != LIBTOPK_E4M3 && r.c.dtype != LIBTOPK_E2M1 && type != r.type)
+    type_error(std::string("k_new is ") + c10::toString(type) +
+               ", the cache " + c10::toString(r.type));
+  if (kn.dim() != 3) value_error("k_new: expected [tokens, heads, dim]");
+  const int64_t tokens = kn.size(0);
+  if (tokens > INT32_MAX) value_error("k_new: 2^31 tokens or more");
+  struct Rows {
+    int arg;
+    const char* name;
+    const void** p;
+    int64_t *token, *head;
+  };
+  const void* out_p = nullptr;
+  const Rows in[3] = {{0, "k_new", &t.k, &t.k_token_stride, &t.k_head_stride},
+                      {1, "v_new", &t.v, &t.v_token_stride, &t.v_head_stride},
+                      {8, "q", &t.q, &t.q_token_stride, &t.q_head_stride}};
+  const bool queries = a[8] != Py_None;
+  int64_t q_heads = 0;
+  for (int i = 0; i < (queries ? 3 : 2); ++i) {
+    const Tensor& x = tensor(a[in[i].arg], in[i].name);
+    if (i == 2) {
+      if (x.dim() != 3) value_error("q: expected [tokens, query heads, dim]");
+      q_heads = x.size(1);
+      if (q_heads < 1 || q_heads > INT32_MAX)
+        value_error("q: expected at least one head");
+    }
+    expect(x, in[i].name, type, {tokens, i == 2 ? q_heads : r.c.heads, r.c.dim},
+           r.device, false);
+    expect_unit(x, in[i].name);
+    *in[i].p = pointer(x);
+    *in[i].token = step_of(x, 0);
+    *in[i].head = step_of(x, 1);
+  }
+  const Tensor& starts = tensor(a[6], "starts");
+  expect(starts, "starts", at::kInt, {(int64_t)r.c.batch + 1}, r.device);
+  t.starts = (const int32_t*)pointer(starts);
+  if (a[7] != Py_None) {
+    const Tensor& seen = tensor(a[7], "seen");
+    expect(seen, "seen", at::kInt, {r.c.batch}, r.device);
+    t.seen = (const int32_t*)pointer(seen);
+  }
+  if (a[9] != Py_None) {
+    const Tensor& f = tensor(a[9], "freqs");
+    if (f.dim() != 1) value_error("freqs: expected [pairs that turn]");
+    expect(f, "freqs", at::kFloat, f.sizes(), r.device);
+    if (2 * f.size(0) > r.c.dim || f.size(0) % 8)
+      value_error("freqs: expected a multiple of 8 and at most " +
+                  std::to_string(r.c.dim / 2) + " of them");
+    t.freqs = (const float*)pointer(f);
+    t.rot = (int32_t)(2 * f.size(0));
+  }
+  const int turn = PyObject_IsTrue(a[10]);
+  if (turn < 0) throw PythonError{};
+  t.interleaved = turn;
+  t.norm_dtype = type == at::kBFloat16 ? LIBTOPK_BF16 : LIBTOPK_F16;
+  t.dtype = t.norm_dtype;
+  at::ScalarType norm{};
+  for (int i : {0, 1}) {
+    if (a[11 + i] == Py_None) continue;
+    const char* name = i ? "k_norm" : "q_norm";
+    const Tensor& x = tensor(a[11 + i], name);
+    if (x.scalar_type() != type && x.scalar_type() != at::kFloat)
+      type_error(std::string(name) + ": expected float32 or " +
+                 c10::toString(type) + ", got " + c10::toString(x.scalar_type()));
+    if (i && a[11] != Py_None && x.scalar_type() != norm)
+      type_error("q_norm and k_norm: expected one type");
+    norm = x.scalar_type();
+    expect(x, name, norm, {r.c.dim}, r.device);
+    if (norm == at::kFloat) t.norm_dtype = LIBTOPK_F32;
+    (i ? t.k_norm : t.q_norm) = pointer(x);
+  }
+  const double eps = PyFloat_AsDouble(a[13]);
+  if (PyErr_Occurred()) throw PythonError{};
+  if (!(eps >= 0)) value_error("eps: expected a number of at least 0");
+  t.eps = (float)eps;
+  t.k_scale = head_scale(r, a[14], "k_scale");
+  t.v_scale = head_scale(r, a[15], "v_scale");
+  if ((a[16] == Py_None) != (a[17] == Py_None))
+    value_error("weights and positions: expected both or neither");
+  libtopk_ledger_t l = {};
+  const bool led = a[16] != Py_None;
+  if (led) l = ledger(r, a[16], "weights", a[17], "positions");
+  const libtopk_stream_t stream = stream_of(r.device);
+  Tensor out;
+  if (queries) {
+    const Tensor& q = tensor(a[8], "q");
+    if (a[20] == Py_None) {
+      out = at::empty({tokens, q_heads, (int64_t)r.c.dim}, q.options());
+    } else {
+      out = tensor(a[20], "out");
+      expect(out, "out", type, q.sizes(), r.device, false);
+      expect_unit(out, "out");
+    }
+    out_p = pointer(out);
+    t.q_out = const_cast<void*>(out_p);
+    t.q_out_token_stride = step_of(out, 0);
+    t.q_out_head_stride = step_of(out, 1);
+    // An array without elements has no address.
+    if (tokens == 0) t.q = nullptr;
+  } else if (a[20] != Py_None) {
+    value_error("out: only with q");
+  }
+  t.tokens = (int32_t)tokens;
+  t.q_heads = (int32_t)q_heads;
+  Tensor lens = at::empty({r.c.batch}, starts.options());
+  const c10::DeviceGuard guard(r.device);
+  check(cache_extend(&r.c, &t, led ? &l : nullptr, (int32_t*)pointer(lens),
+                     stream),
+        "cache_extend");
+  for (int i : {2, 3, 16, 17, 18, 19})
+    if (a[i] != Py_None) changed(tensor(a[i], ""));
+  PyObject* x = THPVariable_Wrap(std::move(lens));
+  if (!queries) return Py_BuildValue("(NO)", x, Py_None);
+  if (a[20] != Py_None) {
+    changed(out);
+  } else if (at::GradMode::is_enabled()) {
+    // There is no backward pass: one that is asked for is an error.
+    torch::autograd::edge_list edges;
+    for (int i : {8, 11}) {
+      if (a[i] == Py_None) continue;
+      const Tensor& z = tensor(a[i], "");
+      if (z.requires_grad())
+        edges.push_back(torch::autograd::impl::gradient_edge(z));
+    }
+    if (!edges.empty())
+      torch::autograd::set_history(
+          out, std::make_shared<torch::autograd::NotImplemented>(
+                   "cache_extend", std::move(edges)));
+  }
+  return Py_BuildValue("(NN)", x, THPVariable_Wrap(std::move(out)));
 }
 
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
@@ -426,6 +608,7 @@ PyObject* set_error(PyObject*, PyObject* type) {
 PyMethodDef methods[] = {LTK_ENTRY(attend),
                          LTK_ENTRY(append),
                          LTK_ENTRY(evict),
+                         LTK_ENTRY(extend),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

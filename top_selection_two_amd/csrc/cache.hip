@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "libtopk.h"
+#include "cache_extend_kernel.hpp"
 #include "cache_join_kernel.hpp"
 #include "cache_slots_kernel.hpp"
 
@@ -20,7 +21,10 @@ namespace {
 using namespace ltk;
 
 static_assert(kBf16 == LIBTOPK_BF16 && kF16 == LIBTOPK_F16 &&
-                  kE4m3 == LIBTOPK_E4M3,
+                  kE4m3 == LIBTOPK_E4M3 && kF32 == LIBTOPK_F32 &&
+                  kE2m1 == LIBTOPK_E2M1 &&
+                  kBlockElems == LIBTOPK_BLOCK_ELEMS &&
+                  kMaxDim == LIBTOPK_MAX_DIM,
               "the kernels' types are the header's");
 
 constexpr int64_t kMaxSlots = (int64_t)1 << 30;
@@ -235,7 +239,13 @@ int64_t span(const int64_t* n, const int64_t* s, int dims, int64_t row) {
   return all;
 }
 
-int elem_size(int dtype) { return dtype == LIBTOPK_E4M3 ? 1 : 2; }
+// Bytes of what a cache's strides count: an element, or a pair of 4-bit ones.
+int unit_size(int dtype) {
+  return dtype == LIBTOPK_E4M3 || dtype == LIBTOPK_E2M1 ? 1 : 2;
+}
+int64_t row_size(int dtype, int64_t dim) {
+  return dtype == LIBTOPK_E2M1 ? dim / 2 : dim * unit_size(dtype);
+}
 
 // Do the rows of an array (as for span, strides >= 0) lie apart: does each
 // axis, from the innermost on, step over all that the ones within it span?
@@ -254,56 +264,83 @@ bool apart(const int64_t* n, const int64_t* s, int dims, int64_t row) {
   return true;
 }
 
-// Checks a cache and fills in what the kernels take of it; `k` and `v` get
-// the arrays' extents.  Rows that are written must not share a byte.
+// Extents of a cache's arrays.
+struct CacheRanges {
+  Range k{nullptr, 0}, v{nullptr, 0}, table{nullptr, 0}, lens{nullptr, 0};
+  Range kb{nullptr, 0}, vb{nullptr, 0};  // scales of 4-bit rows
+};
+
+// One of the cache's arrays of rows (or of their scales): strides in units of
+// `unit` bytes, rows of `row` bytes; fills in the strides in bytes and the
+// extent.  Rows that are written must not share a byte.
+bool check_rows(const void* p, const int64_t (&n)[3], const int64_t (&stride)[3],
+                int64_t unit, int64_t row, int64_t align, bool written,
+                RowStrides* out, Range* extent) {
+  int64_t b[3];
+  for (int i = 0; i < 3; ++i) {
+    if (stride[i] < 0 || stride[i] > kSpan) return false;
+    b[i] = stride[i] * unit;
+    if (n[i] > 1 && b[i] % align) return false;
+  }
+  const int64_t len = span(n, b, 3, row);
+  if (len < 0 || (written && !apart(n, b, 3, row))) return false;
+  if ((n[0] > 0 && !p) || !aligned(p, (uintptr_t)align)) return false;
+  *out = RowStrides{b[0], b[1], b[2]};
+  *extent = Range(p, len);
+  return true;
+}
+
+// Checks a cache and fills in what the kernels take of it, and the extents of
+// its arrays.
 int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
-                Range* k, Range* v, Range* table, Range* lens) {
+                CacheRanges* r) {
   if (!c) return LIBTOPK_ERR_INVALID;
+  const bool e2m1 = c->dtype == LIBTOPK_E2M1;
   if (c->dtype != LIBTOPK_BF16 && c->dtype != LIBTOPK_F16 &&
-      c->dtype != LIBTOPK_E4M3)
+      c->dtype != LIBTOPK_E4M3 && !e2m1)
     return LIBTOPK_ERR_INVALID;
-  const int es = elem_size(c->dtype);
   if (c->batch < 0 || c->heads < 1 || c->heads > 65535 || c->page < 1 ||
-      c->dim < 1 || c->dim > LIBTOPK_MAX_DIM || c->dim * es % 16 != 0 ||
-      c->table_width < 1 || c->pages < 0 || c->pages > INT32_MAX)
+      c->dim < 1 || c->dim > LIBTOPK_MAX_DIM ||
+      (e2m1 && c->dim % kBlockElems != 0) ||
+      row_size(c->dtype, c->dim) % 16 != 0 || c->table_width < 1 ||
+      c->pages < 0 || c->pages > INT32_MAX)
     return LIBTOPK_ERR_INVALID;
   if ((int64_t)c->table_width * c->page >= kMaxSlots ||
       (int64_t)c->batch * c->heads > INT32_MAX)
     return LIBTOPK_ERR_INVALID;
   if (c->batch > 1 && (c->table_stride < 0 || c->table_stride > kSpan / 4))
     return LIBTOPK_ERR_INVALID;
+  const int64_t n[3] = {c->pages, c->heads, c->page};
   const int64_t ks[3] = {c->k_page_stride, c->k_head_stride, c->k_slot_stride};
   const int64_t vs[3] = {c->v_page_stride, c->v_head_stride, c->v_slot_stride};
-  const int64_t n[3] = {c->pages, c->heads, c->page};
-  int64_t kb[3], vb[3];
-  for (int i = 0; i < 3; ++i) {
-    if (ks[i] < 0 || ks[i] > kSpan || vs[i] < 0 || vs[i] > kSpan)
-      return LIBTOPK_ERR_INVALID;
-    kb[i] = ks[i] * es;
-    vb[i] = vs[i] * es;
-    if (n[i] > 1 && (kb[i] % 16 || vb[i] % 16)) return LIBTOPK_ERR_INVALID;
-  }
-  const int64_t klen = span(n, kb, 3, c->dim * es);
-  const int64_t vlen = span(n, vb, 3, c->dim * es);
-  if (klen < 0 || vlen < 0) return LIBTOPK_ERR_INVALID;
-  if (written && !(apart(n, kb, 3, c->dim * es) && apart(n, vb, 3, c->dim * es)))
+  const int64_t unit = unit_size(c->dtype), row = row_size(c->dtype, c->dim);
+  if (!check_rows(c->k, n, ks, unit, row, 16, written, &p->ks, &r->k) ||
+      !check_rows(c->v, n, vs, unit, row, 16, written, &p->vs, &r->v))
     return LIBTOPK_ERR_INVALID;
-  if (c->pages > 0 && (!c->k || !c->v)) return LIBTOPK_ERR_INVALID;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return LIBTOPK_ERR_INVALID;
+  if (e2m1) {  // older callers' structs end before these
+    const int64_t kbs[3] = {c->k_block_page_stride, c->k_block_head_stride,
+                            c->k_block_slot_stride};
+    const int64_t vbs[3] = {c->v_block_page_stride, c->v_block_head_stride,
+                            c->v_block_slot_stride};
+    p->blocks = c->dim / kBlockElems;
+    if (!check_rows(c->k_blocks, n, kbs, 1, p->blocks, 1, written, &p->kbs,
+                    &r->kb) ||
+        !check_rows(c->v_blocks, n, vbs, 1, p->blocks, 1, written, &p->vbs,
+                    &r->vb))
+      return LIBTOPK_ERR_INVALID;
+    p->kb = (const char*)c->k_blocks;
+    p->vb = (const char*)c->v_blocks;
+  }
   if (c->batch > 0 && (!c->table || !c->lens)) return LIBTOPK_ERR_INVALID;
   if (!aligned(c->table, 4) || !aligned(c->lens, 4))
     return LIBTOPK_ERR_INVALID;
   const int64_t tn[1] = {c->batch}, ts[1] = {c->table_stride * 4};
   const int64_t tlen = span(tn, ts, 1, (int64_t)c->table_width * 4);
   if (tlen < 0) return LIBTOPK_ERR_INVALID;
-  *k = Range(c->k, klen);
-  *v = Range(c->v, vlen);
-  *table = Range(c->table, tlen);
-  *lens = Range(c->lens, (int64_t)c->batch * 4);
+  r->table = Range(c->table, tlen);
+  r->lens = Range(c->lens, (int64_t)c->batch * 4);
   p->k = (const char*)c->k;
   p->v = (const char*)c->v;
-  p->ks = RowStrides{kb[0], kb[1], kb[2]};
-  p->vs = RowStrides{vb[0], vb[1], vb[2]};
   p->table = c->table;
   p->table_stride = c->table_stride;
   p->lens = c->lens;
@@ -313,7 +350,7 @@ int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
   p->heads = c->heads;
   p->dim = c->dim;
   p->cap = c->table_width * c->page;
-  p->row_bytes = c->dim * es;
+  p->row_bytes = (int32_t)row;
   return LIBTOPK_OK;
 }
 
@@ -361,11 +398,33 @@ int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
 
 const void* attend_fn(int q, int c, int dim, bool pg16, bool heads,
                       AttendNeeds* n) {
+  if (c == kE2m1)
+    return q == kBf16 ? attend_fn_dim<kBf16, kE2m1>(dim, pg16, heads, n)
+                      : attend_fn_dim<kF16, kE2m1>(dim, pg16, heads, n);
   if (q == kBf16)
     return c == kE4m3 ? attend_fn_dim<kBf16, kE4m3>(dim, pg16, heads, n)
                       : attend_fn_dim<kBf16, kBf16>(dim, pg16, heads, n);
   return c == kE4m3 ? attend_fn_dim<kF16, kE4m3>(dim, pg16, heads, n)
                     : attend_fn_dim<kF16, kF16>(dim, pg16, heads, n);
+}
+
+template <int Q, int C>
+const void* extend_fn_dim(int dim, int* lanes) {
+  *lanes = dim <= 64 ? 8 : dim <= 128 ? 16 : 32;
+  return dim <= 64    ? (const void*)&extend_kernel<Q, C, 8>
+         : dim <= 128 ? (const void*)&extend_kernel<Q, C, 16>
+                      : (const void*)&extend_kernel<Q, C, 32>;
+}
+// Lanes of a row, and the kernel, for inputs of type q and a cache of type c
+// (q's own or a narrower one).
+const void* extend_fn(int q, int c, int dim, int* lanes) {
+  if (q == kBf16)
+    return c == kE2m1   ? extend_fn_dim<kBf16, kE2m1>(dim, lanes)
+           : c == kE4m3 ? extend_fn_dim<kBf16, kE4m3>(dim, lanes)
+                        : extend_fn_dim<kBf16, kBf16>(dim, lanes);
+  return c == kE2m1   ? extend_fn_dim<kF16, kE2m1>(dim, lanes)
+         : c == kE4m3 ? extend_fn_dim<kF16, kE4m3>(dim, lanes)
+                      : extend_fn_dim<kF16, kF16>(dim, lanes);
 }
 
 constexpr int kMaxRuns = 1024;  // workgroups of an attention call
@@ -399,13 +458,14 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
                  const float* v_scale, const libtopk_ledger_t* ledger,
                  void* out, float* lse, libtopk_stream_t stream) {
   AttendParams p = {};
-  const Range none(nullptr, 0);
-  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
-  int rc = check_cache(cache, false, &p.c, &k, &v, &table, &lens);
+  CacheRanges at;
+  Range w(nullptr, 0), pos(nullptr, 0);
+  int rc = check_cache(cache, false, &p.c, &at);
   if (rc != LIBTOPK_OK) return rc;
   if (q_dtype != LIBTOPK_BF16 && q_dtype != LIBTOPK_F16)
     return LIBTOPK_ERR_INVALID;
-  if (cache->dtype != LIBTOPK_E4M3 && cache->dtype != q_dtype)
+  if (cache->dtype != LIBTOPK_E4M3 && cache->dtype != LIBTOPK_E2M1 &&
+      cache->dtype != q_dtype)
     return LIBTOPK_ERR_INVALID;
   if (q_heads < 1 || q_heads % cache->heads != 0) return LIBTOPK_ERR_INVALID;
   const int64_t rows = (int64_t)cache->batch * q_heads;
@@ -430,9 +490,10 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   if (qlen < 0) return LIBTOPK_ERR_INVALID;
   const Range outs[3] = {Range(out, rows * cache->dim * 2),
                          Range(lse, rows * 4), w};
-  const Range ins[7] = {Range(q, qlen), k, v, table, lens,
+  const Range ins[9] = {Range(q, qlen), at.k, at.v, at.table, at.lens,
                         Range(k_scale, k_scale ? cache->heads * 4 : 0),
-                        Range(v_scale, v_scale ? cache->heads * 4 : 0)};
+                        Range(v_scale, v_scale ? cache->heads * 4 : 0),
+                        at.kb, at.vb};
   for (int i = 0; i < 3; ++i) {
     for (const Range& r : ins)
       if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
@@ -456,7 +517,8 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   // Halves of a tile that lie in one page each get their addresses from
   // scalar registers (and 16 rows must lie within 2^31 bytes).
   const bool pg16 = cache->page % 16 == 0 && p.c.ks.slot < (1 << 27) &&
-                    p.c.vs.slot < (1 << 27);
+                    p.c.vs.slot < (1 << 27) && p.c.kbs.slot < (1 << 27) &&
+                    p.c.vbs.slot < (1 << 27);
   int dev_units = 0;
   rc = units_of(dev, &dev_units);
   if (rc != LIBTOPK_OK) return rc;
@@ -556,15 +618,16 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
                  int32_t* out_lens, int32_t* out_slots,
                  libtopk_stream_t stream) {
   SlotsParams p = {};
-  const Range none(nullptr, 0);
-  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
-  int rc = check_cache(cache, true, &p.c, &k, &v, &table, &lens);
+  CacheRanges at;
+  Range w(nullptr, 0), pos(nullptr, 0);
+  int rc = check_cache(cache, true, &p.c, &at);
   if (rc != LIBTOPK_OK) return rc;
+  if (cache->dtype == LIBTOPK_E2M1) return LIBTOPK_ERR_INVALID;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,
                     &pos);
   if (rc != LIBTOPK_OK) return rc;
   if (limit < 1 || sinks < 0 || recent < 0) return LIBTOPK_ERR_INVALID;
-  const int es = elem_size(cache->dtype);
+  const int es = unit_size(cache->dtype);
   if (new_batch_stride < 0 || new_head_stride < 0 ||
       new_batch_stride > kSpan || new_head_stride > kSpan ||
       (cache->batch > 1 && new_batch_stride * es % 16) ||
@@ -583,9 +646,9 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
   const int64_t rows = (int64_t)cache->batch * cache->heads;
   if (!launchable(rows, kBlock)) return LIBTOPK_ERR_INVALID;
   const Range outs[6] = {Range(out_lens, (int64_t)cache->batch * 4),
-                         Range(out_slots, rows * 4), w, pos, k, v};
-  const Range ins[5] = {Range(k_new, nlen), Range(v_new, nlen), table, lens,
-                        Range(seen, (int64_t)cache->batch * 4)};
+                         Range(out_slots, rows * 4), w, pos, at.k, at.v};
+  const Range ins[5] = {Range(k_new, nlen), Range(v_new, nlen), at.table,
+                        at.lens, Range(seen, (int64_t)cache->batch * 4)};
   for (int i = 0; i < 6; ++i) {
     for (const Range& r : ins)
       if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
@@ -616,10 +679,9 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
                 int32_t recent, const libtopk_ledger_t* after,
                 int32_t* out_lens, libtopk_stream_t stream) {
   SlotsParams p = {};
-  const Range none(nullptr, 0);
-  Range k = none, v = none, table = none, lens = none, w = none, pos = none;
-  Range w2 = none, pos2 = none;
-  int rc = check_cache(cache, true, &p.c, &k, &v, &table, &lens);
+  CacheRanges at;
+  Range w(nullptr, 0), pos(nullptr, 0), w2(nullptr, 0), pos2(nullptr, 0);
+  int rc = check_cache(cache, true, &p.c, &at);
   if (rc != LIBTOPK_OK) return rc;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, false, &p.w, &w,
                     &pos);
@@ -636,16 +698,16 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
     return LIBTOPK_ERR_INVALID;
   if (ledger->slots < p.c.cap) p.c.cap = ledger->slots;
   const int64_t rows = (int64_t)cache->batch * cache->heads;
-  const Range outs[5] = {Range(out_lens, (int64_t)cache->batch * 4), w2, pos2,
-                         k, v};
-  const Range ins[5] = {w, pos, table, lens,
+  const Range outs[7] = {Range(out_lens, (int64_t)cache->batch * 4), w2, pos2,
+                         at.k, at.v, at.kb, at.vb};
+  const Range ins[5] = {w, pos, at.table, at.lens,
                         Range(seen, (int64_t)cache->batch * 4)};
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 7; ++i) {
     for (const Range& r : ins)
       if (outs[i].meets(r)) return LIBTOPK_ERR_INVALID;
-    for (int j = 0; j < i; ++j)
-      if (!(i == 4 && j == 3) && outs[i].meets(outs[j]))
-        return LIBTOPK_ERR_INVALID;
+    // the cache's own arrays may interleave
+    for (int j = 0; j < (i < 3 ? i : 3); ++j)
+      if (outs[i].meets(outs[j])) return LIBTOPK_ERR_INVALID;
   }
   p.seen = seen;
   p.sinks = sinks;
@@ -679,12 +741,12 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
                        state_bytes,
                 1, &work);
   if (rc != LIBTOPK_OK) return rc;
-  char* at = work.base;
-  p.pairs = (int32_t*)at;
-  p.moves = (int32_t*)(at += pair_bytes);
-  p.hist = (uint32_t*)(at += move_bytes);
-  p.counts = (int4*)(at += hist_words * 8);
-  p.state = (int2*)(at += count_bytes);
+  char* area = work.base;
+  p.pairs = (int32_t*)area;
+  p.moves = (int32_t*)(area += pair_bytes);
+  p.hist = (uint32_t*)(area += move_bytes);
+  p.counts = (int4*)(area += hist_words * 8);
+  p.state = (int2*)(area += count_bytes);
   const unsigned wide = (unsigned)(rows * p.chunks);
   if (is_long) {
     rc = fill((uint64_t*)p.hist, hist_words, 0, s);
@@ -713,6 +775,161 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
                 dim3((unsigned)((units + kBlock - 1) / kBlock),
                      (unsigned)(rows < 65535 ? rows : 65535)),
                 kBlock, p, s);
+}
+
+int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
+                 const libtopk_ledger_t* ledger, int32_t* out_lens,
+                 libtopk_stream_t stream) {
+  ExtendParams p = {};
+  CacheRanges at;
+  Range w(nullptr, 0), pos(nullptr, 0);
+  int rc = check_cache(cache, true, &p.c, &at);
+  if (rc != LIBTOPK_OK) return rc;
+  if (ledger) {
+    rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,
+                      &pos);
+    if (rc != LIBTOPK_OK) return rc;
+    if (ledger->slots < p.c.cap) p.c.cap = ledger->slots;
+  }
+  if (!tokens) return LIBTOPK_ERR_INVALID;
+  const libtopk_tokens_t& t = *tokens;
+  if ((t.dtype != LIBTOPK_BF16 && t.dtype != LIBTOPK_F16) ||
+      (cache->dtype != t.dtype && cache->dtype != LIBTOPK_E4M3 &&
+       cache->dtype != LIBTOPK_E2M1))
+    return LIBTOPK_ERR_INVALID;
+  const int32_t dim = cache->dim, q_heads = t.q ? t.q_heads : 0;
+  if (t.tokens < 0 || (t.q && t.q_heads < 1) || dim % kUnit != 0 ||
+      t.rot < 0 || t.rot > dim || t.rot % 16 != 0)
+    return LIBTOPK_ERR_INVALID;
+  if ((t.q_norm || t.k_norm) &&
+      ((t.norm_dtype != LIBTOPK_F32 && t.norm_dtype != t.dtype) ||
+       !(t.eps >= 0.0f)))
+    return LIBTOPK_ERR_INVALID;
+  const int norm_bytes = t.norm_dtype == LIBTOPK_F32 ? 4 : 2;
+  if (!aligned(t.q_norm, (uintptr_t)norm_bytes) ||
+      !aligned(t.k_norm, (uintptr_t)norm_bytes) || !aligned(t.freqs, 4) ||
+      !aligned(t.k_scale, 4) || !aligned(t.v_scale, 4) ||
+      !aligned(t.starts, 4) || !aligned(t.seen, 4) || !aligned(out_lens, 4) ||
+      (t.rot > 0 && !t.freqs))
+    return LIBTOPK_ERR_INVALID;
+  // Rows of the new tokens' arrays: [tokens][heads][dim].
+  auto extent = [&](const void* x, int64_t heads, int64_t ts, int64_t hs,
+                    bool written, int64_t (&bytes)[2], Range* r) {
+    if (ts < 0 || hs < 0 || ts > kSpan || hs > kSpan ||
+        (t.tokens > 1 && ts % 8) || (heads > 1 && hs % 8))
+      return false;
+    const int64_t n[2] = {t.tokens, heads};
+    bytes[0] = ts * 2;
+    bytes[1] = hs * 2;
+    const int64_t len = span(n, bytes, 2, (int64_t)dim * 2);
+    if (len < 0 || (len > 0 && !x) || !aligned(x, 16)) return false;
+    if (written && len > 0 && !apart(n, bytes, 2, (int64_t)dim * 2))
+      return false;
+    *r = Range(x, len);
+    return true;
+  };
+  Range q(nullptr, 0), k(nullptr, 0), v(nullptr, 0), out(nullptr, 0);
+  int64_t qs[2] = {0, 0}, ks[2], vs[2], os[2] = {0, 0};
+  if (!extent(t.k, cache->heads, t.k_token_stride, t.k_head_stride, false, ks,
+              &k) ||
+      !extent(t.v, cache->heads, t.v_token_stride, t.v_head_stride, false, vs,
+              &v) ||
+      (t.q &&
+       (!extent(t.q, q_heads, t.q_token_stride, t.q_head_stride, false, qs,
+                &q) ||
+        !extent(t.q_out, q_heads, t.q_out_token_stride, t.q_out_head_stride,
+                true, os, &out))))
+    return LIBTOPK_ERR_INVALID;
+  if (cache->batch == 0) return LIBTOPK_OK;
+  if (!t.starts || !out_lens) return LIBTOPK_ERR_INVALID;
+  // Queries may be turned where they are, also between the keys and values
+  // of one array: with the same stride from token to token, a token's rows of
+  // the two lie apart within it.
+  const bool same = t.q && t.q == t.q_out && qs[0] == os[0] && qs[1] == os[1];
+  auto beside = [&](const void* x, int64_t heads, const int64_t (&s)[2]) {
+    if (!same || s[0] != os[0] || t.tokens < 1) return false;
+    const int64_t mine = (q_heads - 1) * os[1] + (int64_t)dim * 2;
+    const int64_t its = (heads - 1) * s[1] + (int64_t)dim * 2;
+    if (t.tokens == 1 || s[0] < 1) return false;
+    const uintptr_t a = (uintptr_t)t.q_out, b = (uintptr_t)x;
+    const int64_t d = b >= a ? (int64_t)((b - a) % (uintptr_t)s[0])
+                             : (s[0] - (int64_t)((a - b) % (uintptr_t)s[0])) %
+                                   s[0];
+    return d >= mine && d + its <= s[0];
+  };
+  const bool beside_k = beside(t.k, cache->heads, ks);
+  const bool beside_v = beside(t.v, cache->heads, vs);
+  const int64_t batch = cache->batch;
+  const Range outs[8] = {Range(out_lens, batch * 4), out, w, pos, at.k, at.v,
+                         at.kb, at.vb};
+  const Range ins[12] = {
+      q, k, v, at.table, at.lens,
+      Range(t.starts, (batch + 1) * 4),
+      Range(t.seen, t.seen ? batch * 4 : 0),
+      Range(t.q_norm, t.q_norm ? (int64_t)dim * norm_bytes : 0),
+      Range(t.k_norm, t.k_norm ? (int64_t)dim * norm_bytes : 0),
+      Range(t.freqs, t.freqs ? (int64_t)t.rot / 2 * 4 : 0),
+      Range(t.k_scale, t.k_scale ? (int64_t)cache->heads * 4 : 0),
+      Range(t.v_scale, t.v_scale ? (int64_t)cache->heads * 4 : 0)};
+  for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < 12; ++j)
+      if (!(i == 1 && ((same && j == 0) || (beside_k && j == 1) ||
+                       (beside_v && j == 2))) &&
+          outs[i].meets(ins[j]))
+        return LIBTOPK_ERR_INVALID;
+    // the cache's own arrays may interleave
+    for (int j = 0; j < (i < 4 ? i : 4); ++j)
+      if (outs[i].meets(outs[j])) return LIBTOPK_ERR_INVALID;
+  }
+  p.q = (const char*)t.q;
+  p.k = (const char*)t.k;
+  p.v = (const char*)t.v;
+  p.q_out = (char*)t.q_out;
+  p.qt = qs[0];
+  p.qh = qs[1];
+  p.kt = ks[0];
+  p.kh = ks[1];
+  p.vt = vs[0];
+  p.vh = vs[1];
+  p.ot = os[0];
+  p.oh = os[1];
+  p.starts = t.starts;
+  p.seen = t.seen;
+  p.q_norm = t.q ? t.q_norm : nullptr;
+  p.k_norm = t.k_norm;
+  p.freqs = t.freqs;
+  p.k_scale = t.k_scale;
+  p.v_scale = t.v_scale;
+  p.out_lens = out_lens;
+  p.tokens = t.tokens;
+  p.q_heads = q_heads;
+  p.norm_type = t.norm_dtype;
+  p.half = t.rot / 2;
+  p.interleaved = t.interleaved != 0;
+  p.eps = t.eps;
+  p.dim = dim;
+  int dev = 0;
+  rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  int lanes = 0;
+  const void* fn = extend_fn(t.dtype, cache->dtype, dim, &lanes);
+  const int64_t rows = (int64_t)q_heads + 2 * (int64_t)cache->heads;
+  const int64_t steps = (rows * lanes + kBlock - 1) / kBlock;
+  int units = 0;
+  rc = units_of(dev, &units);
+  if (rc != LIBTOPK_OK) return rc;
+  // Few tokens are dealt out row by row.
+  int64_t splits = 1;
+  if (t.tokens > 0) {
+    splits = ((int64_t)units * 4 + t.tokens - 1) / t.tokens;
+    if (splits > steps) splits = steps;
+  }
+  p.splits = (int32_t)splits;
+  int64_t grid = (int64_t)t.tokens * splits;
+  const int64_t least = (batch + kBlock - 1) / kBlock;
+  if (grid < least) grid = least;
+  if (!launchable(grid, kBlock)) return LIBTOPK_ERR_INVALID;
+  return launch(fn, dim3((unsigned)grid), kBlock, p, (hipStream_t)stream);
 }
 
 void cache_release(void) {

@@ -124,6 +124,21 @@ __device__ __forceinline__ int widen2(int v) {
         int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, HI));
 }
 
+// Two of the eight e2m1 values of a dword times their block's scale, in
+// bfloat16 (exact: it has e8m0's range).  The instruction takes the scale as
+// the exponent bits of a float.
+template <int BYTE>
+__device__ __forceinline__ int widen2(int v, int scale) {
+  return __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
+                                     (unsigned)v, __int_as_float(scale), BYTE));
+}
+__device__ __forceinline__ void widen8(int v, int scale, int (&d)[4]) {
+  d[0] = widen2<0>(v, scale);
+  d[1] = widen2<1>(v, scale);
+  d[2] = widen2<2>(v, scale);
+  d[3] = widen2<3>(v, scale);
+}
+
 // A weight (>= 0 or NaN) as the sum of three bfloat16 numbers, the upper
 // halves of p; 2^-22 of it is left.  Each but the last is the largest number
 // below what is left to hold, so that none is negative and none is 0 unless
@@ -230,19 +245,28 @@ struct Attend {
   // wave to a SIMD instead of two, with twice the bytes in flight each.
   static constexpr int WAVES = NC > 4 ? 4 : 8;
   static constexpr int THREADS = WAVES * kWave;
-  static constexpr int ES = CT == kE4m3 ? 1 : 2;
-  static constexpr int KL = CT == kE4m3 ? (NC + 1) / 2 : NC;  // K loads a half
+  static constexpr int EB = CT == kE2m1 ? 4 : CT == kE4m3 ? 8 : 16;  // bits
+  static constexpr int LE = 128 / EB;  // elements of a 16-byte K load
+  static constexpr int KL = (NC * 32 + 4 * LE - 1) / (4 * LE);  // a half
   static constexpr int VE = NC == 2 ? 4 : 8;
-  static constexpr int VD = VE * ES / 4;             // dwords of a V load
+  static constexpr int VD = (VE * EB + 31) / 32;     // dwords of a V load
   static constexpr int NB = (NC * 32 + 16 * VE - 1) / (16 * VE);
   static constexpr int COLS = NB * 16 * VE;
   // The first chunk that a row of this class can leave short.
   static constexpr int SHORT = NC == 2 ? 0 : NC == 3 ? 2 : NC == 4 ? 3
                                : NC == 6 ? 4 : 6;
   static constexpr int last_chunk(int load) {
-    return (load * 64 + 63) / ES / 32;
+    return (load * 64 + 63) * 8 / EB / 32;
   }
-  static constexpr int QL = CT == kE4m3 ? 2 * KL : NC;  // q fragments
+  // Query fragments: LE / 8 of them meet a K load.  Over 4-bit rows, which
+  // become bfloat16, float16 queries enter as two bfloat16 numbers each.
+  static constexpr int QK = LE / 8;
+  static constexpr int QL = QK * KL;
+  static constexpr bool kTwoParts = CT == kE2m1 && QT == kF16;
+  // The first of the eight elements of fragment f that lane group q holds.
+  __device__ static int q_elem(int f, int q) {
+    return f / QK * (4 * LE) + q * LE + f % QK * 8;
+  }
 
   struct Ids {
     int32_t id[PG16 ? 2 : 10];  // K halves; without PG16 then the 8 V slots
@@ -308,7 +332,7 @@ __global__ __launch_bounds__((Attend<QT, CT, NC, PG16>::THREADS),
 attend_kernel(AttendParams p) {
   typedef Attend<QT, CT, NC, PG16> A;
   constexpr int kAttWaves = A::WAVES, kAttThreads = A::THREADS;
-  constexpr int ES = A::ES, KL = A::KL, VE = A::VE, VD = A::VD, NB = A::NB;
+  constexpr int EB = A::EB, KL = A::KL, VE = A::VE, VD = A::VD, NB = A::NB;
   constexpr int COLS = A::COLS, QL = A::QL;
   __shared__ typename A::Lds lds;
   const CacheParams& c = p.c;
@@ -524,6 +548,8 @@ attend_kernel(AttendParams p) {
     const int32_t tiles = (len + kTileSlots - 1) / kTileSlots;
     const char* kh = c.k + h * c.ks.head;
     const char* vh = c.v + h * c.vs.head;
+    const char* kbh = CT == kE2m1 ? c.kb + h * c.kbs.head : nullptr;
+    const char* vbh = CT == kE2m1 ? c.vb + h * c.vbs.head : nullptr;
     Share cur = {b, hi, len, share < 0 ? r0 / per : wg - share,
                  share < 0 ? (r1 - 1) / per : wg - share + cuts - 1,
                  s0 - r0, 0, held, true};
@@ -536,14 +562,13 @@ attend_kernel(AttendParams p) {
 
     // Query fragments: those of 8-bit rows pair up to match 16-byte loads.
     // Columns past the row's queries repeat the last and are not used.
-    Frag qf[QL];
+    Frag qf[QL], qh[A::kTwoParts ? QL : 1], ql[A::kTwoParts ? QL : 1];
     {
       const char* from = p.q + b * p.qb +
                          (h * p.group + g0 + min(n, queries - 1)) * p.qh;
 #pragma unroll
       for (int f = 0; f < QL; ++f) {
-        const int d = CT == kE4m3 ? f / 2 * 64 + q * 16 + f % 2 * 8
-                                  : f * 32 + q * 8;
+        const int d = A::q_elem(f, q);
         const v4i x = *(const v4i*)(from + (d < c.dim ? d * 2 : 0));
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[f].d[e] = x[e];
@@ -576,6 +601,8 @@ attend_kernel(AttendParams p) {
 
       v4i kr[2][KL];
       int vr[NB][8][VD];
+      // Scales of 4-bit rows, a block for each K load and V load.
+      int ksc[2][CT == kE2m1 ? KL : 1], vsc[NB][CT == kE2m1 ? 8 : 1];
       auto load_k = [&](const typename A::Ids& id) {
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
@@ -591,6 +618,19 @@ attend_kernel(AttendParams p) {
             const int at = k * 64 + q * 16;
             const bool in = A::last_chunk(k) < A::SHORT || at < c.row_bytes;
             kr[tt][k] = ld_once<v4i>(row + (in ? at : 0));
+          }
+          if constexpr (CT == kE2m1) {
+            const char* sc =
+                PG16 ? kbh + (int64_t)pg * c.kbs.page +
+                           (int64_t)id.place[tt] * c.kbs.slot +
+                           (uint32_t)(n * (int32_t)c.kbs.slot)
+                     : kbh + (int64_t)pg * c.kbs.page +
+                           (int64_t)id.place[tt] * c.kbs.slot;
+#pragma unroll
+            for (int k = 0; k < KL; ++k) {
+              const int at = k * 4 + q;
+              ksc[tt][k] = ld_once<uint8_t>(sc + (at < c.blocks ? at : 0));
+            }
           }
         }
       };
@@ -608,7 +648,7 @@ attend_kernel(AttendParams p) {
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
             // Columns past the row repeat its first; they are never stored.
-            const int col = (nb * 16 + n) * VE * ES;
+            const int col = (nb * 16 + n) * VE * EB / 8;
             const char* src = row + (col < c.row_bytes ? col : 0);
             if constexpr (VD == 4) {
               const v4i x = ld_once<v4i>(src);
@@ -618,8 +658,23 @@ attend_kernel(AttendParams p) {
               const v2i x = ld_once<v2i>(src);
               vr[nb][j][0] = x[0];
               vr[nb][j][1] = x[1];
-            } else {
+            } else if constexpr (VE * EB == 32) {
               vr[nb][j][0] = ld_once<int>(src);
+            } else {
+              vr[nb][j][0] = ld_once<uint16_t>(src);
+            }
+          }
+          if constexpr (CT == kE2m1) {
+            const char* sc =
+                PG16 ? vbh + (int64_t)pg * c.vbs.page +
+                           (int64_t)id.place[at] * c.vbs.slot +
+                           (uint32_t)((q * 4 + j % 4) * (int32_t)c.vbs.slot)
+                     : vbh + (int64_t)pg * c.vbs.page +
+                           (int64_t)id.place[at] * c.vbs.slot;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const int blk = (nb * 16 + n) * VE / kBlockElems;
+              vsc[nb][j] = ld_once<uint8_t>(sc + (blk < c.blocks ? blk : 0));
             }
           }
         }
@@ -634,10 +689,25 @@ attend_kernel(AttendParams p) {
       // first tile is on its way).
 #pragma unroll
       for (int f = 0; f < QL; ++f) {
-        const int d = CT == kE4m3 ? f / 2 * 64 + q * 16 + f % 2 * 8
-                                  : f * 32 + q * 8;
+        const int d = A::q_elem(f, q);
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[f].d[e] = d < c.dim ? qf[f].d[e] : 0;
+      }
+      if constexpr (A::kTwoParts) {
+        // float16's 11 bits as 8 and the rest (exact; an infinity has none).
+#pragma unroll
+        for (int f = 0; f < QL; ++f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const f16x2 x = __builtin_bit_cast(f16x2, qf[f].d[e]);
+            const float a = (float)x[0], b = (float)x[1];
+            const bf16x2 hi = {(__bf16)a, (__bf16)b};
+            const float a1 = (float)hi[0], b1 = (float)hi[1];
+            qh[f].d[e] = __builtin_bit_cast(int, hi);
+            ql[f].d[e] = pack2<kBf16>(a == a1 ? 0.0f : a - a1,
+                                      b == b1 ? 0.0f : b - b1);
+          }
+        }
       }
 
       auto step = [&](auto more) {
@@ -654,7 +724,19 @@ attend_kernel(AttendParams p) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) x[e] = in ? x[e] : 0;
             }
-            if constexpr (CT == kE4m3) {
+            if constexpr (CT == kE2m1) {
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                Frag a;
+                widen8(x[f], ksc[tt][k] << 23, a.d);
+                if constexpr (A::kTwoParts) {
+                  s[tt] = mma<kBf16>(a, qh[4 * k + f], s[tt]);
+                  s[tt] = mma<kBf16>(a, ql[4 * k + f], s[tt]);
+                } else {
+                  s[tt] = mma<kBf16>(a, qf[4 * k + f], s[tt]);
+                }
+              }
+            } else if constexpr (CT == kE4m3) {
 #pragma unroll
               for (int f = 0; f < 2; ++f) {
                 const Frag a = {{widen2<QT, false>(x[2 * f]),
@@ -697,6 +779,13 @@ attend_kernel(AttendParams p) {
 #pragma unroll
               for (int e = 0; e < VD; ++e)
                 vr[nb][j][e] = ok[j] ? vr[nb][j][e] : 0;
+          if constexpr (CT == kE2m1) {  // (0 times a scale of NaN is NaN)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                vsc[nb][j] = ok[j] ? vsc[nb][j] : 0;
+          }
         }
         float x[8];
         float hi_x = -INFINITY;
@@ -775,7 +864,12 @@ attend_kernel(AttendParams p) {
             int y[8][VE / 2];  // 8 slots of VE elements
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              if constexpr (CT == kE4m3) {
+              if constexpr (CT == kE2m1) {
+                int d[4];
+                widen8(vr[nb][j][0], vsc[nb][j] << 23, d);
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e) y[j][e] = d[e];
+              } else if constexpr (CT == kE4m3) {
 #pragma unroll
                 for (int e = 0; e < VD; ++e) {
                   y[j][2 * e] = widen2<kBf16, false>(vr[nb][j][e]);

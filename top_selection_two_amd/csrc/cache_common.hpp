@@ -8,7 +8,9 @@
 namespace ltk {
 
 // Element types, as in include/libtopk.h.
-constexpr int kBf16 = 0, kF16 = 1, kE4m3 = 2;
+constexpr int kBf16 = 0, kF16 = 1, kE4m3 = 2, kF32 = 3, kE2m1 = 4;
+constexpr int kMaxDim = 256;
+constexpr int kBlockElems = 32;  // of a 4-bit row that share a scale
 
 struct CacheParams {
   const char* k;
@@ -22,6 +24,11 @@ struct CacheParams {
   int32_t batch, heads, dim;
   int32_t cap;        // slots that the table (and the ledger) can name
   int32_t row_bytes;  // dim elements
+  // Scales of 4-bit rows: a byte for each 32 elements (bytes throughout).
+  const char* kb;
+  const char* vb;
+  RowStrides kbs, vbs;
+  int32_t blocks;     // of a row; 0 where rows have none
 };
 
 struct LedgerParams {

@@ -550,6 +550,17 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(SlotsParams p) {
         (const v4i*)(c.k + row_offset(c.ks, jf, h, zf) + off));
     const v4i y = __builtin_nontemporal_load(
         (const v4i*)(c.v + row_offset(c.vs, jf, h, zf) + off));
+    if (c.blocks > 0 && off == 0) {  // the scales of 4-bit rows go along
+      const char* kf = c.kb + row_offset(c.kbs, jf, h, zf);
+      const char* vf = c.vb + row_offset(c.vbs, jf, h, zf);
+      char* kt = const_cast<char*>(c.kb + row_offset(c.kbs, it, h, zt));
+      char* vt = const_cast<char*>(c.vb + row_offset(c.vbs, it, h, zt));
+      for (int e = 0; e < c.blocks; ++e) {
+        const char s = kf[e], z = vf[e];
+        kt[e] = s;
+        vt[e] = z;
+      }
+    }
     __builtin_nontemporal_store(
         x, (v4i*)const_cast<char*>(c.k + row_offset(c.ks, it, h, zt) + off));
     __builtin_nontemporal_store(
