@@ -634,6 +634,64 @@ void cache_release(void);
  * the cache_* calls on `stream` with pseudo-random words. */
 int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
 
+/* ---------------------------------------------------------------------------
+ * sample_logits -- a token for each row of logits.
+ *
+ * With x the row's logits (NaN counts as -infinity, -0 as 0), M the largest,
+ * w_i = exp((x_i - M) / temperature), and the order "larger logit first, of
+ * equal ones the lower index first":
+ *
+ *   1. the first top_k logits are kept (all, if top_k < 1);
+ *   2. of these the shortest prefix, of one at least, whose weights sum to
+ *      top_p times the sum of all of these (all, unless top_p < 1);
+ *   3. of these those with w_i >= min_p (min_p above 1 counts as 1; all, if
+ *      min_p is not above 0);
+ *   4. token = the lowest index i of a kept logit where the sum of the kept
+ *      weights up to and with i exceeds u times the sum of all kept weights.
+ *
+ * logprob = ln(w_token / sum of the kept weights), what the token was drawn
+ * with.  A temperature that is not above 0 takes the first of the largest
+ * logits, with logprob 0.  A row without a logit above -infinity gets token -1
+ * and logprob -infinity; where M is +infinity the logits that equal it have
+ * weight 1 and the others none.  u is read as within [0, 1) (NaN as 0): at its
+ * upper end the last kept token that has weight is taken.
+ *
+ * Weights are computed in 64 bits and added in units of at most
+ * 2^-(62 - ceil(log2 cols)) of the largest; results do not depend on the order
+ * in which workgroups run.
+ *
+ *   logits   device, dtype[rows][cols] (LIBTOPK_F32, _BF16 or _F16), rows ld
+ *            elements apart, ld >= cols, at any alignment of the type
+ *   rows     0 <= rows < LIBTOPK_MAX_SAMPLE_ROWS
+ *   cols     1 <= cols <= LIBTOPK_MAX_LOGITS
+ *   how      each setting from a device array of a number a row, or, where
+ *            that is NULL, the one number given for all rows
+ *   u        device, float32[rows], uniform random numbers
+ *   tokens   device, int64[rows]
+ *   logprobs device, float32[rows]
+ *
+ * Errors: LIBTOPK_ERR_INVALID for a NULL or misaligned pointer, a size or type
+ * outside the above, or an output that overlaps an input or the other output.
+ */
+#define LIBTOPK_MAX_LOGITS (1 << 24)
+#define LIBTOPK_MAX_SAMPLE_ROWS (1 << 22)
+
+typedef struct libtopk_sampling {
+    const float *temperature; /* device, float32[rows], or NULL */
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+    float temperature_all;
+    int32_t top_k_all;
+    float top_p_all;
+    float min_p_all;
+} libtopk_sampling_t;
+
+int sample_logits(const void *logits, int32_t dtype, int64_t rows,
+                  int64_t cols, int64_t ld, const libtopk_sampling_t *how,
+                  const float *u, int64_t *tokens, float *logprobs,
+                  libtopk_stream_t stream);
+
 /* Static, human-readable text for a status code (never NULL). */
 const char *libtopk_strerror(int status);
 

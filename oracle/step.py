@@ -117,6 +117,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     """(token, log probability) of one row of numbers, in 64 bits; settings as
     float32 holds them."""
     t, p, m = (float(np.float32(x)) for x in (temperature, top_p, min_p))
+    top_k = int(top_k)
     x = [-math.inf if a != a else float(a) for a in logits]
     top = max(x)
     if top == -math.inf:
@@ -126,8 +127,11 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         return order[0], 0.0
 
     def weight(i):
-        return 1.0 if x[i] == top else math.exp((x[i] - top) / t) \
-            if top < math.inf else 0.0
+        if x[i] == top:
+            return 1.0
+        if top == math.inf or x[i] == -math.inf:
+            return 0.0
+        return math.exp((x[i] - top) / t)
 
     if top_k > 0:
         order = order[:top_k]
@@ -135,7 +139,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     if p < 1:
         need, part = p * math.fsum(w), 0.0
         for n, a in enumerate(w):
-            part = math.fsum(w[:n + 1]) if n < 64 else part + a
+            part += a
             if part >= need:
                 break
         order, w = order[:n + 1], w[:n + 1]

@@ -40,6 +40,9 @@ if the library is not built, importing this package raises.
     cache_evict(k, v, table, lens, seen, weights, positions, keep, ...)
                     -> (weights [B, H, keep], positions, lens [B]): the cache
                        cut back to the slots of the largest weight
+    sample(logits, u, temperature, top_k, top_p, min_p)
+                    -> (int64 tokens [B], logprobs [B]): a token for each row
+                       of logits from a given random number
 """
 from __future__ import annotations
 
@@ -85,6 +88,16 @@ class LedgerStruct(ctypes.Structure):
                    ("weights_batch_stride", "weights_head_stride",
                     "positions_batch_stride", "positions_head_stride")]
                 + [("slots", ctypes.c_int32)])
+
+
+class SamplingStruct(ctypes.Structure):
+    """libtopk_sampling_t of include/libtopk.h."""
+    _fields_ = ([(n, _VP) for n in ("temperature", "top_k", "top_p",
+                                    "min_p")]
+                + [("temperature_all", ctypes.c_float),
+                   ("top_k_all", ctypes.c_int32),
+                   ("top_p_all", ctypes.c_float),
+                   ("min_p_all", ctypes.c_float)])
 
 
 class TokensStruct(ctypes.Structure):
@@ -138,6 +151,9 @@ SIGNATURES = {
                       _VP], ctypes.c_int),
     "cache_release": ([], None),
     "cache_debug_scramble": ([_VP, ctypes.c_uint64], ctypes.c_int),
+    "sample_logits": ([_VP, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                       ctypes.c_int64, ctypes.POINTER(SamplingStruct), _VP,
+                       _VP, _VP, _VP], ctypes.c_int),
     "libtopk_strerror": ([ctypes.c_int], ctypes.c_char_p),
     "libtopk_max_k": ([], ctypes.c_int),
     "libtopk_set_grid": ([ctypes.c_int32], ctypes.c_int),
@@ -626,3 +642,22 @@ def cache_extend(k_new, v_new, k, v, table, lens, starts, seen=None, q=None,
                            freqs, interleaved, q_norm, k_norm, eps, k_scale,
                            v_scale, weights, positions, k_blocks, v_blocks,
                            out)
+
+
+# ------------------------------------------------------------------ sampling
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
+           out=None):
+    """A token for each row of logits [B, V] (float32, bfloat16 or float16,
+    unit column stride) from the random numbers u [B], float32 in [0, 1) (see
+    sample_logits in include/libtopk.h).
+
+    Of a row's logits divided by its temperature the top_k largest are kept
+    (0: all), of these the shortest prefix with top_p of their probability,
+    and of these the ones with at least min_p times the largest's probability;
+    the token is the one where the running sum of what is left, in the order
+    of the row, passes u.  Equal logits rank by index.  A temperature of 0
+    takes the largest.  Each setting is a number, or a tensor [B] (float32,
+    top_k int32).  Returns (tokens int64 [B], logprobs float32 [B], with which
+    they were drawn); out may be given as that pair of tensors.  A row without
+    a logit above -infinity gets -1.  No gradient passes through either."""
+    return _binding.sample(logits, u, temperature, top_k, top_p, min_p, out)

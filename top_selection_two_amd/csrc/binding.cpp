@@ -583,6 +583,87 @@ PyObject* extend(PyObject* const* a, Py_ssize_t n) {
   return Py_BuildValue("(NN)", x, THPVariable_Wrap(std::move(out)));
 }
 
+// (logits, u, temperature, top_k, top_p, min_p, out)
+PyObject* sample(PyObject* const* a, Py_ssize_t n) {
+  expect_args(n, 7);
+  const Tensor& x = tensor(a[0], "logits");
+  const at::ScalarType t = x.scalar_type();
+  if (t != at::kFloat && t != at::kBFloat16 && t != at::kHalf)
+    type_error(std::string("logits: expected float32, bfloat16 or float16, "
+                           "got ") + c10::toString(t));
+  if (x.dim() != 2) value_error("logits: expected [rows, vocabulary]");
+  const int64_t rows = x.size(0), cols = x.size(1);
+  if (cols < 1) value_error("logits: expected at least one column");
+  expect_unit(x, "logits");
+  const int64_t ld = rows > 1 ? x.stride(0) : cols;
+  if (ld < cols) value_error("logits: expected rows that lie apart");
+  const at::Device device = x.device();
+  const Tensor& u = tensor(a[1], "u");
+  expect(u, "u", at::kFloat, {rows}, device);
+  libtopk_sampling_t how = {};
+  const char* names[4] = {"temperature", "top_k", "top_p", "min_p"};
+  const void* rowwise[4] = {};
+  double all[4] = {};
+  for (int i = 0; i < 4; ++i) {
+    PyObject* o = a[2 + i];
+    if (THPVariable_Check(o)) {
+      const Tensor& s = THPVariable_Unpack(o);
+      expect(s, names[i], i == 1 ? at::kInt : at::kFloat, {rows}, device);
+      rowwise[i] = pointer(s);
+    } else if (i == 1) {
+      how.top_k_all = integer(o, names[i], 0);
+    } else {
+      all[i] = PyFloat_AsDouble(o);
+      if (PyErr_Occurred()) throw PythonError{};
+      if (!(all[i] >= 0))
+        value_error(std::string(names[i]) + ": expected at least 0");
+    }
+  }
+  how.temperature = (const float*)rowwise[0];
+  how.top_k = (const int32_t*)rowwise[1];
+  how.top_p = (const float*)rowwise[2];
+  how.min_p = (const float*)rowwise[3];
+  how.temperature_all = (float)all[0];
+  how.top_p_all = (float)all[2];
+  how.min_p_all = (float)all[3];
+  if (a[6] != Py_None && (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2))
+    type_error("out: expected a pair of tensors");
+  const libtopk_stream_t stream = stream_of(device);
+  Tensor tokens, logprobs;
+  if (a[6] == Py_None) {
+    tokens = at::empty({rows}, u.options().dtype(at::kLong));
+    logprobs = at::empty({rows}, u.options());
+  } else {
+    tokens = tensor(PyTuple_GET_ITEM(a[6], 0), "out[0]");
+    logprobs = tensor(PyTuple_GET_ITEM(a[6], 1), "out[1]");
+    expect(tokens, "out[0]", at::kLong, {rows}, device);
+    expect(logprobs, "out[1]", at::kFloat, {rows}, device);
+  }
+  const c10::DeviceGuard guard(device);
+  check(sample_logits(pointer(x),
+                      t == at::kFloat      ? LIBTOPK_F32
+                      : t == at::kBFloat16 ? LIBTOPK_BF16
+                                           : LIBTOPK_F16,
+                      rows, cols, ld, &how, (const float*)pointer(u),
+                      (int64_t*)pointer(tokens), (float*)pointer(logprobs),
+                      stream),
+        "sample_logits");
+  if (a[6] != Py_None) {
+    changed(tokens);
+    changed(logprobs);
+  } else if (at::GradMode::is_enabled() && x.requires_grad()) {
+    // There is no backward pass: one that is asked for is an error.
+    torch::autograd::edge_list edges;
+    edges.push_back(torch::autograd::impl::gradient_edge(x));
+    torch::autograd::set_history(
+        logprobs, std::make_shared<torch::autograd::NotImplemented>(
+                      "sample_logits", std::move(edges)));
+  }
+  PyObject* y = THPVariable_Wrap(std::move(tokens));
+  PyObject* z = THPVariable_Wrap(std::move(logprobs));
+  return Py_BuildValue("(NN)", y, z);
+}
+
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   try {
@@ -609,6 +690,7 @@ PyMethodDef methods[] = {LTK_ENTRY(attend),
                          LTK_ENTRY(append),
                          LTK_ENTRY(evict),
                          LTK_ENTRY(extend),
+                         LTK_ENTRY(sample),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
