@@ -907,25 +907,26 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
   p.half = t.rot / 2;
   p.interleaved = t.interleaved != 0;
   p.eps = t.eps;
-  p.dim = dim;
+  p.inv_dim = 1.0 / dim;
   int dev = 0;
   rc = current_device(&dev);
   if (rc != LIBTOPK_OK) return rc;
   int lanes = 0;
   const void* fn = extend_fn(t.dtype, cache->dtype, dim, &lanes);
-  const int64_t rows = (int64_t)q_heads + 2 * (int64_t)cache->heads;
-  const int64_t steps = (rows * lanes + kBlock - 1) / kBlock;
+  const int64_t each = kWave / lanes;  // rows at a time
+  const int64_t groups = (q_heads + each - 1) / each +
+                         2 * ((cache->heads + each - 1) / each);
   int units = 0;
   rc = units_of(dev, &units);
   if (rc != LIBTOPK_OK) return rc;
-  // Few tokens are dealt out row by row.
+  // Few tokens are dealt out row by row, to 16 waves a unit.
   int64_t splits = 1;
   if (t.tokens > 0) {
-    splits = ((int64_t)units * 4 + t.tokens - 1) / t.tokens;
-    if (splits > steps) splits = steps;
+    splits = ((int64_t)units * 16 + t.tokens - 1) / t.tokens;
+    if (splits > groups) splits = groups;
   }
   p.splits = (int32_t)splits;
-  int64_t grid = (int64_t)t.tokens * splits;
+  int64_t grid = ((int64_t)t.tokens * splits + kWaves - 1) / kWaves;
   const int64_t least = (batch + kBlock - 1) / kBlock;
   if (grid < least) grid = least;
   if (!launchable(grid, kBlock)) return LIBTOPK_ERR_INVALID;

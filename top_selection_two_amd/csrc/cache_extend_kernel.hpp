@@ -34,32 +34,15 @@ struct ExtendParams {
   int32_t norm_type;
   int32_t half;         // pairs that turn
   bool interleaved;
-  double eps, dim;
-  int32_t splits;       // workgroups of a token
+  double eps, inv_dim;
+  int32_t splits;       // waves of a token
 };
 
 typedef int v2i_t __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int kUnit = 8;  // elements of a lane: 16 bytes of the input
-
-template <int T>
-__device__ __forceinline__ void widen_pair(int v, double* x) {
-  if constexpr (T == kBf16) {
-    x[0] = (double)__int_as_float(v << 16);
-    x[1] = (double)__int_as_float(v & 0xffff0000);
-  } else {
-    const f16x2_t h = __builtin_bit_cast(f16x2_t, v);
-    x[0] = (double)(float)h[0];
-    x[1] = (double)(float)h[1];
-  }
-}
-template <int T>
-__device__ __forceinline__ void widen_unit(const v4i& v, double (&x)[kUnit]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) widen_pair<T>(v[i], x + 2 * i);
-}
+constexpr int kUnit = 8;  // elements of a lane
 
 // Two numbers rounded to a 16-bit type.
 template <int T>
@@ -112,41 +95,126 @@ __device__ __forceinline__ void angle(int64_t position, float freq,
   sincospi(2.0 * r, sin_, cos_);
 }
 
-// One workgroup takes a token's rows (or with few tokens a part of them),
-// LPH lanes a row and a unit of 8 elements a lane.
+// 1 / sqrt(a) for a normal a > 0: the instruction's approximation and two of
+// Newton's steps, each of which doubles its bits.
+__device__ __forceinline__ double inv_sqrt(double a) {
+  double y = __builtin_amdgcn_rsq(a);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const double e = fma(-a * y, y, 1.0);
+    y = fma(0.5 * y, e, y);
+  }
+  return y;
+}
+
+// Four consecutive numbers of a row, in one of two types.
+typedef int v2i4_t __attribute__((ext_vector_type(2), aligned(4)));
+typedef int v2i2_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef int v4i4_t __attribute__((ext_vector_type(4), aligned(4)));
+template <int T>
+__device__ __forceinline__ void widen4(const v2i_t& v, float* x) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int d = v[i];
+    if constexpr (T == kBf16) {
+      x[2 * i] = __int_as_float(d << 16);
+      x[2 * i + 1] = __int_as_float(d & 0xffff0000);
+    } else {
+      const f16x2_t h = __builtin_bit_cast(f16x2_t, d);
+      x[2 * i] = (float)h[0];
+      x[2 * i + 1] = (float)h[1];
+    }
+  }
+}
+// Weights e .. e + 3 of a norm, of the rows' type or float32.
+template <int QT>
+__device__ __forceinline__ void norm4(const void* g, int type, int e,
+                                      float* w) {
+  if (type == kF32) {
+    const v4i4_t a = *(const v4i4_t*)((const float*)g + e);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __int_as_float(a[i]);
+  } else {
+    const v2i2_t a = *(const v2i2_t*)((const uint16_t*)g + e);
+    widen4<QT>(v2i_t{a[0], a[1]}, w);
+  }
+}
+
+// A wave takes a token's rows, or with few tokens a part of them: 64 / LPH
+// rows at a time, LPH lanes a row, all of one kind (q, k or v).  A lane has 8
+// elements of a row, in two runs of 4: where halves of the row turn against
+// one another, a run of each half, so that it turns its elements by itself.
+// Its runs lie at the same place in every row, so that it has the sines and
+// cosines that it needs, found by all lanes of the wave once a token, and its
+// norm's weights in registers; nothing is shared with other waves.  (Keys for
+// 4-bit rows, whose blocks are consecutive, are turned with another lane's.)
 template <int QT, int CT, int LPH>
 __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
   const CacheParams& c = p.c;
-  __shared__ double cs[kMaxDim / 2], sn[kMaxDim / 2];
-  __shared__ int counts[kWaves];
-  const int tid = threadIdx.x;
+  constexpr int kRows = kWave / LPH;
+  __shared__ double2 turn_lds[kWaves][kMaxDim / 2];
+  const int tid = threadIdx.x, wave = uni(tid / kWave), ln = tid % kWave;
   const int32_t top_len = c.pages > 0 ? c.cap : 0;
-  auto start = [&](int32_t j) {
-    const int32_t s = ld_const(p.starts + j);
-    return s < 0 ? 0 : s > p.tokens ? p.tokens : s;
-  };
+  auto bound = [&](int32_t s) { return s < 0 ? 0 : s > p.tokens ? p.tokens : s; };
   // Lengths after the call, kBlock sequences a workgroup.
   const int64_t mine = (int64_t)blockIdx.x * kBlock + tid;
   if (mine < c.batch) {
     const int32_t len = clamp_len(c.lens[mine], top_len);
-    const int32_t s0 = start((int32_t)mine), s1 = start((int32_t)mine + 1);
+    const int32_t s0 = bound(p.starts[mine]), s1 = bound(p.starts[mine + 1]);
     const int64_t next = (int64_t)len + (s1 > s0 ? s1 - s0 : 0);
     p.out_lens[mine] = next > top_len ? top_len : (int32_t)next;
   }
-  const int32_t token = (int32_t)(blockIdx.x / (unsigned)p.splits);
-  const int part = (int)(blockIdx.x % (unsigned)p.splits);
+  const int64_t task = (int64_t)blockIdx.x * kWaves + wave;
+  const int32_t token = (int32_t)(task / p.splits);
+  const int part = (int)(task % p.splits);
   if (token >= p.tokens) return;
-  // Its sequence: the last whose start is not beyond it.
-  int n = 0;
-  for (int32_t j = tid; j < c.batch; j += kBlock)
-    n += popc(ballot(start(j + 1) <= token)) * (tid % kWave == 0);
-  if (tid % kWave == 0) counts[tid / kWave] = n;
-  __syncthreads();
+
+  const int ul = ln % LPH, sub = ln / LPH;
+  const bool in = ul * kUnit < c.dim;
+  const bool turns = ul < p.half / 4;
+  const bool halves = turns && !p.interleaved;
+  // First elements of the lane's runs, in a row whose halves turn.
+  const int run0 = halves ? 4 * ul : kUnit * ul;
+  const int run1 = halves ? p.half + 4 * ul : kUnit * ul + 4;
+  auto by_halves = [&](int kind) {
+    return kind == 0 || (kind == 1 && CT != kE2m1);
+  };
+  const int gq = (p.q_heads + kRows - 1) / kRows;
+  const int gk = (c.heads + kRows - 1) / kRows;
+  const int groups = gq + 2 * gk;
+  // Rows of a group: of q (0), k (1) or v (2); none past the last head.
+  auto kind_of = [&](int g) { return g < gq ? 0 : g < gq + gk ? 1 : 2; };
+  auto head_of = [&](int g, int kind) {
+    return (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * kRows + sub;
+  };
+  struct Raw {
+    v2i_t a, b;
+  };
+  auto load = [&](int g) {
+    Raw r = {{0, 0}, {0, 0}};
+    if (g >= groups) return r;
+    const int kind = kind_of(g), h = head_of(g, kind);
+    const char* from = kind == 0   ? p.q + token * p.qt + h * p.qh
+                       : kind == 1 ? p.k + token * p.kt + h * p.kh
+                                   : p.v + token * p.vt + h * p.vh;
+    if (in && h < (kind == 0 ? p.q_heads : c.heads)) {
+      const bool split = by_halves(kind);
+      r.a = *(const v2i_t*)(from + (split ? run0 : kUnit * ul) * 2);
+      r.b = *(const v2i_t*)(from + (split ? run1 : kUnit * ul + 4) * 2);
+    }
+    return r;
+  };
+  Raw next = load(part);
+
+  // ---- the token's sequence: the last whose start is not beyond it
   int32_t b = 0;
-  for (int i = 0; i < kWaves; ++i) b += counts[i];
+  for (int32_t j = 0; j < c.batch; j += kWave)
+    b += popc(ballot(j + ln < c.batch &&
+                     bound(p.starts[min(j + ln, c.batch - 1) + 1]) <= token));
   b = uni(b);
-  if (b >= c.batch || start(b) > token) return;
-  const int32_t nth = token - start(b);
+  const int32_t first = b < c.batch ? bound(ld_const(p.starts + b)) : 0;
+  if (b >= c.batch || first > token) return;
+  const int32_t nth = token - first;
   const int32_t len = clamp_len(ld_const(c.lens + b), top_len);
   const int64_t position =
       (int64_t)(p.seen ? ld_const(p.seen + b) : len) + nth;
@@ -154,98 +222,125 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
   int32_t place = 0, page = -1;
   if (slot < top_len)
     page = find_page(c, c.table + b * c.table_stride, (int32_t)slot, &place);
+  page = uni(page);
+  place = uni(place);
+  // ---- its angles: a lane's four are 4 ul .. 4 ul + 3 in either pairing
+  double cs[4], sn[4];
+  double2* const turn = turn_lds[wave];
   if (p.half > 0) {
-    for (int i = tid; i < p.half; i += kBlock)
-      angle(position, p.freqs[i], &cs[i], &sn[i]);
-    __syncthreads();
+    for (int i = ln; i < p.half; i += kWave) {
+      double x, y;
+      angle(position, p.freqs[i], &x, &y);
+      turn[i] = make_double2(x, y);
+    }
+    __builtin_amdgcn_wave_barrier();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const double2 z = turns ? turn[4 * ul + e] : make_double2(1.0, 0.0);
+      cs[e] = z.x;
+      sn[e] = z.y;
+    }
   }
-  const int ul = tid % LPH;
-  const int units = c.dim / kUnit;
-  const bool in = ul < units;
-  const int rows = p.q_heads + 2 * c.heads;
-  constexpr int kRows = kBlock / LPH;
-  for (int r0 = part * kRows; r0 < rows; r0 += p.splits * kRows) {
-    const int row = r0 + tid / LPH;
-    const bool have = in && row < rows;
-    const bool is_q = row < p.q_heads;
-    const bool is_v = row >= p.q_heads + c.heads;
-    const int h = is_q ? row : row - p.q_heads - (is_v ? c.heads : 0);
-    v4i raw = {0, 0, 0, 0};
-    if (have)
-      raw = *(const v4i*)((is_q   ? p.q + token * p.qt + h * p.qh
-                           : is_v ? p.v + token * p.vt + h * p.vh
-                                  : p.k + token * p.kt + h * p.kh) +
-                          ul * 16);
+  // ---- its rows
+  const bool wide_norm = p.norm_type == kF32;
+  int kind = -1;
+  float w[kUnit];  // norm weights of the lane's elements
+  for (int g = part; g < groups; g += p.splits) {
+    const Raw raw = next;
+    next = load(g + p.splits);
+    const int was = kind;
+    kind = kind_of(g);
+    const bool split = by_halves(kind);
+    const int h = head_of(g, kind);
+    const bool have = in && h < (kind == 0 ? p.q_heads : c.heads);
+    const void* norm = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
+    if (norm && kind != was) {
+      norm4<QT>(norm, p.norm_type, !in ? 0 : split ? run0 : kUnit * ul, w);
+      norm4<QT>(norm, p.norm_type, !in ? 0 : split ? run1 : kUnit * ul + 4,
+                w + 4);
+    }
+    float f[kUnit];
+    widen4<QT>(raw.a, f);
+    widen4<QT>(raw.b, f + 4);
     double x[kUnit];
-    widen_unit<QT>(raw, x);
-    // ---- norm
-    const void* g = is_q ? p.q_norm : is_v ? nullptr : p.k_norm;
     double inv = 1.0;
-    auto weight = [&](int e) {
-      return p.norm_type == kF32 ? (double)((const float*)g)[e]
-             : p.norm_type == kBf16
-                 ? (double)__int_as_float((int)((const uint16_t*)g)[e] << 16)
-                 : (double)(float)((const _Float16*)g)[e];
-    };
-    if (p.q_norm || p.k_norm) {
+#pragma unroll
+    for (int e = 0; e < kUnit; ++e) x[e] = (double)f[e];
+    if (norm) {
       double ss = 0.0;
 #pragma unroll
       for (int e = 0; e < kUnit; ++e) ss = fma(x[e], x[e], ss);
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
-      if (g && have) {
-        inv = 1.0 / sqrt(ss / p.dim + p.eps);
+      const double ms = ss * p.inv_dim + p.eps;
+      // (of zeros with eps = 0: infinity, and NaN as 0 times it)
+      inv = ms > 0.0 ? inv_sqrt(ms) : INFINITY;
+      if (!(ms < INFINITY)) inv = ms == INFINITY ? 0.0 : ms;
+      // A product of two 16-bit numbers is exact in float32; the division by
+      // the row's size comes after the turn.
 #pragma unroll
-        for (int e = 0; e < kUnit; ++e) x[e] *= inv * weight(ul * kUnit + e);
-      }
+      for (int e = 0; e < kUnit; ++e)
+        x[e] = wide_norm ? x[e] * (double)w[e] : (double)(f[e] * w[e]);
     }
-    // ---- rotation
-    if (p.half > 0) {
-      if (p.interleaved) {
-        if (!is_v && have && ul * kUnit < 2 * p.half) {
+    if (p.half > 0 && kind != 2) {
+      if (split || p.interleaved) {
+        if (turns) {
 #pragma unroll
-          for (int e = 0; e < kUnit; e += 2) {
-            const int j = (ul * kUnit + e) / 2;
-            const double a = x[e], d = x[e + 1];
-            x[e] = a * cs[j] - d * sn[j];
-            x[e + 1] = d * cs[j] + a * sn[j];
+          for (int e = 0; e < 4; ++e) {
+            const int i = p.interleaved ? 2 * e : e;
+            const int j = p.interleaved ? 2 * e + 1 : 4 + e;
+            const double a = x[i], d = x[j];
+            x[i] = fma(-d, sn[e], a * cs[e]);
+            x[j] = fma(a, sn[e], d * cs[e]);
           }
         }
       } else {
-        // The other half's unit of the row, from its lane.
+        // Units of 8 in a row: turned with the unit of the other half.
         const int step = p.half / kUnit;
-        const bool first = ul < step;
-        const bool turns = ul < 2 * step;
-        const int other = turns ? (first ? ul + step : ul - step) : ul;
-        const int from = tid % kWave - ul + other;
-        v4i far;
+        const bool turned = ul < 2 * step, low = ul < step;
+        const int other = turned ? (low ? ul + step : ul - step) : ul;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) far[i] = __shfl(raw[i], from, kWave);
-        if (!is_v && have && turns) {
-          double z[kUnit];
-          widen_unit<QT>(far, z);
-#pragma unroll
-          for (int e = 0; e < kUnit; ++e) {
-            const int j = (first ? ul : other) * kUnit + e;
-            if (g) z[e] *= inv * weight(other * kUnit + e);
-            x[e] = first ? x[e] * cs[j] - z[e] * sn[j]
-                         : x[e] * cs[j] + z[e] * sn[j];
-          }
+        for (int e = 0; e < kUnit; ++e) {
+          const double z = __shfl(x[e], ln - ul + other, kWave);
+          const double2 t = turned ? turn[(low ? ul : other) * kUnit + e]
+                                   : make_double2(1.0, 0.0);
+          const double y = fma(z, low ? -t.y : t.y, x[e] * t.x);
+          x[e] = turned ? y : x[e];
         }
       }
     }
+    if (norm) {
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) x[e] *= inv;
+    }
     // ---- out
-    if (is_q && have)
-      *(v4i*)(p.q_out + token * p.ot + h * p.oh + ul * 16) =
-          v4i{round_pair<QT>(x[0], x[1]), round_pair<QT>(x[2], x[3]),
-              round_pair<QT>(x[4], x[5]), round_pair<QT>(x[6], x[7])};
+    if (kind == 0) {
+      if (have) {
+        char* to = p.q_out + token * p.ot + h * p.oh;
+        *(v2i_t*)(to + run0 * 2) =
+            v2i_t{round_pair<QT>(x[0], x[1]), round_pair<QT>(x[2], x[3])};
+        *(v2i_t*)(to + run1 * 2) =
+            v2i_t{round_pair<QT>(x[4], x[5]), round_pair<QT>(x[6], x[7])};
+      }
+      continue;
+    }
+    const bool is_v = kind == 2;
     const float* scale = is_v ? p.v_scale : p.k_scale;
-    if (scale && !is_q && have) {
-      const double s = (double)scale[h];
+    if (scale) {
+      const double s = have ? (double)scale[h] : 1.0;
 #pragma unroll
       for (int e = 0; e < kUnit; ++e) x[e] /= s;
     }
-    int byte = 0;
+    if (p.w.w && !is_v && have && ul == 0 && slot < top_len) {
+      p.w.w[b * p.w.wb + h * p.w.wh + slot] = 0.0f;
+      p.w.pos[b * p.w.pb + h * p.w.ph + slot] = (int32_t)position;
+    }
+    if (page < 0) continue;
+    char* dst = const_cast<char*>(
+        is_v ? c.v + row_offset(c.vs, page, h, place)
+             : c.k + row_offset(c.ks, page, h, place));
     if constexpr (CT == kE2m1) {
       double top = 0.0;
       bool odd = false;  // a NaN: max would drop it
@@ -257,23 +352,13 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
       if (odd) top = INFINITY;
       top = fmax(top, __shfl_xor(top, 1, kWave));
       top = fmax(top, __shfl_xor(top, 2, kWave));
-      byte = block_byte(top);
-    }
-    if (is_q || !have) continue;
-    if (p.w.w && !is_v && ul == 0 && slot < top_len) {
-      p.w.w[b * p.w.wb + h * p.w.wh + slot] = 0.0f;
-      p.w.pos[b * p.w.pb + h * p.w.ph + slot] = (int32_t)position;
-    }
-    if (page < 0) continue;
-    char* dst = const_cast<char*>(
-        is_v ? c.v + row_offset(c.vs, page, h, place)
-             : c.k + row_offset(c.ks, page, h, place));
-    if constexpr (CT == kE2m1) {
+      const int byte = block_byte(top);
       unsigned code = 0;
       if (byte < 255) {
 #pragma unroll
         for (int e = 0; e < kUnit; ++e) code |= code_of(x[e], byte) << (4 * e);
       }
+      if (!have) continue;
       *(unsigned*)(dst + ul * 4) = code;
       if (ul % 4 == 0) {
         char* blocks = const_cast<char*>(
@@ -281,22 +366,24 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
                  : c.kb + row_offset(c.kbs, page, h, place));
         blocks[ul / 4] = (char)byte;
       }
-    } else if constexpr (CT == kE4m3) {
-      v2i_t d;
+    } else {
+      if (!have) continue;
+      const int e0 = split ? run0 : kUnit * ul;
+      const int e1 = split ? run1 : kUnit * ul + 4;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        int w = __builtin_amdgcn_cvt_pk_fp8_f32(within_e4m3(x[4 * i]),
-                                                within_e4m3(x[4 * i + 1]), 0,
-                                                false);
-        d[i] = __builtin_amdgcn_cvt_pk_fp8_f32(within_e4m3(x[4 * i + 2]),
-                                               within_e4m3(x[4 * i + 3]), w,
-                                               true);
+        const double* y = x + 4 * i;
+        const int e = i ? e1 : e0;
+        if constexpr (CT == kE4m3) {
+          const int d = __builtin_amdgcn_cvt_pk_fp8_f32(
+              within_e4m3(y[0]), within_e4m3(y[1]), 0, false);
+          *(int*)(dst + e) = __builtin_amdgcn_cvt_pk_fp8_f32(
+              within_e4m3(y[2]), within_e4m3(y[3]), d, true);
+        } else {
+          *(v2i_t*)(dst + e * 2) =
+              v2i_t{round_pair<CT>(y[0], y[1]), round_pair<CT>(y[2], y[3])};
+        }
       }
-      *(v2i_t*)(dst + ul * 8) = d;
-    } else {
-      *(v4i*)(dst + ul * 16) =
-          v4i{round_pair<CT>(x[0], x[1]), round_pair<CT>(x[2], x[3]),
-              round_pair<CT>(x[4], x[5]), round_pair<CT>(x[6], x[7])};
     }
   }
 }
