@@ -44,14 +44,42 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kUnit = 8;  // elements of a lane
 
-// Two numbers rounded to a 16-bit type.
+// Two numbers rounded to float32 and then to a 16-bit type.  (Left to itself
+// the compiler rounds once, by ten instructions more an element.)
 template <int T>
 __device__ __forceinline__ int round_pair(double a, double b) {
+  float x = (float)a, y = (float)b;
+  pin(x);
+  pin(y);
   if constexpr (T == kBf16)
-    return __builtin_bit_cast(int, bf16x2_t{(__bf16)(float)a, (__bf16)(float)b});
+    return __builtin_bit_cast(int, bf16x2_t{(__bf16)x, (__bf16)y});
   else
-    return __builtin_bit_cast(int,
-                              f16x2_t{(_Float16)(float)a, (_Float16)(float)b});
+    return __builtin_bit_cast(int, f16x2_t{(_Float16)x, (_Float16)y});
+}
+
+// The value of a lane that a data-parallel move names.
+template <int CTRL>
+__device__ __forceinline__ double dpp64(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xf,
+                                             0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xf,
+                                             0xf, false);
+  return __hiloint2double(hi, lo);
+}
+constexpr int kDppXor1 = 0xb1;        // within quads
+constexpr int kDppXor2 = 0x4e;
+constexpr int kDppHalfMirror = 0x141; // 7 - i of 8
+constexpr int kDppMirror = 0x140;     // 15 - i of 16
+// Sum over runs of LPH lanes, the same in all of them: after each step the
+// lanes that have been joined agree, so that a mirror is as good as a shift.
+template <int LPH>
+__device__ __forceinline__ double run_sum(double v) {
+  v += dpp64<kDppXor1>(v);
+  v += dpp64<kDppXor2>(v);
+  v += dpp64<kDppHalfMirror>(v);
+  if constexpr (LPH > 8) v += dpp64<kDppMirror>(v);
+  if constexpr (LPH > 16) v += __shfl_xor(v, 16, kWave);
+  return v;
 }
 
 // To e4m3's range (NaN stays).
@@ -72,14 +100,36 @@ __device__ __forceinline__ int block_byte(double top) {
   return e < 0 ? 0 : e > 254 ? 254 : e;
 }
 
-// The 4-bit code of x / 2^(byte - 127): the nearest of 0 .5 1 1.5 2 3 4 6,
-// the even code where two are.
-__device__ __forceinline__ unsigned code_of(double x, int byte) {
-  const double y = ldexp(x, 127 - byte);
-  const double a = fabs(y);
-  const int mag = (a > 0.25) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) +
-                  (a > 2.5) + (a >= 3.5) + (a > 5.0);
-  return (unsigned)mag | ((unsigned)__double2hiint(x) >> 31) << 3;
+// A magnitude of at most 7 or so, and its sign, in float32: the bits that do
+// not fit leave their trace in the last one, so that rounding again to fewer
+// bits is as rounding once.  Below 2^-126 what comes out is tiny, whatever it
+// is.
+__device__ __forceinline__ float sticky_float(double y) {
+  const int hi = __double2hiint(y), lo = __double2loint(y);
+  int t = (hi & 0x7fffffff) - ((1023 - 127) << 20);
+  t = t > 0 ? t : 0;
+  t = t < 0x0fdfffff ? t : 0x0fdfffff;  // float32's largest exponent
+  unsigned m = __builtin_amdgcn_alignbit((unsigned)t, (unsigned)lo, 29);
+  const unsigned rest = (unsigned)lo & 0x1fffffffu;
+  m |= rest < 1u ? rest : 1u;
+  return __uint_as_float(m | ((unsigned)hi & 0x80000000u));
+}
+
+// The 4-bit codes of x / 2^(byte - 127): the nearest of 0 .5 1 1.5 2 3 4 6, of
+// two the even code, and 6 beyond.
+__device__ __forceinline__ unsigned codes_of(const double* x, int byte) {
+  unsigned code = 0;
+  const int by = 127 - byte;
+#define LTK_PAIR(i)                                                     \
+  code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(                      \
+      code, sticky_float(ldexp(x[2 * i], by)),                          \
+      sticky_float(ldexp(x[2 * i + 1], by)), 1.0f, i)
+  LTK_PAIR(0);
+  LTK_PAIR(1);
+  LTK_PAIR(2);
+  LTK_PAIR(3);
+#undef LTK_PAIR
+  return code;
 }
 
 // cos and sin of position * freq.  The turns are taken modulo 1 in 64 bits
@@ -149,7 +199,7 @@ __device__ __forceinline__ void norm4(const void* g, int type, int e,
 // norm's weights in registers; nothing is shared with other waves.  (Keys for
 // 4-bit rows, whose blocks are consecutive, are turned with another lane's.)
 template <int QT, int CT, int LPH>
-__global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
+__global__ __launch_bounds__(kBlock, 4) void extend_kernel(ExtendParams p) {
   const CacheParams& c = p.c;
   constexpr int kRows = kWave / LPH;
   __shared__ double2 turn_lds[kWaves][kMaxDim / 2];
@@ -164,9 +214,11 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
     const int64_t next = (int64_t)len + (s1 > s0 ? s1 - s0 : 0);
     p.out_lens[mine] = next > top_len ? top_len : (int32_t)next;
   }
-  const int64_t task = (int64_t)blockIdx.x * kWaves + wave;
-  const int32_t token = (int32_t)(task / p.splits);
-  const int part = (int)(task % p.splits);
+  // (tasks count in 32 bits)
+  const unsigned task = (unsigned)blockIdx.x * kWaves + (unsigned)wave;
+  const int32_t token =
+      uni((int32_t)(p.splits > 1 ? task / (unsigned)p.splits : task));
+  const int part = uni((int)(task - (unsigned)token * (unsigned)p.splits));
   if (token >= p.tokens) return;
 
   const int ul = ln % LPH, sub = ln / LPH;
@@ -176,28 +228,45 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
   // First elements of the lane's runs, in a row whose halves turn.
   const int run0 = halves ? 4 * ul : kUnit * ul;
   const int run1 = halves ? p.half + 4 * ul : kUnit * ul + 4;
-  auto by_halves = [&](int kind) {
+  auto by_halves = [](int kind) {
     return kind == 0 || (kind == 1 && CT != kE2m1);
   };
   const int gq = (p.q_heads + kRows - 1) / kRows;
   const int gk = (c.heads + kRows - 1) / kRows;
   const int groups = gq + 2 * gk;
-  // Rows of a group: of q (0), k (1) or v (2); none past the last head.
+  // Rows of a group: of q (0), k (1) or v (2); none past the last head.  The
+  // first head is the same in every lane, whose own is `sub` beyond it: only
+  // that part of an address differs from lane to lane.
   auto kind_of = [&](int g) { return g < gq ? 0 : g < gq + gk ? 1 : 2; };
-  auto head_of = [&](int g, int kind) {
-    return (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * kRows + sub;
+  auto first_of = [&](int g, int kind) {
+    return (kind == 0 ? g : kind == 1 ? g - gq : g - gq - gk) * kRows;
   };
+  const int64_t q_lane = sub * p.qh, k_lane = sub * p.kh, v_lane = sub * p.vh;
+  const int64_t o_lane = sub * p.oh;
+  const int64_t ck_lane = sub * c.ks.head, cv_lane = sub * c.vs.head;
   struct Raw {
     v2i_t a, b;
   };
+  const char* const q_tok = p.q + token * p.qt;
+  const char* const k_tok = p.k + token * p.kt;
+  const char* const v_tok = p.v + token * p.vt;
   auto load = [&](int g) {
     Raw r = {{0, 0}, {0, 0}};
     if (g >= groups) return r;
-    const int kind = kind_of(g), h = head_of(g, kind);
-    const char* from = kind == 0   ? p.q + token * p.qt + h * p.qh
-                       : kind == 1 ? p.k + token * p.kt + h * p.kh
-                                   : p.v + token * p.vt + h * p.vh;
-    if (in && h < (kind == 0 ? p.q_heads : c.heads)) {
+    const int kind = kind_of(g), h0 = first_of(g, kind);
+    const char* from;
+    bool have;
+    if (kind == 0) {
+      from = q_tok + h0 * p.qh + q_lane;
+      have = in && h0 + sub < p.q_heads;
+    } else if (kind == 1) {
+      from = k_tok + h0 * p.kh + k_lane;
+      have = in && h0 + sub < p.c.heads;
+    } else {
+      from = v_tok + h0 * p.vh + v_lane;
+      have = in && h0 + sub < p.c.heads;
+    }
+    if (have) {
       const bool split = by_halves(kind);
       r.a = *(const v2i_t*)(from + (split ? run0 : kUnit * ul) * 2);
       r.b = *(const v2i_t*)(from + (split ? run1 : kUnit * ul + 4) * 2);
@@ -253,7 +322,7 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
     const int was = kind;
     kind = kind_of(g);
     const bool split = by_halves(kind);
-    const int h = head_of(g, kind);
+    const int h0 = first_of(g, kind), h = h0 + sub;
     const bool have = in && h < (kind == 0 ? p.q_heads : c.heads);
     const void* norm = kind == 0 ? p.q_norm : kind == 1 ? p.k_norm : nullptr;
     if (norm && kind != was) {
@@ -272,28 +341,37 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
       double ss = 0.0;
 #pragma unroll
       for (int e = 0; e < kUnit; ++e) ss = fma(x[e], x[e], ss);
-#pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor(ss, o, kWave);
-      const double ms = ss * p.inv_dim + p.eps;
+      const double ms = run_sum<LPH>(ss) * p.inv_dim + p.eps;
       // (of zeros with eps = 0: infinity, and NaN as 0 times it)
       inv = ms > 0.0 ? inv_sqrt(ms) : INFINITY;
       if (!(ms < INFINITY)) inv = ms == INFINITY ? 0.0 : ms;
       // A product of two 16-bit numbers is exact in float32; the division by
       // the row's size comes after the turn.
+      if (wide_norm) {
 #pragma unroll
-      for (int e = 0; e < kUnit; ++e)
-        x[e] = wide_norm ? x[e] * (double)w[e] : (double)(f[e] * w[e]);
+        for (int e = 0; e < kUnit; ++e) x[e] *= (double)w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < kUnit; ++e) x[e] = (double)(f[e] * w[e]);
+      }
     }
     if (p.half > 0 && kind != 2) {
-      if (split || p.interleaved) {
+      if (p.interleaved) {
         if (turns) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int i = p.interleaved ? 2 * e : e;
-            const int j = p.interleaved ? 2 * e + 1 : 4 + e;
-            const double a = x[i], d = x[j];
-            x[i] = fma(-d, sn[e], a * cs[e]);
-            x[j] = fma(a, sn[e], d * cs[e]);
+            const double a = x[2 * e], d = x[2 * e + 1];
+            x[2 * e] = fma(-d, sn[e], a * cs[e]);
+            x[2 * e + 1] = fma(a, sn[e], d * cs[e]);
+          }
+        }
+      } else if (split) {
+        if (turns) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const double a = x[e], d = x[4 + e];
+            x[e] = fma(-d, sn[e], a * cs[e]);
+            x[4 + e] = fma(a, sn[e], d * cs[e]);
           }
         }
       } else {
@@ -318,7 +396,7 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
     // ---- out
     if (kind == 0) {
       if (have) {
-        char* to = p.q_out + token * p.ot + h * p.oh;
+        char* to = p.q_out + token * p.ot + h0 * p.oh + o_lane;
         *(v2i_t*)(to + run0 * 2) =
             v2i_t{round_pair<QT>(x[0], x[1]), round_pair<QT>(x[2], x[3])};
         *(v2i_t*)(to + run1 * 2) =
@@ -339,8 +417,8 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
     }
     if (page < 0) continue;
     char* dst = const_cast<char*>(
-        is_v ? c.v + row_offset(c.vs, page, h, place)
-             : c.k + row_offset(c.ks, page, h, place));
+        is_v ? c.v + row_offset(c.vs, page, h0, place) + cv_lane
+             : c.k + row_offset(c.ks, page, h0, place) + ck_lane);
     if constexpr (CT == kE2m1) {
       double top = 0.0;
       bool odd = false;  // a NaN: max would drop it
@@ -350,16 +428,12 @@ __global__ __launch_bounds__(kBlock) void extend_kernel(ExtendParams p) {
         top = fmax(top, fabs(x[e]));
       }
       if (odd) top = INFINITY;
-      top = fmax(top, __shfl_xor(top, 1, kWave));
-      top = fmax(top, __shfl_xor(top, 2, kWave));
+      top = fmax(top, dpp64<kDppXor1>(top));
+      top = fmax(top, dpp64<kDppXor2>(top));
       const int byte = block_byte(top);
-      unsigned code = 0;
-      if (byte < 255) {
-#pragma unroll
-        for (int e = 0; e < kUnit; ++e) code |= code_of(x[e], byte) << (4 * e);
-      }
+      const unsigned code = codes_of(x, byte);
       if (!have) continue;
-      *(unsigned*)(dst + ul * 4) = code;
+      *(unsigned*)(dst + ul * 4) = byte < 255 ? code : 0;
       if (ul % 4 == 0) {
         char* blocks = const_cast<char*>(
             is_v ? c.vb + row_offset(c.vbs, page, h, place)
