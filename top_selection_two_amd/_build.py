@@ -28,6 +28,7 @@ SO = os.path.join(PKG, "libtopk.so")
 BINDING = os.path.join(PKG, "_binding.so")
 # Sources with their definitions: LTK_Q, LTK_C are types of include/libtopk.h.
 UNITS = (("libtopk.hip",), ("cache.hip",), ("sample.hip",),
+         ("workspace.hip",),
          *(("cache_attend.hip", "-DLTK_Q=%d" % q, "-DLTK_C=%d" % c)
            for q, c in ((0, 0), (0, 2), (0, 4), (1, 1), (1, 2), (1, 4))))
 

@@ -3,6 +3,7 @@
 
 #include "libtopk.h"
 #include "sample_kernel.hpp"
+#include "workspace.hpp"
 
 namespace {
 
@@ -18,6 +19,23 @@ bool misaligned(const void* p, uintptr_t a) { return (uintptr_t)p & (a - 1); }
 bool meets(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+constexpr int64_t kSampleWork = (int64_t)1 << 26;
+
+struct Kernels {
+  const void *row, *chunk, *finish;
+};
+template <int T>
+Kernels kernels_of() {
+  return {(const void*)&sample_row_kernel<T>,
+          (const void*)&sample_chunk_kernel<T>,
+          (const void*)&sample_finish_kernel<T>};
+}
+Kernels kernels(int32_t dtype) {
+  return dtype == LIBTOPK_F32    ? kernels_of<kLogF32>()
+         : dtype == LIBTOPK_BF16 ? kernels_of<kLogBf16>()
+                                 : kernels_of<kLogF16>();
 }
 
 int ceil_log2(int32_t n) {
@@ -77,19 +95,37 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.tokens = tokens;
   p.logprobs = logprobs;
   int dev = 0;
-  if (hipGetDevice(&dev) != hipSuccess) {
-    (void)hipGetLastError();
-    return LIBTOPK_ERR_HIP;
+  int rc = current_device(&dev);
+  if (rc != LIBTOPK_OK) return rc;
+  hipStream_t st = (hipStream_t)stream;
+  const Kernels fn = kernels(dtype);
+  const int64_t chunks = (cols + kChunk - 1) / kChunk;
+  if (chunks > kMaxChunks)
+    return launch(fn.row, dim3((unsigned)rows), kSampleThreads, p, st);
+  p.chunks = (int32_t)chunks;
+  // Some 2500 words a row, which one workgroup sorts in about 3 us.
+  const int64_t rank = kMaxList * 5 / 8 / chunks;
+  p.rank = (int32_t)(rank < 2 ? 2 : rank > 32 ? 32 : rank);
+  // Batches of rows share the workspace, which stays below 64 MB.
+  const int64_t per = chunks * (8 + 3 * 4 + 8 * kChunkList);
+  int64_t batch = kSampleWork / per;
+  if (batch > rows) batch = rows;
+  Work work;
+  rc = get_work(dev, st, (size_t)(batch * per), 1, &work);
+  if (rc != LIBTOPK_OK) return rc;
+  const int64_t n = batch * chunks;
+  p.lists = (uint64_t*)work.base;
+  p.chunk_sum = (double*)(p.lists + n * kChunkList);
+  p.chunk_max = (uint32_t*)(p.chunk_sum + n);
+  p.chunk_from = p.chunk_max + n;
+  p.chunk_n = p.chunk_from + n;
+  for (int64_t r = 0; r < rows && rc == LIBTOPK_OK; r += batch) {
+    const int64_t m = rows - r < batch ? rows - r : batch;
+    p.row0 = r;
+    rc = launch(fn.chunk, dim3((unsigned)(m * ((chunks + kWaves - 1) / kWaves))),
+                kBlock, p, st);
+    if (rc == LIBTOPK_OK)
+      rc = launch(fn.finish, dim3((unsigned)m), kSampleThreads, p, st);
   }
-  const void* fn = dtype == LIBTOPK_F32 ? (const void*)&sample_row_kernel<kLogF32>
-                   : dtype == LIBTOPK_BF16
-                       ? (const void*)&sample_row_kernel<kLogBf16>
-                       : (const void*)&sample_row_kernel<kLogF16>;
-  void* args[] = {&p};
-  if (hipLaunchKernel(fn, dim3((unsigned)rows), dim3(kSampleThreads), args, 0,
-                      (hipStream_t)stream) != hipSuccess) {
-    (void)hipGetLastError();
-    return LIBTOPK_ERR_HIP;
-  }
-  return LIBTOPK_OK;
+  return rc;
 }

@@ -44,10 +44,27 @@ struct SampleParams {
   const float* u;
   int64_t* tokens;
   float* logprobs;
+  // Of each row of a batch, [row - row0][chunk]: see sample_chunk_kernel.
+  int64_t row0;
+  int32_t chunks;
+  int32_t rank;
+  uint32_t* chunk_max;
+  uint32_t* chunk_from;
+  uint32_t* chunk_n;
+  double* chunk_sum;
+  uint64_t* lists;  // [row - row0][chunk][kChunkList]
 };
+
+constexpr int kChunk = 1024;     // logits of a wave
+constexpr int kChunkList = 64;   // listed of them at most
+constexpr int kMaxChunks = 1024; // of a row with lists
+constexpr int kMaxList = 4096;   // of a row
+constexpr uint32_t kKeyNone = 0x007fffffu;  // of -infinity
 
 // What a row asks for.
 struct Wanted {
+  __device__ bool all() const { return k == 0 && p >= 1.0 && min_w <= 0.0; }
+
   double inv_t;   // 1 / temperature
   bool greedy;
   int32_t k;      // 0: all
@@ -180,10 +197,18 @@ __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
 
 // LDS of a row.
 struct SampleLds {
-  uint64_t mass[kSampleBins];
-  uint32_t count[kSampleBins];
-  uint64_t tile_mass[kMaxTiles];
-  int32_t tile_ties[kMaxTiles];
+  union {
+    struct {  // passes over the row
+      uint64_t mass[kSampleBins];
+      uint32_t count[kSampleBins];
+      uint64_t tile_mass[kMaxTiles];
+      int32_t tile_ties[kMaxTiles];
+    };
+    struct {  // its list
+      uint64_t sorted[kMaxList];
+      uint64_t listed[kMaxList];
+    };
+  };
   uint64_t sums[kSampleWaves];
   uint64_t found[4];
 };
@@ -408,6 +433,434 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
   }
 }
 
+// ---- lists ------------------------------------------------------------------
+// Few of a row's logits decide it as a rule, and one pass over the row finds
+// them: every wave reads a chunk of 1024 and leaves
+//   the largest, and the sum of the weights next to that (if the row asks);
+//   a bound, and the logits from the bound on, at most 64, in the row's order.
+// The bound is the rank-th largest of what the 64 lanes have as their largest,
+// so that the list has some more than `rank`, whatever the numbers are like.
+// Above the largest bound of a row's chunks nothing is missing in its lists:
+// a prefix of the order that ends above it is found there, by sorting at most
+// 4096 words.  Rows whose prefix goes further are done over.
+template <int T>
+__global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
+  constexpr int SIZE = T == kLogF32 ? 4 : 2;
+  constexpr int VEC = 16 / SIZE;            // logits of a load
+  constexpr int LOADS = kChunk / kWave / VEC;
+  constexpr int N = VEC * LOADS;            // 16
+  const int wg = (a.chunks + kWaves - 1) / kWaves;
+  const int r = (int)(blockIdx.x / (unsigned)wg);
+  const int chunk =
+      uni((int)(blockIdx.x % (unsigned)wg) * kWaves + (int)threadIdx.x / kWave);
+  if (chunk >= a.chunks) return;
+  const int64_t row_i = a.row0 + r;
+  const char* row = a.x + row_i * a.ld;
+  const Wanted want = wanted(a, row_i);
+  const int ln = lane();
+  const int first = chunk * kChunk;
+  float x[N];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int i = first + (j * kWave + ln) * VEC;
+    if (i + VEC <= a.cols) {
+      if constexpr (T == kLogF32) {
+        typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+        const f32x4a v = *(const f32x4a*)(row + (int64_t)i * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j * VEC + e] = v[e];
+      } else {
+        typedef unsigned u32x4a __attribute__((ext_vector_type(4), aligned(2)));
+        const u32x4a v = *(const u32x4a*)(row + (int64_t)i * 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned d = v[e / 2];
+          const unsigned h = e % 2 ? d >> 16 : d & 0xffffu;
+          if constexpr (T == kLogBf16)
+            x[j * VEC + e] = __uint_as_float(h << 16);
+          else
+            x[j * VEC + e] = (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e)
+        x[j * VEC + e] =
+            i + e < a.cols ? read_logit<T>(row, i + e) : -INFINITY;
+    }
+  }
+  uint32_t k[N];
+  uint32_t mine = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    x[e] = x[e] != x[e] ? -INFINITY : x[e] + 0.0f;
+    k[e] = logit_key(x[e]);
+    mine = k[e] > mine ? k[e] : mine;
+  }
+  const int64_t at = (int64_t)r * a.chunks + chunk;
+  const int sorted = wave_sort_desc<kWave>(unbias(mine));
+  const uint32_t top = bias(__builtin_amdgcn_readlane(sorted, 0));
+  const float m = key_logit(top);
+  if (ln == 0) a.chunk_max[at] = top;
+  if (want.greedy || top == kKeyNone) {
+    if (ln == 0) {
+      a.chunk_from[at] = kKeyNone + 1;  // lists all above -infinity: none
+      a.chunk_n[at] = 0;
+      a.chunk_sum[at] = 0.0;
+    }
+    return;
+  }
+  if (want.k == 0 && (want.p < 1.0 || want.min_w <= 0.0)) {
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) sum += weight_of(x[e], m, want.inv_t);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+    if (ln == 0) a.chunk_sum[at] = sum;
+  }
+  if (want.all()) return;
+  // ---- the list
+  uint32_t from = 0;
+  int n = 0;
+  bool fits = false;
+  for (int rank = a.rank; rank > 0 && !fits; rank /= 2) {
+    from = bias(__builtin_amdgcn_readlane(sorted, rank - 1));
+    // (-infinity is never listed)
+    from = from > kKeyNone ? from : kKeyNone + 1;
+    n = 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) n += popc(ballot(k[e] >= from));
+    fits = n <= kChunkList;
+  }
+  if (!fits) {  // more than 64 of the largest: none is listed
+    n = 0;
+    from = top + 1;
+  }
+  if (ln == 0) {
+    a.chunk_from[at] = from;
+    a.chunk_n[at] = (uint32_t)n;
+  }
+  uint64_t* list = a.lists + at * kChunkList;
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) c += k[j * VEC + e] >= from;
+    if (ballot(c > 0) == 0) continue;
+    const int incl = wave_scan_incl(c);
+    int to = before + incl - c;
+    before += __builtin_amdgcn_readlane(incl, kWave - 1);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      if (k[j * VEC + e] >= from) {
+        const uint32_t i = (uint32_t)(first + (j * kWave + ln) * VEC + e);
+        list[to++] = (uint64_t)k[j * VEC + e] << 32 | (uint32_t)~i;
+      }
+    }
+  }
+}
+
+// Keeps LDS accesses of a wave in their order (which the hardware keeps).
+__device__ __forceinline__ void wave_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Sorts 1024 E words in LDS, largest first: a bitonic network in which a wave
+// keeps to its own 64 E words wherever partners are that near.
+template <int E>
+__device__ void sort_words(uint64_t* w) {
+  constexpr int P = kSampleThreads * E, R = P / kSampleWaves;
+  const int ln = lane(), wave = (int)threadIdx.x / kWave;
+  __syncthreads();
+  for (int size = 2; size <= P; size *= 2) {
+    for (int j = size / 2; j > 0; j /= 2) {
+      const bool far = 2 * j > R;
+      if (far) __syncthreads();
+#pragma unroll
+      for (int m = 0; m < (E + 1) / 2; ++m) {
+        const int i = wave * (R / 2) + m * kWave + ln;
+        if (E > 1 || ln < R / 2) {
+          const int lo = (i & ~(j - 1)) * 2 + (i & (j - 1));
+          const uint64_t x = w[lo], y = w[lo + j];
+          if ((x < y) == ((lo & size) == 0)) {
+            w[lo] = y;
+            w[lo + j] = x;
+          }
+        }
+      }
+      if (far)
+        __syncthreads();
+      else
+        wave_fence();
+    }
+  }
+  __syncthreads();
+}
+
+// The prefix of a row whose lists are in s.listed (n words, in the row's order)
+// and s.sorted: the last word kept, or 0 if the lists do not reach so far.
+// Nothing is missing in them from the key `from` on.
+template <int E>
+__device__ uint64_t list_prefix(const SampleParams& a, const Wanted& want,
+                                float top, uint32_t from, double total,
+                                SampleLds& s) {
+  const int tid = threadIdx.x;
+  sort_words<E>(s.sorted);
+  uint64_t w[E], m[E], sum = 0;
+  int sure = 0, rare = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    w[e] = s.sorted[tid * E + e];
+    const uint32_t key = (uint32_t)(w[e] >> 32);
+    const double x =
+        key > kKeyNone ? weight_of(key_logit(key), top, want.inv_t) : 0.0;
+    m[e] = fixed(x, a.frac);
+    sum += m[e];
+    sure += key >= from && key > kKeyNone;
+    rare += key > kKeyNone && x >= want.min_w;
+  }
+  uint64_t all;
+  uint64_t before = scan_block(sum, s, &all);
+  uint64_t counts;
+  scan_block((uint64_t)sure << 32 | (uint32_t)rare, s, &counts);
+  const int n_sure = (int)(counts >> 32);
+  const bool whole = from <= kKeyNone + 1;  // all that has weight is listed
+  if (n_sure < 1 || (want.k > n_sure && want.p < 1.0 && !whole)) return 0;
+  int last = n_sure;  // words kept
+  bool ends = false;  // within what is sure
+  if (want.k > 0) {
+    // (rows of fewer logits above -infinity than k keep them all)
+    if (want.k <= n_sure) ends = true;
+    last = want.k < last ? want.k : last;
+  }
+  if (want.p < 1.0) {
+    // The sum that p is a part of: of the first k, or of the row.
+    if (want.k > 0) {
+      uint64_t part = before;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        part += m[e];
+        if (tid * E + e == last - 1) s.found[0] = part;
+      }
+      __syncthreads();
+      total = (double)s.found[0];
+      __syncthreads();
+    } else {
+      total = ldexp(total, a.frac);
+    }
+    const double part = ceil(want.p * total);
+    const uint64_t goal = part < 1.0 ? 1 : (uint64_t)part;
+    if (tid == 0) s.found[0] = (uint64_t)last;
+    __syncthreads();
+    uint64_t sum2 = before;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const uint64_t next = sum2 + m[e];
+      if (sum2 < goal && goal <= next && tid * E + e < last)
+        s.found[0] = (uint64_t)(tid * E + e + 1) | 1ull << 32;
+      sum2 = next;
+    }
+    __syncthreads();
+    if (s.found[0] >> 32) ends = true;
+    last = (int)(uint32_t)s.found[0];
+    __syncthreads();
+  }
+  if (want.min_w > 0.0) {
+    const int n_rare = (int)(uint32_t)counts;
+    if (n_rare < n_sure) ends = true;
+    last = n_rare < last ? n_rare : last;
+  }
+  return (ends || whole) && last > 0 ? s.sorted[last - 1] : 0;
+}
+
+// Rows: from their chunks, or over again.
+template <int T>
+__global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
+    SampleParams a) {
+  __shared__ SampleLds s;
+  const int tid = threadIdx.x, wave = tid / kWave, ln = lane();
+  const int64_t row_i = a.row0 + blockIdx.x;
+  const char* row = a.x + row_i * a.ld;
+  const Wanted want = wanted(a, row_i);
+  const int64_t base = (int64_t)blockIdx.x * a.chunks;
+  const bool in = tid < a.chunks;
+  const bool lists = !want.all() && !want.greedy;
+  const uint32_t chunk_top = in ? a.chunk_max[base + tid] : 0;
+  const uint32_t chunk_from = in && lists ? a.chunk_from[base + tid] : 0;
+  const int n = in && lists ? (int)a.chunk_n[base + tid] : 0;
+  const uint32_t top_key =
+      (uint32_t)max_block((uint64_t)chunk_top, s);
+  const float top = key_logit(top_key);
+  if (top_key == kKeyNone) {
+    if (tid == 0) {
+      a.tokens[row_i] = -1;
+      a.logprobs[row_i] = -INFINITY;
+    }
+    return;
+  }
+  double mass = 0.0;
+  if (in && want.k == 0 && !want.greedy && (want.p < 1.0 || want.min_w <= 0.0))
+    mass = a.chunk_sum[base + tid] *
+           weight_of(key_logit(chunk_top), top, want.inv_t);
+  if (want.greedy || want.all()) {
+    // ---- the chunk, and its logit
+    // Inclusive sums of the chunks' masses: in a wave, then of the waves.
+    double incl = mass;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const double y = __shfl_up(incl, o, kWave);
+      if (ln >= o) incl += y;
+    }
+    double* sums = (double*)s.sums;
+    __syncthreads();  // the maxima have been read
+    if (ln == kWave - 1) sums[wave] = incl;
+    __syncthreads();
+    double before = 0.0, total = 0.0;
+    for (int i = 0; i < kSampleWaves; ++i) {
+      if (i < wave) before += sums[i];
+      total += sums[i];
+    }
+    incl += before;
+    __syncthreads();
+    const double goal = want.u * total;
+    // The first chunk that passes the goal; where rounding leaves none, the
+    // last one that has weight.
+    const bool past = want.greedy ? chunk_top == top_key
+                                  : mass > 0.0 && incl > goal;
+    uint64_t pick = past ? (uint64_t)(2 * kMaxChunks - tid)
+                    : mass > 0.0 ? (uint64_t)tid + 1 : 0;
+    if (past) pick += kMaxChunks;
+    pick = max_block(pick, s);
+    const int chunk = pick > 2 * kMaxChunks ? (int)(3 * kMaxChunks - pick)
+                      : (int)pick - 1;
+    __syncthreads();
+    if (tid == chunk) sums[0] = incl - mass;
+    __syncthreads();
+    if (wave > 0) return;
+    double part = sums[0];
+    const int64_t i0 = (int64_t)chunk * kChunk + ln * 16;
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float y[kSampleVec];
+      read_logits<T>(row, i0 + j * kSampleVec, a.cols, y);
+#pragma unroll
+      for (int e = 0; e < kSampleVec; ++e) x[j * kSampleVec + e] = y[e];
+    }
+    if (want.greedy) {
+      int at = 16;
+#pragma unroll
+      for (int e = 15; e >= 0; --e)
+        if (logit_key(x[e]) == top_key) at = e;
+      const uint64_t have = ballot(at < 16);
+      if (ln == __builtin_ctzll(have)) {
+        a.tokens[row_i] = i0 + at;
+        a.logprobs[row_i] = 0.0f;
+      }
+      return;
+    }
+    double w[16], sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      w[e] = weight_of(x[e], top, want.inv_t);
+      sum += w[e];
+    }
+    double upto = sum;
+    for (int o = 1; o < kWave; o <<= 1) {
+      const double y = __shfl_up(upto, o, kWave);
+      if (ln >= o) upto += y;
+    }
+    const uint64_t over = ballot(sum > 0.0 && part + upto > goal);
+    const uint64_t some = ballot(sum > 0.0);
+    const int who = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
+    if (ln != who) return;
+    part += upto - sum;
+    int at = 0;
+    bool done = false;
+    double got = 0.0;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      part += w[e];
+      if (!done && w[e] > 0.0) {
+        at = e;
+        got = w[e];
+        done = part > goal;
+      }
+    }
+    a.tokens[row_i] = i0 + at;
+    a.logprobs[row_i] = (float)(log(got) - log(total));
+    return;
+  }
+  // ---- lists: their words in LDS, in the row's order
+  const uint32_t from = (uint32_t)max_block((uint64_t)chunk_from, s);
+  uint64_t all;
+  const uint64_t to = scan_block((uint64_t)n, s, &all);
+  const int count = (int)all;
+  double total = mass;
+  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
+  __syncthreads();
+  if (ln == 0) ((double*)s.sums)[wave] = total;
+  __syncthreads();
+  total = 0.0;
+  for (int i = 0; i < kSampleWaves; ++i) total += ((double*)s.sums)[i];
+  uint64_t cut = 0;
+  if (count <= kMaxList && count > 0) {
+    for (int c = wave * kWave; c < a.chunks; c += kSampleThreads) {
+      // a wave's 64 chunks are those of its own threads
+      for (int i = 0; i < kWave && c + i < a.chunks; ++i) {
+        const int nc = __builtin_amdgcn_readlane(n, i);
+        const int tc = __builtin_amdgcn_readlane((int)to, i);
+        if (ln < nc) {
+          const uint64_t w = a.lists[(base + c + i) * kChunkList + ln];
+          s.listed[tc + ln] = w;
+          s.sorted[tc + ln] = w;
+        }
+      }
+    }
+    const int room = count <= 1024 ? 1024 : count <= 2048 ? 2048 : 4096;
+    for (int i = count + tid; i < room; i += kSampleThreads) {
+      s.listed[i] = 0;
+      s.sorted[i] = 0;
+    }
+    cut = room == 1024   ? list_prefix<1>(a, want, top, from, total, s)
+          : room == 2048 ? list_prefix<2>(a, want, top, from, total, s)
+                         : list_prefix<4>(a, want, top, from, total, s);
+  }
+  if (cut == 0) {
+    __syncthreads();
+    sample_row<T>(a, row_i, s);
+    return;
+  }
+  // ---- in the row's order
+  constexpr int E = kMaxList / kSampleThreads;
+  uint64_t m[E], sum = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int i = tid * E + e;
+    const uint64_t w = i < count ? s.listed[i] : 0;
+    m[e] = w >= cut ? fixed(weight_of(key_logit((uint32_t)(w >> 32)), top,
+                                      want.inv_t),
+                            a.frac)
+                    : 0;
+    sum += m[e];
+  }
+  uint64_t kept;
+  uint64_t part = scan_block(sum, s, &kept);
+  uint64_t goal = (uint64_t)(want.u * (double)kept);
+  if (goal >= kept) goal = kept - 1;
+  if (part <= goal && goal < part + sum) {
+    int e = 0;
+    while (part + m[e] <= goal) part += m[e++];
+    const uint64_t w = s.listed[tid * E + e];
+    a.tokens[row_i] = (int64_t)(uint32_t) ~(uint32_t)w;
+    a.logprobs[row_i] = (float)(
+        log(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t)) -
+        log(ldexp((double)kept, -a.frac)));
+  }
+}
+
+// Rows too long for lists.
 template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_row_kernel(
     SampleParams a) {
