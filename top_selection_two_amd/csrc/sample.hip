@@ -24,13 +24,15 @@ bool meets(const void* a, int64_t na, const void* b, int64_t nb) {
 constexpr int64_t kSampleWork = (int64_t)1 << 26;
 
 struct Kernels {
-  const void *row, *chunk, *finish;
+  const void *row, *chunk, *finish, *bins, *wide;
 };
 template <int T>
 Kernels kernels_of() {
   return {(const void*)&sample_row_kernel<T>,
           (const void*)&sample_chunk_kernel<T>,
-          (const void*)&sample_finish_kernel<T>};
+          (const void*)&sample_finish_kernel<T>,
+          (const void*)&sample_bins_kernel<T>,
+          (const void*)&sample_wide_kernel<T>};
 }
 Kernels kernels(int32_t dtype) {
   return dtype == LIBTOPK_F32    ? kernels_of<kLogF32>()
@@ -107,18 +109,30 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   const int64_t rank = kMaxList * 5 / 8 / chunks;
   p.rank = (int32_t)(rank < 2 ? 2 : rank > 32 ? 32 : rank);
   // Batches of rows share the workspace, which stays below 64 MB.
-  const int64_t per = chunks * (8 + 3 * 4 + 8 * kChunkList);
+  const int64_t per = chunks * (8 + 3 * 4 + 8 + 8 * kChunkList) +
+                      8 * (kWideBins + kMaxList) + (int64_t)sizeof(WideRow);
   int64_t batch = kSampleWork / per;
   if (batch > rows) batch = rows;
   Work work;
-  rc = get_work(dev, st, (size_t)(batch * per), 1, &work);
+  rc = get_work(dev, st, (size_t)(batch * per), (size_t)batch, &work);
   if (rc != LIBTOPK_OK) return rc;
   const int64_t n = batch * chunks;
   p.lists = (uint64_t*)work.base;
   p.chunk_sum = (double*)(p.lists + n * kChunkList);
-  p.chunk_max = (uint32_t*)(p.chunk_sum + n);
+  p.chunk_mass = (uint64_t*)(p.chunk_sum + n);
+  p.bins = p.chunk_mass + n;
+  p.pivots = p.bins + batch * kWideBins;
+  p.wide = (WideRow*)(p.pivots + batch * kMaxList);
+  p.chunk_max = (uint32_t*)(p.wide + batch);
   p.chunk_from = p.chunk_max + n;
   p.chunk_n = p.chunk_from + n;
+  p.ticket = work.tickets;
+  p.epoch = work.epoch;
+  // Settings that lists always meet need no more.
+  const bool wide =
+      (how->top_p || how->top_p_all < 1.0f || how->top_k ||
+       how->top_k_all > 0 || how->min_p || how->min_p_all > 0.0f);
+  const int64_t parts = (chunks + kWideChunks - 1) / kWideChunks;
   for (int64_t r = 0; r < rows && rc == LIBTOPK_OK; r += batch) {
     const int64_t m = rows - r < batch ? rows - r : batch;
     p.row0 = r;
@@ -126,6 +140,10 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
                 kBlock, p, st);
     if (rc == LIBTOPK_OK)
       rc = launch(fn.finish, dim3((unsigned)m), kSampleThreads, p, st);
+    if (rc == LIBTOPK_OK && wide)
+      rc = launch(fn.bins, dim3((unsigned)(m * parts)), kSampleThreads, p, st);
+    if (rc == LIBTOPK_OK && wide)
+      rc = launch(fn.wide, dim3((unsigned)(m * parts)), kSampleThreads, p, st);
   }
   return rc;
 }

@@ -53,7 +53,26 @@ struct SampleParams {
   uint32_t* chunk_n;
   double* chunk_sum;
   uint64_t* lists;  // [row - row0][chunk][kChunkList]
+  // Of rows whose prefix is wide, [row - row0].., see sample_bins_kernel.
+  struct WideRow* wide;
+  uint64_t* bins;        // [kWideBins]
+  uint64_t* chunk_mass;  // [chunk]
+  uint64_t* pivots;      // [kMaxList]
+  uint64_t* ticket;
+  uint32_t epoch;
 };
+
+// What a wide prefix has to reach.
+enum { kNotWide = 0, kWideMass = 1, kWideCount = 2, kWideAll = 3 };
+struct WideRow {
+  uint32_t mode;
+  uint32_t top;     // the largest logit's key
+  uint64_t goal;    // mass or count
+  uint32_t pivots;  // listed so far
+  uint32_t spare;
+};
+constexpr int kWideBins = 2048;
+constexpr int kWideChunks = kSampleThreads / kWave;  // of a workgroup
 
 constexpr int kChunk = 1024;     // logits of a wave
 constexpr int kChunkList = 64;   // listed of them at most
@@ -444,11 +463,59 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
 // a prefix of the order that ends above it is found there, by sorting at most
 // 4096 words.  Rows whose prefix goes further are done over.
 template <int T>
+struct ChunkShape {
+  static constexpr int VEC = 16 / (T == kLogF32 ? 4 : 2);  // logits of a load
+  static constexpr int LOADS = kChunk / kWave / VEC;
+  static constexpr int N = VEC * LOADS;  // of a lane: 16
+  // Index in the chunk of a lane's logit e.
+  __device__ static int at(int e) {
+    return (e / VEC * kWave + lane()) * VEC + e % VEC;
+  }
+};
+// A wave reads a chunk; -infinity for NaN and past the row's end.
+template <int T>
+__device__ __forceinline__ void read_chunk(const char* row, int first,
+                                           int32_t cols,
+                                           float (&x)[ChunkShape<T>::N]) {
+  typedef ChunkShape<T> S;
+#pragma unroll
+  for (int j = 0; j < S::LOADS; ++j) {
+    const int i = first + (j * kWave + lane()) * S::VEC;
+    if (i + S::VEC <= cols) {
+      if constexpr (T == kLogF32) {
+        typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+        const f32x4a v = *(const f32x4a*)(row + (int64_t)i * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j * 4 + e] = v[e];
+      } else {
+        typedef unsigned u32x4a __attribute__((ext_vector_type(4), aligned(2)));
+        const u32x4a v = *(const u32x4a*)(row + (int64_t)i * 2);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const unsigned d = v[e / 2];
+          const unsigned h = e % 2 ? d >> 16 : d & 0xffffu;
+          if constexpr (T == kLogBf16)
+            x[j * 8 + e] = __uint_as_float(h << 16);
+          else
+            x[j * 8 + e] = (float)__builtin_bit_cast(_Float16, (uint16_t)h);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < S::VEC; ++e)
+        x[j * S::VEC + e] =
+            i + e < cols ? read_logit<T>(row, i + e) : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < S::N; ++e)
+    x[e] = x[e] != x[e] ? -INFINITY : x[e] + 0.0f;
+}
+
+template <int T>
 __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
-  constexpr int SIZE = T == kLogF32 ? 4 : 2;
-  constexpr int VEC = 16 / SIZE;            // logits of a load
-  constexpr int LOADS = kChunk / kWave / VEC;
-  constexpr int N = VEC * LOADS;            // 16
+  typedef ChunkShape<T> S;
+  constexpr int VEC = S::VEC, LOADS = S::LOADS, N = S::N;
   const int wg = (a.chunks + kWaves - 1) / kWaves;
   const int r = (int)(blockIdx.x / (unsigned)wg);
   const int chunk =
@@ -460,40 +527,11 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
   const int ln = lane();
   const int first = chunk * kChunk;
   float x[N];
-#pragma unroll
-  for (int j = 0; j < LOADS; ++j) {
-    const int i = first + (j * kWave + ln) * VEC;
-    if (i + VEC <= a.cols) {
-      if constexpr (T == kLogF32) {
-        typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
-        const f32x4a v = *(const f32x4a*)(row + (int64_t)i * 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[j * VEC + e] = v[e];
-      } else {
-        typedef unsigned u32x4a __attribute__((ext_vector_type(4), aligned(2)));
-        const u32x4a v = *(const u32x4a*)(row + (int64_t)i * 2);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const unsigned d = v[e / 2];
-          const unsigned h = e % 2 ? d >> 16 : d & 0xffffu;
-          if constexpr (T == kLogBf16)
-            x[j * VEC + e] = __uint_as_float(h << 16);
-          else
-            x[j * VEC + e] = (float)__builtin_bit_cast(_Float16, (uint16_t)h);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        x[j * VEC + e] =
-            i + e < a.cols ? read_logit<T>(row, i + e) : -INFINITY;
-    }
-  }
+  read_chunk<T>(row, first, a.cols, x);
   uint32_t k[N];
   uint32_t mine = 0;
 #pragma unroll
   for (int e = 0; e < N; ++e) {
-    x[e] = x[e] != x[e] ? -INFINITY : x[e] + 0.0f;
     k[e] = logit_key(x[e]);
     mine = k[e] > mine ? k[e] : mine;
   }
@@ -685,6 +723,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   const char* row = a.x + row_i * a.ld;
   const Wanted want = wanted(a, row_i);
   const int64_t base = (int64_t)blockIdx.x * a.chunks;
+  if (tid == 0 && a.bins) a.wide[blockIdx.x].mode = kNotWide;
   const bool in = tid < a.chunks;
   const bool lists = !want.all() && !want.greedy;
   const uint32_t chunk_top = in ? a.chunk_max[base + tid] : 0;
@@ -829,7 +868,25 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   }
   if (cut == 0) {
     __syncthreads();
-    sample_row<T>(a, row_i, s);
+    const int mode = want.k > 0 ? (want.p < 1.0 ? kNotWide : kWideCount)
+                     : want.p < 1.0 ? kWideMass
+                                    : kWideAll;
+    if (mode == kNotWide || !a.bins) {
+      sample_row<T>(a, row_i, s);
+      return;
+    }
+    uint64_t* bins = a.bins + (int64_t)blockIdx.x * kWideBins;
+    for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
+    if (tid == 0) {
+      const double part = ceil(want.p * ldexp(total, a.frac));
+      WideRow w = {};
+      w.mode = (uint32_t)mode;
+      w.top = top_key;
+      w.goal = mode == kWideCount ? (uint64_t)want.k
+               : part < 1.0       ? 1
+                                  : (uint64_t)part;
+      a.wide[blockIdx.x] = w;
+    }
     return;
   }
   // ---- in the row's order
@@ -857,6 +914,274 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     a.logprobs[row_i] = (float)(
         log(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t)) -
         log(ldexp((double)kept, -a.frac)));
+  }
+}
+
+// ---- wide prefixes ----------------------------------------------------------
+// A prefix beyond the lists (a nucleus of tens of thousands) is found in two
+// more launches over the row, by workgroups of 16 chunks.  The first adds up
+// the masses (or counts) of the logits in 2048 bins of (M - x) / T, 1/64 wide;
+// integers, so that their order is nothing.  The second finds the bin in which
+// the goal lies, adds up each chunk's mass above it, and lists the bin's own
+// logits; the row's last workgroup sorts these, finds the last one kept, the
+// chunk where u times the kept mass lies, and the token in it.
+__device__ __forceinline__ int wide_bin(float x, float top, double c) {
+  const double d = (double)top - (double)x;
+  return d > 0.0 ? (int)fmin(d * c, (double)(kWideBins - 1)) : 0;
+}
+
+template <int T>
+__global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
+    SampleParams a) {
+  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
+  const int r = (int)(blockIdx.x / (unsigned)wg);
+  const WideRow wide = a.wide[r];
+  if (wide.mode != kWideMass && wide.mode != kWideCount) return;
+  __shared__ uint64_t bins[kWideBins];
+  const int tid = threadIdx.x;
+  for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
+  __syncthreads();
+  const int64_t row_i = a.row0 + r;
+  const Wanted want = wanted(a, row_i);
+  const float top = key_logit(wide.top);
+  const int chunk =
+      (int)(blockIdx.x % (unsigned)wg) * kWideChunks + tid / kWave;
+  if (chunk < a.chunks) {
+    typedef ChunkShape<T> S;
+    float x[S::N];
+    read_chunk<T>(a.x + row_i * a.ld, chunk * kChunk, a.cols, x);
+    const double c = 64.0 * want.inv_t;
+#pragma unroll
+    for (int e = 0; e < S::N; ++e) {
+      // What lies in the last bin has no weight to speak of: 2^-46 and less.
+      const int bin = wide_bin(x[e], top, c);
+      if (bin == kWideBins - 1) continue;
+      atomicAdd((unsigned long long*)&bins[bin],
+                wide.mode == kWideCount
+                    ? 1ull
+                    : (unsigned long long)fixed(
+                          weight_of(x[e], top, want.inv_t), a.frac));
+    }
+  }
+  __syncthreads();
+  unsigned long long* all =
+      (unsigned long long*)(a.bins + (int64_t)r * kWideBins);
+  for (int i = tid; i < kWideBins; i += kSampleThreads)
+    if (bins[i]) atomicAdd(all + i, (unsigned long long)bins[i]);
+}
+
+// Sorts the first `count` of s.sorted (the others of a power of two become 0)
+// and finds how many of them, from the largest, it takes to reach `goal`
+// (in masses, or in words); 0 if they do not.
+template <int E>
+__device__ int pivots_kept(const SampleParams& a, const Wanted& want,
+                           const WideRow& wide, uint64_t goal, SampleLds& s) {
+  const int tid = threadIdx.x;
+  sort_words<E>(s.sorted);
+  const float top = key_logit(wide.top);
+  uint64_t m[E], sum = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint64_t w = s.sorted[tid * E + e];
+    m[e] = 0;
+    if (w)
+      m[e] = wide.mode == kWideCount
+                 ? 1
+                 : fixed(weight_of(key_logit((uint32_t)(w >> 32)), top,
+                                   want.inv_t),
+                         a.frac);
+    sum += m[e];
+  }
+  uint64_t all;
+  uint64_t before = scan_block(sum, s, &all);
+  if (tid == 0) s.found[0] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint64_t next = before + m[e];
+    if (before < goal && goal <= next) s.found[0] = (uint64_t)(tid * E + e + 1);
+    before = next;
+  }
+  __syncthreads();
+  const int n = (int)s.found[0];
+  __syncthreads();
+  return n;
+}
+
+template <int T>
+__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
+    SampleParams a) {
+  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
+  const int r = (int)(blockIdx.x / (unsigned)wg);
+  const WideRow wide = a.wide[r];
+  if (wide.mode == kNotWide) return;
+  __shared__ SampleLds s;
+  __shared__ int flag;
+  const int tid = threadIdx.x, ln = lane();
+  const int64_t row_i = a.row0 + r;
+  const char* row = a.x + row_i * a.ld;
+  const Wanted want = wanted(a, row_i);
+  const float top = key_logit(wide.top);
+  const double c = 64.0 * want.inv_t;
+  typedef ChunkShape<T> S;
+  // ---- the bin of the goal
+  int pivot = kWideBins;  // all above it
+  uint64_t above = 0;
+  if (wide.mode != kWideAll) {
+    constexpr int B = kWideBins / kSampleThreads;
+    const uint64_t* bins = a.bins + (int64_t)r * kWideBins;
+    uint64_t b[B], sum = 0;
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      b[i] = bins[tid * B + i];
+      sum += b[i];
+    }
+    uint64_t all;
+    uint64_t before = scan_block(sum, s, &all);
+    if (tid == 0) s.found[0] = kWideBins;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      if (before < wide.goal && wide.goal <= before + b[i]) {
+        s.found[0] = (uint64_t)(tid * B + i);
+        s.found[1] = before;
+      }
+      before += b[i];
+    }
+    __syncthreads();
+    pivot = (int)s.found[0];
+    above = s.found[1];
+    __syncthreads();
+  }
+  // (a goal beyond the bins: the row is done over)
+  const bool lost = wide.mode != kWideAll && pivot == kWideBins;
+  const int chunk =
+      (int)(blockIdx.x % (unsigned)wg) * kWideChunks + tid / kWave;
+  uint64_t* const pivots = a.pivots + (int64_t)r * kMaxList;
+  if (chunk < a.chunks && !lost) {
+    float x[S::N];
+    read_chunk<T>(row, chunk * kChunk, a.cols, x);
+    uint64_t sum = 0;
+    int mine = 0;
+#pragma unroll
+    for (int e = 0; e < S::N; ++e) {
+      const int bin = wide_bin(x[e], top, c);
+      if (bin < pivot) {
+        const double w = weight_of(x[e], top, want.inv_t);
+        if (w >= want.min_w) sum += fixed(w, a.frac);
+      }
+      mine += bin == pivot && pivot < kWideBins;
+    }
+    if (ballot(mine > 0)) {
+      const int incl = wave_scan_incl(mine);
+      unsigned to = 0;
+      if (ln == kWave - 1) to = atomicAdd(&a.wide[r].pivots, (unsigned)incl);
+      to = (unsigned)__builtin_amdgcn_readlane((int)to, kWave - 1);
+      to += (unsigned)(incl - mine);
+#pragma unroll
+      for (int e = 0; e < S::N; ++e) {
+        if (wide_bin(x[e], top, c) != pivot) continue;
+        const uint32_t i = (uint32_t)(chunk * kChunk + S::at(e));
+        // (past the row's end there is -infinity, which is in the last bin)
+        if (to < kMaxList)
+          st_agent(pivots + to,
+                   (uint64_t)logit_key(x[e]) << 32 | (uint32_t)~i);
+        ++to;
+      }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += shfl64(sum, ln ^ o);
+    if (ln == 0) st_agent(a.chunk_mass + (int64_t)r * a.chunks + chunk, sum);
+  }
+  if (!last_to_finish(a.ticket + r, wg, a.epoch, &flag)) return;
+  // ---- the row's last workgroup
+  const unsigned count = ld_agent(&a.wide[r].pivots);
+  uint64_t cut = 0;
+  bool done = !lost;
+  if (wide.mode != kWideAll && done) {
+    done = count <= kMaxList && pivot < kWideBins - 1;
+    if (done) {
+      const int room = count <= 1024 ? 1024 : count <= 2048 ? 2048 : 4096;
+      for (int i = tid; i < room; i += kSampleThreads)
+        s.sorted[i] = i < (int)count ? ld_agent(pivots + i) : 0;
+      const uint64_t goal = wide.goal - above;
+      const int kept =
+          room == 1024   ? pivots_kept<1>(a, want, wide, goal, s)
+          : room == 2048 ? pivots_kept<2>(a, want, wide, goal, s)
+                         : pivots_kept<4>(a, want, wide, goal, s);
+      done = kept > 0;
+      if (done) cut = s.sorted[kept - 1];
+    }
+  }
+  if (!done) {
+    __syncthreads();
+    sample_row<T>(a, row_i, s);
+    return;
+  }
+  // Masses of the chunks, in the other half of LDS.
+  for (int i = tid; i < kMaxChunks; i += kSampleThreads)
+    s.listed[i] = i < a.chunks
+                      ? ld_agent(a.chunk_mass + (int64_t)r * a.chunks + i)
+                      : 0;
+  __syncthreads();
+  if (cut) {
+    for (int i = tid; i < (int)count; i += kSampleThreads) {
+      const uint64_t w = s.sorted[i];
+      if (w < cut) continue;
+      const double x =
+          weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
+      if (x >= want.min_w)
+        atomicAdd((unsigned long long*)
+                      &s.listed[(uint32_t) ~(uint32_t)w / kChunk],
+                  (unsigned long long)fixed(x, a.frac));
+    }
+    __syncthreads();
+  }
+  const uint64_t mass = s.listed[tid];
+  uint64_t total;
+  const uint64_t before = scan_block(mass, s, &total);
+  uint64_t goal = (uint64_t)(want.u * (double)total);
+  if (goal >= total) goal = total - 1;
+  if (before <= goal && goal < before + mass) {
+    s.found[0] = (uint64_t)tid;
+    s.found[1] = before;
+  }
+  __syncthreads();
+  if (tid >= kWave) return;
+  // Lane l takes logits 16 l .. of the chunk.
+  uint64_t part = s.found[1];
+  const int64_t i0 = (int64_t)s.found[0] * kChunk + ln * 16;
+  uint64_t m[16], sum = 0;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float y[kSampleVec];
+    read_logits<T>(row, i0 + j * kSampleVec, a.cols, y);
+#pragma unroll
+    for (int e = 0; e < kSampleVec; ++e) {
+      const int64_t i = i0 + j * kSampleVec + e;
+      const uint64_t word =
+          (uint64_t)logit_key(y[e]) << 32 | (uint32_t) ~(uint32_t)i;
+      const double w = weight_of(y[e], top, want.inv_t);
+      // (-infinity past the end has no weight)
+      m[j * kSampleVec + e] =
+          word >= cut && w >= want.min_w ? fixed(w, a.frac) : 0;
+      sum += m[j * kSampleVec + e];
+    }
+  }
+  part += wave_scan64(sum) - sum;
+  if (part <= goal && goal < part + sum) {
+    int at = 0;
+    bool past = false;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      part += m[e];
+      if (!past) at = e;
+      past = past || part > goal;
+    }
+    a.tokens[row_i] = i0 + at;
+    a.logprobs[row_i] =
+        (float)(log(weight_of(read_logit<T>(row, i0 + at), top, want.inv_t)) -
+                log(ldexp((double)total, -a.frac)));
   }
 }
 
