@@ -84,7 +84,8 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.x = (const char*)logits;
   p.ld = ld * size;
   p.cols = (int32_t)cols;
-  p.frac = 62 - ceil_log2((int32_t)cols);
+  const int frac = 62 - ceil_log2((int32_t)cols);
+  p.unit = (double)((uint64_t)1 << (frac < 51 ? frac : 51));
   p.temperature = how->temperature;
   p.top_k = how->top_k;
   p.top_p = how->top_p;
@@ -128,7 +129,7 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.chunk_n = p.chunk_from + n;
   p.ticket = work.tickets;
   p.epoch = work.epoch;
-  // Settings that lists always meet need no more.
+  // Without settings there are no prefixes, and none that goes beyond lists.
   const bool wide =
       (how->top_p || how->top_p_all < 1.0f || how->top_k ||
        how->top_k_all > 0 || how->min_p || how->min_p_all > 0.0f);

@@ -9,8 +9,9 @@
 //
 // The token must not depend on how sums are ordered, nor lie beside the one
 // that exact arithmetic gives: weights are taken in 64 bits (whose vector
-// instructions run at the rate of those in 32) and added as integers, in units
-// of 2^-S of the largest, S = 62 - ceil(log2 cols): 2^-45 for 131072 logits.
+// instructions run at half the rate of those in 32) and added as integers, in
+// units of 2^-S of the largest, S = 62 - ceil(log2 cols) and at most 51: 2^-45
+// for 131072 logits.
 #pragma once
 
 #include "wave.hpp"
@@ -32,7 +33,7 @@ struct SampleParams {
   const char* x;
   int64_t ld;  // bytes
   int32_t cols;
-  int32_t frac;  // S
+  double unit;   // 2^S
   // NULL: the number after them holds for every row
   const float* temperature;
   const int32_t* top_k;
@@ -63,7 +64,7 @@ struct SampleParams {
 };
 
 // What a wide prefix has to reach.
-enum { kNotWide = 0, kWideMass = 1, kWideCount = 2, kWideAll = 3 };
+enum { kNotWide, kWideMass, kWideCount, kWideAll, kWideRow };
 struct WideRow {
   uint32_t mode;
   uint32_t top;     // the largest logit's key
@@ -72,6 +73,7 @@ struct WideRow {
   uint32_t spare;
 };
 constexpr int kWideBins = 2048;
+constexpr double kWidePerBit = 44.0;  // bins of a factor of 2: 2^-46 in all
 constexpr int kWideChunks = kSampleThreads / kWave;  // of a workgroup
 
 constexpr int kChunk = 1024;     // logits of a wave
@@ -83,8 +85,10 @@ constexpr uint32_t kKeyNone = 0x007fffffu;  // of -infinity
 // What a row asks for.
 struct Wanted {
   __device__ bool all() const { return k == 0 && p >= 1.0 && min_w <= 0.0; }
+  // Does the sum of the row's weights matter?
+  __device__ bool sums() const { return k == 0 && (p < 1.0 || min_w <= 0.0); }
 
-  double inv_t;   // 1 / temperature
+  double inv_t;   // log2 e / temperature
   bool greedy;
   int32_t k;      // 0: all
   double p;       // >= 1: all
@@ -95,7 +99,7 @@ __device__ __forceinline__ Wanted wanted(const SampleParams& a, int64_t row) {
   Wanted r;
   const float t = a.temperature ? a.temperature[row] : a.temperature_all;
   r.greedy = !(t > 0.0f);
-  r.inv_t = 1.0 / (double)t;
+  r.inv_t = 1.44269504088896340736 / (double)t;
   const int32_t k = a.top_k ? a.top_k[row] : a.top_k_all;
   r.k = k > 0 && k < a.cols ? k : 0;
   const float p = a.top_p ? a.top_p[row] : a.top_p_all;
@@ -166,38 +170,39 @@ __device__ __forceinline__ void read_logits(const char* row, int64_t i,
   }
 }
 
-// exp(t) for t <= 0: 2^n 2^f with |f| <= 1/2 and the series of 2^f in f ln 2
-// to the 11th power, which leaves (ln 2 / 2)^12 / 12! = 6e-15.
-__device__ __forceinline__ double exp_neg(double t) {
-  constexpr double kL = 0.693147180559945309417;
-  const double y = t * 1.44269504088896340736;
-  const double n = rint(y);
-  const double f = (y - n) * kL;
-  double s = 1.0 / 39916800.0;
-  s = fma(s, f, 1.0 / 3628800.0);
-  s = fma(s, f, 1.0 / 362880.0);
-  s = fma(s, f, 1.0 / 40320.0);
-  s = fma(s, f, 1.0 / 5040.0);
-  s = fma(s, f, 1.0 / 720.0);
-  s = fma(s, f, 1.0 / 120.0);
-  s = fma(s, f, 1.0 / 24.0);
-  s = fma(s, f, 1.0 / 6.0);
-  s = fma(s, f, 0.5);
+// 2^y for y <= 0: 2^n 2^f with |f| <= 1/2 and the series of 2^f in f ln 2 to
+// the 11th power, which leaves (ln 2 / 2)^12 / 12! = 6e-15.  (Its coefficients
+// are (ln 2)^i / i!.)
+__device__ __forceinline__ double exp2_neg(double y) {
+  // Below 2^-1100 nothing is left; a NaN (0 times infinity) is nothing too.
+  y = fmax(y, -1100.0);
+  const double n = rint(y), f = y - n;
+  double s = 4.4455382718708116e-10;
+  s = fma(s, f, 7.0549116208011233e-09);
+  s = fma(s, f, 1.0178086009239699e-07);
+  s = fma(s, f, 1.3215486790144310e-06);
+  s = fma(s, f, 1.5252733804059840e-05);
+  s = fma(s, f, 1.5403530393381610e-04);
+  s = fma(s, f, 1.3333558146428443e-03);
+  s = fma(s, f, 9.6181291076284772e-03);
+  s = fma(s, f, 5.5504108664821580e-02);
+  s = fma(s, f, 2.4022650695910072e-01);
+  s = fma(s, f, 6.9314718055994531e-01);
   s = fma(s, f, 1.0);
-  s = fma(s, f, 1.0);
-  // n is exact as an int from -1100 on; below that nothing is left.
-  return t < -740.0 ? 0.0 : ldexp(s, (int)n);
+  return ldexp(s, (int)n);
 }
 
-// Weight of a logit next to the row's largest, `top`.
+// Weight of a logit next to the row's largest, `top`; inv_t is log2 e / T.
 __device__ __forceinline__ double weight_of(float x, float top, double inv_t) {
-  if (x == top) return 1.0;
-  // -infinity for a masked logit, and for all next to an infinite one
-  const double d = (double)x - (double)top;
-  return d == -INFINITY ? 0.0 : exp_neg(d * inv_t);
+  // (next to an infinite one: itself 1, and the others -infinity times inv_t)
+  if (top == INFINITY) return x == top ? 1.0 : 0.0;
+  return exp2_neg(((double)x - (double)top) * inv_t);
 }
-__device__ __forceinline__ uint64_t fixed(double w, int frac) {
-  return (uint64_t)(ldexp(w, frac) + 0.5);
+// A weight in units of 2^-S, S <= 51: the sum with 2^52 is rounded to a whole
+// number, which its low bits are.
+__device__ __forceinline__ uint64_t fixed(double w, const SampleParams& a) {
+  const double v = fma(w, a.unit, 0x1p52);
+  return (uint64_t)__double_as_longlong(v) & 0xfffffffffffffull;
 }
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int from) {
@@ -205,13 +210,46 @@ __device__ __forceinline__ uint64_t shfl64(uint64_t v, int from) {
   const uint32_t hi = (uint32_t)__shfl((int)(uint32_t)(v >> 32), from, kWave);
   return ((uint64_t)hi << 32) | lo;
 }
+// A 64-bit value moved between lanes; 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t move64(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(
+      0, (int)(uint32_t)(v >> 32), CTRL, ROWS, 0xf, false);
+  return ((uint64_t)hi << 32) | lo;
+}
+// Inclusive prefix sums over a wave, as wave_scan_incl.
 __device__ __forceinline__ uint64_t wave_scan64(uint64_t v) {
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const uint64_t w = shfl64(v, lane() - o < 0 ? 0 : lane() - o);
-    if (lane() >= o) v += w;
-  }
+  v += move64<0x111, 0xf>(v);
+  v += move64<0x112, 0xf>(v);
+  v += move64<0x114, 0xf>(v);
+  v += move64<0x118, 0xf>(v);
+  v += move64<0x142, 0xa>(v);
+  v += move64<0x143, 0xc>(v);
   return v;
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double move_double(double v) {
+  return __longlong_as_double(
+      (long long)move64<CTRL, ROWS>((uint64_t)__double_as_longlong(v)));
+}
+__device__ __forceinline__ double wave_scan_double(double v) {
+  v += move_double<0x111, 0xf>(v);
+  v += move_double<0x112, 0xf>(v);
+  v += move_double<0x114, 0xf>(v);
+  v += move_double<0x118, 0xf>(v);
+  v += move_double<0x142, 0xa>(v);
+  v += move_double<0x143, 0xc>(v);
+  return v;
+}
+// A lane's 64-bit value in all.
+__device__ __forceinline__ uint64_t lane64(uint64_t v, int from) {
+  const uint32_t lo =
+      (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, from);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), from);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 // LDS of a row.
@@ -223,13 +261,17 @@ struct SampleLds {
       uint64_t tile_mass[kMaxTiles];
       int32_t tile_ties[kMaxTiles];
     };
-    struct {  // its list
-      uint64_t sorted[kMaxList];
-      uint64_t listed[kMaxList];
+    struct {  // words of a list
+      uint64_t words[kMaxList];
+      uint64_t bin_mass[kSampleBins];
+      uint32_t bin_count[kSampleBins];
+      uint64_t chunk_mass[kMaxChunks];
     };
   };
   uint64_t sums[kSampleWaves];
+  uint32_t counts[2][kSampleWaves];
   uint64_t found[4];
+  uint32_t gathered;
 };
 
 // Exclusive prefix of v over the workgroup's threads, and the total.
@@ -300,7 +342,7 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
         const int bin = (int)(k >> shift & ((1u << bits) - 1));
         if constexpr (MASS)
           atomicAdd((unsigned long long*)&s.mass[bin],
-                    fixed(weight_of(x[e], top, inv_t), a.frac));
+                    fixed(weight_of(x[e], top, inv_t), a));
         else
           atomicAdd(&s.count[bin], 1u);
       }
@@ -310,7 +352,7 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
       atomicAdd((unsigned long long*)
                     &s.mass[in.key >> shift & ((1u << bits) - 1)],
                 (uint64_t)in.ties *
-                    fixed(weight_of(key_logit(in.key), top, inv_t), a.frac));
+                    fixed(weight_of(key_logit(in.key), top, inv_t), a));
     __syncthreads();
     // Thread i takes bins 2 i and 2 i + 1 counted from the top.
     const int b = kSampleBins - 1 - 2 * tid;
@@ -331,7 +373,7 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
     __syncthreads();
   }
   uint64_t one = 1;
-  if (MASS) one = fixed(weight_of(key_logit(out.key), top, inv_t), a.frac);
+  if (MASS) one = fixed(weight_of(key_logit(out.key), top, inv_t), a);
   out.ties = (int64_t)((goal - out.above + one - 1) / one);
   return out;
 }
@@ -378,11 +420,11 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
 #pragma unroll
       for (int e = 0; e < kSampleVec; ++e)
         if (logit_key(x[e]) > in.key)
-          mine += fixed(weight_of(x[e], top, want.inv_t), a.frac);
+          mine += fixed(weight_of(x[e], top, want.inv_t), a);
     }
     scan_block(mine, s, &all);
     all += (uint64_t)in.ties *
-           fixed(weight_of(key_logit(in.key), top, want.inv_t), a.frac);
+           fixed(weight_of(key_logit(in.key), top, want.inv_t), a);
     const double part = ceil(want.p * (double)all);
     const uint64_t goal = part < 1.0 ? 1 : (uint64_t)part;
     in = find_prefix<T, true>(a, row, top, want.inv_t, in,
@@ -411,7 +453,7 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
       m[e] = 0;
       if (kept) {
         const double w = weight_of(x[e], top, want.inv_t);
-        if (w >= want.min_w) m[e] = fixed(w, a.frac);
+        if (w >= want.min_w) m[e] = fixed(w, a);
       }
       sum += m[e];
     }
@@ -447,8 +489,8 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
     const int64_t i = (int64_t)t * kSampleTile + (int64_t)tid * kSampleVec + e;
     a.tokens[row_i] = i;
     a.logprobs[row_i] =
-        (float)(log(weight_of(read_logit<T>(row, i), top, want.inv_t)) -
-                log(ldexp((double)total, -a.frac)));
+        (float)log(weight_of(read_logit<T>(row, i), top, want.inv_t) /
+                   ((double)total / a.unit));
   }
 }
 
@@ -548,13 +590,12 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
     }
     return;
   }
-  if (want.k == 0 && (want.p < 1.0 || want.min_w <= 0.0)) {
+  if (want.sums()) {
     double sum = 0.0;
 #pragma unroll
     for (int e = 0; e < N; ++e) sum += weight_of(x[e], m, want.inv_t);
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-    if (ln == 0) a.chunk_sum[at] = sum;
+    sum = wave_scan_double(sum);
+    if (ln == kWave - 1) a.chunk_sum[at] = sum;
   }
   if (want.all()) return;
   // ---- the list
@@ -578,22 +619,28 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
     a.chunk_from[at] = from;
     a.chunk_n[at] = (uint32_t)n;
   }
+  // The lane's listed logits as bits; each load's lie before the next load's.
+  uint32_t bits = 0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) bits |= (k[e] >= from ? 1u : 0u) << e;
   uint64_t* list = a.lists + at * kChunkList;
   int before = 0;
 #pragma unroll
   for (int j = 0; j < LOADS; ++j) {
-    int c = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) c += k[j * VEC + e] >= from;
-    if (ballot(c > 0) == 0) continue;
+    uint32_t left = bits >> (j * VEC) & ((1u << VEC) - 1);
+    const int c = __popc(left);
     const int incl = wave_scan_incl(c);
     int to = before + incl - c;
     before += __builtin_amdgcn_readlane(incl, kWave - 1);
+    while (ballot(left != 0)) {  // two or three times as a rule
+      if (left) {
+        const int e = __builtin_ctz(left);
+        left &= left - 1;
+        uint32_t key = k[j * VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      if (k[j * VEC + e] >= from) {
+        for (int i = 1; i < VEC; ++i) key = e == i ? k[j * VEC + i] : key;
         const uint32_t i = (uint32_t)(first + (j * kWave + ln) * VEC + e);
-        list[to++] = (uint64_t)k[j * VEC + e] << 32 | (uint32_t)~i;
+        list[to++] = (uint64_t)key << 32 | (uint32_t)~i;
       }
     }
   }
@@ -637,80 +684,223 @@ __device__ void sort_words(uint64_t* w) {
   __syncthreads();
 }
 
-// The prefix of a row whose lists are in s.listed (n words, in the row's order)
-// and s.sorted: the last word kept, or 0 if the lists do not reach so far.
-// Nothing is missing in them from the key `from` on.
-template <int E>
-__device__ uint64_t list_prefix(const SampleParams& a, const Wanted& want,
-                                float top, uint32_t from, double total,
-                                SampleLds& s) {
+// The bin of a logit: factors of 2 from the largest weight, kWidePerBit bins
+// to one.
+__device__ __forceinline__ int wide_bin(float x, float top, double c) {
+  const double d = (double)top - (double)x;
+  return d > 0.0 ? (int)fmin(d * c, (double)(kWideBins - 1)) : 0;
+}
+
+// Words of a list (key, and index the other way round) that a workgroup holds,
+// four a thread, with their masses, and how they lie in bins: `count` and
+// `mass` of the thread's two bins and of all before these.
+constexpr int kHeld = kMaxList / kSampleThreads;
+struct Held {
+  uint64_t w[kHeld];  // 0: none
+  uint64_t m[kHeld];
+  int bin[kHeld];
+  uint32_t count[2], count_before, all_count;
+  uint64_t mass[2], mass_before, all_mass;
+};
+// Bins go from the largest logits on: `bin` of a word is set, lower is before.
+__device__ void bin_words(Held& h, SampleLds& s) {
+  const int tid = threadIdx.x, wave = tid / kWave;
+  for (int i = tid; i < kSampleBins; i += kSampleThreads) {
+    s.bin_mass[i] = 0;
+    s.bin_count[i] = 0;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e) {
+    if (h.w[e] == 0) continue;
+    atomicAdd((unsigned long long*)&s.bin_mass[h.bin[e]],
+              (unsigned long long)h.m[e]);
+    atomicAdd(&s.bin_count[h.bin[e]], 1u);
+  }
+  __syncthreads();
+  uint32_t c = 0;
+  uint64_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    h.count[i] = s.bin_count[2 * tid + i];
+    h.mass[i] = s.bin_mass[2 * tid + i];
+    c += h.count[i];
+    m += h.mass[i];
+  }
+  const uint32_t ci = (uint32_t)wave_scan_incl((int)c);
+  const uint64_t mi = wave_scan64(m);
+  if (lane() == kWave - 1) {
+    s.counts[0][wave] = ci;
+    s.sums[wave] = mi;
+  }
+  __syncthreads();
+  h.count_before = ci - c;
+  h.mass_before = mi - m;
+  h.all_count = 0;
+  h.all_mass = 0;
+  for (int i = 0; i < kSampleWaves; ++i) {
+    const uint32_t x = s.counts[0][i];
+    const uint64_t y = s.sums[i];
+    if (i < wave) {
+      h.count_before += x;
+      h.mass_before += y;
+    }
+    h.all_count += x;
+    h.all_mass += y;
+  }
+}
+
+// The shortest prefix of the words, in their order, that reaches `goal` (> 0)
+// words or units of mass: its last word, its words and its mass.  Word 0: all
+// of them do not.
+struct Cut {
+  uint64_t word, mass;
+  int count;
+};
+
+// The same among the `n` words in s.words (in any order; `before` words and
+// `mass` lie before them), by sorting them.
+template <bool MASS, int E, class MassOf>
+__device__ void cut_by_sorting(int n, uint64_t before, uint64_t mass,
+                               uint64_t goal, MassOf mass_of, SampleLds& s) {
   const int tid = threadIdx.x;
-  sort_words<E>(s.sorted);
-  uint64_t w[E], m[E], sum = 0;
-  int sure = 0, rare = 0;
+  for (int i = n + tid; i < kSampleThreads * E; i += kSampleThreads)
+    s.words[i] = 0;
+  sort_words<E>(s.words);
+  uint64_t w[E], m[E], sum = 0, all;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    w[e] = s.sorted[tid * E + e];
-    const uint32_t key = (uint32_t)(w[e] >> 32);
-    const double x =
-        key > kKeyNone ? weight_of(key_logit(key), top, want.inv_t) : 0.0;
-    m[e] = fixed(x, a.frac);
+    w[e] = s.words[tid * E + e];
+    m[e] = w[e] ? mass_of(w[e]) : 0;
     sum += m[e];
-    sure += key >= from && key > kKeyNone;
-    rare += key > kKeyNone && x >= want.min_w;
   }
-  uint64_t all;
-  uint64_t before = scan_block(sum, s, &all);
-  uint64_t counts;
-  scan_block((uint64_t)sure << 32 | (uint32_t)rare, s, &counts);
-  const int n_sure = (int)(counts >> 32);
-  const bool whole = from <= kKeyNone + 1;  // all that has weight is listed
-  if (n_sure < 1 || (want.k > n_sure && want.p < 1.0 && !whole)) return 0;
-  int last = n_sure;  // words kept
-  bool ends = false;  // within what is sure
-  if (want.k > 0) {
-    // (rows of fewer logits above -infinity than k keep them all)
-    if (want.k <= n_sure) ends = true;
-    last = want.k < last ? want.k : last;
+  uint64_t mb = mass + scan_block(sum, s, &all);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const uint64_t c = before + (uint64_t)(tid * E + e);
+    if (w[e] &&
+        (MASS ? mb < goal && goal <= mb + m[e] : c + 1 == goal)) {
+      s.found[0] = w[e];
+      s.found[1] = c + 1;
+      s.found[2] = mb + m[e];
+    }
+    mb += m[e];
+  }
+}
+
+template <bool MASS, class MassOf>
+__device__ Cut find_cut(const Held& h, uint64_t goal, MassOf mass_of,
+                        SampleLds& s) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (tid == 0) {
+    s.found[0] = kSampleBins;
+    s.gathered = 0;
+  }
+  __syncthreads();
+  uint64_t cb = h.count_before, mb = h.mass_before;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t at = MASS ? mb : cb;
+    if (at < goal && goal <= at + (MASS ? h.mass[i] : h.count[i])) {
+      s.found[0] = (uint64_t)(2 * tid + i);
+      s.found[1] = cb;
+      s.found[2] = mb;
+    }
+    cb += h.count[i];
+    mb += h.mass[i];
+  }
+  __syncthreads();
+  const int pivot = (int)s.found[0];
+  if (pivot == kSampleBins) return Cut{0, 0, 0};
+  cb = s.found[1];
+  mb = s.found[2];
+  // The bin's words, in any order.
+#pragma unroll
+  for (int e = 0; e < kHeld; ++e)
+    if (h.w[e] != 0 && h.bin[e] == pivot)
+      s.words[atomicAdd(&s.gathered, 1u)] = h.w[e];
+  __syncthreads();
+  const int n = (int)s.gathered;
+  if (tid == 0) s.found[0] = 0;
+  if (n <= kWave) {
+    // One wave: what lies before each word, word by word.
+    if (tid < kWave) {
+      const uint64_t w = tid < n ? s.words[tid] : 0;
+      const uint64_t m = w ? mass_of(w) : 0;
+      uint64_t c = cb + 1, before = mb;
+      for (int i = 0; i < n; ++i) {
+        const uint64_t wi = lane64(w, i), mi = lane64(m, i);
+        if (wi > w) {
+          ++c;
+          before += mi;
+        }
+      }
+      if (w && (MASS ? before < goal && goal <= before + m : c == goal)) {
+        s.found[0] = w;
+        s.found[1] = c;
+        s.found[2] = before + m;
+      }
+    }
+  } else if (n <= kSampleThreads) {
+    cut_by_sorting<MASS, 1>(n, cb, mb, goal, mass_of, s);
+  } else if (n <= 2 * kSampleThreads) {
+    cut_by_sorting<MASS, 2>(n, cb, mb, goal, mass_of, s);
+  } else {
+    cut_by_sorting<MASS, 4>(n, cb, mb, goal, mass_of, s);
+  }
+  __syncthreads();
+  return Cut{s.found[0], s.found[2], (int)s.found[1]};
+}
+
+// The chunk where `goal` lies in the masses of the row's chunks (one a
+// thread): in every thread, with the mass before it.
+__device__ int find_chunk(uint64_t mass, double u, SampleLds& s,
+                          uint64_t* before, uint64_t* goal, uint64_t* total) {
+  const uint64_t b = scan_block(mass, s, total);
+  *goal = (uint64_t)(u * (double)*total);
+  if (*goal >= *total) *goal = *total - 1;
+  if (b <= *goal && *goal < b + mass) {
+    s.found[0] = (uint64_t)threadIdx.x;
+    s.found[1] = b;
+  }
+  __syncthreads();
+  *before = s.found[1];
+  return (int)s.found[0];
+}
+
+// The prefix of a row whose listed words, as far as nothing is missing, are
+// held: its last word (1 for all of them), or 0 if they do not reach its end.
+// `whole`: the row has no others; `rare`: some of them are below min_p;
+// `total`: the sum of the row's weights, where it is needed.
+template <class MassOf>
+__device__ uint64_t list_cut(const SampleParams& a, const Wanted& want, Held& h,
+                             double total, bool whole, bool rare,
+                             MassOf mass_of, SampleLds& s) {
+  bin_words(h, s);
+  uint64_t word = 1;
+  bool beyond = !whole;
+  uint64_t part = h.all_mass;  // of the first k
+  if (want.k > 0 && want.k <= (int)h.all_count) {
+    const Cut c = find_cut<false>(h, (uint64_t)want.k, mass_of, s);
+    word = c.word;
+    part = c.mass;
+    beyond = false;
   }
   if (want.p < 1.0) {
-    // The sum that p is a part of: of the first k, or of the row.
-    if (want.k > 0) {
-      uint64_t part = before;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        part += m[e];
-        if (tid * E + e == last - 1) s.found[0] = part;
-      }
-      __syncthreads();
-      total = (double)s.found[0];
-      __syncthreads();
-    } else {
-      total = ldexp(total, a.frac);
+    if (want.k > 0 && beyond) return 0;
+    const double of = want.k > 0 ? (double)part : total * a.unit;
+    const double least = ceil(want.p * of);
+    uint64_t goal = least < 1.0 ? 1 : (uint64_t)least;
+    if (want.k > 0 && goal > part) goal = part;
+    const Cut c = find_cut<true>(h, goal, mass_of, s);
+    if (c.word) {
+      word = c.word;
+      beyond = false;
     }
-    const double part = ceil(want.p * total);
-    const uint64_t goal = part < 1.0 ? 1 : (uint64_t)part;
-    if (tid == 0) s.found[0] = (uint64_t)last;
-    __syncthreads();
-    uint64_t sum2 = before;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint64_t next = sum2 + m[e];
-      if (sum2 < goal && goal <= next && tid * E + e < last)
-        s.found[0] = (uint64_t)(tid * E + e + 1) | 1ull << 32;
-      sum2 = next;
-    }
-    __syncthreads();
-    if (s.found[0] >> 32) ends = true;
-    last = (int)(uint32_t)s.found[0];
-    __syncthreads();
   }
-  if (want.min_w > 0.0) {
-    const int n_rare = (int)(uint32_t)counts;
-    if (n_rare < n_sure) ends = true;
-    last = n_rare < last ? n_rare : last;
-  }
-  return (ends || whole) && last > 0 ? s.sorted[last - 1] : 0;
+  // A prefix that goes on does not matter where min_p ends before.
+  return beyond && !rare ? 0 : word;
 }
 
 // Rows: from their chunks, or over again.
@@ -718,19 +908,33 @@ template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     SampleParams a) {
   __shared__ SampleLds s;
-  const int tid = threadIdx.x, wave = tid / kWave, ln = lane();
+  const int tid = threadIdx.x, wave = uni(tid / kWave), ln = lane();
   const int64_t row_i = a.row0 + blockIdx.x;
   const char* row = a.x + row_i * a.ld;
-  const Wanted want = wanted(a, row_i);
   const int64_t base = (int64_t)blockIdx.x * a.chunks;
-  if (tid == 0 && a.bins) a.wide[blockIdx.x].mode = kNotWide;
   const bool in = tid < a.chunks;
-  const bool lists = !want.all() && !want.greedy;
+  // (what a row does not ask for is not written, and not used)
   const uint32_t chunk_top = in ? a.chunk_max[base + tid] : 0;
-  const uint32_t chunk_from = in && lists ? a.chunk_from[base + tid] : 0;
-  const int n = in && lists ? (int)a.chunk_n[base + tid] : 0;
-  const uint32_t top_key =
-      (uint32_t)max_block((uint64_t)chunk_top, s);
+  const uint32_t chunk_from = in ? a.chunk_from[base + tid] : 0;
+  const double chunk_sum = in ? a.chunk_sum[base + tid] : 0.0;
+  int n = in ? (int)a.chunk_n[base + tid] : 0;
+  const Wanted want = wanted(a, row_i);
+  if (tid == 0) a.wide[blockIdx.x].mode = kNotWide;
+  // ---- over the chunks: the largest logit, the bound of the lists
+  {
+    const int x = wave_max(unbias(chunk_top)), y = wave_max(unbias(chunk_from));
+    if (ln == 0) {
+      s.counts[0][wave] = bias(x);
+      s.counts[1][wave] = bias(y);
+    }
+  }
+  __syncthreads();
+  uint32_t top_key = 0, from = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleWaves; ++i) {
+    top_key = max(top_key, s.counts[0][i]);
+    from = max(from, s.counts[1][i]);
+  }
   const float top = key_logit(top_key);
   if (top_key == kKeyNone) {
     if (tid == 0) {
@@ -740,44 +944,53 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     return;
   }
   double mass = 0.0;
-  if (in && want.k == 0 && !want.greedy && (want.p < 1.0 || want.min_w <= 0.0))
-    mass = a.chunk_sum[base + tid] *
-           weight_of(key_logit(chunk_top), top, want.inv_t);
+  if (in && want.sums() && !want.greedy)
+    mass = chunk_sum * weight_of(key_logit(chunk_top), top, want.inv_t);
+  const double incl_w = wave_scan_double(mass);
+  if (want.greedy || want.all()) n = 0;
+  const int n_incl = wave_scan_incl(n);
+  double* const sums = (double*)s.sums;
+  __syncthreads();
+  if (ln == kWave - 1) {
+    sums[wave] = incl_w;
+    s.counts[0][wave] = (uint32_t)n_incl;
+  }
+  __syncthreads();
+  double sum_before = 0.0, total = 0.0;
+  int to = n_incl - n, count = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleWaves; ++i) {
+    if (i < wave) {
+      sum_before += sums[i];
+      to += (int)s.counts[0][i];
+    }
+    total += sums[i];
+    count += (int)s.counts[0][i];
+  }
   if (want.greedy || want.all()) {
-    // ---- the chunk, and its logit
-    // Inclusive sums of the chunks' masses: in a wave, then of the waves.
-    double incl = mass;
-    for (int o = 1; o < kWave; o <<= 1) {
-      const double y = __shfl_up(incl, o, kWave);
-      if (ln >= o) incl += y;
-    }
-    double* sums = (double*)s.sums;
-    __syncthreads();  // the maxima have been read
-    if (ln == kWave - 1) sums[wave] = incl;
-    __syncthreads();
-    double before = 0.0, total = 0.0;
-    for (int i = 0; i < kSampleWaves; ++i) {
-      if (i < wave) before += sums[i];
-      total += sums[i];
-    }
-    incl += before;
-    __syncthreads();
+    // ---- the first chunk with the largest logit, or past the goal; where
+    // rounding leaves none past it, the last one that has weight
+    const double incl = sum_before + incl_w;
     const double goal = want.u * total;
-    // The first chunk that passes the goal; where rounding leaves none, the
-    // last one that has weight.
-    const bool past = want.greedy ? chunk_top == top_key
-                                  : mass > 0.0 && incl > goal;
-    uint64_t pick = past ? (uint64_t)(2 * kMaxChunks - tid)
-                    : mass > 0.0 ? (uint64_t)tid + 1 : 0;
-    if (past) pick += kMaxChunks;
-    pick = max_block(pick, s);
-    const int chunk = pick > 2 * kMaxChunks ? (int)(3 * kMaxChunks - pick)
-                      : (int)pick - 1;
+    const bool past =
+        want.greedy ? chunk_top == top_key : mass > 0.0 && incl > goal;
+    const uint64_t over = ballot(past), some = ballot(mass > 0.0);
     __syncthreads();
-    if (tid == chunk) sums[0] = incl - mass;
+    if (ln == 0) {
+      s.counts[0][wave] = over ? (uint32_t)__builtin_ctzll(over) : kWave;
+      s.counts[1][wave] = some ? (uint32_t)(63 - __builtin_clzll(some)) : kWave;
+    }
     __syncthreads();
-    if (wave > 0) return;
-    double part = sums[0];
+    int chunk = -1, last = 0;
+#pragma unroll
+    for (int i = kSampleWaves - 1; i >= 0; --i)
+      if (s.counts[0][i] < kWave) chunk = i * kWave + (int)s.counts[0][i];
+#pragma unroll
+    for (int i = 0; i < kSampleWaves; ++i)
+      if (s.counts[1][i] < kWave) last = i * kWave + (int)s.counts[1][i];
+    if (chunk < 0) chunk = last;
+    if (wave != chunk / kWave) return;  // the wave that has its sum goes on
+    double part = __shfl(incl - mass, chunk % kWave, kWave);
     const int64_t i0 = (int64_t)chunk * kChunk + ln * 16;
     float x[16];
 #pragma unroll
@@ -805,14 +1018,10 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
       w[e] = weight_of(x[e], top, want.inv_t);
       sum += w[e];
     }
-    double upto = sum;
-    for (int o = 1; o < kWave; o <<= 1) {
-      const double y = __shfl_up(upto, o, kWave);
-      if (ln >= o) upto += y;
-    }
-    const uint64_t over = ballot(sum > 0.0 && part + upto > goal);
-    const uint64_t some = ballot(sum > 0.0);
-    const int who = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
+    const double upto = wave_scan_double(sum);
+    const uint64_t here = ballot(sum > 0.0 && part + upto > goal);
+    const uint64_t any = ballot(sum > 0.0);
+    const int who = here ? __builtin_ctzll(here) : 63 - __builtin_clzll(any);
     if (ln != who) return;
     part += upto - sum;
     int at = 0;
@@ -828,57 +1037,59 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
       }
     }
     a.tokens[row_i] = i0 + at;
-    a.logprobs[row_i] = (float)(log(got) - log(total));
+    a.logprobs[row_i] = (float)log(got / total);
     return;
   }
-  // ---- lists: their words in LDS, in the row's order
-  const uint32_t from = (uint32_t)max_block((uint64_t)chunk_from, s);
-  uint64_t all;
-  const uint64_t to = scan_block((uint64_t)n, s, &all);
-  const int count = (int)all;
-  double total = mass;
-  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, kWave);
-  __syncthreads();
-  if (ln == 0) ((double*)s.sums)[wave] = total;
-  __syncthreads();
-  total = 0.0;
-  for (int i = 0; i < kSampleWaves; ++i) total += ((double*)s.sums)[i];
+  // ---- lists: their words, four a thread
+  auto mass_of = [&](uint64_t w) {
+    return fixed(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
+  };
+  const bool whole = from <= kKeyNone + 1;  // all that has weight is listed
   uint64_t cut = 0;
+  Held h;
+  bool low[kHeld];  // below min_p
   if (count <= kMaxList && count > 0) {
-    for (int c = wave * kWave; c < a.chunks; c += kSampleThreads) {
-      // a wave's 64 chunks are those of its own threads
-      for (int i = 0; i < kWave && c + i < a.chunks; ++i) {
-        const int nc = __builtin_amdgcn_readlane(n, i);
-        const int tc = __builtin_amdgcn_readlane((int)to, i);
-        if (ln < nc) {
-          const uint64_t w = a.lists[(base + c + i) * kChunkList + ln];
-          s.listed[tc + ln] = w;
-          s.sorted[tc + ln] = w;
-        }
+    // a wave copies the lists of its threads' chunks
+    for (int i = 0; i < kWave && wave * kWave + i < a.chunks; ++i) {
+      const int nc = __builtin_amdgcn_readlane(n, i);
+      const int tc = __builtin_amdgcn_readlane(to, i);
+      if (ln < nc)
+        s.words[tc + ln] =
+            a.lists[(base + wave * kWave + i) * kChunkList + ln];
+    }
+    __syncthreads();
+    const double c = kWidePerBit * want.inv_t;
+    bool some_low = false;
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int i = e * kSampleThreads + tid;
+      low[e] = true;
+      h.w[e] = i < count ? s.words[i] : 0;
+      const uint32_t key = (uint32_t)(h.w[e] >> 32);
+      if (key < from) h.w[e] = 0;  // below it others are missing
+      h.m[e] = 0;
+      h.bin[e] = 0;
+      if (h.w[e]) {
+        const float x = key_logit(key);
+        const double w = weight_of(x, top, want.inv_t);
+        h.m[e] = fixed(w, a);
+        h.bin[e] = wide_bin(x, top, c);
+        low[e] = w < want.min_w;
+        some_low = some_low || low[e];
       }
     }
-    const int room = count <= 1024 ? 1024 : count <= 2048 ? 2048 : 4096;
-    for (int i = count + tid; i < room; i += kSampleThreads) {
-      s.listed[i] = 0;
-      s.sorted[i] = 0;
-    }
-    cut = room == 1024   ? list_prefix<1>(a, want, top, from, total, s)
-          : room == 2048 ? list_prefix<2>(a, want, top, from, total, s)
-                         : list_prefix<4>(a, want, top, from, total, s);
+    const bool rare = __syncthreads_or(some_low) != 0;
+    cut = list_cut(a, want, h, total, whole, rare, mass_of, s);
   }
   if (cut == 0) {
-    __syncthreads();
-    const int mode = want.k > 0 ? (want.p < 1.0 ? kNotWide : kWideCount)
+    // (a prefix of a wide one has two goals: by passes over the row)
+    const int mode = want.k > 0 ? (want.p < 1.0 ? kWideRow : kWideCount)
                      : want.p < 1.0 ? kWideMass
                                     : kWideAll;
-    if (mode == kNotWide || !a.bins) {
-      sample_row<T>(a, row_i, s);
-      return;
-    }
     uint64_t* bins = a.bins + (int64_t)blockIdx.x * kWideBins;
     for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
     if (tid == 0) {
-      const double part = ceil(want.p * ldexp(total, a.frac));
+      const double part = ceil(want.p * (total * a.unit));
       WideRow w = {};
       w.mode = (uint32_t)mode;
       w.top = top_key;
@@ -889,47 +1100,43 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     }
     return;
   }
-  // ---- in the row's order
-  constexpr int E = kMaxList / kSampleThreads;
-  uint64_t m[E], sum = 0;
+  // ---- in the row's order: the chunk, then its list
+  s.chunk_mass[tid] = 0;
+  __syncthreads();
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int i = tid * E + e;
-    const uint64_t w = i < count ? s.listed[i] : 0;
-    m[e] = w >= cut ? fixed(weight_of(key_logit((uint32_t)(w >> 32)), top,
-                                      want.inv_t),
-                            a.frac)
-                    : 0;
-    sum += m[e];
-  }
-  uint64_t kept;
-  uint64_t part = scan_block(sum, s, &kept);
-  uint64_t goal = (uint64_t)(want.u * (double)kept);
-  if (goal >= kept) goal = kept - 1;
-  if (part <= goal && goal < part + sum) {
-    int e = 0;
-    while (part + m[e] <= goal) part += m[e++];
-    const uint64_t w = s.listed[tid * E + e];
+  for (int e = 0; e < kHeld; ++e)
+    if (h.w[e] >= cut && !low[e])
+      atomicAdd((unsigned long long*)
+                    &s.chunk_mass[(uint32_t) ~(uint32_t)h.w[e] / kChunk],
+                (unsigned long long)h.m[e]);
+  __syncthreads();
+  uint64_t before, goal, kept;
+  const int chunk =
+      find_chunk(s.chunk_mass[tid], want.u, s, &before, &goal, &kept);
+  if (wave != chunk / kWave) return;
+  const int nc = __builtin_amdgcn_readlane(n, chunk % kWave);
+  const uint64_t w =
+      ln < nc ? a.lists[(base + chunk) * kChunkList + ln] : 0;
+  const double x =
+      w ? weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t) : 0.0;
+  const uint64_t m = w >= cut && (uint32_t)(w >> 32) >= from && x >= want.min_w
+                         ? fixed(x, a)
+                         : 0;
+  before += wave_scan64(m) - m;
+  if (before <= goal && goal < before + m) {
     a.tokens[row_i] = (int64_t)(uint32_t) ~(uint32_t)w;
-    a.logprobs[row_i] = (float)(
-        log(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t)) -
-        log(ldexp((double)kept, -a.frac)));
+    a.logprobs[row_i] = (float)log(x / ((double)kept / a.unit));
   }
 }
 
 // ---- wide prefixes ----------------------------------------------------------
 // A prefix beyond the lists (a nucleus of tens of thousands) is found in two
 // more launches over the row, by workgroups of 16 chunks.  The first adds up
-// the masses (or counts) of the logits in 2048 bins of (M - x) / T, 1/64 wide;
+// the masses (or counts) of the logits in 2048 bins of log2 of their weight;
 // integers, so that their order is nothing.  The second finds the bin in which
 // the goal lies, adds up each chunk's mass above it, and lists the bin's own
 // logits; the row's last workgroup sorts these, finds the last one kept, the
 // chunk where u times the kept mass lies, and the token in it.
-__device__ __forceinline__ int wide_bin(float x, float top, double c) {
-  const double d = (double)top - (double)x;
-  return d > 0.0 ? (int)fmin(d * c, (double)(kWideBins - 1)) : 0;
-}
-
 template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     SampleParams a) {
@@ -950,7 +1157,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     typedef ChunkShape<T> S;
     float x[S::N];
     read_chunk<T>(a.x + row_i * a.ld, chunk * kChunk, a.cols, x);
-    const double c = 64.0 * want.inv_t;
+    const double c = kWidePerBit * want.inv_t;
 #pragma unroll
     for (int e = 0; e < S::N; ++e) {
       // What lies in the last bin has no weight to speak of: 2^-46 and less.
@@ -960,7 +1167,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
                 wide.mode == kWideCount
                     ? 1ull
                     : (unsigned long long)fixed(
-                          weight_of(x[e], top, want.inv_t), a.frac));
+                          weight_of(x[e], top, want.inv_t), a));
     }
   }
   __syncthreads();
@@ -968,44 +1175,6 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
       (unsigned long long*)(a.bins + (int64_t)r * kWideBins);
   for (int i = tid; i < kWideBins; i += kSampleThreads)
     if (bins[i]) atomicAdd(all + i, (unsigned long long)bins[i]);
-}
-
-// Sorts the first `count` of s.sorted (the others of a power of two become 0)
-// and finds how many of them, from the largest, it takes to reach `goal`
-// (in masses, or in words); 0 if they do not.
-template <int E>
-__device__ int pivots_kept(const SampleParams& a, const Wanted& want,
-                           const WideRow& wide, uint64_t goal, SampleLds& s) {
-  const int tid = threadIdx.x;
-  sort_words<E>(s.sorted);
-  const float top = key_logit(wide.top);
-  uint64_t m[E], sum = 0;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint64_t w = s.sorted[tid * E + e];
-    m[e] = 0;
-    if (w)
-      m[e] = wide.mode == kWideCount
-                 ? 1
-                 : fixed(weight_of(key_logit((uint32_t)(w >> 32)), top,
-                                   want.inv_t),
-                         a.frac);
-    sum += m[e];
-  }
-  uint64_t all;
-  uint64_t before = scan_block(sum, s, &all);
-  if (tid == 0) s.found[0] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint64_t next = before + m[e];
-    if (before < goal && goal <= next) s.found[0] = (uint64_t)(tid * E + e + 1);
-    before = next;
-  }
-  __syncthreads();
-  const int n = (int)s.found[0];
-  __syncthreads();
-  return n;
 }
 
 template <int T>
@@ -1017,12 +1186,17 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
   if (wide.mode == kNotWide) return;
   __shared__ SampleLds s;
   __shared__ int flag;
+  if (wide.mode == kWideRow) {
+    if (blockIdx.x % (unsigned)wg == 0)
+      sample_row<T>(a, a.row0 + r, s);
+    return;
+  }
   const int tid = threadIdx.x, ln = lane();
   const int64_t row_i = a.row0 + r;
   const char* row = a.x + row_i * a.ld;
   const Wanted want = wanted(a, row_i);
   const float top = key_logit(wide.top);
-  const double c = 64.0 * want.inv_t;
+  const double c = kWidePerBit * want.inv_t;
   typedef ChunkShape<T> S;
   // ---- the bin of the goal
   int pivot = kWideBins;  // all above it
@@ -1068,7 +1242,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
       const int bin = wide_bin(x[e], top, c);
       if (bin < pivot) {
         const double w = weight_of(x[e], top, want.inv_t);
-        if (w >= want.min_w) sum += fixed(w, a.frac);
+        if (w >= want.min_w) sum += fixed(w, a);
       }
       mine += bin == pivot && pivot < kWideBins;
     }
@@ -1099,18 +1273,47 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
   uint64_t cut = 0;
   bool done = !lost;
   if (wide.mode != kWideAll && done) {
-    done = count <= kMaxList && pivot < kWideBins - 1;
+    done = count <= kMaxList;
     if (done) {
-      const int room = count <= 1024 ? 1024 : count <= 2048 ? 2048 : 4096;
-      for (int i = tid; i < room; i += kSampleThreads)
-        s.sorted[i] = i < (int)count ? ld_agent(pivots + i) : 0;
+      auto mass_of = [&](uint64_t w) {
+        return fixed(
+            weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
+      };
+      Held h;
+#pragma unroll
+      for (int e = 0; e < kHeld; ++e) {
+        const int i = e * kSampleThreads + tid;
+        h.w[e] = i < (int)count ? ld_agent(pivots + i) : 0;
+        h.m[e] = 0;
+        h.bin[e] = 0;
+        if (h.w[e]) {
+          // the bin in 2048 parts
+          const float x = key_logit((uint32_t)(h.w[e] >> 32));
+          const double d = ((double)top - (double)x) * c - pivot;
+          h.m[e] = mass_of(h.w[e]);
+          h.bin[e] = d > 0.0 ? (int)fmin(d * kSampleBins, kSampleBins - 1.0) : 0;
+        }
+      }
+      bin_words(h, s);
       const uint64_t goal = wide.goal - above;
-      const int kept =
-          room == 1024   ? pivots_kept<1>(a, want, wide, goal, s)
-          : room == 2048 ? pivots_kept<2>(a, want, wide, goal, s)
-                         : pivots_kept<4>(a, want, wide, goal, s);
-      done = kept > 0;
-      if (done) cut = s.sorted[kept - 1];
+      cut = (wide.mode == kWideCount ? find_cut<false>(h, goal, mass_of, s)
+                                     : find_cut<true>(h, goal, mass_of, s))
+                .word;
+      done = cut != 0;
+      // Masses of the chunks, and of the bin's words in them.
+      if (done) {
+        s.chunk_mass[tid] = 0;
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kHeld; ++e)
+          if (h.w[e] >= cut && h.w[e] != 0 &&
+              weight_of(key_logit((uint32_t)(h.w[e] >> 32)), top, want.inv_t) >=
+                  want.min_w)
+            atomicAdd((unsigned long long*)
+                          &s.chunk_mass[(uint32_t) ~(uint32_t)h.w[e] / kChunk],
+                      (unsigned long long)h.m[e]);
+        __syncthreads();
+      }
     }
   }
   if (!done) {
@@ -1118,39 +1321,16 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
     sample_row<T>(a, row_i, s);
     return;
   }
-  // Masses of the chunks, in the other half of LDS.
-  for (int i = tid; i < kMaxChunks; i += kSampleThreads)
-    s.listed[i] = i < a.chunks
-                      ? ld_agent(a.chunk_mass + (int64_t)r * a.chunks + i)
-                      : 0;
-  __syncthreads();
-  if (cut) {
-    for (int i = tid; i < (int)count; i += kSampleThreads) {
-      const uint64_t w = s.sorted[i];
-      if (w < cut) continue;
-      const double x =
-          weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
-      if (x >= want.min_w)
-        atomicAdd((unsigned long long*)
-                      &s.listed[(uint32_t) ~(uint32_t)w / kChunk],
-                  (unsigned long long)fixed(x, a.frac));
-    }
-    __syncthreads();
-  }
-  const uint64_t mass = s.listed[tid];
-  uint64_t total;
-  const uint64_t before = scan_block(mass, s, &total);
-  uint64_t goal = (uint64_t)(want.u * (double)total);
-  if (goal >= total) goal = total - 1;
-  if (before <= goal && goal < before + mass) {
-    s.found[0] = (uint64_t)tid;
-    s.found[1] = before;
-  }
-  __syncthreads();
+  uint64_t mass =
+      tid < a.chunks ? ld_agent(a.chunk_mass + (int64_t)r * a.chunks + tid) : 0;
+  if (cut) mass += s.chunk_mass[tid];
+  uint64_t before, goal, total;
+  const int chunk_i =
+      find_chunk(mass, want.u, s, &before, &goal, &total);
   if (tid >= kWave) return;
   // Lane l takes logits 16 l .. of the chunk.
-  uint64_t part = s.found[1];
-  const int64_t i0 = (int64_t)s.found[0] * kChunk + ln * 16;
+  uint64_t part = before;
+  const int64_t i0 = (int64_t)chunk_i * kChunk + ln * 16;
   uint64_t m[16], sum = 0;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -1164,7 +1344,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
       const double w = weight_of(y[e], top, want.inv_t);
       // (-infinity past the end has no weight)
       m[j * kSampleVec + e] =
-          word >= cut && w >= want.min_w ? fixed(w, a.frac) : 0;
+          word >= cut && w >= want.min_w ? fixed(w, a) : 0;
       sum += m[j * kSampleVec + e];
     }
   }
@@ -1180,8 +1360,8 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
     }
     a.tokens[row_i] = i0 + at;
     a.logprobs[row_i] =
-        (float)(log(weight_of(read_logit<T>(row, i0 + at), top, want.inv_t)) -
-                log(ldexp((double)total, -a.frac)));
+        (float)log(weight_of(read_logit<T>(row, i0 + at), top, want.inv_t) /
+                   ((double)total / a.unit));
   }
 }
 
