@@ -263,6 +263,7 @@ struct SampleLds {
     };
     struct {  // words of a list
       uint64_t words[kMaxList];
+      uint64_t some[kMaxList];  // those of one bin
       uint64_t bin_mass[kSampleBins];
       uint32_t bin_count[kSampleBins];
       uint64_t chunk_mass[kMaxChunks];
@@ -380,7 +381,7 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
 
 // A row by as many passes over it as it takes, in one workgroup.
 template <int T>
-__device__ void sample_row(const SampleParams& a, int64_t row_i,
+__device__ __noinline__ void sample_row(const SampleParams& a, int64_t row_i,
                            SampleLds& s) {
   const int tid = threadIdx.x;
   const char* row = a.x + row_i * a.ld;
@@ -502,8 +503,8 @@ __device__ void sample_row(const SampleParams& a, int64_t row_i,
 // The bound is the rank-th largest of what the 64 lanes have as their largest,
 // so that the list has some more than `rank`, whatever the numbers are like.
 // Above the largest bound of a row's chunks nothing is missing in its lists:
-// a prefix of the order that ends above it is found there, by sorting at most
-// 4096 words.  Rows whose prefix goes further are done over.
+// a prefix of the order that ends above it is found there, among at most 4096
+// words.
 template <int T>
 struct ChunkShape {
   static constexpr int VEC = 16 / (T == kLogF32 ? 4 : 2);  // logits of a load
@@ -646,43 +647,7 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
   }
 }
 
-// Keeps LDS accesses of a wave in their order (which the hardware keeps).
-__device__ __forceinline__ void wave_fence() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_wave_barrier();
-}
-
-// Sorts 1024 E words in LDS, largest first: a bitonic network in which a wave
-// keeps to its own 64 E words wherever partners are that near.
-template <int E>
-__device__ void sort_words(uint64_t* w) {
-  constexpr int P = kSampleThreads * E, R = P / kSampleWaves;
-  const int ln = lane(), wave = (int)threadIdx.x / kWave;
-  __syncthreads();
-  for (int size = 2; size <= P; size *= 2) {
-    for (int j = size / 2; j > 0; j /= 2) {
-      const bool far = 2 * j > R;
-      if (far) __syncthreads();
-#pragma unroll
-      for (int m = 0; m < (E + 1) / 2; ++m) {
-        const int i = wave * (R / 2) + m * kWave + ln;
-        if (E > 1 || ln < R / 2) {
-          const int lo = (i & ~(j - 1)) * 2 + (i & (j - 1));
-          const uint64_t x = w[lo], y = w[lo + j];
-          if ((x < y) == ((lo & size) == 0)) {
-            w[lo] = y;
-            w[lo + j] = x;
-          }
-        }
-      }
-      if (far)
-        __syncthreads();
-      else
-        wave_fence();
-    }
-  }
-  __syncthreads();
-}
+constexpr int kHeld = kMaxList / kSampleThreads;  // words of a thread
 
 // The bin of a logit: factors of 2 from the largest weight, kWidePerBit bins
 // to one.
@@ -691,171 +656,158 @@ __device__ __forceinline__ int wide_bin(float x, float top, double c) {
   return d > 0.0 ? (int)fmin(d * c, (double)(kWideBins - 1)) : 0;
 }
 
-// Words of a list (key, and index the other way round) that a workgroup holds,
-// four a thread, with their masses, and how they lie in bins: `count` and
-// `mass` of the thread's two bins and of all before these.
-constexpr int kHeld = kMaxList / kSampleThreads;
-struct Held {
-  uint64_t w[kHeld];  // 0: none
-  uint64_t m[kHeld];
-  int bin[kHeld];
-  uint32_t count[2], count_before, all_count;
-  uint64_t mass[2], mass_before, all_mass;
-};
-// Bins go from the largest logits on: `bin` of a word is set, lower is before.
-__device__ void bin_words(Held& h, SampleLds& s) {
-  const int tid = threadIdx.x, wave = tid / kWave;
-  for (int i = tid; i < kSampleBins; i += kSampleThreads) {
-    s.bin_mass[i] = 0;
-    s.bin_count[i] = 0;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kHeld; ++e) {
-    if (h.w[e] == 0) continue;
-    atomicAdd((unsigned long long*)&s.bin_mass[h.bin[e]],
-              (unsigned long long)h.m[e]);
-    atomicAdd(&s.bin_count[h.bin[e]], 1u);
-  }
-  __syncthreads();
-  uint32_t c = 0;
-  uint64_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    h.count[i] = s.bin_count[2 * tid + i];
-    h.mass[i] = s.bin_mass[2 * tid + i];
-    c += h.count[i];
-    m += h.mass[i];
-  }
-  const uint32_t ci = (uint32_t)wave_scan_incl((int)c);
-  const uint64_t mi = wave_scan64(m);
-  if (lane() == kWave - 1) {
-    s.counts[0][wave] = ci;
-    s.sums[wave] = mi;
-  }
-  __syncthreads();
-  h.count_before = ci - c;
-  h.mass_before = mi - m;
-  h.all_count = 0;
-  h.all_mass = 0;
-  for (int i = 0; i < kSampleWaves; ++i) {
-    const uint32_t x = s.counts[0][i];
-    const uint64_t y = s.sums[i];
-    if (i < wave) {
-      h.count_before += x;
-      h.mass_before += y;
-    }
-    h.all_count += x;
-    h.all_mass += y;
-  }
-}
+// Words are a logit's key, and its index the other way round: the order is
+// that of larger words first.
 
 // The shortest prefix of the words, in their order, that reaches `goal` (> 0)
 // words or units of mass: its last word, its words and its mass.  Word 0: all
 // of them do not.
 struct Cut {
   uint64_t word, mass;
+  uint64_t all;  // mass of all the words
   int count;
 };
 
-// The same among the `n` words in s.words (in any order; `before` words and
-// `mass` lie before them), by sorting them.
-template <bool MASS, int E, class MassOf>
-__device__ void cut_by_sorting(int n, uint64_t before, uint64_t mass,
-                               uint64_t goal, MassOf mass_of, SampleLds& s) {
-  const int tid = threadIdx.x;
-  for (int i = n + tid; i < kSampleThreads * E; i += kSampleThreads)
-    s.words[i] = 0;
-  sort_words<E>(s.words);
-  uint64_t w[E], m[E], sum = 0, all;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    w[e] = s.words[tid * E + e];
-    m[e] = w[e] ? mass_of(w[e]) : 0;
-    sum += m[e];
-  }
-  uint64_t mb = mass + scan_block(sum, s, &all);
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint64_t c = before + (uint64_t)(tid * E + e);
-    if (w[e] &&
-        (MASS ? mb < goal && goal <= mb + m[e] : c + 1 == goal)) {
-      s.found[0] = w[e];
-      s.found[1] = c + 1;
-      s.found[2] = mb + m[e];
+// `n` words in s.words; `bin_of` puts them in bins, in their order.  A bin with
+// more than 64 words is parted again, by the first bits in which they differ.
+template <class MassOf, class BinOf>
+__device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
+                                        MassOf mass_of, BinOf bin_of,
+                                        SampleLds& s) {
+  const int tid = threadIdx.x, wave = tid / kWave;
+  uint64_t cb = 0, mb = 0;  // words and mass before the ones in question
+  Cut out = {0, 0, 0, 0};
+  int shift = -1;  // of the words, which are the bins then
+  const uint64_t* from = s.words;
+  auto bin = [&](uint64_t w) {
+    return shift < 0 ? bin_of(w)
+                     : kSampleBins - 1 -
+                           (int)((w >> shift) & (uint64_t)(kSampleBins - 1));
+  };
+  for (;;) {
+    for (int i = tid; i < kSampleBins; i += kSampleThreads) {
+      s.bin_mass[i] = 0;
+      s.bin_count[i] = 0;
     }
-    mb += m[e];
-  }
-}
-
-template <bool MASS, class MassOf>
-__device__ Cut find_cut(const Held& h, uint64_t goal, MassOf mass_of,
-                        SampleLds& s) {
-  const int tid = threadIdx.x;
-  __syncthreads();
-  if (tid == 0) {
-    s.found[0] = kSampleBins;
-    s.gathered = 0;
-  }
-  __syncthreads();
-  uint64_t cb = h.count_before, mb = h.mass_before;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint64_t at = MASS ? mb : cb;
-    if (at < goal && goal <= at + (MASS ? h.mass[i] : h.count[i])) {
-      s.found[0] = (uint64_t)(2 * tid + i);
-      s.found[1] = cb;
-      s.found[2] = mb;
+    if (tid == 0) {
+      s.found[0] = kSampleBins;
+      s.gathered = 0;
     }
-    cb += h.count[i];
-    mb += h.mass[i];
-  }
-  __syncthreads();
-  const int pivot = (int)s.found[0];
-  if (pivot == kSampleBins) return Cut{0, 0, 0};
-  cb = s.found[1];
-  mb = s.found[2];
-  // The bin's words, in any order.
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < n; i += kSampleThreads) {
+      const uint64_t w = from[i];
+      if (w == 0) continue;
+      const int b = bin(w);
+      atomicAdd((unsigned long long*)&s.bin_mass[b],
+                (unsigned long long)mass_of(w));
+      atomicAdd(&s.bin_count[b], 1u);
+    }
+    __syncthreads();
+    // A thread has two bins.
+    uint32_t c[2], ct = 0;
+    uint64_t m[2], mt = 0;
 #pragma unroll
-  for (int e = 0; e < kHeld; ++e)
-    if (h.w[e] != 0 && h.bin[e] == pivot)
-      s.words[atomicAdd(&s.gathered, 1u)] = h.w[e];
-  __syncthreads();
-  const int n = (int)s.gathered;
-  if (tid == 0) s.found[0] = 0;
-  if (n <= kWave) {
-    // One wave: what lies before each word, word by word.
-    if (tid < kWave) {
-      const uint64_t w = tid < n ? s.words[tid] : 0;
-      const uint64_t m = w ? mass_of(w) : 0;
-      uint64_t c = cb + 1, before = mb;
-      for (int i = 0; i < n; ++i) {
-        const uint64_t wi = lane64(w, i), mi = lane64(m, i);
-        if (wi > w) {
-          ++c;
-          before += mi;
-        }
+    for (int i = 0; i < 2; ++i) {
+      c[i] = s.bin_count[2 * tid + i];
+      m[i] = s.bin_mass[2 * tid + i];
+      ct += c[i];
+      mt += m[i];
+    }
+    const uint32_t ci = (uint32_t)wave_scan_incl((int)ct);
+    const uint64_t mi = wave_scan64(mt);
+    if (lane() == kWave - 1) {
+      s.counts[0][wave] = ci;
+      s.sums[wave] = mi;
+    }
+    __syncthreads();
+    uint64_t c0 = cb + (ci - ct), m0 = mb + (mi - mt), all = 0;
+    for (int i = 0; i < kSampleWaves; ++i) {
+      const uint64_t x = s.sums[i];
+      if (i < wave) {
+        c0 += s.counts[0][i];
+        m0 += x;
       }
-      if (w && (MASS ? before < goal && goal <= before + m : c == goal)) {
-        s.found[0] = w;
-        s.found[1] = c;
-        s.found[2] = before + m;
+      all += x;
+    }
+    if (shift < 0) out.all = all;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint64_t at = by_mass ? m0 : c0;
+      if (at < goal && goal <= at + (by_mass ? m[i] : c[i])) {
+        s.found[0] = (uint64_t)(2 * tid + i);
+        s.found[1] = c0;
+        s.found[2] = m0;
+      }
+      c0 += c[i];
+      m0 += m[i];
+    }
+    __syncthreads();
+    const int pivot = (int)s.found[0];
+    if (pivot == kSampleBins) return out;
+    cb = s.found[1];
+    mb = s.found[2];
+    const uint32_t count = s.bin_count[pivot];
+    // The bin's words, in any order.  (In the list of a bin's words itself
+    // they move once all threads have read it: at most four each.)
+    uint64_t w[kHeld];
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e) {
+      const int i = e * kSampleThreads + tid;
+      w[e] = i < n ? from[i] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kHeld; ++e)
+      if (w[e] != 0 && bin(w[e]) == pivot)
+        s.some[atomicAdd(&s.gathered, 1u)] = w[e];
+    n = (int)count;
+    from = s.some;
+    __syncthreads();
+    if (n <= kWave) break;
+    // The first bit in which the words differ (some do).
+    const uint64_t first = from[0];
+    uint64_t differ = 0;
+    for (int i = tid; i < n; i += kSampleThreads) differ |= from[i] ^ first;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) differ |= shfl64(differ, lane() ^ o);
+    if (lane() == 0) s.sums[wave] = differ;
+    __syncthreads();
+    for (int i = 0; i < kSampleWaves; ++i) differ |= s.sums[i];
+    const int high = 63 - __builtin_clzll(differ);
+    shift = high > 10 ? high - 10 : 0;
+    __syncthreads();
+  }
+  // One wave: what lies before each word, word by word.
+  if (tid < kWave) {
+    if (tid == 0) s.found[0] = 0;
+    const uint64_t w = tid < n ? s.some[tid] : 0;
+    const uint64_t m = w ? mass_of(w) : 0;
+    uint64_t c = cb + 1, before = mb;
+    for (int i = 0; i < n; ++i) {
+      const uint64_t wi = lane64(w, i), mi = lane64(m, i);
+      if (wi > w) {
+        ++c;
+        before += mi;
       }
     }
-  } else if (n <= kSampleThreads) {
-    cut_by_sorting<MASS, 1>(n, cb, mb, goal, mass_of, s);
-  } else if (n <= 2 * kSampleThreads) {
-    cut_by_sorting<MASS, 2>(n, cb, mb, goal, mass_of, s);
-  } else {
-    cut_by_sorting<MASS, 4>(n, cb, mb, goal, mass_of, s);
+    if (w && (by_mass ? before < goal && goal <= before + m : c == goal)) {
+      s.found[0] = w;
+      s.found[1] = c;
+      s.found[2] = before + m;
+    }
   }
   __syncthreads();
-  return Cut{s.found[0], s.found[2], (int)s.found[1]};
+  out.word = s.found[0];
+  out.mass = s.found[2];
+  out.count = (int)s.found[1];
+  __syncthreads();
+  return out;
 }
 
 // The chunk where `goal` lies in the masses of the row's chunks (one a
 // thread): in every thread, with the mass before it.
-__device__ int find_chunk(uint64_t mass, double u, SampleLds& s,
+__device__ __forceinline__ int find_chunk(uint64_t mass, double u, SampleLds& s,
                           uint64_t* before, uint64_t* goal, uint64_t* total) {
   const uint64_t b = scan_block(mass, s, total);
   *goal = (uint64_t)(u * (double)*total);
@@ -869,31 +821,29 @@ __device__ int find_chunk(uint64_t mass, double u, SampleLds& s,
   return (int)s.found[0];
 }
 
-// The prefix of a row whose listed words, as far as nothing is missing, are
-// held: its last word (1 for all of them), or 0 if they do not reach its end.
-// `whole`: the row has no others; `rare`: some of them are below min_p;
+// The prefix of a row whose `n` words from which on nothing is missing are in
+// s.words: its last word (1 for all of them), or 0 if they do not reach its
+// end.  `whole`: the row has no others; `rare`: some of them are below min_p;
 // `total`: the sum of the row's weights, where it is needed.
-template <class MassOf>
-__device__ uint64_t list_cut(const SampleParams& a, const Wanted& want, Held& h,
+template <class MassOf, class BinOf>
+__device__ __forceinline__ uint64_t list_cut(const SampleParams& a, const Wanted& want, int n,
                              double total, bool whole, bool rare,
-                             MassOf mass_of, SampleLds& s) {
-  bin_words(h, s);
+                             MassOf mass_of, BinOf bin_of, SampleLds& s) {
   uint64_t word = 1;
   bool beyond = !whole;
-  uint64_t part = h.all_mass;  // of the first k
-  if (want.k > 0 && want.k <= (int)h.all_count) {
-    const Cut c = find_cut<false>(h, (uint64_t)want.k, mass_of, s);
-    word = c.word;
-    part = c.mass;
-    beyond = false;
-  }
-  if (want.p < 1.0) {
-    if (want.k > 0 && beyond) return 0;
-    const double of = want.k > 0 ? (double)part : total * a.unit;
-    const double least = ceil(want.p * of);
-    uint64_t goal = least < 1.0 ? 1 : (uint64_t)least;
-    if (want.k > 0 && goal > part) goal = part;
-    const Cut c = find_cut<true>(h, goal, mass_of, s);
+  uint64_t part = 0;  // the mass of the first k
+#pragma unroll 1
+  for (int step = want.k > 0 ? 0 : 1; step < (want.p < 1.0 ? 2 : 1); ++step) {
+    uint64_t goal = (uint64_t)want.k;
+    if (step == 1) {
+      if (want.k > 0 && beyond) return 0;
+      const double of = want.k > 0 ? (double)part : total * a.unit;
+      const double least = ceil(want.p * of);
+      goal = least < 1.0 ? 1 : (uint64_t)least;
+      if (want.k > 0 && goal > part) goal = part;
+    }
+    const Cut c = find_cut(n, step == 1, goal, mass_of, bin_of, s);
+    if (step == 0) part = c.word ? c.mass : c.all;
     if (c.word) {
       word = c.word;
       beyond = false;
@@ -989,55 +939,39 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     for (int i = 0; i < kSampleWaves; ++i)
       if (s.counts[1][i] < kWave) last = i * kWave + (int)s.counts[1][i];
     if (chunk < 0) chunk = last;
-    if (wave != chunk / kWave) return;  // the wave that has its sum goes on
-    double part = __shfl(incl - mass, chunk % kWave, kWave);
-    const int64_t i0 = (int64_t)chunk * kChunk + ln * 16;
-    float x[16];
+    // A logit a thread.
+    if (tid == chunk) s.found[0] = (uint64_t)__double_as_longlong(incl - mass);
+    const int64_t i = (int64_t)chunk * kChunk + tid;
+    const float x = i < a.cols ? read_logit<T>(row, i) : -INFINITY;
+    double w = weight_of(x, top, want.inv_t);
+    if (want.greedy) w = x == top ? 1.0 : 0.0;
+    const double upto_w = wave_scan_double(w);
+    __syncthreads();
+    if (ln == kWave - 1) sums[wave] = upto_w;
+    __syncthreads();
+    double upto = __longlong_as_double((long long)s.found[0]) + upto_w;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float y[kSampleVec];
-      read_logits<T>(row, i0 + j * kSampleVec, a.cols, y);
-#pragma unroll
-      for (int e = 0; e < kSampleVec; ++e) x[j * kSampleVec + e] = y[e];
+    for (int j = 0; j < kSampleWaves; ++j)
+      if (j < wave) upto += sums[j];
+    const bool here = w > 0.0 && (want.greedy || upto > goal);
+    const uint64_t first_here = ballot(here), last_some = ballot(w > 0.0);
+    if (ln == 0) {
+      s.counts[0][wave] =
+          first_here ? (uint32_t)__builtin_ctzll(first_here) : kWave;
+      s.counts[1][wave] =
+          last_some ? (uint32_t)(63 - __builtin_clzll(last_some)) : kWave;
     }
-    if (want.greedy) {
-      int at = 16;
+    __syncthreads();
+    int who = -1, end = 0;
 #pragma unroll
-      for (int e = 15; e >= 0; --e)
-        if (logit_key(x[e]) == top_key) at = e;
-      const uint64_t have = ballot(at < 16);
-      if (ln == __builtin_ctzll(have)) {
-        a.tokens[row_i] = i0 + at;
-        a.logprobs[row_i] = 0.0f;
-      }
-      return;
-    }
-    double w[16], sum = 0.0;
+    for (int j = kSampleWaves - 1; j >= 0; --j)
+      if (s.counts[0][j] < kWave) who = j * kWave + (int)s.counts[0][j];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      w[e] = weight_of(x[e], top, want.inv_t);
-      sum += w[e];
-    }
-    const double upto = wave_scan_double(sum);
-    const uint64_t here = ballot(sum > 0.0 && part + upto > goal);
-    const uint64_t any = ballot(sum > 0.0);
-    const int who = here ? __builtin_ctzll(here) : 63 - __builtin_clzll(any);
-    if (ln != who) return;
-    part += upto - sum;
-    int at = 0;
-    bool done = false;
-    double got = 0.0;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      part += w[e];
-      if (!done && w[e] > 0.0) {
-        at = e;
-        got = w[e];
-        done = part > goal;
-      }
-    }
-    a.tokens[row_i] = i0 + at;
-    a.logprobs[row_i] = (float)log(got / total);
+    for (int j = 0; j < kSampleWaves; ++j)
+      if (s.counts[1][j] < kWave) end = j * kWave + (int)s.counts[1][j];
+    if (tid != (who < 0 ? end : who)) return;
+    a.tokens[row_i] = i;
+    a.logprobs[row_i] = want.greedy ? 0.0f : (float)log(w / total);
     return;
   }
   // ---- lists: their words, four a thread
@@ -1045,41 +979,48 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     return fixed(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
   };
   const bool whole = from <= kKeyNone + 1;  // all that has weight is listed
+  auto bin_of = [&](uint64_t w) {
+    return wide_bin(key_logit((uint32_t)(w >> 32)), top,
+                    kWidePerBit * want.inv_t);
+  };
   uint64_t cut = 0;
-  Held h;
-  bool low[kHeld];  // below min_p
   if (count <= kMaxList && count > 0) {
-    // a wave copies the lists of its threads' chunks
-    for (int i = 0; i < kWave && wave * kWave + i < a.chunks; ++i) {
-      const int nc = __builtin_amdgcn_readlane(n, i);
-      const int tc = __builtin_amdgcn_readlane(to, i);
-      if (ln < nc)
-        s.words[tc + ln] =
-            a.lists[(base + wave * kWave + i) * kChunkList + ln];
+    // Chunks are dealt to the waves; eight lists of each are on their way
+    // together.  Words below the bound are dropped: others are missing there.
+    s.bin_count[tid] = (uint32_t)to << 7 | (uint32_t)n;
+    __syncthreads();
+    bool some_low = false;
+    constexpr int U = 8;
+    for (int c0 = wave; c0 < a.chunks; c0 += U * kSampleWaves) {
+      uint64_t w[U];
+      uint32_t at[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * kSampleWaves;
+        at[u] = c < a.chunks ? s.bin_count[c] : 0;
+        w[u] = ln < (int)(at[u] & 127)
+                   ? a.lists[(base + c) * kChunkList + ln]
+                   : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (ln >= (int)(at[u] & 127)) continue;
+        if ((uint32_t)(w[u] >> 32) < from) w[u] = 0;
+        s.words[(at[u] >> 7) + ln] = w[u];
+      }
     }
     __syncthreads();
-    const double c = kWidePerBit * want.inv_t;
-    bool some_low = false;
-#pragma unroll
-    for (int e = 0; e < kHeld; ++e) {
-      const int i = e * kSampleThreads + tid;
-      low[e] = true;
-      h.w[e] = i < count ? s.words[i] : 0;
-      const uint32_t key = (uint32_t)(h.w[e] >> 32);
-      if (key < from) h.w[e] = 0;  // below it others are missing
-      h.m[e] = 0;
-      h.bin[e] = 0;
-      if (h.w[e]) {
-        const float x = key_logit(key);
-        const double w = weight_of(x, top, want.inv_t);
-        h.m[e] = fixed(w, a);
-        h.bin[e] = wide_bin(x, top, c);
-        low[e] = w < want.min_w;
-        some_low = some_low || low[e];
+    if (want.min_w > 0.0) {
+#pragma unroll 1
+      for (int i = tid; i < count; i += kSampleThreads) {
+        const uint64_t w = s.words[i];
+        if (w && weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t) <
+                     want.min_w)
+          some_low = true;
       }
     }
     const bool rare = __syncthreads_or(some_low) != 0;
-    cut = list_cut(a, want, h, total, whole, rare, mass_of, s);
+    cut = list_cut(a, want, count, total, whole, rare, mass_of, bin_of, s);
   }
   if (cut == 0) {
     // (a prefix of a wide one has two goals: by passes over the row)
@@ -1103,12 +1044,17 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   // ---- in the row's order: the chunk, then its list
   s.chunk_mass[tid] = 0;
   __syncthreads();
-#pragma unroll
-  for (int e = 0; e < kHeld; ++e)
-    if (h.w[e] >= cut && !low[e])
+#pragma unroll 1
+  for (int i = tid; i < count; i += kSampleThreads) {
+    const uint64_t w = s.words[i];
+    if (w < cut) continue;
+    const double x =
+        weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
+    if (x >= want.min_w)
       atomicAdd((unsigned long long*)
-                    &s.chunk_mass[(uint32_t) ~(uint32_t)h.w[e] / kChunk],
-                (unsigned long long)h.m[e]);
+                    &s.chunk_mass[(uint32_t) ~(uint32_t)w / kChunk],
+                (unsigned long long)fixed(x, a));
+  }
   __syncthreads();
   uint64_t before, goal, kept;
   const int chunk =
@@ -1135,7 +1081,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
 // the masses (or counts) of the logits in 2048 bins of log2 of their weight;
 // integers, so that their order is nothing.  The second finds the bin in which
 // the goal lies, adds up each chunk's mass above it, and lists the bin's own
-// logits; the row's last workgroup sorts these, finds the last one kept, the
+// logits; the row's last workgroup finds the last one of these that is kept, the
 // chunk where u times the kept mass lies, and the token in it.
 template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
@@ -1279,39 +1225,33 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
         return fixed(
             weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
       };
-      Held h;
-#pragma unroll
-      for (int e = 0; e < kHeld; ++e) {
-        const int i = e * kSampleThreads + tid;
-        h.w[e] = i < (int)count ? ld_agent(pivots + i) : 0;
-        h.m[e] = 0;
-        h.bin[e] = 0;
-        if (h.w[e]) {
-          // the bin in 2048 parts
-          const float x = key_logit((uint32_t)(h.w[e] >> 32));
-          const double d = ((double)top - (double)x) * c - pivot;
-          h.m[e] = mass_of(h.w[e]);
-          h.bin[e] = d > 0.0 ? (int)fmin(d * kSampleBins, kSampleBins - 1.0) : 0;
-        }
-      }
-      bin_words(h, s);
+      auto bin_of = [&](uint64_t w) {  // the bin in 2048 parts
+        const float x = key_logit((uint32_t)(w >> 32));
+        const double d = ((double)top - (double)x) * c - pivot;
+        return d > 0.0 ? (int)fmin(d * kSampleBins, kSampleBins - 1.0) : 0;
+      };
+      for (int i = tid; i < (int)count; i += kSampleThreads)
+        s.words[i] = ld_agent(pivots + i);
+      __syncthreads();
       const uint64_t goal = wide.goal - above;
-      cut = (wide.mode == kWideCount ? find_cut<false>(h, goal, mass_of, s)
-                                     : find_cut<true>(h, goal, mass_of, s))
-                .word;
+      cut = find_cut((int)count, wide.mode != kWideCount, goal, mass_of, bin_of,
+                     s).word;
       done = cut != 0;
       // Masses of the chunks, and of the bin's words in them.
       if (done) {
         s.chunk_mass[tid] = 0;
         __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kHeld; ++e)
-          if (h.w[e] >= cut && h.w[e] != 0 &&
-              weight_of(key_logit((uint32_t)(h.w[e] >> 32)), top, want.inv_t) >=
-                  want.min_w)
+#pragma unroll 1
+        for (int i = tid; i < (int)count; i += kSampleThreads) {
+          const uint64_t w = s.words[i];
+          if (w < cut) continue;
+          const double x =
+              weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
+          if (x >= want.min_w)
             atomicAdd((unsigned long long*)
-                          &s.chunk_mass[(uint32_t) ~(uint32_t)h.w[e] / kChunk],
-                      (unsigned long long)h.m[e]);
+                          &s.chunk_mass[(uint32_t) ~(uint32_t)w / kChunk],
+                      (unsigned long long)fixed(x, a));
+        }
         __syncthreads();
       }
     }
