@@ -111,11 +111,11 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.rank = (int32_t)(rank < 2 ? 2 : rank > 32 ? 32 : rank);
   // Batches of rows share the workspace, which stays below 64 MB.
   const int64_t per = chunks * (8 + 3 * 4 + 8 + 8 * kChunkList) +
-                      8 * (kWideBins + kMaxList) + (int64_t)sizeof(WideRow);
+                      8 * (kWideBins + kMaxList) + (int64_t)sizeof(WideRow) + 4;
   int64_t batch = kSampleWork / per;
   if (batch > rows) batch = rows;
   Work work;
-  rc = get_work(dev, st, (size_t)(batch * per), (size_t)batch, &work);
+  rc = get_work(dev, st, (size_t)(batch * per + 4), (size_t)batch, &work);
   if (rc != LIBTOPK_OK) return rc;
   const int64_t n = batch * chunks;
   p.lists = (uint64_t*)work.base;
@@ -127,6 +127,7 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.chunk_max = (uint32_t*)(p.wide + batch);
   p.chunk_from = p.chunk_max + n;
   p.chunk_n = p.chunk_from + n;
+  p.wide_list = p.chunk_n + n;
   p.ticket = work.tickets;
   p.epoch = work.epoch;
   // Without settings there are no prefixes, and none that goes beyond lists.
@@ -134,6 +135,9 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
       (how->top_p || how->top_p_all < 1.0f || how->top_k ||
        how->top_k_all > 0 || how->min_p || how->min_p_all > 0.0f);
   const int64_t parts = (chunks + kWideChunks - 1) / kWideChunks;
+  int units = 0;
+  rc = units_of(dev, &units);
+  if (rc != LIBTOPK_OK) return rc;
   for (int64_t r = 0; r < rows && rc == LIBTOPK_OK; r += batch) {
     const int64_t m = rows - r < batch ? rows - r : batch;
     p.row0 = r;
@@ -141,10 +145,12 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
                 kBlock, p, st);
     if (rc == LIBTOPK_OK)
       rc = launch(fn.finish, dim3((unsigned)m), kSampleThreads, p, st);
+    // The parts of whatever rows are wide, a workgroup a unit.
+    const unsigned grid = (unsigned)(m * parts < units ? m * parts : units);
     if (rc == LIBTOPK_OK && wide)
-      rc = launch(fn.bins, dim3((unsigned)(m * parts)), kSampleThreads, p, st);
+      rc = launch(fn.bins, dim3(grid), kSampleThreads, p, st);
     if (rc == LIBTOPK_OK && wide)
-      rc = launch(fn.wide, dim3((unsigned)(m * parts)), kSampleThreads, p, st);
+      rc = launch(fn.wide, dim3(grid), kSampleThreads, p, st);
   }
   return rc;
 }

@@ -56,6 +56,7 @@ struct SampleParams {
   uint64_t* lists;  // [row - row0][chunk][kChunkList]
   // Of rows whose prefix is wide, [row - row0].., see sample_bins_kernel.
   struct WideRow* wide;
+  uint32_t* wide_list;   // how many, and which rows they are, in any order
   uint64_t* bins;        // [kWideBins]
   uint64_t* chunk_mass;  // [chunk]
   uint64_t* pivots;      // [kMaxList]
@@ -64,7 +65,7 @@ struct SampleParams {
 };
 
 // What a wide prefix has to reach.
-enum { kNotWide, kWideMass, kWideCount, kWideAll, kWideRow };
+enum { kWideMass, kWideCount, kWideAll, kWideRow };
 struct WideRow {
   uint32_t mode;
   uint32_t top;     // the largest logit's key
@@ -270,39 +271,86 @@ struct SampleLds {
     };
   };
   uint64_t sums[kSampleWaves];
-  uint32_t counts[2][kSampleWaves];
   uint64_t found[4];
   uint32_t gathered;
 };
 
+// What a workgroup's waves have, in turn: every wave reads all 16 (one a lane)
+// and folds them by moves between lanes, which is less code, and quicker, than
+// a loop over them.
+__device__ __forceinline__ uint64_t wave_item(const uint64_t* x) {
+  return lane() < kSampleWaves ? x[lane()] : 0;
+}
+
 // Exclusive prefix of v over the workgroup's threads, and the total.
 __device__ __forceinline__ uint64_t scan_block(uint64_t v, SampleLds& s,
                                                uint64_t* total) {
+  const int wave = uni((int)threadIdx.x / kWave);
   const uint64_t incl = wave_scan64(v);
   __syncthreads();  // the last call's sums have been read
-  if (lane() == kWave - 1) s.sums[threadIdx.x / kWave] = incl;
+  if (lane() == kWave - 1) s.sums[wave] = incl;
   __syncthreads();
-  uint64_t before = 0, all = 0;
-  for (int i = 0; i < kSampleWaves; ++i) {
-    const uint64_t x = s.sums[i];
-    if (i < (int)threadIdx.x / kWave) before += x;
-    all += x;
-  }
-  *total = all;
-  return before + incl - v;
+  const uint64_t all = wave_scan64(wave_item(s.sums));
+  *total = lane64(all, kSampleWaves - 1);
+  return (wave ? lane64(all, wave - 1) : 0) + incl - v;
 }
-
-__device__ __forceinline__ uint64_t max_block(uint64_t v, SampleLds& s) {
+__device__ __forceinline__ double scan_block(double v, SampleLds& s,
+                                             double* total) {
+  const int wave = uni((int)threadIdx.x / kWave);
+  const double incl = wave_scan_double(v);
+  __syncthreads();
+  if (lane() == kWave - 1)
+    s.sums[wave] = (uint64_t)__double_as_longlong(incl);
+  __syncthreads();
+  const double all =
+      wave_scan_double(__longlong_as_double((long long)wave_item(s.sums)));
+  auto of = [&](int w) {
+    return __longlong_as_double(
+        (long long)lane64((uint64_t)__double_as_longlong(all), w));
+  };
+  *total = of(kSampleWaves - 1);
+  return (wave ? of(wave - 1) : 0.0) + (incl - v);
+}
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) {
     const uint64_t w = shfl64(v, lane() ^ o);
     v = w > v ? w : v;
   }
+  return v;
+}
+__device__ __forceinline__ uint64_t max_block(uint64_t v, SampleLds& s) {
+  v = wave_max64(v);
   __syncthreads();
   if (lane() == 0) s.sums[threadIdx.x / kWave] = v;
   __syncthreads();
-  for (int i = 0; i < kSampleWaves; ++i) v = s.sums[i] > v ? s.sums[i] : v;
-  return v;
+  return wave_max64(wave_item(s.sums));
+}
+// The largest of two numbers each.
+__device__ __forceinline__ void max_block(uint32_t* x, uint32_t* y,
+                                          SampleLds& s) {
+  const int a = wave_max(unbias(*x)), b = wave_max(unbias(*y));
+  __syncthreads();
+  if (lane() == 0)
+    s.sums[threadIdx.x / kWave] = (uint64_t)bias(a) << 32 | bias(b);
+  __syncthreads();
+  const uint64_t v = wave_item(s.sums);
+  *x = bias(wave_max(unbias((uint32_t)(v >> 32))));
+  *y = bias(wave_max(unbias((uint32_t)v)));
+}
+// The first thread where `a` holds; where it does in none, the last where `b`
+// does.
+__device__ __forceinline__ int first_or_last(bool a, bool b, SampleLds& s) {
+  const int wave = (int)threadIdx.x / kWave;
+  const uint64_t x = ballot(a), y = ballot(b);
+  // the larger is the one: 2^16 - thread for the first, thread + 1 for the last
+  const uint32_t i =
+      x ? 0x10000u - (uint32_t)(wave * kWave + __builtin_ctzll(x)) : 0u;
+  const uint32_t j =
+      y ? (uint32_t)(wave * kWave + 64 - __builtin_clzll(y)) : 0u;
+  uint32_t p = i, q = j;
+  max_block(&p, &q, s);
+  return p ? (int)(0x10000u - p) : (int)q - 1;
 }
 
 // A prefix of the order: all logits with a key above `key`, and the first
@@ -563,6 +611,7 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
   const int r = (int)(blockIdx.x / (unsigned)wg);
   const int chunk =
       uni((int)(blockIdx.x % (unsigned)wg) * kWaves + (int)threadIdx.x / kWave);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.wide_list[0] = 0;
   if (chunk >= a.chunks) return;
   const int64_t row_i = a.row0 + r;
   const char* row = a.x + row_i * a.ld;
@@ -674,7 +723,7 @@ template <class MassOf, class BinOf>
 __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
                                         MassOf mass_of, BinOf bin_of,
                                         SampleLds& s) {
-  const int tid = threadIdx.x, wave = tid / kWave;
+  const int tid = threadIdx.x;
   uint64_t cb = 0, mb = 0;  // words and mass before the ones in question
   Cut out = {0, 0, 0, 0};
   int shift = -1;  // of the words, which are the bins then
@@ -714,22 +763,9 @@ __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
       ct += c[i];
       mt += m[i];
     }
-    const uint32_t ci = (uint32_t)wave_scan_incl((int)ct);
-    const uint64_t mi = wave_scan64(mt);
-    if (lane() == kWave - 1) {
-      s.counts[0][wave] = ci;
-      s.sums[wave] = mi;
-    }
-    __syncthreads();
-    uint64_t c0 = cb + (ci - ct), m0 = mb + (mi - mt), all = 0;
-    for (int i = 0; i < kSampleWaves; ++i) {
-      const uint64_t x = s.sums[i];
-      if (i < wave) {
-        c0 += s.counts[0][i];
-        m0 += x;
-      }
-      all += x;
-    }
+    uint64_t all, counts;
+    uint64_t m0 = mb + scan_block(mt, s, &all);
+    uint64_t c0 = cb + scan_block((uint64_t)ct, s, &counts);
     if (shift < 0) out.all = all;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -769,14 +805,10 @@ __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
     const uint64_t first = from[0];
     uint64_t differ = 0;
     for (int i = tid; i < n; i += kSampleThreads) differ |= from[i] ^ first;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) differ |= shfl64(differ, lane() ^ o);
-    if (lane() == 0) s.sums[wave] = differ;
-    __syncthreads();
-    for (int i = 0; i < kSampleWaves; ++i) differ |= s.sums[i];
+    // (the largest has its highest bit)
+    differ = max_block(differ, s);
     const int high = 63 - __builtin_clzll(differ);
     shift = high > 10 ? high - 10 : 0;
-    __syncthreads();
   }
   // One wave: what lies before each word, word by word.
   if (tid < kWave) {
@@ -867,24 +899,10 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   const uint32_t chunk_top = in ? a.chunk_max[base + tid] : 0;
   const uint32_t chunk_from = in ? a.chunk_from[base + tid] : 0;
   const double chunk_sum = in ? a.chunk_sum[base + tid] : 0.0;
-  int n = in ? (int)a.chunk_n[base + tid] : 0;
+  const int n = in ? (int)a.chunk_n[base + tid] : 0;
   const Wanted want = wanted(a, row_i);
-  if (tid == 0) a.wide[blockIdx.x].mode = kNotWide;
-  // ---- over the chunks: the largest logit, the bound of the lists
-  {
-    const int x = wave_max(unbias(chunk_top)), y = wave_max(unbias(chunk_from));
-    if (ln == 0) {
-      s.counts[0][wave] = bias(x);
-      s.counts[1][wave] = bias(y);
-    }
-  }
-  __syncthreads();
-  uint32_t top_key = 0, from = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWaves; ++i) {
-    top_key = max(top_key, s.counts[0][i]);
-    from = max(from, s.counts[1][i]);
-  }
+  uint32_t top_key = chunk_top, from = chunk_from;
+  max_block(&top_key, &from, s);
   const float top = key_logit(top_key);
   if (top_key == kKeyNone) {
     if (tid == 0) {
@@ -896,84 +914,36 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   double mass = 0.0;
   if (in && want.sums() && !want.greedy)
     mass = chunk_sum * weight_of(key_logit(chunk_top), top, want.inv_t);
-  const double incl_w = wave_scan_double(mass);
-  if (want.greedy || want.all()) n = 0;
-  const int n_incl = wave_scan_incl(n);
-  double* const sums = (double*)s.sums;
-  __syncthreads();
-  if (ln == kWave - 1) {
-    sums[wave] = incl_w;
-    s.counts[0][wave] = (uint32_t)n_incl;
-  }
-  __syncthreads();
-  double sum_before = 0.0, total = 0.0;
-  int to = n_incl - n, count = 0;
-#pragma unroll
-  for (int i = 0; i < kSampleWaves; ++i) {
-    if (i < wave) {
-      sum_before += sums[i];
-      to += (int)s.counts[0][i];
-    }
-    total += sums[i];
-    count += (int)s.counts[0][i];
-  }
+  double total;
+  const double before_mass = scan_block(mass, s, &total);
   if (want.greedy || want.all()) {
     // ---- the first chunk with the largest logit, or past the goal; where
     // rounding leaves none past it, the last one that has weight
-    const double incl = sum_before + incl_w;
     const double goal = want.u * total;
-    const bool past =
-        want.greedy ? chunk_top == top_key : mass > 0.0 && incl > goal;
-    const uint64_t over = ballot(past), some = ballot(mass > 0.0);
-    __syncthreads();
-    if (ln == 0) {
-      s.counts[0][wave] = over ? (uint32_t)__builtin_ctzll(over) : kWave;
-      s.counts[1][wave] = some ? (uint32_t)(63 - __builtin_clzll(some)) : kWave;
-    }
-    __syncthreads();
-    int chunk = -1, last = 0;
-#pragma unroll
-    for (int i = kSampleWaves - 1; i >= 0; --i)
-      if (s.counts[0][i] < kWave) chunk = i * kWave + (int)s.counts[0][i];
-#pragma unroll
-    for (int i = 0; i < kSampleWaves; ++i)
-      if (s.counts[1][i] < kWave) last = i * kWave + (int)s.counts[1][i];
-    if (chunk < 0) chunk = last;
+    const int chunk = first_or_last(
+        want.greedy ? chunk_top == top_key
+                    : mass > 0.0 && before_mass + mass > goal,
+        mass > 0.0, s);
     // A logit a thread.
-    if (tid == chunk) s.found[0] = (uint64_t)__double_as_longlong(incl - mass);
+    if (tid == chunk)
+      s.found[0] = (uint64_t)__double_as_longlong(before_mass);
     const int64_t i = (int64_t)chunk * kChunk + tid;
     const float x = i < a.cols ? read_logit<T>(row, i) : -INFINITY;
     double w = weight_of(x, top, want.inv_t);
     if (want.greedy) w = x == top ? 1.0 : 0.0;
-    const double upto_w = wave_scan_double(w);
-    __syncthreads();
-    if (ln == kWave - 1) sums[wave] = upto_w;
-    __syncthreads();
-    double upto = __longlong_as_double((long long)s.found[0]) + upto_w;
-#pragma unroll
-    for (int j = 0; j < kSampleWaves; ++j)
-      if (j < wave) upto += sums[j];
-    const bool here = w > 0.0 && (want.greedy || upto > goal);
-    const uint64_t first_here = ballot(here), last_some = ballot(w > 0.0);
-    if (ln == 0) {
-      s.counts[0][wave] =
-          first_here ? (uint32_t)__builtin_ctzll(first_here) : kWave;
-      s.counts[1][wave] =
-          last_some ? (uint32_t)(63 - __builtin_clzll(last_some)) : kWave;
-    }
-    __syncthreads();
-    int who = -1, end = 0;
-#pragma unroll
-    for (int j = kSampleWaves - 1; j >= 0; --j)
-      if (s.counts[0][j] < kWave) who = j * kWave + (int)s.counts[0][j];
-#pragma unroll
-    for (int j = 0; j < kSampleWaves; ++j)
-      if (s.counts[1][j] < kWave) end = j * kWave + (int)s.counts[1][j];
-    if (tid != (who < 0 ? end : who)) return;
+    double all;
+    double upto = w + scan_block(w, s, &all);
+    upto += __longlong_as_double((long long)s.found[0]);
+    const int who =
+        first_or_last(w > 0.0 && (want.greedy || upto > goal), w > 0.0, s);
+    if (tid != who) return;
     a.tokens[row_i] = i;
     a.logprobs[row_i] = want.greedy ? 0.0f : (float)log(w / total);
     return;
   }
+  uint64_t listed;
+  const int to = (int)scan_block((uint64_t)n, s, &listed);
+  const int count = (int)listed;
   // ---- lists: their words, four a thread
   auto mass_of = [&](uint64_t w) {
     return fixed(weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
@@ -1038,6 +1008,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
                : part < 1.0       ? 1
                                   : (uint64_t)part;
       a.wide[blockIdx.x] = w;
+      a.wide_list[1 + atomicAdd(a.wide_list, 1u)] = blockIdx.x;
     }
     return;
   }
@@ -1087,54 +1058,52 @@ template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     SampleParams a) {
   const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
-  const int r = (int)(blockIdx.x / (unsigned)wg);
-  const WideRow wide = a.wide[r];
-  if (wide.mode != kWideMass && wide.mode != kWideCount) return;
+  const int tasks = (int)a.wide_list[0] * wg;
   __shared__ uint64_t bins[kWideBins];
   const int tid = threadIdx.x;
-  for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
-  __syncthreads();
-  const int64_t row_i = a.row0 + r;
-  const Wanted want = wanted(a, row_i);
-  const float top = key_logit(wide.top);
-  const int chunk =
-      (int)(blockIdx.x % (unsigned)wg) * kWideChunks + tid / kWave;
-  if (chunk < a.chunks) {
-    typedef ChunkShape<T> S;
-    float x[S::N];
-    read_chunk<T>(a.x + row_i * a.ld, chunk * kChunk, a.cols, x);
-    const double c = kWidePerBit * want.inv_t;
+  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+    const int r = (int)a.wide_list[1 + task / wg];
+    const WideRow wide = a.wide[r];
+    if (wide.mode != kWideMass && wide.mode != kWideCount) continue;
+    for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
+    __syncthreads();
+    const int64_t row_i = a.row0 + r;
+    const Wanted want = wanted(a, row_i);
+    const float top = key_logit(wide.top);
+    const int chunk = task % wg * kWideChunks + tid / kWave;
+    if (chunk < a.chunks) {
+      typedef ChunkShape<T> S;
+      float x[S::N];
+      read_chunk<T>(a.x + row_i * a.ld, chunk * kChunk, a.cols, x);
+      const double c = kWidePerBit * want.inv_t;
 #pragma unroll
-    for (int e = 0; e < S::N; ++e) {
-      // What lies in the last bin has no weight to speak of: 2^-46 and less.
-      const int bin = wide_bin(x[e], top, c);
-      if (bin == kWideBins - 1) continue;
-      atomicAdd((unsigned long long*)&bins[bin],
-                wide.mode == kWideCount
-                    ? 1ull
-                    : (unsigned long long)fixed(
-                          weight_of(x[e], top, want.inv_t), a));
+      for (int e = 0; e < S::N; ++e) {
+        // What lies in the last bin has no weight to speak of: 2^-46 and less.
+        const int bin = wide_bin(x[e], top, c);
+        if (bin == kWideBins - 1) continue;
+        atomicAdd((unsigned long long*)&bins[bin],
+                  wide.mode == kWideCount
+                      ? 1ull
+                      : (unsigned long long)fixed(
+                            weight_of(x[e], top, want.inv_t), a));
+      }
     }
+    __syncthreads();
+    unsigned long long* all =
+        (unsigned long long*)(a.bins + (int64_t)r * kWideBins);
+    for (int i = tid; i < kWideBins; i += kSampleThreads)
+      if (bins[i]) atomicAdd(all + i, (unsigned long long)bins[i]);
+    __syncthreads();
   }
-  __syncthreads();
-  unsigned long long* all =
-      (unsigned long long*)(a.bins + (int64_t)r * kWideBins);
-  for (int i = tid; i < kWideBins; i += kSampleThreads)
-    if (bins[i]) atomicAdd(all + i, (unsigned long long)bins[i]);
 }
 
+// Part `part` of the `wg` of row r.
 template <int T>
-__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
-    SampleParams a) {
-  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
-  const int r = (int)(blockIdx.x / (unsigned)wg);
+__device__ void wide_part(const SampleParams& a, int r, int part, int wg,
+                          SampleLds& s, int* flag) {
   const WideRow wide = a.wide[r];
-  if (wide.mode == kNotWide) return;
-  __shared__ SampleLds s;
-  __shared__ int flag;
   if (wide.mode == kWideRow) {
-    if (blockIdx.x % (unsigned)wg == 0)
-      sample_row<T>(a, a.row0 + r, s);
+    if (part == 0) sample_row<T>(a, a.row0 + r, s);
     return;
   }
   const int tid = threadIdx.x, ln = lane();
@@ -1176,7 +1145,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
   // (a goal beyond the bins: the row is done over)
   const bool lost = wide.mode != kWideAll && pivot == kWideBins;
   const int chunk =
-      (int)(blockIdx.x % (unsigned)wg) * kWideChunks + tid / kWave;
+      part * kWideChunks + tid / kWave;
   uint64_t* const pivots = a.pivots + (int64_t)r * kMaxList;
   if (chunk < a.chunks && !lost) {
     float x[S::N];
@@ -1213,7 +1182,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
     for (int o = 32; o > 0; o >>= 1) sum += shfl64(sum, ln ^ o);
     if (ln == 0) st_agent(a.chunk_mass + (int64_t)r * a.chunks + chunk, sum);
   }
-  if (!last_to_finish(a.ticket + r, wg, a.epoch, &flag)) return;
+  if (!last_to_finish(a.ticket + r, wg, a.epoch, flag)) return;
   // ---- the row's last workgroup
   const unsigned count = ld_agent(&a.wide[r].pivots);
   uint64_t cut = 0;
@@ -1269,7 +1238,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
       find_chunk(mass, want.u, s, &before, &goal, &total);
   if (tid >= kWave) return;
   // Lane l takes logits 16 l .. of the chunk.
-  uint64_t part = before;
+  uint64_t upto = before;
   const int64_t i0 = (int64_t)chunk_i * kChunk + ln * 16;
   uint64_t m[16], sum = 0;
 #pragma unroll
@@ -1288,20 +1257,33 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
       sum += m[j * kSampleVec + e];
     }
   }
-  part += wave_scan64(sum) - sum;
-  if (part <= goal && goal < part + sum) {
+  upto += wave_scan64(sum) - sum;
+  if (upto <= goal && goal < upto + sum) {
     int at = 0;
     bool past = false;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      part += m[e];
+      upto += m[e];
       if (!past) at = e;
-      past = past || part > goal;
+      past = past || upto > goal;
     }
     a.tokens[row_i] = i0 + at;
     a.logprobs[row_i] =
         (float)log(weight_of(read_logit<T>(row, i0 + at), top, want.inv_t) /
                    ((double)total / a.unit));
+  }
+}
+
+template <int T>
+__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
+    SampleParams a) {
+  __shared__ SampleLds s;
+  __shared__ int flag;
+  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
+  const int tasks = (int)a.wide_list[0] * wg;
+  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+    wide_part<T>(a, (int)a.wide_list[1 + task / wg], task % wg, wg, s, &flag);
+    __syncthreads();
   }
 }
 
