@@ -24,7 +24,7 @@ bool meets(const void* a, int64_t na, const void* b, int64_t nb) {
 constexpr int64_t kSampleWork = (int64_t)1 << 26;
 
 struct Kernels {
-  const void *row, *chunk, *finish, *bins, *wide;
+  const void *row, *chunk, *finish, *bins, *wide, *last;
 };
 template <int T>
 Kernels kernels_of() {
@@ -32,7 +32,8 @@ Kernels kernels_of() {
           (const void*)&sample_chunk_kernel<T>,
           (const void*)&sample_finish_kernel<T>,
           (const void*)&sample_bins_kernel<T>,
-          (const void*)&sample_wide_kernel<T>};
+          (const void*)&sample_wide_kernel<T>,
+          (const void*)&sample_last_kernel<T>};
 }
 Kernels kernels(int32_t dtype) {
   return dtype == LIBTOPK_F32    ? kernels_of<kLogF32>()
@@ -115,7 +116,7 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   int64_t batch = kSampleWork / per;
   if (batch > rows) batch = rows;
   Work work;
-  rc = get_work(dev, st, (size_t)(batch * per + 4), (size_t)batch, &work);
+  rc = get_work(dev, st, (size_t)(batch * per + 4), 1, &work);
   if (rc != LIBTOPK_OK) return rc;
   const int64_t n = batch * chunks;
   p.lists = (uint64_t*)work.base;
@@ -128,8 +129,6 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   p.chunk_from = p.chunk_max + n;
   p.chunk_n = p.chunk_from + n;
   p.wide_list = p.chunk_n + n;
-  p.ticket = work.tickets;
-  p.epoch = work.epoch;
   // Without settings there are no prefixes, and none that goes beyond lists.
   const bool wide =
       (how->top_p || how->top_p_all < 1.0f || how->top_k ||
@@ -151,6 +150,9 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
       rc = launch(fn.bins, dim3(grid), kSampleThreads, p, st);
     if (rc == LIBTOPK_OK && wide)
       rc = launch(fn.wide, dim3(grid), kSampleThreads, p, st);
+    if (rc == LIBTOPK_OK && wide)
+      rc = launch(fn.last, dim3((unsigned)(m < units ? m : units)),
+                  kSampleThreads, p, st);
   }
   return rc;
 }

@@ -60,8 +60,6 @@ struct SampleParams {
   uint64_t* bins;        // [kWideBins]
   uint64_t* chunk_mass;  // [chunk]
   uint64_t* pivots;      // [kMaxList]
-  uint64_t* ticket;
-  uint32_t epoch;
 };
 
 // What a wide prefix has to reach.
@@ -254,7 +252,12 @@ __device__ __forceinline__ uint64_t lane64(uint64_t v, int from) {
 }
 
 // LDS of a row.
-struct SampleLds {
+// What scans of a workgroup need.
+struct ScanLds {
+  uint64_t sums[kSampleWaves];
+  uint64_t found[4];
+};
+struct SampleLds : ScanLds {
   union {
     struct {  // passes over the row
       uint64_t mass[kSampleBins];
@@ -270,8 +273,6 @@ struct SampleLds {
       uint64_t chunk_mass[kMaxChunks];
     };
   };
-  uint64_t sums[kSampleWaves];
-  uint64_t found[4];
   uint32_t gathered;
 };
 
@@ -283,7 +284,7 @@ __device__ __forceinline__ uint64_t wave_item(const uint64_t* x) {
 }
 
 // Exclusive prefix of v over the workgroup's threads, and the total.
-__device__ __forceinline__ uint64_t scan_block(uint64_t v, SampleLds& s,
+__device__ __forceinline__ uint64_t scan_block(uint64_t v, ScanLds& s,
                                                uint64_t* total) {
   const int wave = uni((int)threadIdx.x / kWave);
   const uint64_t incl = wave_scan64(v);
@@ -294,7 +295,7 @@ __device__ __forceinline__ uint64_t scan_block(uint64_t v, SampleLds& s,
   *total = lane64(all, kSampleWaves - 1);
   return (wave ? lane64(all, wave - 1) : 0) + incl - v;
 }
-__device__ __forceinline__ double scan_block(double v, SampleLds& s,
+__device__ __forceinline__ double scan_block(double v, ScanLds& s,
                                              double* total) {
   const int wave = uni((int)threadIdx.x / kWave);
   const double incl = wave_scan_double(v);
@@ -319,7 +320,7 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
   }
   return v;
 }
-__device__ __forceinline__ uint64_t max_block(uint64_t v, SampleLds& s) {
+__device__ __forceinline__ uint64_t max_block(uint64_t v, ScanLds& s) {
   v = wave_max64(v);
   __syncthreads();
   if (lane() == 0) s.sums[threadIdx.x / kWave] = v;
@@ -328,7 +329,7 @@ __device__ __forceinline__ uint64_t max_block(uint64_t v, SampleLds& s) {
 }
 // The largest of two numbers each.
 __device__ __forceinline__ void max_block(uint32_t* x, uint32_t* y,
-                                          SampleLds& s) {
+                                          ScanLds& s) {
   const int a = wave_max(unbias(*x)), b = wave_max(unbias(*y));
   __syncthreads();
   if (lane() == 0)
@@ -340,7 +341,7 @@ __device__ __forceinline__ void max_block(uint32_t* x, uint32_t* y,
 }
 // The first thread where `a` holds; where it does in none, the last where `b`
 // does.
-__device__ __forceinline__ int first_or_last(bool a, bool b, SampleLds& s) {
+__device__ __forceinline__ int first_or_last(bool a, bool b, ScanLds& s) {
   const int wave = (int)threadIdx.x / kWave;
   const uint64_t x = ballot(a), y = ballot(b);
   // the larger is the one: 2^16 - thread for the first, thread + 1 for the last
@@ -1047,13 +1048,12 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
 }
 
 // ---- wide prefixes ----------------------------------------------------------
-// A prefix beyond the lists (a nucleus of tens of thousands) is found in two
-// more launches over the row, by workgroups of 16 chunks.  The first adds up
+// A prefix beyond the lists (a nucleus of tens of thousands) is found in three
+// more launches, two of them over the row by workgroups of 16 chunks.  The first adds up
 // the masses (or counts) of the logits in 2048 bins of log2 of their weight;
 // integers, so that their order is nothing.  The second finds the bin in which
 // the goal lies, adds up each chunk's mass above it, and lists the bin's own
-// logits; the row's last workgroup finds the last one of these that is kept, the
-// chunk where u times the kept mass lies, and the token in it.
+// logits; the third ends the row (finish_wide).
 template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     SampleParams a) {
@@ -1097,61 +1097,68 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
   }
 }
 
-// Part `part` of the `wg` of row r.
+// The bin of a wide row's goal: kWideBins if the goal is beyond the bins, or
+// if there is none (all of them count).
+struct Pivot {
+  int bin;
+  uint64_t above;  // mass or count
+};
+__device__ __forceinline__ Pivot find_pivot(const SampleParams& a, int r,
+                                            const WideRow& wide, ScanLds& s) {
+  Pivot out = {kWideBins, 0};
+  if (wide.mode == kWideAll) return out;
+  const int tid = threadIdx.x;
+  constexpr int B = kWideBins / kSampleThreads;
+  const uint64_t* bins = a.bins + (int64_t)r * kWideBins;
+  uint64_t b[B], sum = 0;
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    b[i] = bins[tid * B + i];
+    sum += b[i];
+  }
+  uint64_t all;
+  uint64_t before = scan_block(sum, s, &all);
+  if (tid == 0) s.found[0] = kWideBins;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < B; ++i) {
+    if (before < wide.goal && wide.goal <= before + b[i]) {
+      s.found[0] = (uint64_t)(tid * B + i);
+      s.found[1] = before;
+    }
+    before += b[i];
+  }
+  __syncthreads();
+  out.bin = (int)s.found[0];
+  out.above = s.found[1];
+  return out;
+}
+
 template <int T>
-__device__ void wide_part(const SampleParams& a, int r, int part, int wg,
-                          SampleLds& s, int* flag) {
-  const WideRow wide = a.wide[r];
-  if (wide.mode == kWideRow) {
-    if (part == 0) sample_row<T>(a, a.row0 + r, s);
-    return;
-  }
+__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
+    SampleParams a) {
+  __shared__ ScanLds s;
+  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
+  const int tasks = (int)a.wide_list[0] * wg;
   const int tid = threadIdx.x, ln = lane();
-  const int64_t row_i = a.row0 + r;
-  const char* row = a.x + row_i * a.ld;
-  const Wanted want = wanted(a, row_i);
-  const float top = key_logit(wide.top);
-  const double c = kWidePerBit * want.inv_t;
   typedef ChunkShape<T> S;
-  // ---- the bin of the goal
-  int pivot = kWideBins;  // all above it
-  uint64_t above = 0;
-  if (wide.mode != kWideAll) {
-    constexpr int B = kWideBins / kSampleThreads;
-    const uint64_t* bins = a.bins + (int64_t)r * kWideBins;
-    uint64_t b[B], sum = 0;
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      b[i] = bins[tid * B + i];
-      sum += b[i];
-    }
-    uint64_t all;
-    uint64_t before = scan_block(sum, s, &all);
-    if (tid == 0) s.found[0] = kWideBins;
+  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
+    const int r = (int)a.wide_list[1 + task / wg];
+    const WideRow wide = a.wide[r];
+    if (wide.mode == kWideRow) continue;
+    const int64_t row_i = a.row0 + r;
+    const Wanted want = wanted(a, row_i);
+    const float top = key_logit(wide.top);
+    const double c = kWidePerBit * want.inv_t;
+    const int pivot = find_pivot(a, r, wide, s).bin;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      if (before < wide.goal && wide.goal <= before + b[i]) {
-        s.found[0] = (uint64_t)(tid * B + i);
-        s.found[1] = before;
-      }
-      before += b[i];
-    }
-    __syncthreads();
-    pivot = (int)s.found[0];
-    above = s.found[1];
-    __syncthreads();
-  }
-  // (a goal beyond the bins: the row is done over)
-  const bool lost = wide.mode != kWideAll && pivot == kWideBins;
-  const int chunk =
-      part * kWideChunks + tid / kWave;
-  uint64_t* const pivots = a.pivots + (int64_t)r * kMaxList;
-  if (chunk < a.chunks && !lost) {
+    if (pivot == kWideBins && wide.mode != kWideAll) continue;
+    const int chunk = task % wg * kWideChunks + tid / kWave;
+    if (chunk >= a.chunks) continue;
     float x[S::N];
-    read_chunk<T>(row, chunk * kChunk, a.cols, x);
+    read_chunk<T>(a.x + row_i * a.ld, chunk * kChunk, a.cols, x);
     uint64_t sum = 0;
-    int mine = 0;
+    uint32_t bits = 0;
 #pragma unroll
     for (int e = 0; e < S::N; ++e) {
       const int bin = wide_bin(x[e], top, c);
@@ -1159,130 +1166,110 @@ __device__ void wide_part(const SampleParams& a, int r, int part, int wg,
         const double w = weight_of(x[e], top, want.inv_t);
         if (w >= want.min_w) sum += fixed(w, a);
       }
-      mine += bin == pivot && pivot < kWideBins;
+      // (past the row's end there is -infinity, which is in the last bin)
+      bits |= (bin == pivot ? 1u : 0u) << e;
     }
-    if (ballot(mine > 0)) {
-      const int incl = wave_scan_incl(mine);
-      unsigned to = 0;
-      if (ln == kWave - 1) to = atomicAdd(&a.wide[r].pivots, (unsigned)incl);
-      to = (unsigned)__builtin_amdgcn_readlane((int)to, kWave - 1);
-      to += (unsigned)(incl - mine);
+    sum = wave_scan64(sum);
+    if (ln == kWave - 1) a.chunk_mass[(int64_t)r * a.chunks + chunk] = sum;
+    const int mine = __popc(bits);
+    if (ballot(mine > 0) == 0) continue;
+    const int incl = wave_scan_incl(mine);
+    unsigned to = 0;
+    if (ln == kWave - 1) to = atomicAdd(&a.wide[r].pivots, (unsigned)incl);
+    to = (unsigned)__builtin_amdgcn_readlane((int)to, kWave - 1);
+    to += (unsigned)(incl - mine);
+    uint64_t* const pivots = a.pivots + (int64_t)r * kMaxList;
 #pragma unroll
-      for (int e = 0; e < S::N; ++e) {
-        if (wide_bin(x[e], top, c) != pivot) continue;
-        const uint32_t i = (uint32_t)(chunk * kChunk + S::at(e));
-        // (past the row's end there is -infinity, which is in the last bin)
-        if (to < kMaxList)
-          st_agent(pivots + to,
-                   (uint64_t)logit_key(x[e]) << 32 | (uint32_t)~i);
-        ++to;
-      }
+    for (int e = 0; e < S::N; ++e) {
+      if (!(bits >> e & 1)) continue;
+      const uint32_t i = (uint32_t)(chunk * kChunk + S::at(e));
+      if (to < kMaxList)
+        pivots[to] = (uint64_t)logit_key(x[e]) << 32 | (uint32_t)~i;
+      ++to;
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) sum += shfl64(sum, ln ^ o);
-    if (ln == 0) st_agent(a.chunk_mass + (int64_t)r * a.chunks + chunk, sum);
-  }
-  if (!last_to_finish(a.ticket + r, wg, a.epoch, flag)) return;
-  // ---- the row's last workgroup
-  const unsigned count = ld_agent(&a.wide[r].pivots);
-  uint64_t cut = 0;
-  bool done = !lost;
-  if (wide.mode != kWideAll && done) {
-    done = count <= kMaxList;
-    if (done) {
-      auto mass_of = [&](uint64_t w) {
-        return fixed(
-            weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t), a);
-      };
-      auto bin_of = [&](uint64_t w) {  // the bin in 2048 parts
-        const float x = key_logit((uint32_t)(w >> 32));
-        const double d = ((double)top - (double)x) * c - pivot;
-        return d > 0.0 ? (int)fmin(d * kSampleBins, kSampleBins - 1.0) : 0;
-      };
-      for (int i = tid; i < (int)count; i += kSampleThreads)
-        s.words[i] = ld_agent(pivots + i);
-      __syncthreads();
-      const uint64_t goal = wide.goal - above;
-      cut = find_cut((int)count, wide.mode != kWideCount, goal, mass_of, bin_of,
-                     s).word;
-      done = cut != 0;
-      // Masses of the chunks, and of the bin's words in them.
-      if (done) {
-        s.chunk_mass[tid] = 0;
-        __syncthreads();
-#pragma unroll 1
-        for (int i = tid; i < (int)count; i += kSampleThreads) {
-          const uint64_t w = s.words[i];
-          if (w < cut) continue;
-          const double x =
-              weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
-          if (x >= want.min_w)
-            atomicAdd((unsigned long long*)
-                          &s.chunk_mass[(uint32_t) ~(uint32_t)w / kChunk],
-                      (unsigned long long)fixed(x, a));
-        }
-        __syncthreads();
-      }
-    }
-  }
-  if (!done) {
-    __syncthreads();
-    sample_row<T>(a, row_i, s);
-    return;
-  }
-  uint64_t mass =
-      tid < a.chunks ? ld_agent(a.chunk_mass + (int64_t)r * a.chunks + tid) : 0;
-  if (cut) mass += s.chunk_mass[tid];
-  uint64_t before, goal, total;
-  const int chunk_i =
-      find_chunk(mass, want.u, s, &before, &goal, &total);
-  if (tid >= kWave) return;
-  // Lane l takes logits 16 l .. of the chunk.
-  uint64_t upto = before;
-  const int64_t i0 = (int64_t)chunk_i * kChunk + ln * 16;
-  uint64_t m[16], sum = 0;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float y[kSampleVec];
-    read_logits<T>(row, i0 + j * kSampleVec, a.cols, y);
-#pragma unroll
-    for (int e = 0; e < kSampleVec; ++e) {
-      const int64_t i = i0 + j * kSampleVec + e;
-      const uint64_t word =
-          (uint64_t)logit_key(y[e]) << 32 | (uint32_t) ~(uint32_t)i;
-      const double w = weight_of(y[e], top, want.inv_t);
-      // (-infinity past the end has no weight)
-      m[j * kSampleVec + e] =
-          word >= cut && w >= want.min_w ? fixed(w, a) : 0;
-      sum += m[j * kSampleVec + e];
-    }
-  }
-  upto += wave_scan64(sum) - sum;
-  if (upto <= goal && goal < upto + sum) {
-    int at = 0;
-    bool past = false;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      upto += m[e];
-      if (!past) at = e;
-      past = past || upto > goal;
-    }
-    a.tokens[row_i] = i0 + at;
-    a.logprobs[row_i] =
-        (float)log(weight_of(read_logit<T>(row, i0 + at), top, want.inv_t) /
-                   ((double)total / a.unit));
   }
 }
 
+// A wide row's end: the last of the bin's logits that is kept, the chunk where
+// u times the kept mass lies, and the token in it.  False: the row is done over.
 template <int T>
-__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
+__device__ __forceinline__ bool finish_wide(const SampleParams& a, int r,
+                                            SampleLds& s) {
+  const int tid = threadIdx.x;
+  const WideRow wide = a.wide[r];
+  if (wide.mode == kWideRow) return false;
+  const int64_t row_i = a.row0 + r;
+  const Wanted want = wanted(a, row_i);
+  const float top = key_logit(wide.top);
+  const double c = kWidePerBit * want.inv_t;
+  const Pivot pivot = find_pivot(a, r, wide, s);
+  uint64_t mass =
+      tid < a.chunks ? a.chunk_mass[(int64_t)r * a.chunks + tid] : 0;
+  uint64_t cut = 0;
+  auto word_weight = [&](uint64_t w) {
+    return weight_of(key_logit((uint32_t)(w >> 32)), top, want.inv_t);
+  };
+  if (wide.mode != kWideAll) {
+    const int count = (int)wide.pivots;
+    if (pivot.bin == kWideBins || wide.pivots > (uint32_t)kMaxList)
+      return false;
+    const uint64_t* const pivots = a.pivots + (int64_t)r * kMaxList;
+    for (int i = tid; i < count; i += kSampleThreads) s.words[i] = pivots[i];
+    __syncthreads();
+    auto mass_of = [&](uint64_t w) { return fixed(word_weight(w), a); };
+    auto bin_of = [&](uint64_t w) {  // the bin in 2048 parts
+      const float x = key_logit((uint32_t)(w >> 32));
+      const double d = ((double)top - (double)x) * c - pivot.bin;
+      return d > 0.0 ? (int)fmin(d * kSampleBins, kSampleBins - 1.0) : 0;
+    };
+    cut = find_cut(count, wide.mode != kWideCount, wide.goal - pivot.above,
+                   mass_of, bin_of, s)
+              .word;
+    if (cut == 0) return false;
+    // Masses of the bin's words in their chunks.
+    s.chunk_mass[tid] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int i = tid; i < count; i += kSampleThreads) {
+      const uint64_t w = s.words[i];
+      if (w < cut) continue;
+      const double x = word_weight(w);
+      if (x >= want.min_w)
+        atomicAdd((unsigned long long*)
+                      &s.chunk_mass[(uint32_t) ~(uint32_t)w / kChunk],
+                  (unsigned long long)fixed(x, a));
+    }
+    __syncthreads();
+    mass += s.chunk_mass[tid];
+  }
+  uint64_t before, goal, total;
+  const int chunk = find_chunk(mass, want.u, s, &before, &goal, &total);
+  // A logit a thread.  (-infinity past the end has no weight.)
+  const int64_t i = (int64_t)chunk * kChunk + tid;
+  const float x = i < a.cols ? read_logit<T>(a.x + row_i * a.ld, i) : -INFINITY;
+  const uint64_t word = (uint64_t)logit_key(x) << 32 | (uint32_t) ~(uint32_t)i;
+  const double w = weight_of(x, top, want.inv_t);
+  const uint64_t m = word >= cut && w >= want.min_w ? fixed(w, a) : 0;
+  uint64_t all;
+  before += scan_block(m, s, &all);
+  if (before <= goal && goal < before + m) {
+    a.tokens[row_i] = i;
+    a.logprobs[row_i] = (float)log(w / ((double)total / a.unit));
+  }
+  return true;
+}
+
+template <int T>
+__global__ __launch_bounds__(kSampleThreads) void sample_last_kernel(
     SampleParams a) {
   __shared__ SampleLds s;
-  __shared__ int flag;
-  const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
-  const int tasks = (int)a.wide_list[0] * wg;
-  for (int task = (int)blockIdx.x; task < tasks; task += (int)gridDim.x) {
-    wide_part<T>(a, (int)a.wide_list[1 + task / wg], task % wg, wg, s, &flag);
+  const int rows = (int)a.wide_list[0];
+  for (int i = (int)blockIdx.x; i < rows; i += (int)gridDim.x) {
+    const int r = (int)a.wide_list[1 + i];
+    if (!finish_wide<T>(a, r, s)) {
+      __syncthreads();
+      sample_row<T>(a, a.row0 + r, s);
+    }
     __syncthreads();
   }
 }
