@@ -191,6 +191,15 @@ __device__ __forceinline__ double exp2_neg(double y) {
   return ldexp(s, (int)n);
 }
 
+// ln r, 0 < r <= 1, for float32: y from the instruction, which is some 2^-20
+// off, and the series of ln (r / e^y) as far as it takes.
+__device__ __forceinline__ float ln_of(double r) {
+  double y = (double)__builtin_amdgcn_logf((float)r);
+  y = y < 0.0 ? y : 0.0;
+  const double d = r / exp2_neg(y) - 1.0;
+  return (float)fma(y, 0.693147180559945309417, d - 0.5 * d * d);
+}
+
 // Weight of a logit next to the row's largest, `top`; inv_t is log2 e / T.
 __device__ __forceinline__ double weight_of(float x, float top, double inv_t) {
   // (next to an infinite one: itself 1, and the others -infinity times inv_t)
@@ -260,14 +269,13 @@ struct ScanLds {
 struct SampleLds : ScanLds {
   union {
     struct {  // passes over the row
-      uint64_t mass[kSampleBins];
-      uint32_t count[kSampleBins];
+      uint64_t mass[kSampleBins];  // or counts
       uint64_t tile_mass[kMaxTiles];
       int32_t tile_ties[kMaxTiles];
     };
     struct {  // words of a list
       uint64_t words[kMaxList];
-      uint64_t some[kMaxList];  // those of one bin
+      uint64_t some[2][kMaxList];  // those of one bin, in turn
       uint64_t bin_mass[kSampleBins];
       uint32_t bin_count[kSampleBins];
       uint64_t chunk_mass[kMaxChunks];
@@ -362,14 +370,16 @@ struct Prefix {
   uint64_t above;  // count or mass of those above the key
 };
 
-// The shortest prefix within `in` whose count (MASS false) or mass reaches
-// `goal`, by digits of the key from the top: 11, 11 and 10 bits.
-template <int T, bool MASS>
-__device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
-                              double inv_t, const Prefix& in, uint64_t goal,
-                              SampleLds& s) {
+// The shortest prefix within `in` whose count or mass reaches `goal`, by digits of the key from the top: 11, 11 and 10 bits.
+template <int T>
+__device__ __forceinline__ Prefix find_prefix(const SampleParams& a,
+                                              const char* row, float top,
+                                              double inv_t, bool by_mass,
+                                              const Prefix& in, uint64_t goal,
+                                              SampleLds& s) {
   Prefix out = {0, 0, 0};
   const int tid = threadIdx.x;
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bits = pass == 2 ? 10 : 11;
@@ -378,7 +388,6 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
       return high == 32 || k >> high == out.key >> high;
     };
     for (int i = tid; i < kSampleBins; i += kSampleThreads) {
-      s.count[i] = 0;
       s.mass[i] = 0;
     }
     __syncthreads();
@@ -388,17 +397,17 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
 #pragma unroll
       for (int e = 0; e < kSampleVec; ++e) {
         const uint32_t k = logit_key(x[e]);
-        if (i + e >= a.cols || !inside(k) || (MASS && k <= in.key)) continue;
-        const int bin = (int)(k >> shift & ((1u << bits) - 1));
-        if constexpr (MASS)
-          atomicAdd((unsigned long long*)&s.mass[bin],
-                    fixed(weight_of(x[e], top, inv_t), a));
-        else
-          atomicAdd(&s.count[bin], 1u);
+        if (i + e < a.cols && inside(k) && !(by_mass && k <= in.key))
+          atomicAdd(
+              (unsigned long long*)&s.mass[k >> shift & ((1u << bits) - 1)],
+              by_mass
+                  ? (unsigned long long)fixed(weight_of(x[e], top, inv_t), a)
+                  : 1ull);
+        __builtin_amdgcn_sched_barrier(0);  // one at a time: fewer registers
       }
     }
     // of the ties at the bound of `in` only its own count
-    if (MASS && tid == 0 && in.ties > 0 && inside(in.key))
+    if (by_mass && tid == 0 && in.ties > 0 && inside(in.key))
       atomicAdd((unsigned long long*)
                     &s.mass[in.key >> shift & ((1u << bits) - 1)],
                 (uint64_t)in.ties *
@@ -406,8 +415,7 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
     __syncthreads();
     // Thread i takes bins 2 i and 2 i + 1 counted from the top.
     const int b = kSampleBins - 1 - 2 * tid;
-    const uint64_t c0 = MASS ? s.mass[b] : s.count[b];
-    const uint64_t c1 = MASS ? s.mass[b - 1] : s.count[b - 1];
+    const uint64_t c0 = s.mass[b], c1 = s.mass[b - 1];
     uint64_t all;
     const uint64_t before = out.above + scan_block(c0 + c1, s, &all);
     if (before < goal && goal <= before + c0) {
@@ -423,14 +431,14 @@ __device__ Prefix find_prefix(const SampleParams& a, const char* row, float top,
     __syncthreads();
   }
   uint64_t one = 1;
-  if (MASS) one = fixed(weight_of(key_logit(out.key), top, inv_t), a);
+  if (by_mass) one = fixed(weight_of(key_logit(out.key), top, inv_t), a);
   out.ties = (int64_t)((goal - out.above + one - 1) / one);
   return out;
 }
 
 // A row by as many passes over it as it takes, in one workgroup.
 template <int T>
-__device__ __noinline__ void sample_row(const SampleParams& a, int64_t row_i,
+__device__ __forceinline__ void sample_row(const SampleParams& a, int64_t row_i,
                            SampleLds& s) {
   const int tid = threadIdx.x;
   const char* row = a.x + row_i * a.ld;
@@ -459,26 +467,30 @@ __device__ __noinline__ void sample_row(const SampleParams& a, int64_t row_i,
   }
   // ---- the prefixes
   Prefix in = {0, 0, 0};  // every key is above 0: all
-  if (want.k > 0)
-    in = find_prefix<T, false>(a, row, top, want.inv_t, in, (uint64_t)want.k,
-                               s);
-  if (want.p < 1.0) {
-    uint64_t mine = 0, all = 0;
-    for (int64_t i = (int64_t)tid * kSampleVec; i < a.cols; i += kSampleTile) {
-      float x[kSampleVec];
-      read_logits<T>(row, i, a.cols, x);
+#pragma unroll 1
+  for (int step = want.k > 0 ? 0 : 1; step < (want.p < 1.0 ? 2 : 1); ++step) {
+    uint64_t goal = (uint64_t)want.k;
+    if (step == 1) {
+      uint64_t mine = 0, all = 0;
+      for (int64_t i = (int64_t)tid * kSampleVec; i < a.cols;
+           i += kSampleTile) {
+        float x[kSampleVec];
+        read_logits<T>(row, i, a.cols, x);
 #pragma unroll
-      for (int e = 0; e < kSampleVec; ++e)
-        if (logit_key(x[e]) > in.key)
-          mine += fixed(weight_of(x[e], top, want.inv_t), a);
+        for (int e = 0; e < kSampleVec; ++e) {
+          if (logit_key(x[e]) > in.key)
+            mine += fixed(weight_of(x[e], top, want.inv_t), a);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      scan_block(mine, s, &all);
+      all += (uint64_t)in.ties *
+             fixed(weight_of(key_logit(in.key), top, want.inv_t), a);
+      const double part = ceil(want.p * (double)all);
+      goal = part < 1.0 ? 1 : (uint64_t)part;
+      goal = goal < all ? goal : all;
     }
-    scan_block(mine, s, &all);
-    all += (uint64_t)in.ties *
-           fixed(weight_of(key_logit(in.key), top, want.inv_t), a);
-    const double part = ceil(want.p * (double)all);
-    const uint64_t goal = part < 1.0 ? 1 : (uint64_t)part;
-    in = find_prefix<T, true>(a, row, top, want.inv_t, in,
-                              goal < all ? goal : all, s);
+    in = find_prefix<T>(a, row, top, want.inv_t, step == 1, in, goal, s);
   }
   // ---- in the order of the row
   // Thread t of a tile has its elements 8 t .. 8 t + 7.
@@ -506,6 +518,7 @@ __device__ __noinline__ void sample_row(const SampleParams& a, int64_t row_i,
         if (w >= want.min_w) m[e] = fixed(w, a);
       }
       sum += m[e];
+      __builtin_amdgcn_sched_barrier(0);
     }
     return sum;
   };
@@ -539,7 +552,7 @@ __device__ __noinline__ void sample_row(const SampleParams& a, int64_t row_i,
     const int64_t i = (int64_t)t * kSampleTile + (int64_t)tid * kSampleVec + e;
     a.tokens[row_i] = i;
     a.logprobs[row_i] =
-        (float)log(weight_of(read_logit<T>(row, i), top, want.inv_t) /
+        ln_of(weight_of(read_logit<T>(row, i), top, want.inv_t) /
                    ((double)total / a.unit));
   }
 }
@@ -697,8 +710,6 @@ __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
   }
 }
 
-constexpr int kHeld = kMaxList / kSampleThreads;  // words of a thread
-
 // The bin of a logit: factors of 2 from the largest weight, kWidePerBit bins
 // to one.
 __device__ __forceinline__ int wide_bin(float x, float top, double c) {
@@ -734,7 +745,7 @@ __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
                      : kSampleBins - 1 -
                            (int)((w >> shift) & (uint64_t)(kSampleBins - 1));
   };
-  for (;;) {
+  for (int level = 0;; ++level) {
     for (int i = tid; i < kSampleBins; i += kSampleThreads) {
       s.bin_mass[i] = 0;
       s.bin_count[i] = 0;
@@ -785,21 +796,15 @@ __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
     cb = s.found[1];
     mb = s.found[2];
     const uint32_t count = s.bin_count[pivot];
-    // The bin's words, in any order.  (In the list of a bin's words itself
-    // they move once all threads have read it: at most four each.)
-    uint64_t w[kHeld];
-#pragma unroll
-    for (int e = 0; e < kHeld; ++e) {
-      const int i = e * kSampleThreads + tid;
-      w[e] = i < n ? from[i] : 0;
+    // The bin's words, in any order.
+    uint64_t* const to = s.some[level & 1];
+#pragma unroll 1
+    for (int i = tid; i < n; i += kSampleThreads) {
+      const uint64_t w = from[i];
+      if (w != 0 && bin(w) == pivot) to[atomicAdd(&s.gathered, 1u)] = w;
     }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < kHeld; ++e)
-      if (w[e] != 0 && bin(w[e]) == pivot)
-        s.some[atomicAdd(&s.gathered, 1u)] = w[e];
     n = (int)count;
-    from = s.some;
+    from = to;
     __syncthreads();
     if (n <= kWave) break;
     // The first bit in which the words differ (some do).
@@ -814,7 +819,7 @@ __device__ __forceinline__ Cut find_cut(int n, bool by_mass, uint64_t goal,
   // One wave: what lies before each word, word by word.
   if (tid < kWave) {
     if (tid == 0) s.found[0] = 0;
-    const uint64_t w = tid < n ? s.some[tid] : 0;
+    const uint64_t w = tid < n ? from[tid] : 0;
     const uint64_t m = w ? mass_of(w) : 0;
     uint64_t c = cb + 1, before = mb;
     for (int i = 0; i < n; ++i) {
@@ -939,7 +944,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
         first_or_last(w > 0.0 && (want.greedy || upto > goal), w > 0.0, s);
     if (tid != who) return;
     a.tokens[row_i] = i;
-    a.logprobs[row_i] = want.greedy ? 0.0f : (float)log(w / total);
+    a.logprobs[row_i] = want.greedy ? 0.0f : ln_of(w / total);
     return;
   }
   uint64_t listed;
@@ -1043,7 +1048,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   before += wave_scan64(m) - m;
   if (before <= goal && goal < before + m) {
     a.tokens[row_i] = (int64_t)(uint32_t) ~(uint32_t)w;
-    a.logprobs[row_i] = (float)log(x / ((double)kept / a.unit));
+    a.logprobs[row_i] = ln_of(x / ((double)kept / a.unit));
   }
 }
 
@@ -1254,7 +1259,7 @@ __device__ __forceinline__ bool finish_wide(const SampleParams& a, int r,
   before += scan_block(m, s, &all);
   if (before <= goal && goal < before + m) {
     a.tokens[row_i] = i;
-    a.logprobs[row_i] = (float)log(w / ((double)total / a.unit));
+    a.logprobs[row_i] = ln_of(w / ((double)total / a.unit));
   }
   return true;
 }
@@ -1266,10 +1271,16 @@ __global__ __launch_bounds__(kSampleThreads) void sample_last_kernel(
   const int rows = (int)a.wide_list[0];
   for (int i = (int)blockIdx.x; i < rows; i += (int)gridDim.x) {
     const int r = (int)a.wide_list[1 + i];
-    if (!finish_wide<T>(a, r, s)) {
-      __syncthreads();
-      sample_row<T>(a, a.row0 + r, s);
-    }
+    const bool done = finish_wide<T>(a, r, s);
+    __syncthreads();
+    if (!done && threadIdx.x == 0) a.wide[r].mode = kWideRow;
+  }
+  __syncthreads();
+  // (apart from the others, which need other registers)
+  for (int i = (int)blockIdx.x; i < rows; i += (int)gridDim.x) {
+    const int r = (int)a.wide_list[1 + i];
+    if (a.wide[r].mode != kWideRow) continue;
+    sample_row<T>(a, a.row0 + r, s);
     __syncthreads();
   }
 }
