@@ -107,7 +107,7 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
   if (chunks > kMaxChunks)
     return launch(fn.row, dim3((unsigned)rows), kSampleThreads, p, st);
   p.chunks = (int32_t)chunks;
-  // Some 2500 words a row, which one workgroup sorts in about 3 us.
+  // Some 3000 words a row at most.
   const int64_t rank = kMaxList * 5 / 8 / chunks;
   p.rank = (int32_t)(rank < 2 ? 2 : rank > 32 ? 32 : rank);
   // Batches of rows share the workspace, which stays below 64 MB.
@@ -144,12 +144,13 @@ extern "C" int sample_logits(const void* logits, int32_t dtype, int64_t rows,
                 kBlock, p, st);
     if (rc == LIBTOPK_OK)
       rc = launch(fn.finish, dim3((unsigned)m), kSampleThreads, p, st);
-    // The parts of whatever rows are wide, a workgroup a unit.
-    const unsigned grid = (unsigned)(m * parts < units ? m * parts : units);
+    // The parts of whatever rows are wide, two workgroups a unit.
+    const int64_t most = 2 * (int64_t)units;
+    const unsigned grid = (unsigned)(m * parts < most ? m * parts : most);
     if (rc == LIBTOPK_OK && wide)
-      rc = launch(fn.bins, dim3(grid), kSampleThreads, p, st);
+      rc = launch(fn.bins, dim3(grid), kWideThreads, p, st);
     if (rc == LIBTOPK_OK && wide)
-      rc = launch(fn.wide, dim3(grid), kSampleThreads, p, st);
+      rc = launch(fn.wide, dim3(grid), kWideThreads, p, st);
     if (rc == LIBTOPK_OK && wide)
       rc = launch(fn.last, dim3((unsigned)(m < units ? m : units)),
                   kSampleThreads, p, st);

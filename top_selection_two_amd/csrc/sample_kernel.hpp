@@ -73,7 +73,8 @@ struct WideRow {
 };
 constexpr int kWideBins = 2048;
 constexpr double kWidePerBit = 44.0;  // bins of a factor of 2: 2^-46 in all
-constexpr int kWideChunks = kSampleThreads / kWave;  // of a workgroup
+constexpr int kWideThreads = 512;
+constexpr int kWideChunks = kWideThreads / kWave;  // of a workgroup
 
 constexpr int kChunk = 1024;     // logits of a wave
 constexpr int kChunkList = 64;   // listed of them at most
@@ -169,24 +170,23 @@ __device__ __forceinline__ void read_logits(const char* row, int64_t i,
   }
 }
 
-// 2^y for y <= 0: 2^n 2^f with |f| <= 1/2 and the series of 2^f in f ln 2 to
-// the 11th power, which leaves (ln 2 / 2)^12 / 12! = 6e-15.  (Its coefficients
-// are (ln 2)^i / i!.)
+// 2^y for y <= 0: 2^n 2^f with |f| <= 1/2, and 2^f = 1 + f g(f) with g the
+// polynomial that meets (2^f - 1) / f at the ten zeros of a Chebyshev
+// polynomial: 6e-16 of 2^f are left, and 2^0 is 1.
 __device__ __forceinline__ double exp2_neg(double y) {
   // Below 2^-1100 nothing is left; a NaN (0 times infinity) is nothing too.
   y = fmax(y, -1100.0);
   const double n = rint(y), f = y - n;
-  double s = 4.4455382718708116e-10;
-  s = fma(s, f, 7.0549116208011233e-09);
-  s = fma(s, f, 1.0178086009239699e-07);
-  s = fma(s, f, 1.3215486790144310e-06);
-  s = fma(s, f, 1.5252733804059840e-05);
-  s = fma(s, f, 1.5403530393381610e-04);
-  s = fma(s, f, 1.3333558146428443e-03);
-  s = fma(s, f, 9.6181291076284772e-03);
-  s = fma(s, f, 5.5504108664821580e-02);
-  s = fma(s, f, 2.4022650695910072e-01);
-  s = fma(s, f, 6.9314718055994531e-01);
+  double s = 7.07097786650813825e-09;
+  s = fma(s, f, 1.02059054137655955e-07);
+  s = fma(s, f, 1.32154516332214336e-06);
+  s = fma(s, f, 1.52526729248507372e-05);
+  s = fma(s, f, 1.54035304247765285e-04);
+  s = fma(s, f, 1.33335582007945925e-03);
+  s = fma(s, f, 9.61812910761866528e-03);
+  s = fma(s, f, 5.55041086646516704e-02);
+  s = fma(s, f, 2.40226506959100750e-01);
+  s = fma(s, f, 6.93147180559946174e-01);
   s = fma(s, f, 1.0);
   return ldexp(s, (int)n);
 }
@@ -287,11 +287,13 @@ struct SampleLds : ScanLds {
 // What a workgroup's waves have, in turn: every wave reads all 16 (one a lane)
 // and folds them by moves between lanes, which is less code, and quicker, than
 // a loop over them.
+template <int WAVES = kSampleWaves>
 __device__ __forceinline__ uint64_t wave_item(const uint64_t* x) {
-  return lane() < kSampleWaves ? x[lane()] : 0;
+  return lane() < WAVES ? x[lane()] : 0;
 }
 
 // Exclusive prefix of v over the workgroup's threads, and the total.
+template <int WAVES = kSampleWaves>
 __device__ __forceinline__ uint64_t scan_block(uint64_t v, ScanLds& s,
                                                uint64_t* total) {
   const int wave = uni((int)threadIdx.x / kWave);
@@ -299,8 +301,8 @@ __device__ __forceinline__ uint64_t scan_block(uint64_t v, ScanLds& s,
   __syncthreads();  // the last call's sums have been read
   if (lane() == kWave - 1) s.sums[wave] = incl;
   __syncthreads();
-  const uint64_t all = wave_scan64(wave_item(s.sums));
-  *total = lane64(all, kSampleWaves - 1);
+  const uint64_t all = wave_scan64(wave_item<WAVES>(s.sums));
+  *total = lane64(all, WAVES - 1);
   return (wave ? lane64(all, wave - 1) : 0) + incl - v;
 }
 __device__ __forceinline__ double scan_block(double v, ScanLds& s,
@@ -564,6 +566,10 @@ __device__ __forceinline__ void sample_row(const SampleParams& a, int64_t row_i,
 //   a bound, and the logits from the bound on, at most 64, in the row's order.
 // The bound is the rank-th largest of what the 64 lanes have as their largest,
 // so that the list has some more than `rank`, whatever the numbers are like.
+// (The least of the maxima of 8 or 16 groups of lanes is found in 12 steps
+// instead of the sort's 63, 34 us against 39 for 256 rows of 131072, but varies
+// so much that its largest over the chunks leaves lists too short for a top-k
+// of 500.)
 // Above the largest bound of a row's chunks nothing is missing in its lists:
 // a prefix of the order that ends above it is found there, among at most 4096
 // words.
@@ -1054,13 +1060,13 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
 
 // ---- wide prefixes ----------------------------------------------------------
 // A prefix beyond the lists (a nucleus of tens of thousands) is found in three
-// more launches, two of them over the row by workgroups of 16 chunks.  The first adds up
+// more launches, two of them over the row by workgroups of 8 chunks.  The first adds up
 // the masses (or counts) of the logits in 2048 bins of log2 of their weight;
 // integers, so that their order is nothing.  The second finds the bin in which
 // the goal lies, adds up each chunk's mass above it, and lists the bin's own
 // logits; the third ends the row (finish_wide).
 template <int T>
-__global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
+__global__ __launch_bounds__(kWideThreads) void sample_bins_kernel(
     SampleParams a) {
   const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
   const int tasks = (int)a.wide_list[0] * wg;
@@ -1070,7 +1076,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     const int r = (int)a.wide_list[1 + task / wg];
     const WideRow wide = a.wide[r];
     if (wide.mode != kWideMass && wide.mode != kWideCount) continue;
-    for (int i = tid; i < kWideBins; i += kSampleThreads) bins[i] = 0;
+    for (int i = tid; i < kWideBins; i += kWideThreads) bins[i] = 0;
     __syncthreads();
     const int64_t row_i = a.row0 + r;
     const Wanted want = wanted(a, row_i);
@@ -1096,7 +1102,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_bins_kernel(
     __syncthreads();
     unsigned long long* all =
         (unsigned long long*)(a.bins + (int64_t)r * kWideBins);
-    for (int i = tid; i < kWideBins; i += kSampleThreads)
+    for (int i = tid; i < kWideBins; i += kWideThreads)
       if (bins[i]) atomicAdd(all + i, (unsigned long long)bins[i]);
     __syncthreads();
   }
@@ -1108,12 +1114,13 @@ struct Pivot {
   int bin;
   uint64_t above;  // mass or count
 };
+template <int THREADS>
 __device__ __forceinline__ Pivot find_pivot(const SampleParams& a, int r,
                                             const WideRow& wide, ScanLds& s) {
   Pivot out = {kWideBins, 0};
   if (wide.mode == kWideAll) return out;
   const int tid = threadIdx.x;
-  constexpr int B = kWideBins / kSampleThreads;
+  constexpr int B = kWideBins / THREADS;
   const uint64_t* bins = a.bins + (int64_t)r * kWideBins;
   uint64_t b[B], sum = 0;
 #pragma unroll
@@ -1122,7 +1129,7 @@ __device__ __forceinline__ Pivot find_pivot(const SampleParams& a, int r,
     sum += b[i];
   }
   uint64_t all;
-  uint64_t before = scan_block(sum, s, &all);
+  uint64_t before = scan_block<THREADS / kWave>(sum, s, &all);
   if (tid == 0) s.found[0] = kWideBins;
   __syncthreads();
 #pragma unroll
@@ -1140,7 +1147,7 @@ __device__ __forceinline__ Pivot find_pivot(const SampleParams& a, int r,
 }
 
 template <int T>
-__global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
+__global__ __launch_bounds__(kWideThreads) void sample_wide_kernel(
     SampleParams a) {
   __shared__ ScanLds s;
   const int wg = (a.chunks + kWideChunks - 1) / kWideChunks;
@@ -1155,7 +1162,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_wide_kernel(
     const Wanted want = wanted(a, row_i);
     const float top = key_logit(wide.top);
     const double c = kWidePerBit * want.inv_t;
-    const int pivot = find_pivot(a, r, wide, s).bin;
+    const int pivot = find_pivot<kWideThreads>(a, r, wide, s).bin;
     __syncthreads();
     if (pivot == kWideBins && wide.mode != kWideAll) continue;
     const int chunk = task % wg * kWideChunks + tid / kWave;
@@ -1207,7 +1214,7 @@ __device__ __forceinline__ bool finish_wide(const SampleParams& a, int r,
   const Wanted want = wanted(a, row_i);
   const float top = key_logit(wide.top);
   const double c = kWidePerBit * want.inv_t;
-  const Pivot pivot = find_pivot(a, r, wide, s);
+  const Pivot pivot = find_pivot<kSampleThreads>(a, r, wide, s);
   uint64_t mass =
       tid < a.chunks ? a.chunk_mass[(int64_t)r * a.chunks + tid] : 0;
   uint64_t cut = 0;
