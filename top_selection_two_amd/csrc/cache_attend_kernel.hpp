@@ -249,8 +249,6 @@ struct Attend {
   // wave to a SIMD instead of two, with twice the bytes in flight each.
   static constexpr int WAVES = NC > 4 ? 4 : 8;
   static constexpr int THREADS = WAVES * kWave;
-  // Tiles of a step of a wave.
-  static constexpr int PT = CT == kE2m1 && QT == kBf16 && PG16 ? 2 : 1;
   static constexpr int EB = CT == kE2m1 ? 4 : CT == kE4m3 ? 8 : 16;  // bits
   static constexpr int LE = 128 / EB;  // elements of a 16-byte K load
   static constexpr int KL = (NC * 32 + 4 * LE - 1) / (4 * LE);  // a half
@@ -618,19 +616,13 @@ attend_kernel(AttendParams p) {
       const int32_t t1 = te < tiles ? te : tiles;
       if (t >= t1) continue;
 
-      // A tile on its way: K and V rows (4-bit ones as UV lanes a row have
-      // them), the scales of 4-bit rows as they are loaded (lane l has K's of
-      // slot l, lane 32 + l V's), and the pages of this tile and of the next
-      // one here.
-      struct Tile {
-        v4i kr[2][KL];
-        int vr[A::k4 ? 1 : NB][A::k4 ? 1 : 8][A::k4 ? 1 : VD];
-        v4i vu[A::k4 ? A::VL : 1];
-        unsigned sw[A::k4 ? A::SW : 1];
-        typename A::Ids cur, next;
-      };
-      Tile tile[A::PT];
-      auto load_k = [&](Tile& z, const typename A::Ids& id) {
+      v4i kr[2][KL];
+      int vr[A::k4 ? 1 : NB][A::k4 ? 1 : 8][A::k4 ? 1 : VD];
+      // 4-bit V rows as UV lanes a row have them, and the scales as they are
+      // loaded: lane l has K's of slot l, lane 32 + l V's.
+      v4i vu[A::k4 ? A::VL : 1];
+      unsigned sw[A::k4 ? A::SW : 1];
+      auto load_k = [&](const typename A::Ids& id) {
 #pragma unroll
         for (int tt = 0; tt < 2; ++tt) {
           const int32_t pg = page_ok(id.id[tt], c.pages) ? id.id[tt] : 0;
@@ -644,7 +636,7 @@ attend_kernel(AttendParams p) {
           for (int k = 0; k < KL; ++k) {
             const int at = k * 64 + q * 16;
             const bool in = A::last_chunk(k) < A::SHORT || at < c.row_bytes;
-            z.kr[tt][k] = ld_once<v4i>(row + (in ? at : 0));
+            kr[tt][k] = ld_once<v4i>(row + (in ? at : 0));
           }
         }
         if constexpr (A::k4) {
@@ -660,16 +652,16 @@ attend_kernel(AttendParams p) {
           if constexpr (NC == 2 || NC == 3) {
 #pragma unroll
             for (int i = 0; i < A::SW; ++i)
-              z.sw[i] = ld_once<uint8_t>(sc + (i < c.blocks ? i : 0));
+              sw[i] = ld_once<uint8_t>(sc + (i < c.blocks ? i : 0));
           } else {
-            z.sw[0] = __builtin_nontemporal_load((const u32u*)sc);
+            sw[0] = __builtin_nontemporal_load((const u32u*)sc);
             if constexpr (NC > 4)
-              z.sw[1] =
+              sw[1] =
                   __builtin_nontemporal_load((const u32u*)(sc + c.blocks - 4));
           }
         }
       };
-      auto load_v = [&](Tile& z, const typename A::Ids& id) {
+      auto load_v = [&](const typename A::Ids& id) {
         if constexpr (A::k4) {
 #pragma unroll
           for (int i = 0; i < A::VL; ++i) {
@@ -683,7 +675,7 @@ attend_kernel(AttendParams p) {
                       : (half ? id.place[1] : id.place[0]) + slot % 16;
             const int32_t pg = page_ok(id1, c.pages) ? id1 : 0;
             const int at = ln % A::UV * 16;
-            z.vu[i] = ld_once<v4i>(vh + row_offset(c.vs, pg, 0, pl) +
+            vu[i] = ld_once<v4i>(vh + row_offset(c.vs, pg, 0, pl) +
                                    (at < c.row_bytes ? at : 0));
           }
           return;
@@ -706,29 +698,23 @@ attend_kernel(AttendParams p) {
             if constexpr (VD == 4) {
               const v4i x = ld_once<v4i>(src);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) z.vr[nb][j][e] = x[e];
+              for (int e = 0; e < 4; ++e) vr[nb][j][e] = x[e];
             } else if constexpr (VD == 2) {
               const v2i x = ld_once<v2i>(src);
-              z.vr[nb][j][0] = x[0];
-              z.vr[nb][j][1] = x[1];
+              vr[nb][j][0] = x[0];
+              vr[nb][j][1] = x[1];
             } else {
-              z.vr[nb][j][0] = ld_once<int>(src);
+              vr[nb][j][0] = ld_once<int>(src);
             }
           }
         }
       };
 
-#pragma unroll
-      for (int i = 0; i < A::PT; ++i) {
-        Tile& z = tile[i];
-        z.cur = find_tile<A, PG16>(c, table, t + i * ts, len, q, n);
-        load_k(z, z.cur);
-        load_v(z, z.cur);
-      }
-#pragma unroll
-      for (int i = 0; i < A::PT; ++i)
-        tile[i].next = find_tile<A, PG16>(c, table, t + (A::PT + i) * ts,
-                                          len, q, n);
+      typename A::Ids cur = find_tile<A, PG16>(c, table, t, len, q, n);
+      load_k(cur);
+      load_v(cur);
+      typename A::Ids next =
+          find_tile<A, PG16>(c, table, t + ts, len, q, n);
       // Elements past the row's end are 0 in K and in q (here, where the
       // first tile is on its way).
 #pragma unroll
@@ -754,54 +740,36 @@ attend_kernel(AttendParams p) {
         }
       }
 
-      // Tiles t + u ts, u < PT; `more` come after them.
-      constexpr int PT = A::PT;
       auto step = [&](auto more) {
-        // Scales of 4-bit rows: four a dword.
-        unsigned sc[PT][A::SCALES];
+        // Scales of 4-bit rows, four a dword: a lane's slot's, and those of its
+        // K blocks' slots.
+        unsigned kw[A::k4 ? 2 : 1][A::SCALES];
+        unsigned sc[A::SCALES];
         if constexpr (A::k4) {
-#pragma unroll
-          for (int u = 0; u < PT; ++u) {
-            const unsigned* const sw = tile[u].sw;
-            sc[u][0] = NC == 2   ? sw[0] | sw[A::SW > 1] << 8
-                       : NC == 3 ? sw[0] | sw[A::SW > 1] << 8 |
-                                       sw[A::SW > 2 ? 2 : 0] << 16
-                                 : sw[0];
-            // the last four; block 4 first
-            if constexpr (NC > 4) sc[u][1] = sw[1] >> (8 * (8 - c.blocks));
-          }
-        }
-        // Those of this lane's K blocks and V slots, asked for well before they
-        // are needed.
-        unsigned kw[A::k4 ? 2 * PT : 1][A::SCALES];
-        unsigned vw[A::k4 ? 8 * PT : 1][A::SCALES];
-        if constexpr (A::k4) {
+          sc[0] = NC == 2   ? sw[0] | sw[A::SW > 1] << 8
+                  : NC == 3 ? sw[0] | sw[A::SW > 1] << 8 |
+                                  sw[A::SW > 2 ? 2 : 0] << 16
+                            : sw[0];
+          // the last four; block 4 first
+          if constexpr (NC > 4) sc[1] = sw[A::SW > 1] >> (8 * (8 - c.blocks));
 #pragma unroll
           for (int i = 0; i < A::SCALES; ++i) {
 #pragma unroll
-            for (int ut = 0; ut < 2 * PT; ++ut)
-              kw[ut][i] = (unsigned)__shfl((int)sc[ut / 2][i],
-                                           ut % 2 * 16 + n, kWave);
-#pragma unroll
-            for (int uj = 0; uj < 8 * PT; ++uj)
-              vw[uj][i] = (unsigned)__shfl(
-                  (int)sc[uj / 8][i], 32 + uj % 8 / 4 * 16 + q * 4 + uj % 4,
-                  kWave);
+            for (int tt = 0; tt < 2; ++tt)
+              kw[tt][i] = (unsigned)__shfl((int)sc[i], tt * 16 + n, kWave);
           }
         }
-        // Scores of 2 x 16 slots each.
-        f32x4 s[2 * PT];
+        // Scores of 2 x 16 slots.
+        f32x4 s[2];
 #pragma unroll
-        for (int ut = 0; ut < 2 * PT; ++ut) {
-          const int tt = ut % 2;
-          const Tile& z = tile[ut / 2];
-          s[ut] = f32x4{0, 0, 0, 0};
+        for (int tt = 0; tt < 2; ++tt) {
+          s[tt] = f32x4{0, 0, 0, 0};
 #pragma unroll
           for (int k = 0; k < KL; ++k) {
-            v4i x = z.kr[tt][k];
+            v4i x = kr[tt][k];
             // (a lane's 32 elements are a block)
             const int ksc =
-                A::k4 ? (int)(kw[ut][k % A::SCALES] >> (8 * q) & 255u) : 0;
+                A::k4 ? (int)(kw[tt][k % A::SCALES] >> (8 * q) & 255u) : 0;
             if (A::last_chunk(k) >= A::SHORT) {
               const bool in = k * 64 + q * 16 < c.row_bytes;
 #pragma unroll
@@ -813,10 +781,10 @@ attend_kernel(AttendParams p) {
                 Frag a;
                 widen8(x[f], ksc << 23, a.d);
                 if constexpr (A::kTwoParts) {
-                  s[ut] = mma<kBf16>(a, qh[4 * k + f], s[ut]);
-                  s[ut] = mma<kBf16>(a, ql[4 * k + f], s[ut]);
+                  s[tt] = mma<kBf16>(a, qh[4 * k + f], s[tt]);
+                  s[tt] = mma<kBf16>(a, ql[4 * k + f], s[tt]);
                 } else {
-                  s[ut] = mma<kBf16>(a, qf[4 * k + f], s[ut]);
+                  s[tt] = mma<kBf16>(a, qf[4 * k + f], s[tt]);
                 }
               }
             } else if constexpr (CT == kE4m3) {
@@ -826,124 +794,110 @@ attend_kernel(AttendParams p) {
                                  widen2<QT, true>(x[2 * f]),
                                  widen2<QT, false>(x[2 * f + 1]),
                                  widen2<QT, true>(x[2 * f + 1])}};
-                s[ut] = mma<QT>(a, qf[2 * k + f], s[ut]);
+                s[tt] = mma<QT>(a, qf[2 * k + f], s[tt]);
               }
             } else {
-              s[ut] = mma<QT>(Frag{{x[0], x[1], x[2], x[3]}}, qf[k], s[ut]);
+              s[tt] = mma<QT>(Frag{{x[0], x[1], x[2], x[3]}}, qf[k], s[tt]);
             }
           }
         }
         // The next tile's K goes on its way, then the page numbers of the
         // tile after it: the wait for these, next time, leaves the V loads
         // behind them in flight.
-        typename A::Ids after[PT];
+        typename A::Ids after;
         sched_fence();
         if constexpr (decltype(more)::value) {
-#pragma unroll
-          for (int u = 0; u < PT; ++u) load_k(tile[u], tile[u].next);
-#pragma unroll
-          for (int u = 0; u < PT; ++u)
-            after[u] = find_tile<A, PG16>(c, table, t + (2 * PT + u) * ts, len,
-                                          q, n);
+          load_k(next);
+          after = find_tile<A, PG16>(c, table, t + 2 * ts, len, q, n);
         }
         sched_fence();
         // 4-bit V rows change lanes: a lane's VE elements of 8 slots.  Row
         // 4 i + q of LDS is slot 4 q + i of a half, so that the four groups of
         // lanes read neighbouring rows.  LDS keeps a wave's accesses in order;
-        // the compiler, which sees one lane's alone, has to be told.
-        auto keep_order = [] { asm volatile("" ::: "memory"); };
-        int vd[A::k4 ? PT : 1][A::k4 ? NB : 1][A::k4 ? 8 : 1];
+        // the compiler, which sees one lane's alone, has to be told (and is by
+        // the fences, too, which keep the next tile's loads here).
+        int vd[A::k4 ? NB : 1][A::k4 ? 8 : 1];
+        unsigned vw[A::k4 ? 8 : 1][A::SCALES];
         if constexpr (A::k4) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < A::SCALES; ++i)
+              vw[j][i] = (unsigned)__shfl(
+                  (int)sc[i], 32 + j / 4 * 16 + q * 4 + j % 4, kWave);
           char* const st = (char*)(join + wave * p.lds_rows * COLS);
 #pragma unroll
-          for (int u = 0; u < PT; ++u) {
+          for (int i = 0; i < A::VL; ++i) {
+            const int slot = i * A::VROWS + ln / A::UV;
+            const int r = slot / 16 * 16 + slot % 4 * 4 + slot % 16 / 4;
+            const int at = ln % A::UV * 16;
+            if (at < c.row_bytes)
+              *(v4i_any*)(st + r * c.row_bytes + at) = vu[i];
+          }
+          asm volatile("" ::: "memory");
 #pragma unroll
-            for (int i = 0; i < A::VL; ++i) {
-              const int slot = i * A::VROWS + ln / A::UV;
-              const int r = slot / 16 * 16 + slot % 4 * 4 + slot % 16 / 4;
-              const int at = ln % A::UV * 16;
-              if (at < c.row_bytes)
-                *(v4i_any*)(st + r * c.row_bytes + at) = tile[u].vu[i];
+          for (int j = 0; j < 8; ++j) {
+            const char* const row =
+                st + (j / 4 * 16 + j % 4 * 4 + q) * c.row_bytes;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              const int col = (nb * 16 + n) * VE / 2;
+              const char* const src = row + (col < c.row_bytes ? col : 0);
+              if constexpr (VE == 8)
+                vd[nb][j] = *(const int_any*)src;
+              else
+                vd[nb][j] = *(const u16_any*)src;
             }
-            keep_order();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const char* const row =
-                  st + (j / 4 * 16 + j % 4 * 4 + q) * c.row_bytes;
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb) {
-                const int col = (nb * 16 + n) * VE / 2;
-                const char* const src = row + (col < c.row_bytes ? col : 0);
-                if constexpr (VE == 8)
-                  vd[u][nb][j] = *(const int_any*)src;
-                else
-                  vd[u][nb][j] = *(const u16_any*)src;
-              }
-            }
-            keep_order();
           }
           sched_fence();
-          if constexpr (decltype(more)::value) {
-#pragma unroll
-            for (int u = 0; u < PT; ++u) load_v(tile[u], tile[u].next);
-          }
+          if constexpr (decltype(more)::value) load_v(next);
           sched_fence();
         }
-        float x[8 * PT];
-        float hi_x = -INFINITY;
-        bool mask[PT][8];
+        // Slots that count.
+        bool ok[8];
+        bool all = (t + 1) * kTileSlots <= len;
+        uint64_t lost[2] = {0, 0};  // slots (by lane n) without a page
+        if constexpr (!PG16 && A::k4) {
 #pragma unroll
-        for (int u = 0; u < PT; ++u) {
-          Tile& z = tile[u];
-          // Slots that count.  (A step's last tiles may lie past the end.)
-          const int32_t tu = t + u * ts;
-          const int32_t end = u == 0 || tu < t1 ? len : 0;
-          bool ok[8];
-          bool all = (tu + 1) * kTileSlots <= end;
-          uint64_t lost[2];  // slots (by lane n) without a page
-          if constexpr (!PG16 && A::k4) {
+          for (int tt = 0; tt < 2; ++tt)
+            lost[tt] = ballot(!page_ok(cur.id[tt], c.pages));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int32_t slot = t * kTileSlots + j / 4 * 16 + q * 4 + j % 4;
+          const bool good =
+              !PG16 && A::k4
+                  ? !(lost[j / 4] >> (q * 4 + j % 4) & 1)
+                  : page_ok(cur.id[PG16 || A::k4 ? j / 4 : j + 2], c.pages);
+          ok[j] = slot < len && good;
+          all = all && good;
+        }
+        // (The scales of 4-bit rows are masked where they are used.)
+        if (!A::k4 && (PG16 ? !all : ballot(!all) != 0)) {
+#pragma unroll
+          for (int j = 0; j < (A::k4 ? 1 : 8); ++j)
+#pragma unroll
+            for (int nb = 0; nb < (A::k4 ? 1 : NB); ++nb)
+#pragma unroll
+              for (int e = 0; e < (A::k4 ? 1 : VD); ++e)
+                vr[nb][j][e] = ok[j] ? vr[nb][j][e] : 0;
+        }
+        float x[8];
+        float hi_x = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = ok[j] ? s[j / 4][j % 4] * scale : -INFINITY;
+          hi_x = fmaxf(hi_x, x[j]);
+        }
+        if (tile_scores) {
+          if (n < queries) {
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt)
-              lost[tt] = ballot(!page_ok(z.cur.id[tt], c.pages));
+              *(f32x4*)(tile_scores + score_at(n, tt * 4 + q)) =
+                  f32x4{x[4 * tt], x[4 * tt + 1], x[4 * tt + 2],
+                        x[4 * tt + 3]};
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int32_t slot = tu * kTileSlots + j / 4 * 16 + q * 4 + j % 4;
-            const bool good =
-                !PG16 && A::k4
-                    ? !(lost[j / 4] >> (q * 4 + j % 4) & 1)
-                    : page_ok(z.cur.id[PG16 || A::k4 ? j / 4 : j + 2], c.pages);
-            ok[j] = slot < end && good;
-            all = all && good;
-          }
-          if constexpr (A::k4) {  // (scales are masked below)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) mask[u][j] = ok[j];
-          } else if (PG16 ? !all : ballot(!all) != 0) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < VD; ++e)
-                  z.vr[nb][j][e] = ok[j] ? z.vr[nb][j][e] : 0;
-          }
-          float* const xu = x + 8 * u;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            xu[j] = ok[j] ? s[2 * u + j / 4][j % 4] * scale : -INFINITY;
-            hi_x = fmaxf(hi_x, xu[j]);
-          }
-          if (tile_scores && (u == 0 || tu < t1)) {
-            if (n < queries) {
-#pragma unroll
-              for (int tt = 0; tt < 2; ++tt)
-                *(f32x4*)(tile_scores + score_at(n, tt * 4 + q)) =
-                    f32x4{xu[4 * tt], xu[4 * tt + 1], xu[4 * tt + 2],
-                          xu[4 * tt + 3]};
-            }
-            tile_scores += ts * tile_floats;
-          }
+          tile_scores += ts * tile_floats;
         }
         // The reference m of a query only moves when a score passes it by
         // 2^8: until then exp2(x - m) stays below 2^8 and nothing has to be
@@ -961,104 +915,95 @@ attend_kernel(AttendParams p) {
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        float w[8 * PT];
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8 * PT; ++j) w[j] = exp2_fast(x[j] - ref);
+        for (int j = 0; j < 8; ++j) w[j] = exp2_fast(x[j] - ref);
 #pragma unroll
-        for (int j = 0; j < 8 * PT; j += 2) l += w[j] + w[j + 1];
+        for (int j = 0; j < 8; j += 2) l += w[j] + w[j + 1];
+        if constexpr (CT == kF16) {
+          // Product in float32: a weight counts however small it is, where the
+          // rows of the larger ones are zero, and below 2^-14 float16 has not
+          // the bits, below 2^-25 not the range.  Instruction j of a column
+          // block contracts over the j-th slot of the four lane groups.
+          // Against 16-bit operands these are eight times the matrix cycles:
+          // 133 us against 132 for 48 sequences of up to 8000 slots, 8 heads
+          // of 4 queries of 128 elements, 11.0 against 9.4 for 211 slots.
 #pragma unroll
-        for (int u = 0; u < PT; ++u) {
-          const Tile& z = tile[u];
-          const float* const wu = w + 8 * u;
-          if constexpr (CT == kF16) {
-            // Product in float32: a weight counts however small it is, where the
-            // rows of the larger ones are zero, and below 2^-14 float16 has not
-            // the bits, below 2^-25 not the range.  Instruction j of a column
-            // block contracts over the j-th slot of the four lane groups.
-            // Against 16-bit operands these are eight times the matrix cycles:
-            // 133 us against 132 for 48 sequences of up to 8000 slots, 8 heads
-            // of 4 queries of 128 elements, 11.0 against 9.4 for 211 slots.
+          for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
+            for (int j = 0; j < 8; ++j)
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
+              for (int e = 0; e < VE; e += 2) {
+                const f16x2 y = __builtin_bit_cast(f16x2, vr[nb][j][e / 2]);
+                f32x4* acc = &o[nb * VE + e];
+                acc[0] = mma4(w[j], (float)y[0], acc[0]);
+                acc[1] = mma4(w[j], (float)y[1], acc[1]);
+              }
+        } else {
+          // Weights enter the product as three bfloat16 numbers each (see
+          // split3), which has the range of float32: out is rounded once, at
+          // the end.  (bfloat16 holds e4m3 rows exactly.)
+          Frag part[3];
 #pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                  const f16x2 y = __builtin_bit_cast(f16x2, z.vr[nb][j][e / 2]);
-                  f32x4* acc = &o[nb * VE + e];
-                  acc[0] = mma4(wu[j], (float)y[0], acc[0]);
-                  acc[1] = mma4(wu[j], (float)y[1], acc[1]);
+          for (int j = 0; j < 8; j += 2) {
+            unsigned a[3], b[3];
+            split3(w[j], a);
+            split3(w[j + 1], b);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+              part[i].d[j / 2] =
+                  (int)__builtin_amdgcn_perm(b[i], a[i], 0x07060302u);
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            int y[8][VE / 2];  // 8 slots of VE elements
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if constexpr (CT == kE2m1) {
+                // its block's scale (masked: 0 times one of NaN is NaN)
+                constexpr int per = kBlockElems / VE;
+                const unsigned w = vw[j][nb % A::SCALES];
+                const int vsc = ok[j] ? (int)(w >> (8 * (n / per)) & 255u) : 0;
+                int d[4];
+                widen8(vd[nb][j], vsc << 23, d);
+#pragma unroll
+                for (int e = 0; e < VE / 2; ++e) y[j][e] = d[e];
+              } else if constexpr (CT == kE4m3) {
+#pragma unroll
+                for (int e = 0; e < VD; ++e) {
+                  y[j][2 * e] = widen2<kBf16, false>(vr[nb][j][e]);
+                  y[j][2 * e + 1] = widen2<kBf16, true>(vr[nb][j][e]);
                 }
-          } else {
-            // Weights enter the product as three bfloat16 numbers each (see
-            // split3), which has the range of float32: out is rounded once, at
-            // the end.  (bfloat16 holds e4m3 rows exactly.)
-            Frag part[3];
+              } else {
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              unsigned a[3], b[3];
-              split3(wu[j], a);
-              split3(wu[j + 1], b);
-#pragma unroll
-              for (int i = 0; i < 3; ++i)
-                part[i].d[j / 2] =
-                    (int)__builtin_amdgcn_perm(b[i], a[i], 0x07060302u);
+                for (int e = 0; e < VD; ++e) y[j][e] = vr[nb][j][e];
+              }
             }
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
-              int y[8][VE / 2];  // 8 slots of VE elements
+            for (int e = 0; e < VE; ++e) {
+              // element e of the 8 slots: low or high halves, in pairs
+              const unsigned sel = e % 2 ? 0x07060302u : 0x05040100u;
+              Frag v;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if constexpr (CT == kE2m1) {
-                  int d[4];
-                  // its block's scale, in the lane that has V's of the slot
-                  constexpr int per = kBlockElems / VE;
-                  const unsigned w = vw[8 * u + j][nb % A::SCALES];
-                  const int vsc =
-                      mask[u][j] ? (int)(w >> (8 * (n / per)) & 255u) : 0;
-                  widen8(vd[u][nb][j], vsc << 23, d);
+              for (int j = 0; j < 4; ++j)
+                v.d[j] = (int)__builtin_amdgcn_perm((unsigned)y[2 * j + 1][e / 2],
+                                                    (unsigned)y[2 * j][e / 2],
+                                                    sel);
+              f32x4& acc = o[nb * VE + e];
 #pragma unroll
-                  for (int e = 0; e < VE / 2; ++e) y[j][e] = d[e];
-                } else if constexpr (CT == kE4m3) {
-#pragma unroll
-                  for (int e = 0; e < VD; ++e) {
-                    y[j][2 * e] = widen2<kBf16, false>(z.vr[nb][j][e]);
-                    y[j][2 * e + 1] = widen2<kBf16, true>(z.vr[nb][j][e]);
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < VD; ++e) y[j][e] = z.vr[nb][j][e];
-                }
-              }
-#pragma unroll
-              for (int e = 0; e < VE; ++e) {
-                // element e of the 8 slots: low or high halves, in pairs
-                const unsigned sel = e % 2 ? 0x07060302u : 0x05040100u;
-                Frag v;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  v.d[j] = (int)__builtin_amdgcn_perm((unsigned)y[2 * j + 1][e / 2],
-                                                      (unsigned)y[2 * j][e / 2],
-                                                      sel);
-                f32x4& acc = o[nb * VE + e];
-#pragma unroll
-                for (int i = 0; i < 3; ++i) acc = mma<kBf16>(part[i], v, acc);
-              }
+              for (int i = 0; i < 3; ++i) acc = mma<kBf16>(part[i], v, acc);
             }
           }
         }
         sched_fence();
         if constexpr (decltype(more)::value) {
-#pragma unroll
-          for (int u = 0; u < PT; ++u) {
-            if constexpr (!A::k4) load_v(tile[u], tile[u].next);
-            tile[u].cur = tile[u].next;
-            tile[u].next = after[u];
-          }
+          if constexpr (!A::k4) load_v(next);
+          cur = next;
+          next = after;
           sched_fence();
         }
       };
-      for (; t + PT * ts < t1; t += PT * ts) step(std::true_type());
+      for (; t + ts < t1; t += ts) step(std::true_type());
       step(std::false_type());
     }
     l = quad_sum(l);
