@@ -453,8 +453,8 @@ typedef struct libtopk_ledger {
  *     weights[b][h][t] += sum_{j of h} exp(x[j][t] - lse[b][j])
  *
  * A sequence with no slot gets out = 0 and lse = -infinity.  Scores, weights,
- * sums and the running output are float32 (the weights that multiply bfloat16
- * and 8-bit rows to 2^-22); only out is rounded, once.  Results do not depend
+ * sums and the running output are float32 (the weights that multiply bfloat16,
+ * 8-bit and 4-bit rows to 2^-22); only out is rounded, once.  Results do not depend
  * on the order in which workgroups run.
  *
  * Every weight counts that float32 can hold next to the largest (scores down
@@ -466,8 +466,9 @@ typedef struct libtopk_ledger {
  * attention over the prompt.
  *
  *   q        device, q_dtype (LIBTOPK_BF16 or LIBTOPK_F16; the cache's own,
- *            or either over an LIBTOPK_E4M3 or LIBTOPK_E2M1 cache), 16-byte aligned, element
- *            strides q_batch_stride and q_head_stride (multiples of 8)
+ *            or either over an LIBTOPK_E4M3 or LIBTOPK_E2M1 cache), 16-byte
+ *            aligned, element strides q_batch_stride and q_head_stride
+ *            (multiples of 8)
  *   q_heads  a positive multiple of cache->heads
  *   k_scale, v_scale   device, float32[heads], or NULL for 1
  *   ledger   NULL, or where the weights are accumulated (positions unused)
@@ -625,13 +626,13 @@ int cache_extend(const libtopk_cache_t *cache, const libtopk_tokens_t *tokens,
                  const libtopk_ledger_t *ledger, int32_t *out_lens,
                  libtopk_stream_t stream);
 
-/* Free the workspaces of the cache_* calls after synchronising their
- * devices.  Must not race with other calls, nor precede the replay of a graph
+/* Free the workspaces of the cache_* calls and sample_logits after
+ * synchronising their devices.  Must not race with other calls, nor precede the replay of a graph
  * that captured one. */
 void cache_release(void);
 
 /* Test hook, as libtopk_debug_scramble: overwrite the completion tickets of
- * the cache_* calls on `stream` with pseudo-random words. */
+ * the cache_* calls and sample_logits on `stream` with pseudo-random words. */
 int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
 
 /* ---------------------------------------------------------------------------
@@ -656,9 +657,10 @@ int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
  * weight 1 and the others none.  u is read as within [0, 1) (NaN as 0): at its
  * upper end the last kept token that has weight is taken.
  *
- * Weights are computed in 64 bits and added in units of at most
- * 2^-(62 - ceil(log2 cols)) of the largest; results do not depend on the order
- * in which workgroups run.
+ * Weights are computed in 64 bits and added as integers in units of
+ * 2^-min(51, 62 - ceil(log2 cols)) of the largest (2^-45 for 131072 logits), to
+ * the nearest of which each is rounded; results do not depend on the order in
+ * which workgroups run.
  *
  *   logits   device, dtype[rows][cols] (LIBTOPK_F32, _BF16 or _F16), rows ld
  *            elements apart, ld >= cols, at any alignment of the type
@@ -670,8 +672,15 @@ int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
  *   tokens   device, int64[rows]
  *   logprobs device, float32[rows]
  *
+ * Workspace: that of the cache_* calls on the stream (the same rules, for a
+ * capture too), about 50 KiB a row and 540 bytes for every 1024 logits, and at
+ * most 64 MiB: more rows go in batches.  Two launches a batch, five with any of
+ * top_k, top_p and min_p; rows of more than 2^20 logits take one launch, no
+ * workspace, and a workgroup a row.
+ *
  * Errors: LIBTOPK_ERR_INVALID for a NULL or misaligned pointer, a size or type
- * outside the above, or an output that overlaps an input or the other output.
+ * outside the above, or an output that overlaps an input or the other output;
+ * LIBTOPK_ERR_NOMEM if the workspace cannot grow.
  */
 #define LIBTOPK_MAX_LOGITS (1 << 24)
 #define LIBTOPK_MAX_SAMPLE_ROWS (1 << 22)

@@ -2,9 +2,10 @@
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of libtopk.so, whose C interface is include/libtopk.h.  PyTorch
-supplies device memory and the current stream.  (The cache_* calls, made once
-a layer and token, are marshalled in C++: csrc/binding.cpp.)  There is no CPU fallback:
-if the library is not built, importing this package raises.
+supplies device memory and the current stream.  (The cache_* calls and
+sample, made once a layer or token, are marshalled in C++: csrc/binding.cpp.)
+There is no CPU fallback: if the library is not built, importing this package
+raises.
 
     topk(x, k)      -> int32 tensor [k], the k largest of x, descending
     reduce(x, op)   -> int64 tensor [1]: SUM, MAX or MIN of x

@@ -2,11 +2,13 @@
 
 The translation units, compiled side by side, hold the C entry points and
 include their kernel headers: csrc/libtopk.hip (selection and reductions),
-csrc/cache.hip (the operators on a paged key-value cache) and
-csrc/cache_attend.hip (its attention kernels, once for each pair of types).  The flags disable
-packed-FP32 instruction selection (every HIP build in this project carries
-the flag), emit code for gfx950 only, and pin code object version 5, which both the ROCm runtime in /opt/rocm and the one bundled with
-PyTorch load.  They also turn off the compiler's atomic optimizer: every
+csrc/cache.hip (the operators on a paged key-value cache),
+csrc/cache_attend.hip (its attention kernels, once for each pair of types),
+csrc/sample.hip (tokens from logits) and csrc/workspace.hip (workspaces of the
+last three).  The flags disable packed-FP32 instruction selection (every HIP
+build in this project carries the flag), emit code for gfx950 only, and pin code
+object version 5, which both the ROCm runtime in /opt/rocm and the one bundled
+with PyTorch load.  They also turn off the compiler's atomic optimizer: every
 atomic here is issued by one lane or targets a distinct address per lane,
 and the optimizer's wave-wide combining would only add a scalar loop.
 
