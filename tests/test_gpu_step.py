@@ -264,3 +264,53 @@ def test_rows_beyond_a_million_logits(dtype):
     smp._check(x, u, top_p=0.9)
     smp._check(x, u, top_k=30, min_p=0.01, temperature=0.7)
     smp._check(x, u)
+
+
+@pytest.mark.parametrize("page", [512, 100])
+def test_4_bit_rows_past_32_bits(page):
+    """Rows (and scales) more than 2^32 bytes apart, the last pages of the
+    cache: attention, and eviction from and to them."""
+    rng = np.random.default_rng(6)
+    dim, slots, blocks = 128, 700, 4
+    pages = (1 << 32) // (page * 64) + 30
+    dev = torch.device("cuda")
+    used = -(-slots // page)
+    table = np.arange(pages - used, pages, dtype=np.int32)[None, ::-1].copy()
+    sizes = {"k": 64, "v": 64, "k_blocks": blocks, "v_blocks": blocks}
+    big, small = {}, {}
+    for name, n in sizes.items():
+        step = 64 if name == "k_blocks" else n  # scales as far apart as rows
+        x = torch.zeros(pages, 1, page, step, dtype=torch.uint8, device=dev)
+        x = x[..., :n]
+        bits = rng.integers(118, 128, (used, 1, page, n)) if "blocks" in name \
+            else rng.integers(0, 256, (used, 1, page, n))
+        small[name] = torch.from_numpy(bits.astype(np.uint8)).to(dev)
+        x[pages - used:] = small[name]
+        kind = torch.float8_e8m0fnu if "blocks" in name else \
+            torch.float4_e2m1fn_x2
+        big[name], small[name] = x.view(kind), small[name].view(kind)
+    assert big["k"].numel() > 1 << 32
+    lens = torch.tensor([slots], dtype=torch.int32, device=dev)
+    q = base._q(rng, 1, 4, dim, "bf16", 0.05)
+    tables = [torch.from_numpy(t).to(dev)
+              for t in (table, table - (pages - used))]
+    seen = torch.tensor([slots], dtype=torch.int32, device=dev)
+    results = []
+    for cache, t in zip((big, small), tables):
+        w = torch.zeros(1, 1, used * page, device=dev)
+        got = ltk.cache_attend(q, cache["k"], cache["v"], t, lens, weights=w,
+                               k_blocks=cache["k_blocks"],
+                               v_blocks=cache["v_blocks"])
+        pos = torch.arange(used * page, dtype=torch.int32, device=dev)
+        cut = ltk.cache_evict(cache["k"], cache["v"], t, lens, seen, w,
+                              pos.view(1, 1, -1).contiguous(), 300,
+                              k_blocks=cache["k_blocks"],
+                              v_blocks=cache["v_blocks"])
+        results.append((*got, w, *cut))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert float(results[0][2].sum()) == pytest.approx(4.0, abs=1e-3)
+    for name in sizes:
+        assert torch.equal(big[name].view(torch.uint8)[pages - used:],
+                           small[name].view(torch.uint8)), name
+        assert not big[name].view(torch.uint8)[:2].any()
