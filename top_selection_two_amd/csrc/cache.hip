@@ -101,6 +101,7 @@ bool check_rows(const void* p, const int64_t (&n)[3], const int64_t (&stride)[3]
 // Checks a cache and fills in what the kernels take of it, and the extents of
 // its arrays.
 int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
+                BlockParams* blocks,
                 CacheRanges* r) {
   if (!c) return LIBTOPK_ERR_INVALID;
   const bool e2m1 = c->dtype == LIBTOPK_E2M1;
@@ -130,14 +131,14 @@ int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
                             c->k_block_slot_stride};
     const int64_t vbs[3] = {c->v_block_page_stride, c->v_block_head_stride,
                             c->v_block_slot_stride};
-    p->blocks = c->dim / kBlockElems;
-    if (!check_rows(c->k_blocks, n, kbs, 1, p->blocks, 1, written, &p->kbs,
+    blocks->n = c->dim / kBlockElems;
+    if (!check_rows(c->k_blocks, n, kbs, 1, blocks->n, 1, written, &blocks->ks,
                     &r->kb) ||
-        !check_rows(c->v_blocks, n, vbs, 1, p->blocks, 1, written, &p->vbs,
+        !check_rows(c->v_blocks, n, vbs, 1, blocks->n, 1, written, &blocks->vs,
                     &r->vb))
       return LIBTOPK_ERR_INVALID;
-    p->kb = (const char*)c->k_blocks;
-    p->vb = (const char*)c->v_blocks;
+    blocks->k = (const char*)c->k_blocks;
+    blocks->v = (const char*)c->v_blocks;
   }
   if (c->batch > 0 && (!c->table || !c->lens)) return LIBTOPK_ERR_INVALID;
   if (!aligned(c->table, 4) || !aligned(c->lens, 4))
@@ -265,10 +266,10 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
                  int64_t q_head_stride, float scale, const float* k_scale,
                  const float* v_scale, const libtopk_ledger_t* ledger,
                  void* out, float* lse, libtopk_stream_t stream) {
-  AttendParams p = {};
+  Attend4Params p = {};
   CacheRanges at;
   Range w(nullptr, 0), pos(nullptr, 0);
-  int rc = check_cache(cache, false, &p.c, &at);
+  int rc = check_cache(cache, false, &p.c, &p.s, &at);
   if (rc != LIBTOPK_OK) return rc;
   if (q_dtype != LIBTOPK_BF16 && q_dtype != LIBTOPK_F16)
     return LIBTOPK_ERR_INVALID;
@@ -325,8 +326,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   // Halves of a tile that lie in one page each get their addresses from
   // scalar registers (and 16 rows must lie within 2^31 bytes).
   const bool pg16 = cache->page % 16 == 0 && p.c.ks.slot < (1 << 27) &&
-                    p.c.vs.slot < (1 << 27) && p.c.kbs.slot < (1 << 27) &&
-                    p.c.vbs.slot < (1 << 27);
+                    p.c.vs.slot < (1 << 27);
   int dev_units = 0;
   rc = units_of(dev, &dev_units);
   if (rc != LIBTOPK_OK) return rc;
@@ -415,7 +415,11 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   p.q_type = q_dtype;
   p.ticket = work.tickets;
   p.epoch = work.epoch;
-  rc = launch(fn, dim3((unsigned)grid), needs.threads, p, s, lds);
+  const dim3 blocks((unsigned)grid);
+  const AttendParams& base = p;
+  rc = cache->dtype == LIBTOPK_E2M1
+           ? launch(fn, blocks, needs.threads, p, s, lds)
+           : launch(fn, blocks, needs.threads, base, s, lds);
   if (rc != LIBTOPK_OK || !ledger || p.direct) return rc;
   const int64_t wrows = (int64_t)cache->batch * cache->heads;
   // Few rows: workgroups enough to share out the joining, too.
@@ -425,7 +429,7 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
   return launch((const void*)&attend_join_kernel,
                 dim3((unsigned)chunks,
                      (unsigned)(wrows < 65535 ? wrows : 65535)),
-                kBlock, p, s);
+                kBlock, base, s);
 }
 
 int cache_append(const libtopk_cache_t* cache, const void* k_new,
@@ -435,9 +439,10 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
                  int32_t* out_lens, int32_t* out_slots,
                  libtopk_stream_t stream) {
   SlotsParams p = {};
+  BlockParams none = {};
   CacheRanges at;
   Range w(nullptr, 0), pos(nullptr, 0);
-  int rc = check_cache(cache, true, &p.c, &at);
+  int rc = check_cache(cache, true, &p.c, &none, &at);
   if (rc != LIBTOPK_OK) return rc;
   if (cache->dtype == LIBTOPK_E2M1) return LIBTOPK_ERR_INVALID;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,
@@ -495,10 +500,11 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
                 const libtopk_ledger_t* ledger, int32_t keep, int32_t sinks,
                 int32_t recent, const libtopk_ledger_t* after,
                 int32_t* out_lens, libtopk_stream_t stream) {
-  SlotsParams p = {};
+  Slots4Params all = {};
+  SlotsParams& p = all;
   CacheRanges at;
   Range w(nullptr, 0), pos(nullptr, 0), w2(nullptr, 0), pos2(nullptr, 0);
-  int rc = check_cache(cache, true, &p.c, &at);
+  int rc = check_cache(cache, true, &p.c, &all.s, &at);
   if (rc != LIBTOPK_OK) return rc;
   rc = check_ledger(ledger, cache->batch, cache->heads, true, false, &p.w, &w,
                     &pos);
@@ -588,10 +594,13 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
   }
   if (rc != LIBTOPK_OK) return rc;
   const int64_t units = (int64_t)p.pair_cap * p.row_units.d;
-  return launch((const void*)&evict_move_kernel,
-                dim3((unsigned)((units + kBlock - 1) / kBlock),
-                     (unsigned)(rows < 65535 ? rows : 65535)),
-                kBlock, p, s);
+  const dim3 grid((unsigned)((units + kBlock - 1) / kBlock),
+                  (unsigned)(rows < 65535 ? rows : 65535));
+  return cache->dtype == LIBTOPK_E2M1
+             ? launch((const void*)&evict_move_kernel<true>, grid, kBlock, all,
+                      s)
+             : launch((const void*)&evict_move_kernel<false>, grid, kBlock, p,
+                      s);
 }
 
 int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
@@ -600,7 +609,7 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
   ExtendParams p = {};
   CacheRanges at;
   Range w(nullptr, 0), pos(nullptr, 0);
-  int rc = check_cache(cache, true, &p.c, &at);
+  int rc = check_cache(cache, true, &p.c, &p.s, &at);
   if (rc != LIBTOPK_OK) return rc;
   if (ledger) {
     rc = check_ledger(ledger, cache->batch, cache->heads, true, true, &p.w, &w,

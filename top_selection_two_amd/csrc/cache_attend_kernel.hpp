@@ -83,6 +83,9 @@ struct AttendParams {
   void* out;
   float* lse;
 };
+struct Attend4Params : AttendParams {
+  BlockParams s;
+};
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -355,7 +358,8 @@ __device__ __forceinline__ typename A::Ids find_tile(const CacheParams& c,
 template <int QT, int CT, int NC, bool PG16, int HS>
 __global__ __launch_bounds__((Attend<QT, CT, NC, PG16>::THREADS),
                              (Attend<QT, CT, NC, PG16>::WAVES / 4)) void
-attend_kernel(AttendParams p) {
+attend_kernel(
+    std::conditional_t<CT == kE2m1, Attend4Params, AttendParams> p) {
   typedef Attend<QT, CT, NC, PG16> A;
   constexpr int kAttWaves = A::WAVES, kAttThreads = A::THREADS;
   constexpr int EB = A::EB, KL = A::KL, VE = A::VE, VD = A::VD, NB = A::NB;
@@ -574,8 +578,13 @@ attend_kernel(AttendParams p) {
     const int32_t tiles = (len + kTileSlots - 1) / kTileSlots;
     const char* kh = c.k + h * c.ks.head;
     const char* vh = c.v + h * c.vs.head;
-    const char* kbh = CT == kE2m1 ? c.kb + h * c.kbs.head : nullptr;
-    const char* vbh = CT == kE2m1 ? c.vb + h * c.vbs.head : nullptr;
+    const char *kbh = nullptr, *vbh = nullptr;  // scales of 4-bit rows
+    int blocks = 0;
+    if constexpr (A::k4) {
+      kbh = p.s.k + h * p.s.ks.head;
+      vbh = p.s.v + h * p.s.vs.head;
+      blocks = p.s.n;
+    }
     Share cur = {b, hi, len, share < 0 ? r0 / per : wg - share,
                  share < 0 ? (r1 - 1) / per : wg - share + cuts - 1,
                  s0 - r0, 0, held, true};
@@ -655,18 +664,18 @@ attend_kernel(AttendParams p) {
           const int32_t pg = page_ok(id1, c.pages) ? id1 : 0;
           const int32_t at = PG16 ? n : 0;
           const char* sc =
-              ln < 32 ? kbh + row_offset(c.kbs, pg, 0, pl + at)
-                      : vbh + row_offset(c.vbs, pg, 0, pl + at);
+              ln < 32 ? kbh + row_offset(p.s.ks, pg, 0, pl + at)
+                      : vbh + row_offset(p.s.vs, pg, 0, pl + at);
           typedef unsigned u32u __attribute__((aligned(1)));
           if constexpr (NC == 2 || NC == 3) {
 #pragma unroll
             for (int i = 0; i < A::SW; ++i)
-              sw[i] = ld_once<uint8_t>(sc + (i < c.blocks ? i : 0));
+              sw[i] = ld_once<uint8_t>(sc + (i < blocks ? i : 0));
           } else {
             sw[0] = __builtin_nontemporal_load((const u32u*)sc);
             if constexpr (NC > 4)
               sw[1] =
-                  __builtin_nontemporal_load((const u32u*)(sc + c.blocks - 4));
+                  __builtin_nontemporal_load((const u32u*)(sc + blocks - 4));
           }
         }
       };
@@ -760,7 +769,7 @@ attend_kernel(AttendParams p) {
                                   sw[A::SW > 2 ? 2 : 0] << 16
                             : sw[0];
           // the last four; block 4 first
-          if constexpr (NC > 4) sc[1] = sw[A::SW > 1] >> (8 * (8 - c.blocks));
+          if constexpr (NC > 4) sc[1] = sw[A::SW > 1] >> (8 * (8 - blocks));
 #pragma unroll
           for (int i = 0; i < A::SCALES; ++i) {
 #pragma unroll

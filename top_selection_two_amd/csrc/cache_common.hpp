@@ -24,11 +24,15 @@ struct CacheParams {
   int32_t batch, heads, dim;
   int32_t cap;        // slots that the table (and the ledger) can name
   int32_t row_bytes;  // dim elements
-  // Scales of 4-bit rows: a byte for each 32 elements (bytes throughout).
-  const char* kb;
-  const char* vb;
-  RowStrides kbs, vbs;
-  int32_t blocks;     // of a row; 0 where rows have none
+};
+
+// Scales of 4-bit rows: a byte for each 32 elements (bytes throughout).  Apart
+// from the rest, so that calls without them do not carry them.
+struct BlockParams {
+  const char* k;
+  const char* v;
+  RowStrides ks, vs;
+  int32_t n;  // of a row
 };
 
 struct LedgerParams {

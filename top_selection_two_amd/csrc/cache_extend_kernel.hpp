@@ -25,6 +25,7 @@ namespace ltk {
 
 struct ExtendParams {
   CacheParams c;
+  BlockParams s;
   LedgerParams w;     // w.w NULL: none
   const char* q;      // NULL: none
   const char* k;
@@ -445,8 +446,8 @@ __global__ __launch_bounds__(kBlock, 4) void extend_kernel(ExtendParams p) {
       *(unsigned*)(dst + ul * 4) = byte < 255 ? code : 0;
       if (ul % 4 == 0) {
         char* blocks = const_cast<char*>(
-            is_v ? c.vb + row_offset(c.vbs, page, h, place)
-                 : c.kb + row_offset(c.kbs, page, h, place));
+            is_v ? p.s.v + row_offset(p.s.vs, page, h, place)
+                 : p.s.k + row_offset(p.s.ks, page, h, place));
         blocks[ul / 4] = (char)byte;
       }
     } else {

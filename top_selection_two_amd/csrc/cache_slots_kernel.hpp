@@ -6,6 +6,8 @@
 // that order, eviction keeps the first `keep`.
 #pragma once
 
+#include <type_traits>
+
 #include "cache_common.hpp"
 
 namespace ltk {
@@ -36,6 +38,9 @@ struct SlotsParams {
   int2* state;        // [rows][4]: cut and want before each digit, long rows
   int32_t chunks;
   int32_t* out_lens;
+};
+struct Slots4Params : SlotsParams {
+  BlockParams s;
 };
 
 __device__ __forceinline__ uint64_t min64(uint64_t a, uint64_t b) {
@@ -525,7 +530,9 @@ __global__ __launch_bounds__(kEvThreads) void evict_list_kernel(
 // or four pairs a thread were slower (16 prompts of up to 8192 slots cut to
 // 2048, slots outside heads: 33 us against 35 and 41), as were separate
 // threads for K and V, which find the same pages twice (46 us).
-__global__ __launch_bounds__(kBlock) void evict_move_kernel(SlotsParams p) {
+template <bool BLOCKS>
+__global__ __launch_bounds__(kBlock) void evict_move_kernel(
+    std::conditional_t<BLOCKS, Slots4Params, SlotsParams> p) {
   const CacheParams& c = p.c;
   const int32_t i = blockIdx.x * kBlock + threadIdx.x;
   const int32_t pair = quotient(p.row_units, i);
@@ -550,15 +557,18 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(SlotsParams p) {
         (const v4i*)(c.k + row_offset(c.ks, jf, h, zf) + off));
     const v4i y = __builtin_nontemporal_load(
         (const v4i*)(c.v + row_offset(c.vs, jf, h, zf) + off));
-    if (c.blocks > 0 && off == 0) {  // the scales of 4-bit rows go along
-      const char* kf = c.kb + row_offset(c.kbs, jf, h, zf);
-      const char* vf = c.vb + row_offset(c.vbs, jf, h, zf);
-      char* kt = const_cast<char*>(c.kb + row_offset(c.kbs, it, h, zt));
-      char* vt = const_cast<char*>(c.vb + row_offset(c.vbs, it, h, zt));
-      for (int e = 0; e < c.blocks; ++e) {
-        const char s = kf[e], z = vf[e];
-        kt[e] = s;
-        vt[e] = z;
+    if constexpr (BLOCKS) {  // the scales of 4-bit rows go along
+      if (off == 0) {
+        const BlockParams& s = p.s;
+        const char* kf = s.k + row_offset(s.ks, jf, h, zf);
+        const char* vf = s.v + row_offset(s.vs, jf, h, zf);
+        char* kt = const_cast<char*>(s.k + row_offset(s.ks, it, h, zt));
+        char* vt = const_cast<char*>(s.v + row_offset(s.vs, it, h, zt));
+        for (int e = 0; e < s.n; ++e) {
+          const char a = kf[e], b = vf[e];
+          kt[e] = a;
+          vt[e] = b;
+        }
       }
     }
     __builtin_nontemporal_store(
