@@ -314,3 +314,42 @@ def test_4_bit_rows_past_32_bits(page):
         assert torch.equal(big[name].view(torch.uint8)[pages - used:],
                            small[name].view(torch.uint8)), name
         assert not big[name].view(torch.uint8)[:2].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [5003, 70001])
+def test_settings_at_their_ends(cols, dtype):
+    """Prefixes that are all but the whole row, next to nothing, and
+    temperatures beyond any use."""
+    print("ends", cols, dtype, flush=True)
+    rng = np.random.default_rng(cols + 1)
+    x = smp._logits(rng, 3, cols, dtype, peak=0.9)
+    u = rng.random(3)
+    nearly = float(np.nextafter(np.float32(1), np.float32(0)))
+    for how in (dict(top_p=nearly), dict(top_p=1e-30), dict(min_p=1e-38),
+                dict(temperature=1e-30, top_p=0.9),
+                dict(temperature=1e-45), dict(temperature=1e30, top_p=0.5),
+                dict(temperature=3e38), dict(top_k=cols - 1, top_p=nearly),
+                dict(top_k=2 ** 31 - 1, min_p=1e-6)):
+        smp._check(x, u, **how)
+
+
+def test_workspaces_that_held_anything():
+    """Neither the tickets nor the rest of a workspace say anything to the
+    next call."""
+    rng = np.random.default_rng(8)
+    x = smp._logits(rng, 9, 60000, "f16", peak=0.7)
+    u = torch.from_numpy(rng.random(9).astype(np.float32)).cuda()
+    p = torch.tensor([1, .5, .9, .98, 1, .999, .3, .97, .95], device="cuda")
+    want = ltk.sample(x, u, top_p=p, top_k=30000)
+    _, dev, _ = ext._case4(2, [3000, 9000], 2, 64, 16)
+    q = base._q(rng, 2, 32, 64, "bf16", 0.05)
+    stream = torch.cuda.current_stream().cuda_stream
+    for i in range(3):
+        w = torch.zeros(2, 2, dev["table"].shape[1] * 16, device="cuda")
+        ltk.cache_attend(q, dev["k"], dev["v"], dev["table"], dev["lens"],
+                         weights=w, k_blocks=dev["k_blocks"],
+                         v_blocks=dev["v_blocks"])
+        assert ltk.lib.cache_debug_scramble(stream, 5 + i) == ltk.OK
+        got = ltk.sample(x, u, top_p=p, top_k=30000)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
