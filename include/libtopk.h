@@ -632,7 +632,8 @@ int cache_extend(const libtopk_cache_t *cache, const libtopk_tokens_t *tokens,
 void cache_release(void);
 
 /* Test hook, as libtopk_debug_scramble: overwrite the completion tickets of
- * the cache_* calls and sample_logits on `stream` with pseudo-random words. */
+ * the cache_* calls and sample_logits on `stream` with pseudo-random
+ * words. */
 int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
 
 /* ---------------------------------------------------------------------------

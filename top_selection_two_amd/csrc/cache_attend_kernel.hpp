@@ -28,12 +28,13 @@
 //
 // Over 4-bit rows the widening to bfloat16 (exact: a code has two bits, a scale
 // none) and the softmax take more time than the bytes: some 480 vector
-// instructions a tile, of two waves a SIMD, which 208 registers a lane allow.  48 sequences
-// of 100 to 8000 slots, 8 heads of 4 queries of 128, 0.23 GB: 80 us with the
-// weights (2.8 TB/s; 70 here, 10 in the second launch), 150 in bfloat16 (0.8 GB);
-// a document of 131072 slots, 4 heads of 8: 31 us (2.3 TB/s), 51 in bfloat16.
-// Two tiles a step took 89 and 31 us, V rows and scales read as each lane needs
-// them (2 or 4 bytes a load, which cost the address unit as much as 16) 95 and 33.
+// instructions a tile, of two waves a SIMD, which 208 registers a lane allow.
+// 48 sequences of 100 to 8000 slots, 8 heads of 4 queries of 128, 0.23 GB: 81 us
+// with the weights (2.8 TB/s; 70 here, 11 in the second launch), 152 in bfloat16
+// (0.8 GB); a document of 131072 slots, 4 heads of 8: 32 us (2.3 TB/s), 51 in
+// bfloat16.  Two tiles a step took 89 and 31 us, V rows and scales read as each
+// lane needs them (2 or 4 bytes a load, which cost the address unit as much as
+// 16) 95 and 33.
 #pragma once
 
 #include <type_traits>

@@ -4,19 +4,19 @@
 // A row (one head of one token) of `dim` elements x becomes, for q and k,
 // y = x (mean x^2 + eps)^-1/2 g and then pairs (a, b) of y turned by the angle
 // position * freqs[j]: (a cos - b sin, b cos + a sin).  All of it is computed
-// in 64 bits (4.4 cycles an instruction, 2.9 in 32 bits) and rounded at the end,
-// through float32 where the type has 16 or 8 bits: a cache's 4-bit row, where a
-// unit in the last place of a float32 can move an element by half its value, does
-// not depend on how the sums were ordered.
+// in 64 bits (4.4 cycles an instruction, 2.9 in 32 bits) and rounded at the
+// end, through float32 where the type has 16 or 8 bits: a cache's 4-bit row,
+// where a unit in the last place of a float32 can move an element by half its
+// value, does not depend on how the sums were ordered.
 //
 // Bytes bound long calls: x is read once and y written once, a lane has 16 bytes
 // of a row (extend_kernel, below).  12 prompts of 100 to 4001 tokens, 32 + 8 + 8
 // heads of 128, bfloat16, 0.60 GB: 141 us (4.3 TB/s; a large copy reaches 5.2);
 // into 4 bits, 6 prompts of 700 to 2048 tokens, 16 + 4 + 4 heads, 90 MB: 39 us
 // (2.3 TB/s; the vector unit is busy half of the time with norms, turns and
-// codes).  Few tokens are dealt out row by row: a token of 64 sequences takes 10.7
-// us among other calls, 6 by itself, four dependent reads (starts, length, table,
-// rows) and a launch.
+// codes).  Few tokens are dealt out row by row: a token of 64 sequences takes
+// 6 us, four dependent reads (starts, length, table, rows) and a launch; among
+// other calls 10.7, which the host needs.
 #pragma once
 
 #include "cache_common.hpp"

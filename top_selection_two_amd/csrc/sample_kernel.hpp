@@ -375,7 +375,8 @@ struct Prefix {
   uint64_t above;  // count or mass of those above the key
 };
 
-// The shortest prefix within `in` whose count or mass reaches `goal`, by digits of the key from the top: 11, 11 and 10 bits.
+// The shortest prefix within `in` whose count or mass reaches `goal`, by digits
+// of the key from the top: 11, 11 and 10 bits.
 template <int T>
 __device__ __forceinline__ Prefix find_prefix(const SampleParams& a,
                                               const char* row, float top,
@@ -905,8 +906,8 @@ __device__ __forceinline__ uint64_t list_cut(const SampleParams& a, const Wanted
 }
 
 // Rows: from their chunks, or over again.  A workgroup a row, of 1024 threads
-// with the words in LDS, all of it latency: one row of 32000 takes 14.5 us, 256 of
-// 131072 together 21.
+// with the words in LDS, all of it latency: one row of 32000 takes 14.5 us, 256
+// of 131072 together 21.
 template <int T>
 __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
     SampleParams a) {
@@ -1071,11 +1072,11 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
 // A prefix beyond the lists (a nucleus of tens of thousands) is found in three
 // more launches, two of them over the row by workgroups of 8 chunks.  The first
 // adds up the masses (or counts) of the logits in 2048 bins of log2 of their
-// weight; integers, so that their order is nothing.  The second finds the bin in
-// which the goal lies, adds up each chunk's mass above it, and lists the bin's own
-// logits; the third ends the row (finish_wide).  32 rows of 200000 in float16, all
-// wide: 19, 21 and 17 us (a weight a logit twice more, and atomics; a workgroup
-// a row at the end); with no wide row the three take 1.3 us each.
+// weight; integers, so that their order is nothing.  The second finds the bin
+// in which the goal lies, adds up each chunk's mass above it, and lists the
+// bin's own logits; the third ends the row (finish_wide).  32 rows of 200000 in
+// float16, all wide: 19, 21 and 17 us (a weight a logit twice more, and atomics;
+// a workgroup a row at the end); with no wide row the three take 1.4 us each.
 template <int T>
 __global__ __launch_bounds__(kWideThreads) void sample_bins_kernel(
     SampleParams a) {
