@@ -194,13 +194,14 @@ __device__ __forceinline__ double exp2_neg(double y) {
   return ldexp(s, (int)n);
 }
 
-// ln r, 0 < r <= 1, for float32: y from the instruction, which is some 2^-20
-// off, and the series of ln (r / e^y) as far as it takes.
-__device__ __forceinline__ float ln_of(double r) {
+// ln r, 2^-126 <= r <= 1 (the instruction takes no smaller float32), for
+// float32: y from the instruction, which is some 2^-20 off, and the series of
+// ln (r / e^y) as far as it takes.
+__device__ __forceinline__ double ln_of(double r) {
   double y = (double)__builtin_amdgcn_logf((float)r);
   y = y < 0.0 ? y : 0.0;
   const double d = r / exp2_neg(y) - 1.0;
-  return (float)fma(y, 0.693147180559945309417, d - 0.5 * d * d);
+  return fma(y, 0.693147180559945309417, d - 0.5 * d * d);
 }
 
 // Weight of a logit next to the row's largest, `top`; inv_t is log2 e / T.
@@ -558,8 +559,8 @@ __device__ __forceinline__ void sample_row(const SampleParams& a, int64_t row_i,
     const int64_t i = (int64_t)t * kSampleTile + (int64_t)tid * kSampleVec + e;
     a.tokens[row_i] = i;
     a.logprobs[row_i] =
-        ln_of(weight_of(read_logit<T>(row, i), top, want.inv_t) /
-                   ((double)total / a.unit));
+        (float)ln_of(weight_of(read_logit<T>(row, i), top, want.inv_t) /
+                     ((double)total / a.unit));
   }
 }
 
@@ -960,7 +961,12 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
         first_or_last(w > 0.0 && (want.greedy || upto > goal), w > 0.0, s);
     if (tid != who) return;
     a.tokens[row_i] = i;
-    a.logprobs[row_i] = want.greedy ? 0.0f : ln_of(w / total);
+    // Any weight may be drawn here, down to 2^-1074 of the largest: its
+    // logarithm is the logit's difference, and `total` is 1 at least.
+    const double y = x == top ? 0.0 : ((double)x - (double)top) * want.inv_t;
+    a.logprobs[row_i] =
+        want.greedy ? 0.0f
+                    : (float)fma(y, 0.693147180559945309417, ln_of(1.0 / total));
     return;
   }
   uint64_t listed;
@@ -1064,7 +1070,7 @@ __global__ __launch_bounds__(kSampleThreads) void sample_finish_kernel(
   before += wave_scan64(m) - m;
   if (before <= goal && goal < before + m) {
     a.tokens[row_i] = (int64_t)(uint32_t) ~(uint32_t)w;
-    a.logprobs[row_i] = ln_of(x / ((double)kept / a.unit));
+    a.logprobs[row_i] = (float)ln_of(x / ((double)kept / a.unit));
   }
 }
 
@@ -1280,7 +1286,7 @@ __device__ __forceinline__ bool finish_wide(const SampleParams& a, int r,
   before += scan_block(m, s, &all);
   if (before <= goal && goal < before + m) {
     a.tokens[row_i] = i;
-    a.logprobs[row_i] = ln_of(w / ((double)total / a.unit));
+    a.logprobs[row_i] = (float)ln_of(w / ((double)total / a.unit));
   }
   return true;
 }
