@@ -355,9 +355,10 @@ __global__ __launch_bounds__(kBlock, 4) void extend_kernel(ExtendParams p) {
       // (of zeros with eps = 0: infinity, and NaN as 0 times it)
       inv = ms > 0.0 ? inv_sqrt(ms) : INFINITY;
       if (!(ms < INFINITY)) inv = ms == INFINITY ? 0.0 : ms;
-      // A product of two 16-bit numbers is exact in float32; the division by
-      // the row's size comes after the turn.
-      if (wide_norm) {
+      // A product of two float16 numbers is exact in float32 (one of bfloat16
+      // numbers is not: it can leave its range); the division by the row's size
+      // comes after the turn.
+      if (QT == kBf16 || wide_norm) {
 #pragma unroll
         for (int e = 0; e < kUnit; ++e) x[e] *= (double)w[e];
       } else {
