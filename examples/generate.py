@@ -110,7 +110,9 @@ def generate(model, prompts, steps, budget, graph=False, seed=1, top_k=50,
              top_p=0.95, temperature=0.8):
     """Tokens [steps, B] after the prompts (lists of tokens), log
     probabilities, and the cache; a sequence's cache is cut to half of
-    `budget` slots when it is full."""
+    `budget` slots when it is full.  With `graph` the current stream is one
+    that can be captured (not the default one), and has waited for whatever
+    made the model."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     batch = len(prompts)
     longest = max(map(len, prompts))
@@ -155,12 +157,13 @@ def generate(model, prompts, steps, budget, graph=False, seed=1, top_k=50,
     return torch.stack(tokens), torch.stack(logprobs), cache
 
 
-if __name__ == "__main__":
+def main():
     model = Decoder(vocab=32000, heads=8, group=4, dim=128)
     r = torch.Generator().manual_seed(2)
     prompts = [torch.randint(32000, (n,), generator=r).tolist()
                for n in (700, 3, 251, 1024)]
     side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())  # which makes the weights
     with torch.cuda.stream(side):
         tokens, logprobs, cache = generate(model, prompts, 200, budget=512,
                                            graph=True)
@@ -168,3 +171,7 @@ if __name__ == "__main__":
     print("200 steps of %d sequences; lengths seen %s, held %s; mean log "
           "probability %.2f" % (len(prompts), cache.seen.tolist(),
                                 cache.lens.tolist(), float(logprobs.mean())))
+
+
+if __name__ == "__main__":
+    main()
