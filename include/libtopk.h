@@ -586,7 +586,8 @@ int cache_evict(const libtopk_cache_t *cache, const int32_t *seen,
  * out_lens[b] is the length with the new slots.  Where a slot would lie beyond
  * the table or the ledger, nothing is written for it (q_out is) and the length
  * stops there; where the table names no page, no row is written.  Tokens that
- * belong to no sequence (from starts[batch] on) are left alone, in q_out too.
+ * belong to no sequence (before starts[0] and from starts[batch] on) are left
+ * alone, in q_out too unless `rest` is set.
  *
  *   starts   device, int32[batch + 1], non-decreasing within [0, tokens]: the
  *            caller's promise; otherwise which rows are written is
@@ -620,6 +621,8 @@ typedef struct libtopk_tokens {
     int32_t rot;          /* 0 <= rot <= dim, a multiple of 16               */
     int32_t interleaved;
     float eps;            /* >= 0                                            */
+    int32_t rest;         /* q_out's rows of tokens that belong to no sequence:
+                             0 left alone, 1 their rows of q as they are     */
 } libtopk_tokens_t;
 
 int cache_extend(const libtopk_cache_t *cache, const libtopk_tokens_t *tokens,

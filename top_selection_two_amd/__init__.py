@@ -112,7 +112,7 @@ class TokensStruct(ctypes.Structure):
                 + [(n, ctypes.c_int32) for n in
                    ("tokens", "q_heads", "dtype", "norm_dtype", "rot",
                     "interleaved")]
-                + [("eps", ctypes.c_float)])
+                + [("eps", ctypes.c_float), ("rest", ctypes.c_int32)])
 
 
 _CACHE = ctypes.POINTER(CacheStruct)
@@ -636,7 +636,8 @@ def cache_extend(k_new, v_new, k, v, table, lens, starts, seen=None, q=None,
     the new slots become 0 and their position.
 
     Returns (lens [B], q [N, Hq, D] or None); out may be given for the
-    latter, and may be q itself.  Tokens of no sequence are left as they were.
+    latter, and may be q itself.  Tokens of no sequence are left as they were;
+    in a q that is made here their rows are those given.
     No gradient passes through the rows written; one through the queries
     returned is an error."""
     return _binding.extend(k_new, v_new, k, v, table, lens, starts, seen, q,

@@ -539,6 +539,7 @@ PyObject* extend(PyObject* const* a, Py_ssize_t n) {
     const Tensor& q = tensor(a[8], "q");
     if (a[20] == Py_None) {
       out = at::empty({tokens, q_heads, (int64_t)r.c.dim}, q.options());
+      t.rest = 1;  // no row of it is left as memory happens to be
     } else {
       out = tensor(a[20], "out");
       expect(out, "out", type, q.sizes(), r.device, false);

@@ -666,8 +666,9 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
         !extent(t.q_out, q_heads, t.q_out_token_stride, t.q_out_head_stride,
                 true, os, &out))))
     return LIBTOPK_ERR_INVALID;
-  if (cache->batch == 0) return LIBTOPK_OK;
-  if (!t.starts || !out_lens) return LIBTOPK_ERR_INVALID;
+  const bool rest = t.q && t.rest != 0;
+  if (cache->batch == 0 && !(rest && t.tokens > 0)) return LIBTOPK_OK;
+  if (cache->batch > 0 && (!t.starts || !out_lens)) return LIBTOPK_ERR_INVALID;
   // Queries may be turned where they are, also between the keys and values
   // of one array: with the same stride from token to token, a token's rows of
   // the two lie apart within it.
@@ -690,7 +691,7 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
                          at.kb, at.vb};
   const Range ins[12] = {
       q, k, v, at.table, at.lens,
-      Range(t.starts, (batch + 1) * 4),
+      Range(t.starts, t.starts ? (batch + 1) * 4 : 0),
       Range(t.seen, t.seen ? batch * 4 : 0),
       Range(t.q_norm, t.q_norm ? (int64_t)dim * norm_bytes : 0),
       Range(t.k_norm, t.k_norm ? (int64_t)dim * norm_bytes : 0),
@@ -732,6 +733,7 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
   p.norm_type = t.norm_dtype;
   p.half = t.rot / 2;
   p.interleaved = t.interleaved != 0;
+  p.rest = rest;
   p.eps = t.eps;
   p.inv_dim = 1.0 / dim;
   int dev = 0;

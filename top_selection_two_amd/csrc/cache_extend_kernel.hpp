@@ -44,6 +44,7 @@ struct ExtendParams {
   int32_t norm_type;
   int32_t half;         // pairs that turn
   bool interleaved;
+  bool rest;            // queries of no sequence go to q_out as they are
   double eps, inv_dim;
   int32_t splits;       // waves of a token
 };
@@ -284,6 +285,26 @@ __global__ __launch_bounds__(kBlock, 4) void extend_kernel(ExtendParams p) {
     return r;
   };
   Raw next = load(part);
+
+  if (p.rest) {  // queries of no sequence, a row at a time
+    const int32_t lo = c.batch > 0 ? bound(ld_const(p.starts)) : 0;
+    const int32_t hi = c.batch > 0 ? bound(ld_const(p.starts + c.batch)) : 0;
+    if (token < lo || token >= hi) {
+      // (The launch's parameters are read again: kept for here they would cost
+      // the loop below registers: prompts into 4 bits 9 us more.)
+      typedef const __attribute__((address_space(4))) ExtendParams Again;
+      uintptr_t again = (uintptr_t)__builtin_amdgcn_kernarg_segment_ptr();
+      int32_t at = token, h = part;
+      asm volatile("" : "+s"(again), "+s"(at), "+s"(h));
+      Again& a = *(Again*)again;
+      if (ln * 16 < a.c.dim * 2)
+#pragma unroll 1
+        for (; h < a.q_heads; h += a.splits)
+          *(v4i*)(a.q_out + at * a.ot + h * a.oh + ln * 16) =
+              *(const v4i*)(a.q + at * a.qt + h * a.qh + ln * 16);
+      return;
+    }
+  }
 
   // ---- the token's sequence: the last whose start is not beyond it
   int32_t b = 0;
