@@ -375,7 +375,11 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
  *    read or written.
  *  - Pages that append, evict or extend write to must belong to one sequence
  *    alone; attention may share them.  For these calls each axis of k, and of v,
- *    steps over all that the axes within it span (no stride of 0).
+ *    steps over all that the axes within it span (no stride of 0), and no two
+ *    of k, v and their scales share a byte.  They may interleave: from the
+ *    outermost axis to the one within which they lie side by side, both then
+ *    have the same axis and stride.  (In evict, and in append with one array
+ *    of new rows, k and v may be one array.)
  *
  * Workspace: per (device, stream), grown on demand by doubling; an area is
  * kept until cache_release() (or process exit) once it has been used, so a

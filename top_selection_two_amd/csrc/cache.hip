@@ -163,6 +163,69 @@ int check_cache(const libtopk_cache_t* c, bool written, CacheParams* p,
   return LIBTOPK_OK;
 }
 
+// An array of a cache's rows, or of their scales: strides and rows in bytes.
+struct Rows {
+  const char* at;
+  RowStrides s;
+  int64_t row;
+};
+
+// Do two arrays of rows, each with its own apart, share a byte, the second `d`
+// bytes behind the first?  Taken axis by axis from the outermost on, which has
+// to be the same axis and stride in both (arrays that interleave any other way
+// count as shared): of its slices only a few, next to one another, can meet.
+bool shared(const int64_t (&n)[3], const Rows& a, const Rows& b, int64_t d,
+            unsigned done) {
+  const int64_t sa[3] = {a.s.page, a.s.head, a.s.slot};
+  const int64_t sb[3] = {b.s.page, b.s.head, b.s.slot};
+  int64_t la = a.row, lb = b.row;
+  int ia = -1, ib = -1;
+  for (int i = 0; i < 3; ++i) {
+    if (done >> i & 1 || n[i] < 2) continue;
+    la += (n[i] - 1) * sa[i];
+    lb += (n[i] - 1) * sb[i];
+    if (ia < 0 || sa[i] > sa[ia]) ia = i;
+    if (ib < 0 || sb[i] > sb[ib]) ib = i;
+  }
+  if (d >= la || d + lb <= 0) return false;
+  if (ia < 0 || ia != ib || sa[ia] != sb[ia]) return true;
+  // Slice i + k of b against slice i of a: d + k s behind it.
+  const int64_t s = sa[ia], most = n[ia] - 1;
+  la -= most * s;
+  lb -= most * s;
+  int64_t k = -(d + lb) / s - 1, last = (la - d) / s + 1;
+  if (k < -most) k = -most;
+  if (last > most) last = most;
+  for (; k <= last; ++k)
+    if (shared(n, a, b, d + k * s, done | 1u << ia)) return true;
+  return false;
+}
+
+// Are the arrays that a call writes to arrays of their own?  They may
+// interleave.  With `twins` k and v, and so their scales, may be one array.
+bool distinct(const CacheParams& c, const BlockParams& s, bool e2m1,
+              bool twins) {
+  const int64_t n[3] = {c.pages, c.heads, c.page.d};
+  if (c.pages < 1) return true;
+  const Rows x[4] = {{c.k, c.ks, c.row_bytes},
+                     {c.v, c.vs, c.row_bytes},
+                     {s.k, s.ks, s.n},
+                     {s.v, s.vs, s.n}};
+  auto same = [&](const Rows& a, const Rows& b) {
+    return a.at == b.at && (n[0] < 2 || a.s.page == b.s.page) &&
+           (n[1] < 2 || a.s.head == b.s.head) &&
+           (n[2] < 2 || a.s.slot == b.s.slot);
+  };
+  twins = twins && same(x[0], x[1]) && (!e2m1 || same(x[2], x[3]));
+  for (int i = 1; i < (e2m1 ? 4 : 2); ++i)
+    for (int j = 0; j < i; ++j)
+      if (!(twins && i == j + 1 && j != 1) &&
+          shared(n, x[j], x[i], (int64_t)((uintptr_t)x[i].at -
+                                          (uintptr_t)x[j].at), 0))
+        return false;
+  return true;
+}
+
 // Checks a ledger; its rows must not share an entry where they are written.
 int check_ledger(const libtopk_ledger_t* l, int64_t batch, int64_t heads,
                  bool positions, bool written, LedgerParams* p, Range* w,
@@ -479,6 +542,7 @@ int cache_append(const libtopk_cache_t* cache, const void* k_new,
       if (!(i == 5 && j == 4) && outs[i].meets(outs[j]))
         return LIBTOPK_ERR_INVALID;
   }
+  if (!distinct(p.c, none, false, k_new == v_new)) return LIBTOPK_ERR_INVALID;
   p.seen = seen;
   p.sinks = sinks;
   p.recent = recent;
@@ -532,6 +596,8 @@ int cache_evict(const libtopk_cache_t* cache, const int32_t* seen,
     for (int j = 0; j < (i < 3 ? i : 3); ++j)
       if (outs[i].meets(outs[j])) return LIBTOPK_ERR_INVALID;
   }
+  if (!distinct(p.c, all.s, cache->dtype == LIBTOPK_E2M1, true))
+    return LIBTOPK_ERR_INVALID;
   p.seen = seen;
   p.sinks = sinks;
   p.recent = recent;
@@ -708,6 +774,8 @@ int cache_extend(const libtopk_cache_t* cache, const libtopk_tokens_t* tokens,
     for (int j = 0; j < (i < 4 ? i : 4); ++j)
       if (outs[i].meets(outs[j])) return LIBTOPK_ERR_INVALID;
   }
+  if (!distinct(p.c, p.s, cache->dtype == LIBTOPK_E2M1, false))
+    return LIBTOPK_ERR_INVALID;
   p.q = (const char*)t.q;
   p.k = (const char*)t.k;
   p.v = (const char*)t.v;
