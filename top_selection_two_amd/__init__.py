@@ -581,8 +581,8 @@ def cache_attend(q, k, v, table, lens, scale=None, weights=None, k_scale=None,
     may be given as that pair of tensors.
 
     There is no backward pass: with inputs that require gradients, a gradient
-    through the outputs is an error (through outputs given as `out` there is
-    none)."""
+    through the outputs is an error, as are inputs with a forward-mode tangent
+    (through outputs given as `out` there is neither)."""
     return _binding.attend(q, k, v, table, lens, scale, weights, k_scale,
                            v_scale, out, k_blocks, v_blocks)
 
@@ -639,7 +639,7 @@ def cache_extend(k_new, v_new, k, v, table, lens, starts, seen=None, q=None,
     latter, and may be q itself.  Tokens of no sequence are left as they were;
     in a q that is made here their rows are those given.
     No gradient passes through the rows written; one through the queries
-    returned is an error."""
+    returned (to q, q_norm or freqs) is an error, as for cache_attend."""
     return _binding.extend(k_new, v_new, k, v, table, lens, starts, seen, q,
                            freqs, interleaved, q_norm, k_norm, eps, k_scale,
                            v_scale, weights, positions, k_blocks, v_blocks,
@@ -661,5 +661,6 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
     takes the largest.  Each setting is a number, or a tensor [B] (float32,
     top_k int32).  Returns (tokens int64 [B], logprobs float32 [B], with which
     they were drawn); out may be given as that pair of tensors.  A row without
-    a logit above -infinity gets -1.  No gradient passes through either."""
+    a logit above -infinity gets -1.  A gradient through the logprobs returned
+    (to logits or temperature) is an error, as for cache_attend."""
     return _binding.sample(logits, u, temperature, top_k, top_p, min_p, out)

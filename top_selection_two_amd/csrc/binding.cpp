@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/DeviceGuard.h>
 
+#include <initializer_list>
 #include <string>
 
 #include "libtopk.h"
@@ -260,6 +261,32 @@ void changed(const Tensor& x) {
   if (!x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
 }
 
+// The calls have no derivatives.  Where they make their outputs, one that is
+// asked for, by the inputs `in` that outputs depend on smoothly, is an error and
+// not zero: a tangent (forward mode) at once, a gradient where it is computed.
+void refuse_tangents(const char* name, PyObject* const* a,
+                     std::initializer_list<int> in) {
+  for (int i : in)
+    if (THPVariable_Check(a[i]) &&
+        torch::autograd::isFwGradDefined(THPVariable_Unpack(a[i])))
+      throw Refusal{PyExc_NotImplementedError,
+                    std::string(name) + " has no forward-mode derivative"};
+}
+void refuse_gradients(const char* name, PyObject* const* a,
+                      std::initializer_list<int> in,
+                      std::initializer_list<const Tensor*> out) {
+  if (!at::GradMode::is_enabled()) return;
+  torch::autograd::edge_list edges;
+  for (int i : in)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).requires_grad())
+      edges.push_back(
+          torch::autograd::impl::gradient_edge(THPVariable_Unpack(a[i])));
+  if (edges.empty()) return;
+  const auto node =
+      std::make_shared<torch::autograd::NotImplemented>(name, std::move(edges));
+  for (const Tensor* x : out) torch::autograd::set_history(*x, node);
+}
+
 void expect_args(Py_ssize_t n, Py_ssize_t want) {
   if (n != want) type_error("wrong number of arguments");
 }
@@ -303,6 +330,8 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n) {
                             head_scale(r, a[8], "v_scale")};
   libtopk_ledger_t l = {};
   const bool weights = a[6] != Py_None;
+  const std::initializer_list<int> smooth = {0, 1, 2, 6, 7, 8};
+  if (a[9] == Py_None) refuse_tangents("cache_attend", a, smooth);
   if (weights) l = ledger(r, a[6], "weights", nullptr, nullptr);
   const libtopk_stream_t stream = [&] {
     if (a[9] != Py_None && (!PyTuple_Check(a[9]) || PyTuple_GET_SIZE(a[9]) != 2))
@@ -330,22 +359,8 @@ PyObject* attend(PyObject* const* a, Py_ssize_t n) {
   if (a[9] != Py_None) {
     changed(out);
     changed(lse);
-  } else if (at::GradMode::is_enabled()) {
-    // There is no backward pass: one that is asked for is an error, and not a
-    // gradient of zero.
-    torch::autograd::edge_list edges;
-    for (int i : {0, 1, 2, 6, 7, 8}) {
-      if (a[i] == Py_None) continue;
-      const Tensor& x = tensor(a[i], "");
-      if (x.requires_grad())
-        edges.push_back(torch::autograd::impl::gradient_edge(x));
-    }
-    if (!edges.empty()) {
-      const auto node = std::make_shared<torch::autograd::NotImplemented>(
-          "cache_attend", std::move(edges));
-      torch::autograd::set_history(out, node);
-      torch::autograd::set_history(lse, node);
-    }
+  } else {
+    refuse_gradients("cache_attend", a, smooth, {&out, &lse});
   }
   PyObject* o = THPVariable_Wrap(std::move(out));
   PyObject* z = THPVariable_Wrap(std::move(lse));
@@ -533,6 +548,8 @@ PyObject* extend(PyObject* const* a, Py_ssize_t n) {
   libtopk_ledger_t l = {};
   const bool led = a[16] != Py_None;
   if (led) l = ledger(r, a[16], "weights", a[17], "positions");
+  const std::initializer_list<int> smooth = {8, 9, 11};
+  if (queries && a[20] == Py_None) refuse_tangents("cache_extend", a, smooth);
   const libtopk_stream_t stream = stream_of(r.device);
   Tensor out;
   if (queries) {
@@ -567,19 +584,8 @@ PyObject* extend(PyObject* const* a, Py_ssize_t n) {
   if (!queries) return Py_BuildValue("(NO)", x, Py_None);
   if (a[20] != Py_None) {
     changed(out);
-  } else if (at::GradMode::is_enabled()) {
-    // There is no backward pass: one that is asked for is an error.
-    torch::autograd::edge_list edges;
-    for (int i : {8, 11}) {
-      if (a[i] == Py_None) continue;
-      const Tensor& z = tensor(a[i], "");
-      if (z.requires_grad())
-        edges.push_back(torch::autograd::impl::gradient_edge(z));
-    }
-    if (!edges.empty())
-      torch::autograd::set_history(
-          out, std::make_shared<torch::autograd::NotImplemented>(
-                   "cache_extend", std::move(edges)));
+  } else {
+    refuse_gradients("cache_extend", a, smooth, {&out});
   }
   return Py_BuildValue("(NN)", x, THPVariable_Wrap(std::move(out)));
 }
@@ -629,6 +635,9 @@ PyObject* sample(PyObject* const* a, Py_ssize_t n) {
   how.min_p_all = (float)all[3];
   if (a[6] != Py_None && (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2))
     type_error("out: expected a pair of tensors");
+  // (logprobs depend on u, top_k, top_p and min_p by steps alone)
+  const std::initializer_list<int> smooth = {0, 2};
+  if (a[6] == Py_None) refuse_tangents("sample_logits", a, smooth);
   const libtopk_stream_t stream = stream_of(device);
   Tensor tokens, logprobs;
   if (a[6] == Py_None) {
@@ -652,13 +661,8 @@ PyObject* sample(PyObject* const* a, Py_ssize_t n) {
   if (a[6] != Py_None) {
     changed(tokens);
     changed(logprobs);
-  } else if (at::GradMode::is_enabled() && x.requires_grad()) {
-    // There is no backward pass: one that is asked for is an error.
-    torch::autograd::edge_list edges;
-    edges.push_back(torch::autograd::impl::gradient_edge(x));
-    torch::autograd::set_history(
-        logprobs, std::make_shared<torch::autograd::NotImplemented>(
-                      "sample_logits", std::move(edges)));
+  } else {
+    refuse_gradients("sample_logits", a, smooth, {&logprobs});
   }
   PyObject* y = THPVariable_Wrap(std::move(tokens));
   PyObject* z = THPVariable_Wrap(std::move(logprobs));
