@@ -665,10 +665,14 @@ int cache_debug_scramble(libtopk_stream_t stream, uint64_t seed);
  * weight 1 and the others none.  u is read as within [0, 1) (NaN as 0): at its
  * upper end the last kept token that has weight is taken.
  *
- * Weights are computed in 64 bits and added as integers in units of
- * 2^-min(51, 62 - ceil(log2 cols)) of the largest (2^-45 for 131072 logits), to
- * the nearest of which each is rounded; results do not depend on the order in
- * which workgroups run.
+ * Weights are computed in 64 bits.  The kept ones are added as integers in
+ * units of 2^-min(51, 62 - ceil(log2 cols)) of the largest (2^-45 for 131072
+ * logits), to the nearest of which each is rounded, so that one below half a
+ * unit is never drawn.  Sums of all weights of a row of at most 2^20 logits are
+ * added in 64-bit floating point instead, to 2^-46 of them: those that a row
+ * without top_k, top_p and min_p is drawn by, which draws weights down to 2^-1074
+ * of the largest, and what top_p without top_k is taken of.  Results do not
+ * depend on the order in which workgroups run.
  *
  *   logits   device, dtype[rows][cols] (LIBTOPK_F32, _BF16 or _F16), rows ld
  *            elements apart, ld >= cols, at any alignment of the type

@@ -104,3 +104,23 @@ def test_norm_weights_at_the_ends_of_float16(ctype):
     for weight in (1.5, 100.0, 2.0 ** -20):
         print("norm f16", ctype, weight, flush=True)
         _with_norm(rows, weight, 0.0, ctype, 64, "f16")
+
+
+def test_what_counts_as_a_weight():
+    """Without settings a row of at most 2^20 logits draws whatever has a
+    weight in 64 bits; where weights are added as integers, one below half a
+    unit (2^-51 of the largest here, 2^-41 of 2^20 + 1 logits) is none."""
+    for cols, gap in ((2, 40.0), (2000, 40.0), ((1 << 20) + 1, 30.0)):
+        print("sample units", cols, flush=True)
+        x = torch.full((1, cols), -float("inf"))
+        x[0, 0], x[0, cols - 1] = -gap, 0.0
+        x = x.cuda()
+        u = torch.zeros(1).cuda()
+        for how in (dict(), dict(min_p=1e-38), dict(top_k=cols - 1, min_p=1e-38),
+                    dict(top_p=0.9999999)):
+            tokens, lp = ltk.sample(x, u, **how)
+            if not how and cols < 1 << 20:
+                assert tokens.tolist() == [0]
+                assert abs(float(lp) + gap) <= gap * 2.0 ** -24
+            else:
+                assert tokens.tolist() == [cols - 1] and float(lp) == 0

@@ -9,9 +9,12 @@
 //
 // The token must not depend on how sums are ordered, nor lie beside the one
 // that exact arithmetic gives: weights are taken in 64 bits (4.4 cycles a vector
-// instruction, 2.9 in 32 bits) and added as integers, in
-// units of 2^-S of the largest, S = 62 - ceil(log2 cols) and at most 51: 2^-45
-// for 131072 logits.
+// instruction, 2.9 in 32 bits) and, where some are kept and others not, added as
+// integers, in units of 2^-S of the largest, S = 62 - ceil(log2 cols) and at
+// most 51: 2^-45 for 131072 logits.  Sums of a whole row, which one pass finds
+// from chunks that do not know the row's largest, are 64-bit floating point, of
+// terms of one sign in a fixed order: some 40 roundings and 2^-50.6 for the
+// weights, less than 2^-46 in all.
 #pragma once
 
 #include "wave.hpp"
