@@ -387,7 +387,8 @@ int histogram_i32(const int32_t *in, int64_t n, int32_t lo, int32_t shift,
  * allocated: a call that needs a larger area then returns LIBTOPK_ERR_NOMEM,
  * so make one call of the same sizes on the stream before capturing it.  A
  * captured graph uses the workspace of the stream that it was captured on:
- * its replays must not overlap with calls on that stream.
+ * its replays must not overlap with calls on that stream, nor with replays of
+ * other graphs that were captured on it.
  * ------------------------------------------------------------------------ */
 
 /* Element types of queries and cache rows. */
@@ -458,8 +459,9 @@ typedef struct libtopk_ledger {
  *
  * A sequence with no slot gets out = 0 and lse = -infinity.  Scores, weights,
  * sums and the running output are float32 (the weights that multiply bfloat16,
- * 8-bit and 4-bit rows to 2^-22); only out is rounded, once.  Results do not depend
- * on the order in which workgroups run.
+ * 8-bit and 4-bit rows to 2^-22); only out is rounded, once.  Elements of 4-bit
+ * rows below 2^-126 may count as 0.  Results do not depend on the order in which
+ * workgroups run.
  *
  * Every weight counts that float32 can hold next to the largest (scores down
  * to 87 below it); an infinite V element under one makes its column infinite

@@ -436,7 +436,8 @@ int cache_attend(const libtopk_cache_t* cache, const void* q, int32_t q_dtype,
     // cost in tiles stops growing with shorter rows, and halves of a row are
     // worth joining sooner.  (7 sequences of up to 1777 slots, 12 heads of 64
     // elements: 19.1 us as for rows of their bytes, 16.9 us so; 48 of up to
-    // 8000 slots, 8 heads of 128: 80 us at 32, 88 at 16, 84 at 64.)
+    // 8000 slots, 8 heads of 128: 80 us at 32, 88 at 16, 84 at 64.  These two
+    // are what it was measured by: 32 is the best of the powers of two there.)
     if (p.row_cost > 32) p.row_cost = 32;
     p.min_tiles = kMinTiles / 2;
   }

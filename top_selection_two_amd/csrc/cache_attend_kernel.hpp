@@ -27,10 +27,10 @@
 // of the time over bfloat16 rows, 15 % over 8-bit ones, 36 % over float16.
 //
 // Over 4-bit rows the widening to bfloat16 (exact: a code has two bits, a scale
-// none) and the softmax take more time than the bytes: some 480 vector
+// none; numbers below 2^-126 may come as 0) and the softmax take more time than the bytes: some 480 vector
 // instructions a tile, of two waves a SIMD, which 208 registers a lane allow.
 // 48 sequences of 100 to 8000 slots, 8 heads of 4 queries of 128, 0.23 GB: 81 us
-// with the weights (2.8 TB/s; 70 here, 11 in the second launch), 152 in bfloat16
+// with the weights (2.8 TB/s; profiled, 72 here and 15 in the second launch), 152 in bfloat16
 // (0.8 GB); a document of 131072 slots, 4 heads of 8: 32 us (2.3 TB/s), 51 in
 // bfloat16.  Two tiles a step took 89 and 31 us, V rows and scales read as each
 // lane needs them (2 or 4 bytes a load, which cost the address unit as much as
@@ -138,7 +138,8 @@ __device__ __forceinline__ int widen2(int v) {
 }
 
 // Two of the eight e2m1 values of a dword times their block's scale, in
-// bfloat16 (exact: it has e8m0's range).  The instruction takes the scale as
+// bfloat16 (exact, it has e8m0's range, but for numbers below 2^-126, which may
+// come as 0 from here or from the products).  The instruction takes the scale as
 // the exponent bits of a float.
 template <int BYTE>
 __device__ __forceinline__ int widen2(int v, int scale) {

@@ -11,12 +11,12 @@
 //
 // Bytes bound long calls: x is read once and y written once, a lane has 16 bytes
 // of a row (extend_kernel, below).  12 prompts of 100 to 4001 tokens, 32 + 8 + 8
-// heads of 128, bfloat16, 0.60 GB: 141 us (4.3 TB/s; a large copy reaches 5.2);
-// into 4 bits, 6 prompts of 700 to 2048 tokens, 16 + 4 + 4 heads, 90 MB: 39 us
+// heads of 128, bfloat16, 0.60 GB: 139 us (4.3 TB/s; a large copy reaches 5.2);
+// into 4 bits, 6 prompts of 700 to 2048 tokens, 16 + 4 + 4 heads, 90 MB: 40 us
 // (2.3 TB/s; the vector unit is busy half of the time with norms, turns and
 // codes).  Few tokens are dealt out row by row: a token of 64 sequences takes
 // 6 us, four dependent reads (starts, length, table, rows) and a launch; among
-// other calls 10.7, which the host needs.
+// other calls 10.9, which the host needs.
 #pragma once
 
 #include "cache_common.hpp"

@@ -557,7 +557,10 @@ __global__ __launch_bounds__(kBlock) void evict_move_kernel(
         (const v4i*)(c.k + row_offset(c.ks, jf, h, zf) + off));
     const v4i y = __builtin_nontemporal_load(
         (const v4i*)(c.v + row_offset(c.vs, jf, h, zf) + off));
-    if constexpr (BLOCKS) {  // the scales of 4-bit rows go along
+    // The scales of 4-bit rows go along, by the thread of a row's first unit.
+    // (16 prompts of up to 8192 slots cut to 2048, 8 heads of 128: 31 us in 4
+    // bits, 36 with slots outside heads; 44 and 43 in bfloat16.)
+    if constexpr (BLOCKS) {
       if (off == 0) {
         const BlockParams& s = p.s;
         const char* kf = s.k + row_offset(s.ks, jf, h, zf);

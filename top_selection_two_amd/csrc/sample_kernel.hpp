@@ -634,7 +634,7 @@ __device__ __forceinline__ void read_chunk(const char* row, int first,
 // Arithmetic bounds it, about 650 vector instructions a chunk (three quarters of
 // them in 64 bits, for the weights), where bytes would take a third of the time:
 // 256 rows of 131072 in bfloat16, 67 MB, 38 us (1.8 TB/s); 64 rows of 100003 in
-// float32 12 us (2.2 TB/s).  Rows that ask for no sum are spared it.
+// float32 14 us (1.8 TB/s).  Rows that ask for no sum are spared it.
 template <int T>
 __global__ __launch_bounds__(kBlock) void sample_chunk_kernel(SampleParams a) {
   typedef ChunkShape<T> S;
