@@ -71,12 +71,12 @@ def test_interleaved_rows_are_taken(kw):
     dict(v_blocks=FAKE + 2048), dict(v=FAKE), dict(v=FAKE + 16),
     dict(k_blocks=(FAKE << 12) + 512), dict(v_blocks=(FAKE << 12) + 2047),
     # rows and scales in one slot, one byte too near
-    dict(k_slot_stride=48, k_head_stride=768, k_page_stride=3072,
-         k_blocks=FAKE + 31, k_block_slot_stride=48, k_block_head_stride=768,
-         k_block_page_stride=3072),
-    dict(k_slot_stride=48, k_head_stride=768, k_page_stride=3072,
-         k_blocks=FAKE + 47, k_block_slot_stride=48, k_block_head_stride=768,
-         k_block_page_stride=3072),
+    dict(k_slot_stride=64, k_head_stride=1024, k_page_stride=4096,
+         k_blocks=FAKE + 31, k_block_slot_stride=64, k_block_head_stride=1024,
+         k_block_page_stride=4096),
+    dict(k_slot_stride=64, k_head_stride=1024, k_page_stride=4096,
+         k_blocks=FAKE + 63, k_block_slot_stride=64, k_block_head_stride=1024,
+         k_block_page_stride=4096),
 ], ids=str)
 def test_shared_scales_are_refused(kw):
     c = step._c4(**kw)
@@ -85,12 +85,12 @@ def test_shared_scales_are_refused(kw):
 
 @pytest.mark.parametrize("kw", [
     # rows and scales in one slot
-    dict(k_slot_stride=48, k_head_stride=768, k_page_stride=3072,
-         k_blocks=FAKE + 32, k_block_slot_stride=48, k_block_head_stride=768,
-         k_block_page_stride=3072),
-    dict(k_slot_stride=48, k_head_stride=768, k_page_stride=3072,
-         k_blocks=FAKE + 46, k_block_slot_stride=48, k_block_head_stride=768,
-         k_block_page_stride=3072),
+    dict(k_slot_stride=64, k_head_stride=1024, k_page_stride=4096,
+         k_blocks=FAKE + 32, k_block_slot_stride=64, k_block_head_stride=1024,
+         k_block_page_stride=4096),
+    dict(k_slot_stride=64, k_head_stride=1024, k_page_stride=4096,
+         k_blocks=FAKE + 62, k_block_slot_stride=64, k_block_head_stride=1024,
+         k_block_page_stride=4096),
     # all four in one page
     dict(k_page_stride=4352, v_page_stride=4352, k_block_page_stride=4352,
          v_block_page_stride=4352, v=FAKE + 2048, k_blocks=FAKE + 4096,
